@@ -18,12 +18,13 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
 
 FA_FP16, FA_BF16 = 0, 1
 FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, -1, -2, -3, -4
-FA_ERR_INTERNAL = -5
+FA_ERR_INTERNAL, FA_ERR_INDEX = -5, -6
+FA_ROPE_PLAIN, FA_ROPE_LINEAR, FA_ROPE_NTK, FA_ROPE_BY_PARTS, FA_ROPE_BANDS = 0, 1, 2, 3, 4
 FA_NOALLOC_MAX_ROWS = 1 << 20  # B*H*N limit of fa_bwd_noalloc
 
 # exported names and their signatures, in the order include/fa.h declares them
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-_u64 = ctypes.c_ulonglong
+_u64, _f64 = ctypes.c_ulonglong, ctypes.c_double
 SIGNATURES = {
     "fa_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _vp]),
     "fa_fwd_blocksparse": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _vp, _vp]),
@@ -50,6 +51,15 @@ SIGNATURES = {
     "fa_decode_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "fa_decode": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp,
                        _sz, _vp]),
+    "fa_rope_frequencies": (_i, [_vp, _vp, _i, _f64, _i, _f64, _f64, _f64, _f64]),
+    "fa_rope": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
+                     _vp]),
+    "fa_paged_check": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i]),
+    "fa_paged_append": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i,
+                             _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp]),
+    "fa_paged_attn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
+    "fa_paged_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
+                           _i, _i, _i, _f, _i, _vp, _sz, _vp]),
     "fa_sync_status": (_i, [_vp]),
     "fa_status_string": (ctypes.c_char_p, [_i]),
     "fa_debug_set_visit_log": (_i, [_vp, _sz]),
@@ -390,6 +400,294 @@ def bwd_dropout(q, k, v, o, lse, dout, p_drop: float, seed: int, offset: int = 0
                               int(bool(causal)), mask_ptr, float(p_drop), int(seed), int(offset),
                               _stream(stream, q)), "fa_bwd_dropout")
     return dq, dk, dv
+
+
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+    else torch.cuda.current_device
+
+
+def _elsewhere(call, stream, device, tensors):
+    """call() with `device` current and its launches and allocations on `stream`.  Tensors that
+    belong to other streams are marked as used on it, so that their memory is not handed out
+    again while the call's work may still read it."""
+    if stream is not None and stream.device != device:
+        raise ValueError("stream must belong to the tensors' device")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        result = call()
+        if stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+    return result
+
+
+def _on_device(dev: int, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the same device as the others")
+
+
+def _int32(t, name, shape):
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {list(shape)}")
+
+
+def _freq_table(freq, d: int) -> int:
+    """Checks a frequency table; the number of rotated elements."""
+    if freq.dtype != torch.int64 or freq.dim() != 1 or not freq.is_contiguous():
+        raise ValueError("freq must be a contiguous int64 table of rope_frequencies()")
+    return 2 * freq.shape[0]
+
+
+_SCALINGS = {"plain": FA_ROPE_PLAIN, "linear": FA_ROPE_LINEAR, "ntk": FA_ROPE_NTK,
+             "by_parts": FA_ROPE_BY_PARTS, "bands": FA_ROPE_BANDS}
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain",
+                     factor: float = 1.0, original_len: float = 0.0, low: float = 0.0,
+                     high: float = 0.0, device=None) -> Tuple[torch.Tensor, float]:
+    """The frequency table of rotary positions and its mscale (fa_rope_frequencies).
+
+    The table (int64 bits of turns per position in units of 2^-64) is laid out once and passed to
+    rope, rope_bwd and paged_append.  scaling: "plain", "linear", "ntk", "by_parts" or "bands";
+    factor, original_len, low and high as its formula wants them.
+    """
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
+    table = torch.empty(max(rot_dim // 2, 0), dtype=torch.int64)
+    mscale = ctypes.c_float()
+    _check(load().fa_rope_frequencies(table.data_ptr() or None, ctypes.addressof(mscale), rot_dim,
+                                      base, _SCALINGS[scaling], factor, original_len, low, high),
+           "fa_rope_frequencies")
+    return table.to(device) if device is not None else table, float(mscale.value)
+
+
+def _rope(q, k, freq, positions, interleaved, mscale, out_q, out_k, inverse, stream):
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    if stream is not None or dev != _current_device():
+        return _elsewhere(lambda: _rope(q, k, freq, positions, interleaved, mscale, out_q, out_k,
+                                        inverse, None),
+                          stream, q.device, (q, k, freq, positions, out_q, out_k))
+    _on_device(dev, k=k, freq=freq, positions=positions, out_q=out_q, out_k=out_k)
+    B, H, N, d = _shape(q)
+    rot = _freq_table(freq, d)
+    dtype = _dtype_code(q)
+    Hkv = 0
+    if k is not None:
+        kb, Hkv, kn, kd = _shape(k)
+        if kb != B or kn != N or kd != d or k.dtype != q.dtype:
+            raise ValueError("k must be [B, H_kv, N, d] with the dtype of q")
+    elif out_k is not None:
+        raise ValueError("out_k needs k")
+    if positions is not None:
+        _int32(positions, "positions", (B, N))
+    if out_q is None:
+        out_q = q.new_empty((B, H, N, d))
+    elif out_q.shape != q.shape or out_q.dtype != q.dtype:
+        raise ValueError("out_q must match q in shape and dtype")
+    if k is not None:
+        if out_k is None:
+            out_k = k.new_empty((B, Hkv, N, d))
+        elif out_k.shape != k.shape or out_k.dtype != k.dtype:
+            raise ValueError("out_k must match k in shape and dtype")
+    st = q.stride() + out_q.stride()
+    if k is not None:
+        st += k.stride() + out_k.stride()
+    if any(x != 1 for x in st[3::4]):
+        raise ValueError("the rows of q, k and the outputs must be contiguous")
+    strides = (ctypes.c_longlong * 12)(*(x for i, x in enumerate(st) if i & 3 != 3))
+    _check(load().fa_rope(q.data_ptr(), out_q.data_ptr(), None if k is None else k.data_ptr(),
+                          None if k is None else out_k.data_ptr(), strides, freq.data_ptr(),
+                          None if positions is None else positions.data_ptr(), B, H, Hkv, N, d,
+                          rot, dtype, int(bool(interleaved)), inverse, mscale, _raw(dev)),
+           "fa_rope")
+    return out_q if k is None else (out_q, out_k)
+
+
+def _raw(dev: int) -> int:
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def rope(q, k, freq, positions=None, interleaved: bool = False, mscale: float = 1.0, out_q=None,
+         out_k=None, stream=None):
+    """q [B, H, N, d] and k [B, H_kv, N, d] turned to their positions in one launch (fa_rope).
+
+    k may be None: then only q's result is returned.  freq: a table of rope_frequencies() on the
+    device; it rotates the first 2 * len(freq) elements of a row.  positions: int32 [B, N], or None
+    for 0 .. N - 1.  Any strides with contiguous rows will do (slices of a joint projection);
+    results are dense unless out_q, out_k are given, which may be q and k themselves.
+    """
+    return _rope(q, k, freq, positions, interleaved, mscale, out_q, out_k, 0, stream)
+
+
+def rope_bwd(dq, dk, freq, positions=None, interleaved: bool = False, mscale: float = 1.0,
+             out_q=None, out_k=None, stream=None):
+    """The gradients of rope's q and k from those of its results (fa_rope with inverse set).
+
+    out_q and out_k may be slices of the joint projection's gradient.
+    """
+    return _rope(dq, dk, freq, positions, interleaved, mscale, out_q, out_k, 1, stream)
+
+
+def _paged_shapes(q, k_pages, v_pages, block_table, kv_len, q_start):
+    """T, H, H_kv, d, num_pages, page_size, B, max_pages of a paged batch (q or k: [T, heads, d])."""
+    if q.dim() != 3:
+        raise ValueError("tokens must be [T, heads, d]")
+    T, H, d = q.shape
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != d \
+            or k_pages.dtype != q.dtype or v_pages.dtype != q.dtype:
+        raise ValueError("k_pages and v_pages must be [num_pages, H_kv, page_size, d] with the dtype "
+                         "of the tokens")
+    num_pages, Hkv, page_size, _ = k_pages.shape
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous int32 [B, max_pages]")
+    B, max_pages = block_table.shape
+    _int32(kv_len, "kv_len", (B,))
+    if q_start is not None:
+        _int32(q_start, "q_start", (B + 1,))
+    return T, H, Hkv, d, num_pages, page_size, B, max_pages
+
+
+def paged_check(block_table, kv_len, q_start, num_pages: int, page_size: int,
+                max_q: Optional[int] = None, tokens: Optional[int] = None) -> bool:
+    """Whether CPU copies of a batch's index arrays are in range (fa_paged_check).
+
+    tokens: T of the batch, when q_start is None (tokens / B each) or the batch is padded.
+    """
+    for name, t in (("block_table", block_table), ("kv_len", kv_len), ("q_start", q_start)):
+        if t is not None and (t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 CPU tensor")
+    B, max_pages = block_table.shape
+    if kv_len.shape != (B,) or (q_start is not None and q_start.shape != (B + 1,)):
+        raise ValueError("kv_len must be [B] and q_start [B + 1]")
+    if tokens is None:
+        tokens = B if q_start is None else int(q_start[-1])
+    rc = load().fa_paged_check(block_table.data_ptr(), kv_len.data_ptr(),
+                               None if q_start is None else q_start.data_ptr(), tokens, B,
+                               num_pages, page_size, max_pages, tokens if max_q is None else max_q)
+    if rc == FA_ERR_INDEX:
+        return False
+    _check(rc, "fa_paged_check")
+    return True
+
+
+def paged_append(k, v, k_pages, v_pages, block_table, kv_len, q_start=None, q=None, out_q=None,
+                 freq=None, positions=None, interleaved: bool = False, mscale: float = 1.0,
+                 stream=None):
+    """New tokens' k (rotated) and v [T, H_kv, d] into the paged cache (fa_paged_append).
+
+    k_pages, v_pages: [num_pages, H_kv, page_size, d]; block_table int32 [B, max_pages]; kv_len int32
+    [B], the new tokens included; q_start int32 [B + 1], or None for T / B tokens each.  With
+    q [T, H, d] its rotated copy is returned (written to out_q, which may be q).  freq: a table of
+    rope_frequencies(), or None for no rotation; positions int32 [T] rotates to other positions
+    than the places in the cache.
+    """
+    dev = k.get_device()
+    if dev < 0:
+        raise ValueError("k must be a CUDA tensor")
+    if stream is not None or dev != _current_device():
+        return _elsewhere(lambda: paged_append(k, v, k_pages, v_pages, block_table, kv_len, q_start,
+                                               q, out_q, freq, positions, interleaved, mscale),
+                          stream, k.device, (k, v, k_pages, v_pages, block_table, kv_len, q_start, q,
+                                             out_q, freq, positions))
+    _on_device(dev, v=v, k_pages=k_pages, v_pages=v_pages, block_table=block_table, kv_len=kv_len,
+               q_start=q_start, q=q, out_q=out_q, freq=freq, positions=positions)
+    T, Hkv, pool_heads, d, num_pages, page_size, B, max_pages = \
+        _paged_shapes(k, k_pages, v_pages, block_table, kv_len, q_start)
+    if Hkv != pool_heads or v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be [T, H_kv, d] with the H_kv and dtype of the pages")
+    dtype = _dtype_code(k)
+    rot = 0 if freq is None else _freq_table(freq, d)
+    if positions is not None:
+        _int32(positions, "positions", (T,))
+    H, st = Hkv, (0, 0, 1, 8, 8, 1)
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d or q.dtype != k.dtype:
+            raise ValueError("q must be [T, H, d] with the dtype of k")
+        H = q.shape[1]
+        if out_q is None:
+            out_q = q.new_empty((T, H, d))
+        elif out_q.shape != q.shape or out_q.dtype != q.dtype:
+            raise ValueError("out_q must match q in shape and dtype")
+        st = q.stride() + out_q.stride()
+    elif out_q is not None:
+        raise ValueError("out_q needs q")
+    st += k.stride() + v.stride()
+    ps = k_pages.stride() + v_pages.stride()
+    if st[2::3] != (1, 1, 1, 1) or ps[3::4] != (1, 1):
+        raise ValueError("the rows of q, k, v and the pages must be contiguous")
+    strides = (ctypes.c_longlong * 14)(st[0], st[1], st[3], st[4], st[6], st[7], st[9], st[10],
+                                       *ps[:3], *ps[4:7])
+    _check(load().fa_paged_append(
+        None if q is None else q.data_ptr(), None if q is None else out_q.data_ptr(), k.data_ptr(),
+        v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), strides, block_table.data_ptr(),
+        kv_len.data_ptr(), None if q_start is None else q_start.data_ptr(),
+        None if positions is None else positions.data_ptr(),
+        None if freq is None else freq.data_ptr(), T, B, H, Hkv, d, num_pages, page_size, max_pages,
+        rot, dtype, int(bool(interleaved)), mscale, _raw(dev)), "fa_paged_append")
+    return out_q
+
+
+def paged_workspace_bytes(T: int, B: int, H: int, H_kv: int, d: int, max_q: int, page_size: int,
+                          max_pages: int) -> int:
+    return int(load().fa_paged_attn_workspace_bytes(T, B, H, H_kv, d, max_q, page_size, max_pages))
+
+
+def paged_attention(q, k_pages, v_pages, block_table, kv_len, q_start=None,
+                    max_q: Optional[int] = None, scale: Optional[float] = None,
+                    causal: bool = True, out=None, lse=None, workspace=None, stream=None):
+    """O, LSE of every sequence's new tokens q [T, H, d] over its paged cache (fa_paged_attn).
+
+    The cache (see paged_append) already holds the new tokens' keys and values; row i of the n new
+    ones of sequence b sees keys j <= kv_len[b] - n + i, or with causal=False all kv_len[b].  max_q:
+    the most new tokens that any sequence brings, when the caller knows it.  LSE is fp32 [T, H].
+    """
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    if stream is not None or dev != _current_device():
+        return _elsewhere(lambda: paged_attention(q, k_pages, v_pages, block_table, kv_len, q_start,
+                                                  max_q, scale, causal, out, lse, workspace),
+                          stream, q.device, (q, k_pages, v_pages, block_table, kv_len, q_start, out,
+                                             lse, workspace))
+    _on_device(dev, k_pages=k_pages, v_pages=v_pages, block_table=block_table, kv_len=kv_len,
+               q_start=q_start, out=out, lse=lse, workspace=workspace)
+    T, H, Hkv, d, num_pages, page_size, B, max_pages = \
+        _paged_shapes(q, k_pages, v_pages, block_table, kv_len, q_start)
+    dtype = _dtype_code(q)
+    lib = load()
+    if max_q is None:
+        max_q = T if q_start is not None else max(T // max(B, 1), 1)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = q.new_empty((T, H, d))
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must match q in shape and dtype")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [T, H]")
+    st = q.stride() + out.stride()
+    ps = k_pages.stride() + v_pages.stride()
+    if st[2::3] != (1, 1) or ps[3::4] != (1, 1):
+        raise ValueError("the rows of q, out and the pages must be contiguous")
+    nbytes = lib.fa_paged_attn_workspace_bytes(T, B, H, Hkv, d, max_q, page_size, max_pages)
+    if workspace is None:
+        if nbytes > 0:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError("workspace must be contiguous, of paged_workspace_bytes() bytes")
+    strides = (ctypes.c_longlong * 10)(st[0], st[1], st[3], st[4], *ps[:3], *ps[4:7])
+    _check(lib.fa_paged_attn(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        strides, block_table.data_ptr(), kv_len.data_ptr(),
+        None if q_start is None else q_start.data_ptr(), T, B, H, Hkv, d, num_pages, page_size,
+        max_pages, max_q, dtype, scale, int(bool(causal)),
+        None if workspace is None else workspace.data_ptr(), nbytes, _raw(dev)), "fa_paged_attn")
+    return out, lse
 
 
 def sync_status(stream=None) -> int:

@@ -2,6 +2,7 @@
 // per-device status word that bounded pipeline waits report into.  See include/fa.h.
 #include "fa.h"
 #include "fa_internal.h"
+#include "paged.cuh"
 
 #include <cmath>
 #include <cstdio>
@@ -456,6 +457,65 @@ int noalloc_scratch(int dev, float **out) {
     return FA_OK;
 }
 
+// Strides of a caller's tensors, in elements.  16-byte pieces of every row have to be aligned, so
+// each is a multiple of 8; zero (a broadcast input) is allowed where nothing is written; that of an
+// axis of extent 1 is never used and replaced.  Returns the strides to use in out[].
+int take_strides(const long long *s, std::initializer_list<long long> extents, bool written,
+                 long long *out) {
+    int i = 0;
+    for (long long n : extents) {
+        out[i] = n == 1 ? 8 : s[i];
+        if (out[i] < (written ? 8 : 0) || out[i] % 8 != 0 || out[i] >= (1ll << 39))
+            return FA_ERR_INVALID;
+        ++i;
+    }
+    return FA_OK;
+}
+
+int check_rot(int rot_dim, int d) {
+    return rot_dim >= 16 && rot_dim <= d && rot_dim % 16 == 0 ? FA_OK : FA_ERR_UNSUPPORTED;
+}
+
+// Sizes of a paged batch; fills the view except for its pointers.
+int check_paged(int T, int B, int H, int Hkv, int d, int num_pages, int page_size, int max_pages,
+                int dtype, fa::PagedView *c) {
+    if (T < 1 || B < 1 || H < 1 || num_pages < 1 || page_size < 1 || max_pages < 1)
+        return FA_ERR_INVALID;
+    if (check_heads(H, Hkv) != FA_OK) return FA_ERR_INVALID;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_INVALID;
+    if (static_cast<long long>(T) * (H + 2ll * Hkv) >= (1ll << 31) ||
+        static_cast<long long>(num_pages) * page_size >= (1ll << 31) ||
+        static_cast<long long>(max_pages) * page_size >= (1ll << 31))
+        return FA_ERR_INVALID;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
+        return FA_ERR_UNSUPPORTED;
+    int shift = 0;
+    while ((1 << shift) < page_size) ++shift;
+    c->T = T;
+    c->B = B;
+    c->H = H;
+    c->Hkv = Hkv;
+    c->num_pages = num_pages;
+    c->page_shift = shift;
+    c->max_pages = max_pages;
+    c->max_q = T;
+    c->status = nullptr;
+    return FA_OK;
+}
+
+// The index arrays of a paged batch: int32, the uniform batch (no q_start) divides evenly.
+int check_paged_index(const int *table, const int *kv_len, const int *q_start, fa::PagedView *c) {
+    for (const void *x : {static_cast<const void *>(table), static_cast<const void *>(kv_len)})
+        if (x == nullptr || (reinterpret_cast<uintptr_t>(x) & 3u) != 0) return FA_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(q_start) & 3u) != 0) return FA_ERR_INVALID;
+    if (q_start == nullptr && c->T % c->B != 0) return FA_ERR_INVALID;
+    c->table = table;
+    c->kv_len = kv_len;
+    c->q_start = q_start;
+    return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -679,6 +739,227 @@ int fa_decode(const void *q, const void *k, const void *v, void *o, float *lse,
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+int fa_rope_frequencies(uint64_t *freq, float *mscale, int rot_dim, double base, int scaling,
+                        double factor, double original_len, double low, double high) {
+    if (freq == nullptr || rot_dim < 2 || rot_dim % 2 != 0 || !(std::isfinite(base) && base > 1.0))
+        return FA_ERR_INVALID;
+    if (scaling < FA_ROPE_PLAIN || scaling > FA_ROPE_BANDS) return FA_ERR_INVALID;
+    if (scaling != FA_ROPE_PLAIN && !(std::isfinite(factor) && factor >= 1.0)) return FA_ERR_INVALID;
+    const bool mixed = scaling == FA_ROPE_BY_PARTS || scaling == FA_ROPE_BANDS;
+    if (mixed && !(std::isfinite(original_len) && original_len > 0.0 && std::isfinite(low) &&
+                   std::isfinite(high) && 0.0 < low && low < high))
+        return FA_ERR_INVALID;
+    const double two_pi = 6.283185307179586476925;
+    if (scaling == FA_ROPE_NTK) {
+        if (rot_dim < 4) return FA_ERR_INVALID;
+        base *= std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+    }
+    // by parts: the pair (counted from 0, as a real number) that turns `r` times over the
+    // original length
+    auto pair_of = [&](double r) {
+        return rot_dim * std::log(original_len / (r * two_pi)) / (2.0 * std::log(base));
+    };
+    double first = 0.0, last = 1.0;
+    if (scaling == FA_ROPE_BY_PARTS) {
+        first = std::fmax(std::floor(pair_of(high)), 0.0);
+        last = std::fmin(std::ceil(pair_of(low)), rot_dim - 1.0);
+        if (last <= first) last = first + 0.001;  // a step, no division by zero
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot_dim);  // radians per position
+        if (scaling == FA_ROPE_LINEAR) {
+            f /= factor;
+        } else if (scaling == FA_ROPE_BY_PARTS) {
+            const double ramp = std::fmin(std::fmax((i - first) / (last - first), 0.0), 1.0);
+            f = f * (1.0 - ramp) + f / factor * ramp;
+        } else if (scaling == FA_ROPE_BANDS) {
+            const double rounds = original_len * f / two_pi;
+            const double keep = std::fmin(std::fmax((rounds - low) / (high - low), 0.0), 1.0);
+            f = f * keep + f / factor * (1.0 - keep);
+        }
+        double turns = f / two_pi;
+        turns -= std::floor(turns);
+        const double units = std::ldexp(turns, 64);  // exact; below 2^64 since turns < 1
+        freq[i] = static_cast<uint64_t>(units);
+    }
+    if (mscale != nullptr)
+        *mscale = scaling == FA_ROPE_BY_PARTS ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+    return FA_OK;
+}
+
+int fa_rope(const void *q, void *q_out, const void *k, void *k_out, const long long *strides,
+            const uint64_t *freq, const int *positions, int B, int H, int H_kv, int N, int d,
+            int rot_dim, int dtype, int interleaved, int inverse, float mscale, void *stream) {
+    int rc = check_shape(B, H, N, d, dtype, mscale);
+    if (rc != FA_OK) return rc;
+    if (k != nullptr ? H_kv < 1 || static_cast<long long>(B) * H_kv * N >= (1ll << 31) : H_kv != 0)
+        return FA_ERR_INVALID;
+    rc = check_rot(rot_dim, d);
+    if (rc != FA_OK) return rc;
+    rc = check_ptrs({q, q_out, freq});
+    if (rc == FA_OK && k != nullptr) rc = check_ptrs({k, k_out});
+    if (rc != FA_OK) return rc;
+    if ((reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return FA_ERR_INVALID;
+    if (static_cast<long long>(H) + H_kv > 65535) return FA_ERR_INVALID;
+    const long long qb = static_cast<long long>(H) * N * d, kb = static_cast<long long>(H_kv) * N * d;
+    const long long row = d, head = static_cast<long long>(N) * d;
+    const long long dense[12] = {qb, head, row, qb, head, row, kb, head, row, kb, head, row};
+    const long long *given = strides != nullptr ? strides : dense;
+    long long s[12] = {};
+    for (int i = 0; i < (k != nullptr ? 12 : 6); i += 3) {
+        rc = take_strides(given + i, {B, i < 6 ? H : H_kv, N}, i % 6 == 3, s + i);
+        if (rc != FA_OK) return rc;
+    }
+    int dev = 0, *status = nullptr;
+    rc = device_setup(&dev, &status);
+    if (rc != FA_OK) return rc;
+    fa::RopeParams p = {};
+    auto side = [&](fa::RopeSide *x, const void *in, void *out, const long long *t) {
+        x->in = static_cast<const uint16_t *>(in);
+        x->out = static_cast<uint16_t *>(out);
+        x->in_b = t[0], x->in_h = t[1], x->in_n = t[2];
+        x->out_b = t[3], x->out_h = t[4], x->out_n = t[5];
+    };
+    side(&p.q, q, q_out, s);
+    if (k != nullptr) side(&p.k, k, k_out, s + 6);
+    p.freq = reinterpret_cast<const unsigned long long *>(freq);
+    p.positions = positions;
+    p.rows = static_cast<long>(B) * N;
+    p.N = N;
+    p.H = H;
+    p.Hkv = H_kv;
+    p.rot = rot_dim;
+    p.inverse = inverse ? 1 : 0;
+    p.mscale = mscale;
+    cudaError_t e = fa::launch_rope(p, d, dtype == FA_BF16, interleaved != 0,
+                                    static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_paged_check(const int *block_table, const int *kv_len, const int *q_start, int T, int B,
+                   int num_pages, int page_size, int max_pages, int max_q) {
+    fa::PagedView c = {};
+    int rc = check_paged(T, B, 1, 1, 64, num_pages, page_size, max_pages, FA_BF16, &c);
+    if (rc != FA_OK) return rc;
+    if (max_q < 1) return FA_ERR_INVALID;
+    rc = check_paged_index(block_table, kv_len, q_start, &c);
+    if (rc != FA_OK) return rc;
+    c.max_q = max_q;
+    for (int b = 0; b < B; ++b) {
+        const fa::PagedSeq s = fa::paged_seq(c, b);
+        if (s.bad) return FA_ERR_INDEX;
+        for (long pos = 0; pos < s.len; pos += page_size)
+            if (fa::paged_page(c, b, static_cast<int>(pos)) < 0) return FA_ERR_INDEX;
+    }
+    return FA_OK;
+}
+
+int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, void *k_pages,
+                    void *v_pages, const long long *strides, const int *block_table,
+                    const int *kv_len, const int *q_start, const int *positions,
+                    const uint64_t *freq, int T, int B, int H, int H_kv, int d, int num_pages,
+                    int page_size, int max_pages, int rot_dim, int dtype, int interleaved,
+                    float mscale, void *stream) {
+    fa::PagedAppendParams p = {};
+    int rc = check_paged(T, B, H, H_kv, d, num_pages, page_size, max_pages, dtype, &p.c);
+    if (rc != FA_OK) return rc;
+    rc = check_paged_index(block_table, kv_len, q_start, &p.c);
+    if (rc != FA_OK) return rc;
+    rc = check_ptrs({k, v, k_pages, v_pages});
+    if (rc == FA_OK && q != nullptr) rc = check_ptrs({q, q_out});
+    if (rc == FA_OK && freq != nullptr) {
+        rc = check_ptrs({freq});
+        if (rc == FA_OK) rc = check_rot(rot_dim, d);
+        if (rc == FA_OK && !(std::isfinite(mscale) && mscale > 0.f)) rc = FA_ERR_INVALID;
+    }
+    if (rc != FA_OK) return rc;
+    if ((reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return FA_ERR_INVALID;
+    const long long row = d, slab = static_cast<long long>(page_size) * d;
+    const long long dense[14] = {H * row, row, H * row, row, H_kv * row, row, H_kv * row, row,
+                                 H_kv * slab, slab, row, H_kv * slab, slab, row};
+    const long long *given = strides != nullptr ? strides : dense;
+    long long s[14] = {};
+    for (int i = q != nullptr ? 0 : 4; i < 8 && rc == FA_OK; i += 2)  // q, q_out, k, v
+        rc = take_strides(given + i, {T, i < 4 ? H : H_kv}, i == 2, s + i);
+    for (int i = 8; i < 14 && rc == FA_OK; i += 3)  // k_pages, v_pages
+        rc = take_strides(given + i, {num_pages, H_kv, page_size}, true, s + i);
+    if (rc != FA_OK) return rc;
+    int dev = 0;
+    rc = device_setup(&dev, &p.c.status);
+    if (rc != FA_OK) return rc;
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(k);
+    p.v = static_cast<const uint16_t *>(v);
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.k_pages = static_cast<uint16_t *>(k_pages);
+    p.v_pages = static_cast<uint16_t *>(v_pages);
+    p.q_t = s[0], p.q_h = s[1], p.qo_t = s[2], p.qo_h = s[3];
+    p.k_t = s[4], p.k_h = s[5], p.v_t = s[6], p.v_h = s[7];
+    p.kp_p = s[8], p.kp_h = s[9], p.kp_r = s[10];
+    p.vp_p = s[11], p.vp_h = s[12], p.vp_r = s[13];
+    p.freq = reinterpret_cast<const unsigned long long *>(freq);
+    p.positions = positions;
+    p.rot = rot_dim;
+    p.mscale = mscale;
+    cudaError_t e = fa::launch_paged_append(p, d, dtype == FA_BF16, interleaved != 0,
+                                            static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_paged_attn_workspace_bytes(int T, int B, int H, int H_kv, int d, int max_q,
+                                     int page_size, int max_pages) {
+    fa::PagedView c = {};
+    if (max_q < 1 || check_paged(T, B, H, H_kv, d, 1, page_size, max_pages, FA_BF16, &c) != FA_OK)
+        return 0;
+    return 0;
+}
+
+int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void *o, float *lse,
+                  const long long *strides, const int *block_table, const int *kv_len,
+                  const int *q_start, int T, int B, int H, int H_kv, int d, int num_pages,
+                  int page_size, int max_pages, int max_q, int dtype, float scale, int causal,
+                  void *workspace, size_t workspace_bytes, void *stream) {
+    fa::PagedAttnParams p = {};
+    int rc = check_paged(T, B, H, H_kv, d, num_pages, page_size, max_pages, dtype, &p.c);
+    if (rc != FA_OK) return rc;
+    if (max_q < 1 || !(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID;
+    if (H / H_kv > 128) return FA_ERR_UNSUPPORTED;
+    rc = check_paged_index(block_table, kv_len, q_start, &p.c);
+    if (rc != FA_OK) return rc;
+    rc = check_ptrs({q, k_pages, v_pages, o, lse});
+    if (rc != FA_OK) return rc;
+    const long long row = d, slab = static_cast<long long>(page_size) * d;
+    const long long dense[10] = {H * row, row, H * row, row, H_kv * slab, slab, row,
+                                 H_kv * slab, slab, row};
+    const long long *given = strides != nullptr ? strides : dense;
+    long long s[10] = {};
+    for (int i = 0; i < 4 && rc == FA_OK; i += 2)  // q, o
+        rc = take_strides(given + i, {T, H}, i == 2, s + i);
+    for (int i = 4; i < 10 && rc == FA_OK; i += 3)  // k_pages, v_pages
+        rc = take_strides(given + i, {num_pages, H_kv, page_size}, true, s + i);
+    if (rc != FA_OK) return rc;
+    const size_t need = fa_paged_attn_workspace_bytes(T, B, H, H_kv, d, max_q, page_size, max_pages);
+    if (need > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need))
+        return FA_ERR_INVALID;
+    int dev = 0;
+    rc = device_setup(&dev, &p.c.status);
+    if (rc != FA_OK) return rc;
+    p.c.max_q = max_q;
+    p.q = static_cast<const uint16_t *>(q);
+    p.k_pages = static_cast<const uint16_t *>(k_pages);
+    p.v_pages = static_cast<const uint16_t *>(v_pages);
+    p.o = static_cast<uint16_t *>(o);
+    p.lse = lse;
+    p.q_t = s[0], p.q_h = s[1], p.o_t = s[2], p.o_h = s[3];
+    p.kp_p = s[4], p.kp_h = s[5], p.kp_r = s[6];
+    p.vp_p = s[7], p.vp_h = s[8], p.vp_r = s[9];
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.causal = causal ? 1 : 0;
+    if (make_ctl(p.c.status, 0, 0, &p.ctl) != FA_OK) return FA_ERR_INVALID;
+    cudaError_t e = fa::launch_paged_attn(p, d, dtype == FA_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 int fa_sync_status(void *stream) {
     int dev = 0, *status = nullptr;
     int rc = device_setup(&dev, &status);
@@ -699,6 +980,7 @@ const char *fa_status_string(int code) {
         case FA_ERR_UNSUPPORTED: return "unsupported head dimension or device";
         case FA_ERR_CUDA: return "CUDA runtime error";
         case FA_ERR_TIMEOUT: return "device pipeline wait timed out";
+        case FA_ERR_INDEX: return "page id, token offset or length out of range";
         case FA_ERR_INTERNAL: return "kernel found its shared memory misaligned";
         default: return "unknown status";
     }

@@ -55,9 +55,25 @@ enum {
     FA_ERR_UNSUPPORTED = -2,  /* head dimension other than 64/128, or no sm_103 device */
     FA_ERR_CUDA = -3,         /* a CUDA runtime call failed (launch, attribute, symbol) */
     FA_ERR_TIMEOUT = -4,      /* a device pipeline wait ran out of time (from fa_sync_status) */
-    FA_ERR_INTERNAL = -5      /* a kernel found its shared memory misplaced (its base not
+    FA_ERR_INTERNAL = -5,     /* a kernel found its shared memory misplaced (its base not
                                  1024-byte aligned) and returned without computing; never
                                  expected (from fa_sync_status) */
+    FA_ERR_INDEX = -6         /* an index array on the device (page ids, token offsets, lengths)
+                                 holds a value out of range; what it named was not accessed
+                                 (from fa_sync_status), or fa_paged_check found it on the host */
+};
+
+/* How fa_rope_frequencies stretches the positions for contexts longer than the trained one. */
+enum {
+    FA_ROPE_PLAIN = 0,        /* not at all */
+    FA_ROPE_LINEAR = 1,       /* every frequency divided by factor */
+    FA_ROPE_NTK = 2,          /* base multiplied by factor^(rot_dim / (rot_dim - 2)) */
+    FA_ROPE_BY_PARTS = 3,     /* a linear ramp over the pairs between the one that turns `high`
+                                 times over original_len (kept) and the one that turns `low`
+                                 times (divided by factor); mscale = 0.1 ln(factor) + 1 */
+    FA_ROPE_BANDS = 4         /* pairs that turn at least `high` times over original_len kept,
+                                 those that turn at most `low` times divided by factor, a linear
+                                 blend in the number of turns between */
 };
 
 /*
@@ -240,6 +256,108 @@ size_t fa_decode_workspace_bytes(int B, int H, int H_kv, int Nq, int Nk, int d);
 int fa_decode(const void *q, const void *k, const void *v, void *o, float *lse,
               const int *kv_len, int B, int H, int H_kv, int Nq, int Nk, int d, int dtype,
               float scale, int causal, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary positions.  Pair j of a row at position p is turned by the angle p * f_j and scaled:
+ * (a, c) -> mscale * (a cos - c sin, c cos + a sin).  The first rot_dim elements of a row hold
+ * rot_dim / 2 pairs: elements (j, j + rot_dim / 2), or (2j, 2j + 1) when interleaved != 0; the
+ * elements behind them are copied as they are.
+ *   freq      : device uint64 [rot_dim / 2], 16-byte aligned: f_j as turns per position in units
+ *               of 2^-64 turns (rounded down), so that p * f_j modulo a turn is exact integer
+ *               arithmetic at any int32 position, negative ones included.
+ *   positions : device int32 [B, N], or NULL for 0 .. N - 1 in every sequence.
+ *   q, q_out  : [B,H,N,d];  k, k_out : [B,H_kv,N,d], or NULL with H_kv = 0 (Q alone).  H_kv need
+ *               not divide H here.
+ *   strides   : host array of 12 strides in elements: batch, head and row of q, of q_out, of k and
+ *               of k_out (the last six are not read without k); NULL for dense tensors.  Rows are
+ *               contiguous; strides are multiples of 8 below 2^39, at least 0 for the inputs and
+ *               at least 8 for the outputs (that of an axis of
+ *               extent 1 is not looked at), and no two elements of an output may share a place.
+ *               An output may be its input with the same strides (in place); any other overlap is
+ *               undefined.
+ *   inverse   : != 0 turns by -p f_j: with the same mscale this is the transpose of the forward,
+ *               which takes the gradients of q_out and k_out to those of q and k.
+ * d is 64 or 128; rot_dim is a multiple of 16, at most d (otherwise FA_ERR_UNSUPPORTED); mscale is
+ * finite and > 0.  Products and sums are fp32, rounded once.
+ *
+ * fa_rope_frequencies fills freq (HOST memory, rot_dim / 2 values; rot_dim >= 2 and even) from
+ * f_j = base^(-2 j / rot_dim) radians per position, stretched as `scaling` (FA_ROPE_*) says, and
+ * *mscale (may be NULL).  factor >= 1, original_len > 0 and 0 < low < high are looked at only
+ * where the scaling uses them.
+ */
+int fa_rope_frequencies(uint64_t *freq, float *mscale, int rot_dim, double base, int scaling,
+                        double factor, double original_len, double low, double high);
+int fa_rope(const void *q, void *q_out, const void *k, void *k_out, const long long *strides,
+            const uint64_t *freq, const int *positions, int B, int H, int H_kv, int N, int d,
+            int rot_dim, int dtype, int interleaved, int inverse, float mscale, void *stream);
+
+/*
+ * Paged K/V cache.  The cache is a pool of num_pages pages; a page holds page_size positions of
+ * all H_kv heads.  A batch brings T new tokens of B sequences, token-major: sequence b has the
+ * tokens [q_start[b], q_start[b + 1]) and, counting them, kv_len[b] positions; token i of its n
+ * new ones stands at position kv_len[b] - n + i (as in fa_decode).
+ *   k_pages, v_pages : [num_pages, H_kv, page_size, d] of one 16-bit type (any order of the first
+ *               three axes through `strides`).  page_size is a power of two from 8 to 1024
+ *               (otherwise FA_ERR_UNSUPPORTED).
+ *   block_table : device int32 [B, max_pages]: page block_table[b][i] holds positions
+ *               [i * page_size, (i + 1) * page_size) of sequence b.  Entries behind the last
+ *               position are not read.  Sequences may share pages that they only read.
+ *   kv_len    : device int32 [B], at most max_pages * page_size.
+ *   q_start   : device int32 [B + 1], not decreasing, or NULL: T / B tokens each (B divides T).
+ *               Tokens before q_start[0] and from q_start[B] on belong to no sequence: nothing is
+ *               read, written or computed for them (a padded batch).
+ * The index arrays live on the device, so the call cannot refuse a bad value: lengths and offsets
+ * are clamped, a page id outside [0, num_pages) is not accessed (a new token's row is not written,
+ * its keys and values read as zeros), and fa_sync_status() returns FA_ERR_INDEX.
+ * T (H + 2 H_kv), num_pages page_size and max_pages page_size are below 2^31.
+ *
+ * fa_paged_check applies the same rules on the host to HOST copies of the arrays, for a scheduler
+ * that builds them there: FA_OK, or FA_ERR_INDEX.
+ */
+int fa_paged_check(const int *block_table, const int *kv_len, const int *q_start, int T, int B,
+                   int num_pages, int page_size, int max_pages, int max_q);
+
+/*
+ * Appends the new tokens to the cache in one launch: K rotated to its position and V as it is go
+ * to their rows; Q, when given, is rotated beside them.
+ *   q, q_out  : [T,H,d] or NULL (q_out may be q with the same strides);  k, v : [T,H_kv,d].
+ *   strides   : host array of 14 strides in elements: token and head of q, q_out, k and v, then page,
+ *               head and row of k_pages and v_pages; NULL for dense tensors; limits as in fa_rope.
+ *   freq      : as in fa_rope, or NULL for no rotation (rot_dim, mscale and positions unused).
+ *   positions : device int32 [T], the positions to rotate to, or NULL for the places in the cache.
+ * A token whose position is below 0 (kv_len[b] < n) has no row and is not stored.  Two tokens that
+ * name the same row (tables that share a page they both write) leave it undefined.
+ */
+int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, void *k_pages,
+                    void *v_pages, const long long *strides, const int *block_table,
+                    const int *kv_len, const int *q_start, const int *positions,
+                    const uint64_t *freq, int T, int B, int H, int H_kv, int d, int num_pages,
+                    int page_size, int max_pages, int rot_dim, int dtype, int interleaved,
+                    float mscale, void *stream);
+
+/*
+ * Attention of every sequence's new tokens (one, a few, or a prompt chunk, mixed in one batch) over
+ * its paged cache, which already holds them.  Heads are grouped as in fa_fwd_gqa, at most 128
+ * query heads to a K/V head (otherwise FA_ERR_UNSUPPORTED).
+ *   q, o      : [T,H,d];  lse : [T,H] fp32 (natural log, as everywhere).
+ *   strides   : host array of 10 strides in elements: token and head of q and o, then page, head
+ *               and row of k_pages and v_pages; NULL for dense tensors; limits as in fa_rope.
+ *   max_q     : no sequence brings more new tokens than this (T is always safe, the true maximum is
+ *               faster); tokens beyond it are left out and reported as FA_ERR_INDEX.
+ *   causal    : != 0: row i of sequence b sees keys j <= kv_len[b] - n + i; 0: all kv_len[b] keys.
+ *               A row that sees no key gets O = 0 and LSE = -inf.  Whatever the cache holds behind
+ *               kv_len[b] (NaN included) has no influence.
+ *   workspace, workspace_bytes : device scratch of fa_paged_attn_workspace_bytes() bytes, 16-byte
+ *               aligned (may be NULL when that is 0); it needs no initialisation and keeps nothing
+ *               from call to call, but calls that may overlap on the GPU need one each.
+ */
+size_t fa_paged_attn_workspace_bytes(int T, int B, int H, int H_kv, int d, int max_q,
+                                     int page_size, int max_pages);
+int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void *o, float *lse,
+                  const long long *strides, const int *block_table, const int *kv_len,
+                  const int *q_start, int T, int B, int H, int H_kv, int d, int num_pages,
+                  int page_size, int max_pages, int max_q, int dtype, float scale, int causal,
+                  void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Synchronises `stream`, then returns and clears the current device's status word:
