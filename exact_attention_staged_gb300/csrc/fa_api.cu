@@ -516,6 +516,46 @@ int check_paged_index(const int *table, const int *kv_len, const int *q_start, f
     return FA_OK;
 }
 
+// 4-D 16-bit tensor map, x contiguous: extents and (for y, z, w) strides in elements, boxes of 64
+// elements times the given rows, 128-byte swizzle.
+int make_map_4d(CUtensorMap *m, const void *base, int dtype, const long long (&ext)[4],
+                const long long (&stride)[3], const int (&box)[3]) {
+    cuuint64_t dims[4], strides[3];
+    for (int i = 0; i < 4; ++i) dims[i] = static_cast<cuuint64_t>(ext[i]);
+    // an axis of extent 1 has no stride of its own: it gets the dense one
+    for (int i = 0; i < 3; ++i)
+        strides[i] = ext[i + 1] > 1 ? static_cast<cuuint64_t>(stride[i]) * 2
+                                    : dims[i] * (i > 0 ? strides[i - 1] : 2);
+    cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box[0]), static_cast<cuuint32_t>(box[1]),
+                           static_cast<cuuint32_t>(box[2])};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = g_encode(m,
+                          dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          4, const_cast<void *>(base), dims, strides, boxes, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+// How paged attention lays its rows out: a query tile is floor(128 / rep) tokens of one head group;
+// one tile per unit while no sequence brings more tokens than that, two otherwise.
+struct PagedTiling {
+    int rep, tile_toks, tiles, part_rows;
+};
+PagedTiling paged_tiling(int H, int Hkv, int max_q) {
+    PagedTiling t;
+    t.rep = H / Hkv;
+    t.tile_toks = 128 / t.rep;
+    t.tiles = max_q > t.tile_toks ? 2 : 1;
+    t.part_rows = t.tiles == 2 ? 256 : max_q * t.rep;
+    return t;
+}
+
+// Scratch of paged attention: what to merge, then per slot the running statistics and O~.
+constexpr size_t kPagedSlots = 2 * fa::kPagedCtas;
+constexpr size_t kPagedCutBytes = kPagedSlots * sizeof(int4);
+
 }  // namespace
 
 extern "C" {
@@ -909,9 +949,12 @@ int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, vo
 size_t fa_paged_attn_workspace_bytes(int T, int B, int H, int H_kv, int d, int max_q,
                                      int page_size, int max_pages) {
     fa::PagedView c = {};
-    if (max_q < 1 || check_paged(T, B, H, H_kv, d, 1, page_size, max_pages, FA_BF16, &c) != FA_OK)
+    if (max_q < 1 || check_paged(T, B, H, H_kv, d, 1, page_size, max_pages, FA_BF16, &c) != FA_OK ||
+        H / H_kv > 128)
         return 0;
-    return 0;
+    if (max_pages * page_size <= fa::kPagedKeys) return 0;  // one key tile: nothing to merge
+    return kPagedCutBytes + kPagedSlots * paged_tiling(H, H_kv, max_q < T ? max_q : T).part_rows *
+                                (sizeof(float2) + d * sizeof(float));
 }
 
 int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void *o, float *lse,
@@ -933,8 +976,8 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
                                  H_kv * slab, slab, row};
     const long long *given = strides != nullptr ? strides : dense;
     long long s[10] = {};
-    for (int i = 0; i < 4 && rc == FA_OK; i += 2)  // q, o
-        rc = take_strides(given + i, {T, H}, i == 2, s + i);
+    for (int i = 0; i < 4 && rc == FA_OK; i += 2)  // q (read by TMA: no zero strides), o
+        rc = take_strides(given + i, {T, H}, true, s + i);
     for (int i = 4; i < 10 && rc == FA_OK; i += 3)  // k_pages, v_pages
         rc = take_strides(given + i, {num_pages, H_kv, page_size}, true, s + i);
     if (rc != FA_OK) return rc;
@@ -944,20 +987,87 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
     int dev = 0;
     rc = device_setup(&dev, &p.c.status);
     if (rc != FA_OK) return rc;
-    p.c.max_q = max_q;
-    p.q = static_cast<const uint16_t *>(q);
-    p.k_pages = static_cast<const uint16_t *>(k_pages);
-    p.v_pages = static_cast<const uint16_t *>(v_pages);
+    p.c.max_q = max_q < T ? max_q : T;
+    const PagedTiling tl = paged_tiling(H, H_kv, p.c.max_q);
     p.o = static_cast<uint16_t *>(o);
     p.lse = lse;
-    p.q_t = s[0], p.q_h = s[1], p.o_t = s[2], p.o_h = s[3];
-    p.kp_p = s[4], p.kp_h = s[5], p.kp_r = s[6];
-    p.vp_p = s[7], p.vp_h = s[8], p.vp_r = s[9];
+    p.o_t = s[2], p.o_h = s[3];
+    p.rep = tl.rep;
+    p.tile_toks = tl.tile_toks;
+    p.q_box_toks = p.c.max_q < tl.tile_toks ? p.c.max_q : tl.tile_toks;
+    p.part_rows = tl.part_rows;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.causal = causal ? 1 : 0;
+    if (need > 0) {
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        p.cut = reinterpret_cast<int4 *>(ws);
+        p.part_ml = reinterpret_cast<float2 *>(ws + kPagedCutBytes);
+        p.part_o = reinterpret_cast<float *>(p.part_ml + kPagedSlots * tl.part_rows);
+    }
     if (make_ctl(p.c.status, 0, 0, &p.ctl) != FA_OK) return FA_ERR_INVALID;
-    cudaError_t e = fa::launch_paged_attn(p, d, dtype == FA_BF16, static_cast<cudaStream_t>(stream));
+    fa::PagedMaps maps;
+    const int rows = page_size < fa::kPagedKeys ? page_size : fa::kPagedKeys;
+    // the inner axis is the one with the smaller stride
+    maps.rows_inner = H_kv == 1 || s[6] <= s[5] ? 1 : 0;
+    if (H_kv > 1 && (s[9] <= s[8]) != (maps.rows_inner != 0)) return FA_ERR_INVALID;
+    auto pages_map = [&](CUtensorMap *m, const void *base, const long long *t) {
+        if (maps.rows_inner)
+            return make_map_4d(m, base, dtype, {d, page_size, H_kv, num_pages}, {t[2], t[1], t[0]},
+                               {rows, 1, 1});
+        return make_map_4d(m, base, dtype, {d, H_kv, page_size, num_pages}, {t[1], t[2], t[0]},
+                           {1, rows, 1});
+    };
+    if (make_map_4d(&maps.q, q, dtype, {d, tl.rep, H_kv, T},
+                    {s[1], s[1] * tl.rep, s[0]},
+                    {tl.rep, 1, p.q_box_toks}) ||
+        pages_map(&maps.k, k_pages, s + 4) || pages_map(&maps.v, v_pages, s + 7))
+        return FA_ERR_CUDA;
+    cudaError_t e = fa::launch_paged_attn(maps, p, d, dtype == FA_BF16, tl.tiles,
+                                          static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, int H_kv,
+                          int page_size, int max_pages, int max_q, int unit_toks, int causal,
+                          int ctas, int *pieces, int max_pieces) {
+    fa::PagedView c = {};
+    int rc = check_paged(T, B, H_kv, H_kv, 64, 1, page_size, max_pages, FA_BF16, &c);
+    if (rc != FA_OK) return rc;
+    const int none = 0;
+    rc = check_paged_index(&none, kv_len, q_start, &c);
+    if (rc != FA_OK) return rc;
+    if (max_q < 1 || unit_toks < 1 || ctas < 1 || pieces == nullptr || max_pieces < 0)
+        return FA_ERR_INVALID;
+    c.max_q = max_q;
+    const fa::PagedWork w = {unit_toks, causal ? 1 : 0};
+    auto weight = [&](int b) -> long {
+        const fa::PagedSeq s = fa::paged_seq(c, b);
+        return s.n > 0 ? H_kv * fa::paged_prefix(s, w, fa::paged_units(s, w)) : 0;
+    };
+    long total = 0;
+    for (int b = 0; b < B; ++b) total += weight(b);
+    const int used = static_cast<int>(total < ctas ? total : ctas);
+    int n = 0;
+    for (int k = 0; k < used; ++k) {
+        long at = fa::paged_border(total, used, k);
+        const long end = fa::paged_border(total, used, k + 1);
+        long before = 0;
+        int b = 0;
+        while (before + weight(b) <= at) before += weight(b++);
+        fa::PagedCursor cur;
+        cur.start(c, w, b, at - before);
+        while (at < end) {
+            const fa::PagedPiece u = cur.take(c, w, end - at);
+            if (n < max_pieces) {
+                int *x = pieces + 8 * n;
+                x[0] = k, x[1] = u.b, x[2] = u.kvh, x[3] = u.tok0, x[4] = u.toks, x[5] = u.t0;
+                x[6] = u.t1, x[7] = u.weight;
+            }
+            ++n;
+            at += u.t1 - u.t0;
+        }
+    }
+    return n;
 }
 
 int fa_sync_status(void *stream) {

@@ -162,68 +162,6 @@ struct Maps {
     CUtensorMap out0, out1;   // outputs written by TMA: O (forward), dK and dV, or dQ
 };
 
-// Rotary positions (see fa_rope.cu).  Strides in elements.
-struct RopeSide {
-    const uint16_t *in;       // [B, heads, N, d], elements of a row contiguous
-    uint16_t *out;            // may be `in`
-    long in_b, in_h, in_n, out_b, out_h, out_n;
-};
-struct RopeParams {
-    RopeSide q, k;            // k unused with Hkv == 0
-    const unsigned long long *freq;  // [rot / 2] turns per position, in units of 2^-64
-    const int *positions;     // [B, N], or nullptr for 0 .. N - 1
-    long rows;                // B * N
-    int N, H, Hkv;
-    int rot;                  // rotated elements of a row, a multiple of 16
-    int chunk;                // heads per thread (set by the launcher)
-    int inverse;              // 1: the transpose
-    float mscale;
-};
-
-// The paged cache as its readers and writers see it (see fa_paged.cu).  Page `id` of the cache
-// holds positions [i * page_size, (i + 1) * page_size) of the sequence whose table has it at i.
-struct PagedView {
-    const int *table;         // [B, max_pages] page ids
-    const int *kv_len;        // [B] cached positions of each sequence, the new tokens included
-    const int *q_start;       // [B + 1] first token of each sequence, or nullptr: T / B each
-    int T, B, H, Hkv;
-    int num_pages, page_shift, max_pages;  // page_size = 1 << page_shift
-    int max_q;                // no sequence has more new tokens
-    int *status;              // device status word
-};
-
-struct PagedAppendParams {
-    PagedView c;
-    const uint16_t *q, *k, *v;       // [T, heads, d]; q may be nullptr
-    uint16_t *q_out, *k_pages, *v_pages;
-    long q_t, q_h, qo_t, qo_h, k_t, k_h, v_t, v_h;   // token and head strides, elements
-    long kp_p, kp_h, kp_r, vp_p, vp_h, vp_r;         // page, head and row strides
-    const unsigned long long *freq;  // nullptr: no rotation
-    const int *positions;            // [T] for the rotation, or nullptr: the places in the cache
-    int rot;
-    int chunks;                      // warps per token (set by the launcher)
-    float mscale;
-};
-
-struct PagedAttnParams {
-    PagedView c;
-    const uint16_t *q;
-    const uint16_t *k_pages, *v_pages;
-    uint16_t *o;
-    float *lse;                      // [T, H]
-    long q_t, q_h, o_t, o_h;
-    long kp_p, kp_h, kp_r, vp_p, vp_h, vp_r;
-    float scale_log2;                // scale * log2(e)
-    int causal;
-    Ctl ctl;
-};
-
-constexpr int kErrIndex = -6;  // an index array on the device holds a value out of range
-
-cudaError_t launch_rope(const RopeParams &p, int d, bool bf16, bool inter, cudaStream_t stream);
-cudaError_t launch_paged_append(const PagedAppendParams &p, int d, bool bf16, bool inter,
-                                cudaStream_t stream);
-cudaError_t launch_paged_attn(const PagedAttnParams &p, int d, bool bf16, cudaStream_t stream);
 cudaError_t launch_fwd(const Maps &maps, const FwdParams &p, int d, bool bf16,
                        cudaStream_t stream);
 // delta[row] = mul * rowsum(dout o o)

@@ -3,7 +3,7 @@
 // reports are one rule.
 #pragma once
 
-#include "fa_internal.h"
+#include "positions.h"
 
 namespace fa {
 
@@ -48,7 +48,151 @@ __host__ __device__ inline int paged_page(const PagedView &c, int b, int pos) {
     return id >= 0 && id < c.num_pages ? id : -1;
 }
 
+// ------------------------------------------------------------------------------------------
+// How the attention's work is cut.  A unit is one K/V head of one sequence with up to
+// `unit_toks` of its new tokens (all query heads of the group), walked over the key tiles that its
+// last token sees; its weight is their number, at least 1.  Units in order (sequence, K/V head,
+// tokens) form one line of W tiles, and CTA c of G takes [c W / G, (c + 1) W / G) of it: every CTA
+// gets the same number of tiles, whatever the mixture of lengths.  A unit that a border cuts is
+// merged from its pieces afterwards.
+constexpr int kPagedKeys = 128;  // keys per tile
+
+struct PagedWork {
+    int unit_toks;  // tokens per unit
+    int causal;
+};
+
+// sum of floor((a i + b) / m) for i < n (a, b >= 0): Euclid's steps on the lattice points below
+// the line (ACM-style floor sum), a handful of divisions.
+__host__ __device__ inline long paged_floor_sum(long n, long m, long a, long b) {
+    long sum = 0;
+    while (n > 0) {
+        if (a >= m) {
+            sum += n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
+        }
+        const long y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const long t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+
+__host__ __device__ inline int paged_units(const PagedSeq &s, const PagedWork &w) {
+    return (s.n + w.unit_toks - 1) / w.unit_toks;  // per K/V head
+}
+
+// Key tiles of the first i units of one K/V head: their weight.
+__host__ __device__ inline long paged_prefix(const PagedSeq &s, const PagedWork &w, long i) {
+    const long full = s.len > 0 ? (s.len + kPagedKeys - 1) / kPagedKeys : 1;
+    if (!w.causal) return i * full;
+    const long last = paged_units(s, w) - 1;
+    const long m = i < last ? i : last;  // units before the last one see len - n + (j + 1) tokens
+    const long ctx = static_cast<long>(s.len) - s.n;
+    long none = ctx < 0 ? -ctx / w.unit_toks : 0;  // units that see nothing weigh 1
+    if (none > m) none = m;
+    long sum = none + paged_floor_sum(m - none, kPagedKeys, w.unit_toks,
+                                      ctx + (none + 1) * w.unit_toks + kPagedKeys - 1);
+    if (i > last) sum += full;
+    return sum;
+}
+
+// Key tiles that the first `toks` new tokens of a sequence see.
+__host__ __device__ inline int paged_tiles(const PagedSeq &s, const PagedWork &w, int toks) {
+    const int end = w.causal ? s.len - s.n + toks : s.len;
+    return end > 0 ? (end + kPagedKeys - 1) / kPagedKeys : 0;
+}
+
+__host__ __device__ inline long paged_border(long total, int ctas, int c) {
+    return total * c / ctas;
+}
+
+// A stretch of one unit's key tiles, [t0, t1) of its `tiles`.
+struct PagedPiece {
+    int tok0;     // first token, in the batch
+    int toks;     // tokens of the unit
+    int kvh;
+    int b;
+    int last0;    // last key that the first token sees (that token j sees: + j when causal)
+    int len;
+    int t0, t1;
+    int weight;   // of the whole unit
+};
+
+struct PagedCursor {
+    PagedSeq s;
+    int b, g, i, t;  // sequence, K/V head, unit and key tile that come next
+
+    // `at`: weight inside sequence b that lies before the position
+    __host__ __device__ void start(const PagedView &c, const PagedWork &w, int seq, long at) {
+        b = seq;
+        s = paged_seq(c, b);
+        const int units = paged_units(s, w);
+        const long each = paged_prefix(s, w, units);
+        g = static_cast<int>(at / each);
+        at -= g * each;
+        int lo = 0, hi = units - 1;  // the last unit whose prefix is <= at
+        while (lo < hi) {
+            const int mid = lo + (hi - lo + 1) / 2;
+            if (paged_prefix(s, w, mid) <= at)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        i = lo;
+        t = static_cast<int>(at - paged_prefix(s, w, lo));
+    }
+    // The next piece, of at most `room` tiles, and past it.
+    __host__ __device__ PagedPiece take(const PagedView &c, const PagedWork &w, long room) {
+        PagedPiece p;
+        const int i0 = i * w.unit_toks;
+        p.tok0 = s.tok0 + i0;
+        p.toks = s.n - i0 < w.unit_toks ? s.n - i0 : w.unit_toks;
+        p.kvh = g;
+        p.b = b;
+        p.last0 = w.causal ? s.len - s.n + i0 : s.len - 1;
+        p.len = s.len;
+        const int tiles = paged_tiles(s, w, i0 + p.toks);
+        p.weight = tiles > 0 ? tiles : 1;
+        p.t0 = t;
+        p.t1 = room < p.weight - t ? t + static_cast<int>(room) : p.weight;
+        t = p.t1;
+        if (t == p.weight) {
+            t = 0;
+            if (++i == paged_units(s, w)) {
+                i = 0;
+                if (++g == c.Hkv) {
+                    g = 0;
+                    do {
+                        if (++b >= c.B) break;
+                        s = paged_seq(c, b);
+                    } while (s.n == 0);
+                }
+            }
+        }
+        return p;
+    }
+};
+
 #ifdef __CUDACC__
+// TMA: 4-D tiled load of one box into shared memory, completing on an mbarrier with its bytes.
+__device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *map, int x, int y,
+                                            int z, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
 __device__ __forceinline__ void paged_report(const PagedView &c) {
     atomicExch(c.status, kErrIndex);
 }

@@ -7,7 +7,7 @@
 // product are the angle to 2^-33 turns; its sine and cosine are taken in 32 bits.
 #pragma once
 
-#include "fa_internal.h"
+#include "positions.h"
 
 namespace fa {
 

@@ -341,7 +341,8 @@ int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, vo
  * query heads to a K/V head (otherwise FA_ERR_UNSUPPORTED).
  *   q, o      : [T,H,d];  lse : [T,H] fp32 (natural log, as everywhere).
  *   strides   : host array of 10 strides in elements: token and head of q and o, then page, head
- *               and row of k_pages and v_pages; NULL for dense tensors; limits as in fa_rope.
+ *               and row of k_pages and v_pages; NULL for dense tensors; limits as for the outputs
+ *               in fa_rope.  k_pages and v_pages order heads and rows the same way.
  *   max_q     : no sequence brings more new tokens than this (T is always safe, the true maximum is
  *               faster); tokens beyond it are left out and reported as FA_ERR_INDEX.
  *   causal    : != 0: row i of sequence b sees keys j <= kv_len[b] - n + i; 0: all kv_len[b] keys.
@@ -385,7 +386,14 @@ const char *fa_status_string(int code);
  * fa_debug_set_dkdv_splits: 0 = automatic; s > 0 splits every K/V head's query group of
  *   fa_bwd_gqa over min(s, H / H_kv) dK/dV CTAs per key tile (changes the workspace size).
  *   Negative: FA_ERR_INVALID.
+ * fa_debug_paged_pieces: how fa_paged_attn would spread a batch's work over `ctas` CTAs, worked out
+ *   on the host from HOST copies of kv_len and q_start, with unit_toks tokens to a unit: 8 ints per
+ *   piece (CTA, sequence, K/V head, first token, tokens, first and end key tile, key tiles of the
+ *   unit) in order.  Returns the number of pieces (only the first max_pieces are stored) or an error.
  */
+int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, int H_kv,
+                          int page_size, int max_pages, int max_q, int unit_toks, int causal,
+                          int ctas, int *pieces, int max_pieces);
 int fa_debug_set_visit_log(uint8_t *buf, size_t bytes);
 int fa_debug_set_wait_limit_ns(unsigned long long ns);
 int fa_debug_set_fault(int mode);
