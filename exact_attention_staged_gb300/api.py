@@ -62,7 +62,7 @@ SIGNATURES = {
                            _i, _i, _i, _f, _i, _vp, _sz, _vp]),
     "fa_sync_status": (_i, [_vp]),
     "fa_status_string": (ctypes.c_char_p, [_i]),
-    "fa_debug_paged_pieces": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _i]),
+    "fa_debug_paged_pieces": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _i]),
     "fa_debug_set_visit_log": (_i, [_vp, _sz]),
     "fa_debug_set_wait_limit_ns": (_i, [ctypes.c_ulonglong]),
     "fa_debug_set_fault": (_i, [_i]),

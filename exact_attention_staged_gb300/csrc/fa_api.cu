@@ -1028,43 +1028,43 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
 }
 
 int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, int H_kv,
-                          int page_size, int max_pages, int max_q, int unit_toks, int causal,
-                          int ctas, int *pieces, int max_pieces) {
+                          int page_size, int max_pages, int max_q, int tile_toks, int tiles,
+                          int causal, int ctas, int *pieces, int max_pieces) {
     fa::PagedView c = {};
     int rc = check_paged(T, B, H_kv, H_kv, 64, 1, page_size, max_pages, FA_BF16, &c);
     if (rc != FA_OK) return rc;
     const int none = 0;
     rc = check_paged_index(&none, kv_len, q_start, &c);
     if (rc != FA_OK) return rc;
-    if (max_q < 1 || unit_toks < 1 || ctas < 1 || pieces == nullptr || max_pieces < 0)
+    if (max_q < 1 || tile_toks < 1 || tiles < 1 || tiles > 2 || ctas < 1 || pieces == nullptr ||
+        max_pieces < 0)
         return FA_ERR_INVALID;
     c.max_q = max_q;
-    const fa::PagedWork w = {unit_toks, causal ? 1 : 0};
+    const fa::PagedWork w = {tile_toks, tiles * tile_toks, fa::paged_unit_cost(tiles), causal ? 1 : 0};
     auto weight = [&](int b) -> long {
         const fa::PagedSeq s = fa::paged_seq(c, b);
         return s.n > 0 ? H_kv * fa::paged_prefix(s, w, fa::paged_units(s, w)) : 0;
     };
     long total = 0;
     for (int b = 0; b < B; ++b) total += weight(b);
-    const int used = static_cast<int>(total < ctas ? total : ctas);
+    const int used = fa::paged_ctas(total, ctas);
     int n = 0;
     for (int k = 0; k < used; ++k) {
-        long at = fa::paged_border(total, used, k);
-        const long end = fa::paged_border(total, used, k + 1);
-        long before = 0;
+        const long at = fa::paged_border(total, used, k);
+        long room = fa::paged_border(total, used, k + 1) - at, before = 0;
         int b = 0;
         while (before + weight(b) <= at) before += weight(b++);
         fa::PagedCursor cur;
         cur.start(c, w, b, at - before);
-        while (at < end) {
-            const fa::PagedPiece u = cur.take(c, w, end - at);
+        while (room > 0) {
+            const fa::PagedPiece u = cur.take(c, w, room);
+            if (u.t0 == u.t1) continue;
             if (n < max_pieces) {
                 int *x = pieces + 8 * n;
                 x[0] = k, x[1] = u.b, x[2] = u.kvh, x[3] = u.tok0, x[4] = u.toks, x[5] = u.t0;
-                x[6] = u.t1, x[7] = u.weight;
+                x[6] = u.t1, x[7] = u.tiles;
             }
             ++n;
-            at += u.t1 - u.t0;
         }
     }
     return n;

@@ -7,26 +7,27 @@
 //
 // Rows.  The query heads of a K/V head's group share its keys, so a query tile of 128 rows is
 // floor(128 / rep) tokens times the rep heads of one group: one TMA box of the token-major Q.  A
-// prompt chunk's unit is two such tiles (256 rows per K/V tile read from L2, as in the forward); a
-// batch whose sequences bring no more than one tile of tokens runs the one-tile form, which has
-// room for more K/V tiles in flight and is bound by reading the cache.
+// prompt chunk's unit is two such tiles, one for each of the two softmax groups, which share every
+// K/V tile (256 rows per tile read from L2, as in the forward).  A unit of no more tokens than one
+// tile (single tokens, drafted ones) gives both groups the same query tile and alternate key
+// tiles: the chain from a score tile to its probabilities takes longer than HBM needs to bring the
+// next tile, and two of them in flight hide it.  At the end the second group's statistics and
+// accumulator (the same tensor-memory lanes) are merged into the first's.
 //
 // Keys.  A tile is 128 positions, whatever the page size: its pages are loaded by one TMA box each
 // into their rows of the 128-byte-swizzled tile (a page of 8 rows or more starts on a swizzle
 // atom); pages behind the sequence's end are loaded from an index outside the pool, which TMA
 // fills with zeros.  Scores behind the end are masked, and V's rows between the end and the end of
 // its page are zeroed in shared memory before the product, so that whatever the cache holds there
-// (NaN included) meets a probability of zero as a zero.
+// (NaN included) meets a probability of zero as a zero.  K and V have a ring and a load warp each:
+// a page of 16 rows is a box of 2 KB, and one warp alone issued them no faster than 5.6 TB/s.
 //
 // Work.  paged.cuh cuts the line of all units' key tiles into one equal stretch per CTA, on the
 // device (the host knows no lengths), so prompt chunks and single tokens of any mixture balance,
-// and a single sequence's keys spread over all SMs.  A tile costs about the same either way: two
-// query tiles' products and softmax take about 2900 cycles per 64 KB of K and V, and 64 KB is
-// what HBM brings one SM in about 2700.
+// and a single sequence's keys spread over all SMs.
 //
-// Warps: 0 loads and walks the units, 1 issues the MMAs, four per query tile run the softmax.  With
-// two query tiles the MMA order per key tile is PV_0(j-1), S_0(j), PV_1(j-1), S_1(j) as in the
-// forward; with one, S has two buffers and S(j+1) is issued before PV(j) as in decode.
+// Warps: 0 walks the units and loads Q and K, 2 loads V, 1 issues the MMAs, 4..7 and 8..11 are the
+// softmax groups.  MMA order per step: PV_0 of the step before, S_0, PV_1, S_1, as in the forward.
 #include "paged.cuh"
 
 #include <type_traits>
@@ -34,25 +35,29 @@
 namespace fa {
 namespace {
 
-template <int D, int TILES>
+// QT: query tiles that a unit may have (1: no sequence brings more tokens than one tile holds).
+template <int D, int QT>
 struct PagedLayout {
     static constexpr int kTileBytes = 128 * D * 2;  // one 128 x d tile of 16-bit values
     static constexpr int kBoxes = D / 64;
     static constexpr int kBoxBytes = 128 * 128;
-    static constexpr int kSlots = D == 128 ? (TILES == 2 ? 5 : 6) : 12;  // K/V ring
-    static constexpr int kSlotOff = TILES * kTileBytes;                  // after the Q tiles
-    static constexpr int kBarOff = kSlotOff + kSlots * kTileBytes;
-    // q_full, q_empty, full[S], empty[S], s_full[2], p_full[2], o_final[2], pv_done,
-    // unit_full[2], unit_empty[2], drain
-    static constexpr int kNumBars = 2 + 2 * kSlots + 12;
+    // K waits only for its S, V for the softmax: with an odd number of slots V gets the more
+    static constexpr int kKSlots = D == 128 ? (QT == 2 ? 2 : 3) : 6;
+    static constexpr int kVSlots = D == 128 ? 3 : 6;
+    static constexpr int kKOff = QT * kTileBytes;  // after the Q tiles
+    static constexpr int kVOff = kKOff + kKSlots * kTileBytes;
+    static constexpr int kBarOff = kVOff + kVSlots * kTileBytes;
+    // q_full, q_empty, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_final[2],
+    // pair_full, pair_read, unit_full[2], unit_empty[2], drain
+    static constexpr int kNumBars = 2 + 2 * kKSlots + 2 * kVSlots + 13;
     static constexpr int kUnitOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // two unit slots
-    static constexpr int kScanOff = kUnitOff + 2 * 32;  // the plan's sums: 16 longs
+    static constexpr int kScanOff = kUnitOff + 2 * 48;  // the plan's sums: 16 longs
     static constexpr int kMiscOff = kScanOff + 16 * 8;  // TMEM base, abort flag
-    static constexpr int kBytes = kMiscOff + 8;
+    static constexpr int kPairOff = kMiscOff + 8;       // the second group's (m, l): float2[128]
+    static constexpr int kBytes = kPairOff + 128 * 8;
     static constexpr int kAlloc = kBytes + 1024;
-    static constexpr int kThreads = TILES == 2 ? 384 : 192;
-    static constexpr int kSoftWarp = TILES == 2 ? 4 : 2;  // first softmax warp
-    static constexpr uint32_t kTmemCols = 512;
+    static constexpr int kThreads = 384;
+    static constexpr uint32_t kTmemCols = 512;  // S_0, S_1 (2 x 128), O_0, O_1 (2 x d)
     static_assert(kAlloc <= 232448, "shared memory per CTA");
 };
 
@@ -65,7 +70,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
     return l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : l;
 }
 
-// A unit's piece as the load warp hands it to the others (one of two slots in shared memory).
+// A unit's piece as the first load warp hands it to the others (one of two slots in shared memory).
 struct PieceSlot {
     int tok0;   // first token, in the batch; -1: no more pieces
     int toks;
@@ -74,9 +79,10 @@ struct PieceSlot {
     int len;
     int t0, t1; // key tiles, t1 not beyond what the unit sees
     int dest;   // -1: O and LSE, otherwise the slot of its partial result
+    int b;      // sequence
 };
 
-// Key tiles of the piece that query tile q takes part in: [t0, first tile it does not see).
+// First key tile from t0 on that query tile q of the piece does not take part in.
 __device__ __forceinline__ int piece_end(const PieceSlot &u, int q, int tile_toks, int causal) {
     const int toks = min(u.toks - q * tile_toks, tile_toks);
     if (toks <= 0) return u.t0;
@@ -115,7 +121,7 @@ __device__ __forceinline__ Stretch find_stretch(const PagedAttnParams &p, const 
     r.total = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) r.total += scan[i];
-    r.ctas = static_cast<int>(min(static_cast<long>(gridDim.x), r.total));
+    r.ctas = paged_ctas(r.total, static_cast<int>(gridDim.x));
     const int c = static_cast<int>(blockIdx.x);
     r.begin = r.end = 0;
     r.seq = 0;
@@ -157,44 +163,86 @@ __device__ __forceinline__ Stretch find_stretch(const PagedAttnParams &p, const 
     return r;
 }
 
-template <int D, bool BF16, int TILES>
-__global__ void __launch_bounds__(PagedLayout<D, TILES>::kThreads, 1)
+// Page ids of a piece's key tiles for one load warp: 32 at a time in the lanes, the next 32 read
+// ahead.  Lane i of a tile's call gets the id of the tile's i-th page; pages behind the sequence's
+// end and ids that are no page of the pool come back as num_pages, outside the pool.
+struct PageWindow {
+    const int *row;
+    int have;  // pages of the sequence
+    int base, now, next;
+    __device__ __forceinline__ int read(const PagedView &c, int first) const {
+        const int i = first + lane_id();
+        return i < have ? row[i] : c.num_pages;
+    }
+    __device__ __forceinline__ void open(const PagedView &c, const PieceSlot &u) {
+        row = c.table + static_cast<long>(u.b) * c.max_pages;
+        have = (u.len + (1 << c.page_shift) - 1) >> c.page_shift;
+        base = ((u.t0 * kPagedKeys) >> c.page_shift) & ~31;
+        now = read(c, base);
+        next = read(c, base + 32);
+    }
+    __device__ __forceinline__ int tile(const PagedView &c, int j, int boxes) {
+        const int page0 = (j * kPagedKeys) >> c.page_shift;
+        if (page0 >= base + 32) {
+            base += 32;
+            now = next;
+            next = read(c, base + 32);
+        }
+        const int i = page0 + lane_id();
+        int id = __shfl_sync(0xffffffffu, now, (i - base) & 31);
+        if (lane_id() < boxes && i < have && (id < 0 || id >= c.num_pages)) {
+            paged_report(c);
+            id = c.num_pages;
+        }
+        return id;
+    }
+};
+
+template <int D, bool BF16, int QT>
+__global__ void __launch_bounds__(384, 1)
     fa_paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedAttnParams p) {
-    using L = PagedLayout<D, TILES>;
+    using L = PagedLayout<D, QT>;
     constexpr uint32_t kIdescS = idesc_f16(128, 128, BF16, false);
     constexpr uint32_t kIdescPV = idesc_f16(128, D, BF16, true);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
     uint64_t *q_full = bars, *q_empty = bars + 1;
-    uint64_t *full = bars + 2, *empty = full + L::kSlots;
-    uint64_t *s_full = empty + L::kSlots;  // [2]: per query tile, or per S buffer
-    uint64_t *p_full = s_full + 2;         // [2]: the same
-    uint64_t *o_final = p_full + 2;        // [2]: per query tile
-    uint64_t *pv_done = o_final + 2;
-    uint64_t *unit_full = pv_done + 1, *unit_empty = unit_full + 2;  // [2] each
+    uint64_t *k_full = bars + 2, *k_empty = k_full + L::kKSlots;
+    uint64_t *v_full = k_empty + L::kKSlots, *v_empty = v_full + L::kVSlots;
+    uint64_t *s_full = v_empty + L::kVSlots;  // [2]: per softmax group, as the next three
+    uint64_t *p_full = s_full + 2;
+    uint64_t *o_final = p_full + 2;
+    uint64_t *pair_full = o_final + 2, *pair_read = pair_full + 1;
+    uint64_t *unit_full = pair_read + 1, *unit_empty = unit_full + 2;  // [2]: per unit slot
     uint64_t *drain = unit_empty + 2;
     volatile int *unit_slot = reinterpret_cast<volatile int *>(smem + L::kUnitOff);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMiscOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMiscOff + 4);
+    float2 *pair_ml = reinterpret_cast<float2 *>(smem + L::kPairOff);
     const int warp = warp_id(), lane = lane_id();
-    const PagedWork work = {TILES * p.tile_toks, p.causal};
+    const PagedWork work = {p.tile_toks, QT * p.tile_toks, paged_unit_cost(QT), p.causal};
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
-        for (int s = 0; s < L::kSlots; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+        for (int s = 0; s < L::kKSlots; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < L::kVSlots; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);  // one arrival per softmax warp of a query tile
+            mbar_init(&p_full[i], 4);  // one arrival per softmax warp of a group
             mbar_init(&o_final[i], 1);
             mbar_init(&unit_full[i], 1);
-            mbar_init(&unit_empty[i], 1 + 4 * TILES);  // the MMA warp and the softmax warps
+            mbar_init(&unit_empty[i], 10);  // the MMA warp, the V warp and the softmax warps
         }
-        mbar_init(pv_done, 1);
+        mbar_init(pair_full, 4);
+        mbar_init(pair_read, 4);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -217,7 +265,7 @@ __global__ void __launch_bounds__(PagedLayout<D, TILES>::kThreads, 1)
 
     auto read_slot = [&](int e) {
         PieceSlot u;
-        volatile int *s = unit_slot + 8 * e;
+        volatile int *s = unit_slot + 12 * e;
         u.tok0 = s[0];
         u.toks = s[1];
         u.kvh = s[2];
@@ -226,68 +274,99 @@ __global__ void __launch_bounds__(PagedLayout<D, TILES>::kThreads, 1)
         u.t0 = s[5];
         u.t1 = s[6];
         u.dest = s[7];
+        u.b = s[8];
         return u;
     };
+    // both groups work on the same query tile and take alternate key tiles
+    auto is_pair = [&](const PieceSlot &u) { return QT == 1 || u.toks <= p.tile_toks; };
 
-    if (warp < L::kSoftWarp) {
-        if constexpr (TILES == 2) regs_dec<80>();
+    if (warp < 4) {
+        // warpgroup 0 gives registers to the softmax groups: 128 x 80 + 256 x 208 = 63488 of the
+        // 384 x 168 = 64512 the CTA is launched with
+        regs_dec<80>();
+        const int box_rows = min(1 << p.c.page_shift, kPagedKeys);  // rows of one page in a tile
+        const int boxes = kPagedKeys / box_rows;                    // pages of a tile
+        // key tile j's pages from K's or V's map into a ring slot: one lane per page
+        auto load_tile = [&](const CUtensorMap *map, const PieceSlot &u, int j, int id,
+                             uint8_t *slot, uint64_t *bar) {
+            if (lane == 0) mbar_arrive_expect_tx(bar, L::kTileBytes);
+            __syncwarp();
+            if (lane < boxes) {
+                const int y = (j * kPagedKeys) & ((1 << p.c.page_shift) - 1);
+                uint8_t *dst = slot + lane * box_rows * 128;
+                for (int b = 0; b < L::kBoxes; ++b)
+                    tma_load_4d(dst + b * L::kBoxBytes, map, b * 64, maps.rows_inner ? y : u.kvh,
+                                maps.rows_inner ? u.kvh : y, id, bar);
+            }
+        };
         if (warp == 0) {
-            // ---------------------------------------------------------------- load warp
-            const int shift = p.c.page_shift;
-            const int box_rows = min(1 << shift, kPagedKeys);  // rows of one page in a tile
-            const int boxes = kPagedKeys / box_rows;           // pages of a tile
-            int n = 0;   // K/V tiles issued into the ring
+            // ------------------------------------------------- units, Q and K
+            int n = 0;   // K tiles issued
             int nq = 0;  // Q loads issued
+            int k = 0;   // pieces so far
             bool ok = true;
             PagedCursor cur;
-            long at = mine.begin;
-            if (at < mine.end) cur.start(p.c, work, mine.seq, at - mine.before);
+            long room = mine.end - mine.begin;
+            if (room > 0) cur.start(p.c, work, mine.seq, mine.begin - mine.before);
             int4 cut0 = make_int4(-1, 0, 0, 0);  // what the merge has to do for this CTA
             int cut_n = 0;
-            for (int k = 0;; ++k) {
+            for (;;) {
+                PieceSlot u;
+                u.tok0 = -1;
+                while (room > 0) {
+                    const long at = mine.end - room;
+                    const PagedPiece x = cur.take(p.c, work, room);
+                    if (x.t0 == x.t1) continue;
+                    const bool whole = x.t1 - x.t0 == x.tiles;
+                    if (!whole && x.t0 == 0) {  // starts a unit that other CTAs finish
+                        const long end = at + x.unit_end;
+                        cut0 = make_int4(x.tok0, x.toks, x.kvh, 0);
+                        cut_n = static_cast<int>((end * mine.ctas + mine.total - 1) / mine.total) -
+                                static_cast<int>(blockIdx.x);
+                    }
+                    u.tok0 = x.tok0;
+                    u.toks = x.toks;
+                    u.kvh = x.kvh;
+                    u.last0 = x.last0;
+                    u.len = x.len;
+                    u.t0 = x.t0;
+                    // a unit that stands before its sequence sees nothing
+                    u.t1 = x.last0 + (p.causal ? x.toks - 1 : 0) < 0 ? x.t0 : x.t1;
+                    u.dest = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (x.t0 == 0 ? 1 : 0);
+                    u.b = x.b;
+                    break;
+                }
                 const int e = k & 1;
                 if (k >= 2 && !mbar_wait_warp(&unit_empty[e], ((k >> 1) - 1) & 1, p.ctl,
                                               abort_flag)) {
                     ok = false;
                     break;
                 }
-                if (at >= mine.end) {
-                    if (lane == 0) {
-                        unit_slot[8 * e] = -1;
-                        mbar_arrive(&unit_full[e]);
-                    }
-                    break;
-                }
-                const PagedPiece u = cur.take(p.c, work, mine.end - at);
-                const bool whole = u.t1 - u.t0 == u.weight;
-                if (!whole && u.t0 == 0) {  // starts a unit that other CTAs finish
-                    const long unit_end = at + u.weight;
-                    const int c1 = static_cast<int>(
-                        (unit_end * mine.ctas + mine.total - 1) / mine.total - 1);
-                    cut0 = make_int4(u.tok0, u.toks, u.kvh, 0);
-                    cut_n = c1 - static_cast<int>(blockIdx.x) + 1;
-                }
-                at += u.t1 - u.t0;
-                // what the unit really sees: nothing, if it stands before its sequence
-                const int seen = u.last0 + (p.causal ? u.toks - 1 : 0) < 0 ? u.t0 : u.t1;
                 if (lane == 0) {
-                    volatile int *s = unit_slot + 8 * e;
+                    volatile int *s = unit_slot + 12 * e;
                     s[0] = u.tok0;
-                    s[1] = u.toks;
-                    s[2] = u.kvh;
-                    s[3] = u.last0;
-                    s[4] = u.len;
-                    s[5] = u.t0;
-                    s[6] = seen;
-                    s[7] = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (u.t0 == 0 ? 1 : 0);
-                    __threadfence_block();
+                    if (u.tok0 >= 0) {
+                        s[1] = u.toks;
+                        s[2] = u.kvh;
+                        s[3] = u.last0;
+                        s[4] = u.len;
+                        s[5] = u.t0;
+                        s[6] = u.t1;
+                        s[7] = u.dest;
+                        s[8] = u.b;
+                    }
                     mbar_arrive(&unit_full[e]);
                 }
+                __syncwarp();
+                if (u.tok0 < 0) break;
+                ++k;
+                PageWindow win;
+                win.open(p.c, u);
                 auto load_q = [&]() {  // the Q tiles are free once the last unit's last S is done
                     if (nq > 0 && !mbar_wait_warp(q_empty, (nq - 1) & 1, p.ctl, abort_flag))
                         return false;
                     if (lane == 0) {
-                        const int tiles = TILES == 2 && u.toks > p.tile_toks ? 2 : 1;
+                        const int tiles = is_pair(u) ? 1 : 2;
                         mbar_arrive_expect_tx(
                             q_full, tiles * L::kBoxes * 128 * p.rep * p.q_box_toks);
                         for (int t = 0; t < tiles; ++t)
@@ -298,51 +377,19 @@ __global__ void __launch_bounds__(PagedLayout<D, TILES>::kThreads, 1)
                     ++nq;
                     return true;
                 };
-                // page ids of the piece, 32 at a time in the lanes, the next 32 read ahead
-                const int *row = p.c.table + static_cast<long>(u.b) * p.c.max_pages;
-                const int have = (u.len + (1 << shift) - 1) >> shift;  // pages of the sequence
-                auto ids = [&](int first) {
-                    const int i = first + lane;
-                    return i < have ? row[i] : p.c.num_pages;  // outside the pool: zeros
-                };
-                int base = ((u.t0 * kPagedKeys) >> shift) & ~31;
-                int now = ids(base), next = ids(base + 32);
                 bool q_done = false;
-                for (int j = u.t0; j < seen && ok; ++j) {
-                    const int page0 = (j * kPagedKeys) >> shift;
-                    if (page0 >= base + 32) {
-                        base += 32;
-                        now = next;
-                        next = ids(base + 32);
+                if (nq == 0) ok = q_done = load_q();  // the first Q needs no page id
+                for (int j = u.t0; j < u.t1 && ok; ++j) {
+                    const int id = win.tile(p.c, j, boxes), s = n % L::kKSlots;
+                    if (!mbar_wait_warp(&k_empty[s], ((n / L::kKSlots) & 1) ^ 1, p.ctl,
+                                        abort_flag)) {
+                        ok = false;
+                        break;
                     }
-                    int id = __shfl_sync(0xffffffffu, now, (page0 - base + lane) & 31);
-                    if (lane < boxes && (id < 0 || id > p.c.num_pages ||
-                                         (id == p.c.num_pages && page0 + lane < have))) {
-                        paged_report(p.c);
-                        id = p.c.num_pages;
-                    }
-                    const int y = (j * kPagedKeys) & ((1 << shift) - 1);
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const int s = n % L::kSlots;
-                        if (!mbar_wait_warp(&empty[s], ((n / L::kSlots) & 1) ^ 1, p.ctl,
-                                            abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kTileBytes);
-                        __syncwarp();
-                        if (lane < boxes) {
-                            uint8_t *dst = smem + L::kSlotOff + s * L::kTileBytes +
-                                           lane * box_rows * 128;
-                            for (int b = 0; b < L::kBoxes; ++b)
-                                tma_load_4d(dst + b * L::kBoxBytes, kv ? &maps.v : &maps.k, b * 64,
-                                            maps.rows_inner ? y : u.kvh,
-                                            maps.rows_inner ? u.kvh : y, id, &full[s]);
-                        }
-                        ++n;
-                    }
-                    // the first K/V pair goes ahead of Q: its slots free before the Q tiles do
-                    if (ok && !q_done) {
+                    load_tile(&maps.k, u, j, id, smem + L::kKOff + s * L::kTileBytes, &k_full[s]);
+                    ++n;
+                    // the first K goes ahead of Q: its slot frees before the Q tiles do
+                    if (!q_done) {
                         ok = load_q();
                         q_done = true;
                     }
@@ -358,48 +405,98 @@ __global__ void __launch_bounds__(PagedLayout<D, TILES>::kThreads, 1)
                 // let every copy still in flight land before shared memory goes away
                 if (lane == 0) {
                     if (nq > 0) drain_wait(q_full, (nq - 1) & 1, p.ctl);
-                    for (int l = n > L::kSlots ? n - L::kSlots : 0; l < n; ++l)
-                        drain_wait(&full[l % L::kSlots], (l / L::kSlots) & 1, p.ctl);
+                    for (int l = n > L::kKSlots ? n - L::kKSlots : 0; l < n; ++l)
+                        drain_wait(&k_full[l % L::kKSlots], (l / L::kKSlots) & 1, p.ctl);
                 }
             }
             __syncwarp();
+        } else if (warp == 2) {
+            // ------------------------------------------------- V
+            int n = 0;
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const int e = k & 1;
+                if (!mbar_wait_warp(&unit_full[e], (k >> 1) & 1, p.ctl, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const PieceSlot u = read_slot(e);
+                if (u.tok0 < 0) break;
+                PageWindow win;
+                win.open(p.c, u);
+                for (int j = u.t0; j < u.t1; ++j) {
+                    const int id = win.tile(p.c, j, boxes), s = n % L::kVSlots;
+                    if (!mbar_wait_warp(&v_empty[s], ((n / L::kVSlots) & 1) ^ 1, p.ctl,
+                                        abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    load_tile(&maps.v, u, j, id, smem + L::kVOff + s * L::kTileBytes, &v_full[s]);
+                    ++n;
+                }
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(&unit_empty[e]);
+            }
+            if (!ok || *abort_flag) {
+                if (lane == 0)
+                    for (int l = n > L::kVSlots ? n - L::kVSlots : 0; l < n; ++l)
+                        drain_wait(&v_full[l % L::kVSlots], (l / L::kVSlots) & 1, p.ctl);
+            }
+            __syncwarp();
         } else if (warp == 1) {
-            // ---------------------------------------------------------------- MMA issuer
-            const SDesc dq0 = sdesc_make(smem_u32(smem), 16, 1024);                 // Q: K-major
-            const SDesc dk0 = sdesc_make(smem_u32(smem + L::kSlotOff), 16, 1024);   // K: K-major
-            const SDesc dv0 = sdesc_make(smem_u32(smem + L::kSlotOff), L::kBoxBytes,
-                                         1024);                                      // V: MN-major
-            auto issue_s = [&](int q, int buf, int ks) {
+            // ------------------------------------------------- MMA issuer
+            const SDesc dq0 = sdesc_make(smem_u32(smem), 16, 1024);              // Q: K-major
+            const SDesc dk0 = sdesc_make(smem_u32(smem + L::kKOff), 16, 1024);   // K: K-major
+            const SDesc dv0 = sdesc_make(smem_u32(smem + L::kVOff), L::kBoxBytes,
+                                         1024);                                   // V: MN-major
+            auto issue_s = [&](int q, int t, int ks) {
                 const SDesc a = sdesc_add(dq0, q * L::kTileBytes);
                 const SDesc b = sdesc_add(dk0, ks * L::kTileBytes);
                 if constexpr (D == 128)
-                    mma_ss_chain_k128(tmem + buf * 128, a, b, kIdescS, 0u);
+                    mma_ss_chain_k128(tmem + t * 128, a, b, kIdescS, 0u);
                 else
-                    mma_ss_chain_k64(tmem + buf * 128, a, b, kIdescS, 0u);
+                    mma_ss_chain_k64(tmem + t * 128, a, b, kIdescS, 0u);
+                umma_commit_el(&s_full[t]);
             };
-            auto issue_pv = [&](int q, int buf, int vs, bool accumulate) {
-                mma_ts_chain_k128(tmem + 256 + q * D, tmem + buf * 128,
+            auto issue_pv = [&](int t, int vs, bool accumulate) {
+                mma_ts_chain_k128(tmem + 256 + t * D, tmem + t * 128,
                                   sdesc_add(dv0, vs * L::kTileBytes), kIdescPV,
                                   accumulate ? 1u : 0u);
             };
-            // V of key tile j in slot vs has landed; its rows from the sequence's end to the end
-            // of that page become zeros (pages behind it were loaded as zeros)
-            auto clear_tail = [&](int len, int j, int vs) {
-                const int r0 = len - j * kPagedKeys;
-                if (r0 >= kPagedKeys) return;
-                const int size = 1 << p.c.page_shift;
-                const int r1 = min(kPagedKeys, (r0 + size - 1) & ~(size - 1));
-                uint8_t *tile = smem + L::kSlotOff + vs * L::kTileBytes;
-                for (int b = 0; b < L::kBoxes; ++b)
-                    for (int x = r0 * 128 + lane * 16; x < r1 * 128; x += 512)
-                        *reinterpret_cast<uint4 *>(tile + b * L::kBoxBytes + x) =
-                            make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-                __syncwarp();
+            auto wait_k = [&](int x) {
+                if (!mbar_wait_warp(&k_full[x % L::kKSlots], (x / L::kKSlots) & 1, p.ctl,
+                                    abort_flag))
+                    return false;
+                tc_fence_after();
+                return true;
             };
-            int n = 0;              // K/V tiles consumed from the ring
-            int pcnt[2] = {0, 0};   // PV products per query tile (TILES == 2)
-            int g = 0;              // key tiles consumed (TILES == 1): S buffer g % 2
+            // V tile x of the ring (key tile j) has landed; its rows from the sequence's end to
+            // the end of that page become zeros (pages behind it were loaded as zeros)
+            auto wait_v = [&](int x, int j, int len) {
+                const int vs = x % L::kVSlots;
+                if (!mbar_wait_warp(&v_full[vs], (x / L::kVSlots) & 1, p.ctl, abort_flag))
+                    return false;
+                const int r0 = len - j * kPagedKeys;
+                if (r0 < kPagedKeys) {
+                    const int size = 1 << p.c.page_shift;
+                    const int r1 = min(kPagedKeys, (r0 + size - 1) & ~(size - 1));
+                    uint8_t *tile = smem + L::kVOff + vs * L::kTileBytes;
+                    for (int b = 0; b < L::kBoxes; ++b)
+                        for (int a = r0 * 128 + lane * 16; a < r1 * 128; a += 512)
+                            *reinterpret_cast<uint4 *>(tile + b * L::kBoxBytes + a) =
+                                make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                return true;
+            };
+            int nt = 0;            // K and V tiles consumed
+            int pcnt[2] = {0, 0};  // PV products per group (p_full phases)
+            auto wait_p = [&](int t) {
+                if (!mbar_wait_warp(&p_full[t], pcnt[t] & 1, p.ctl, abort_flag)) return false;
+                tc_fence_after();
+                return true;
+            };
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 const int e = k & 1;
@@ -414,105 +511,74 @@ __global__ void __launch_bounds__(PagedLayout<D, TILES>::kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                if constexpr (TILES == 2) {
-                    const int end0 = piece_end(u, 0, p.tile_toks, p.causal);
-                    const int end1 = piece_end(u, 1, p.tile_toks, p.causal);
-                    const int last = max(end0, end1) - 1;
-                    const int p0[2] = {pcnt[0], pcnt[1]};
-                    for (int j = u.t0; ok && j <= last + 1; ++j) {
-                        const int ks = n % L::kSlots;  // of tile j; V of tile j - 1 is one before
-                        const int vs = (n + L::kSlots - 1) % L::kSlots;
-                        if (j <= last) {
-                            if (!mbar_wait_warp(&full[ks], (n / L::kSlots) & 1, p.ctl,
-                                                abort_flag)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                        }
-                        bool v_ready = false;
-                        for (int t = 0; t < 2 && ok; ++t) {
-                            const int end = t ? end1 : end0;
-                            if (j > u.t0 && j - 1 < end) {
-                                if (!v_ready) {
-                                    if (!mbar_wait_warp(&full[vs], ((n - 1) / L::kSlots) & 1,
-                                                        p.ctl, abort_flag)) {
-                                        ok = false;
-                                        break;
-                                    }
-                                    clear_tail(u.len, j - 1, vs);
-                                    v_ready = true;
-                                }
-                                if (!mbar_wait_warp(&p_full[t], pcnt[t] & 1, p.ctl, abort_flag)) {
+                const int p0[2] = {pcnt[0], pcnt[1]};
+                const int n0 = nt - u.t0;  // ring index of key tile j is n0 + j
+                if (u.t1 == u.t0) umma_commit_el(q_empty);  // nothing seen: Q is free at once
+                if (is_pair(u)) {
+                    // step by step, group t takes tile j + t
+                    for (int j = u.t0; ok && j - 2 < u.t1; j += 2) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int jp = j + t - 2, jn = j + t;
+                            if (jp >= u.t0 && jp < u.t1) {
+                                if (!wait_v(n0 + jp, jp, u.len) || !wait_p(t)) {
                                     ok = false;
                                     break;
                                 }
-                                tc_fence_after();
-                                issue_pv(t, t, vs, pcnt[t] > p0[t]);
+                                issue_pv(t, (n0 + jp) % L::kVSlots, pcnt[t] > p0[t]);
+                                ++pcnt[t];
+                                umma_commit_el(&v_empty[(n0 + jp) % L::kVSlots]);
+                            }
+                            if (jn < u.t1) {
+                                if (!wait_k(n0 + jn)) {
+                                    ok = false;
+                                    break;
+                                }
+                                issue_s(0, t, (n0 + jn) % L::kKSlots);
+                                umma_commit_el(&k_empty[(n0 + jn) % L::kKSlots]);
+                                if (jn == u.t1 - 1) umma_commit_el(q_empty);
+                            }
+                        }
+                    }
+                } else {
+                    // both groups take every tile, group t for query tile t
+                    const int end[2] = {piece_end(u, 0, p.tile_toks, p.causal),
+                                        piece_end(u, 1, p.tile_toks, p.causal)};
+                    for (int j = u.t0; ok && j <= u.t1; ++j) {
+                        const int vs = (n0 + j - 1 + L::kVSlots) % L::kVSlots;
+                        if (j < u.t1 && !wait_k(n0 + j)) {
+                            ok = false;
+                            break;
+                        }
+                        bool v_ready = false;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (j > u.t0 && j - 1 < end[t]) {
+                                if (!v_ready && !wait_v(n0 + j - 1, j - 1, u.len)) {
+                                    ok = false;
+                                    break;
+                                }
+                                v_ready = true;
+                                if (!wait_p(t)) {
+                                    ok = false;
+                                    break;
+                                }
+                                issue_pv(t, vs, pcnt[t] > p0[t]);
                                 ++pcnt[t];
                             }
-                            if (j < end) {
-                                issue_s(t, t, ks);
-                                umma_commit_el(&s_full[t]);
-                            }
+                            if (j < end[t]) issue_s(t, t, (n0 + j) % L::kKSlots);
                         }
                         if (!ok) break;
-                        if (j == last) umma_commit_el(q_empty);
-                        if (j > u.t0) umma_commit_el(&empty[vs]);
-                        if (j <= last) {
-                            umma_commit_el(&empty[ks]);
-                            n += 2;
-                        }
+                        if (j == u.t1 - 1) umma_commit_el(q_empty);
+                        if (j > u.t0) umma_commit_el(&v_empty[vs]);
+                        if (j < u.t1) umma_commit_el(&k_empty[(n0 + j) % L::kKSlots]);
                     }
-                    if (!ok) break;
-                    if (last < u.t0) umma_commit_el(q_empty);  // nothing seen: Q is free at once
-                    for (int t = 0; t < 2; ++t)
-                        if (pcnt[t] > p0[t]) umma_commit_el(&o_final[t]);
-                } else {
-                    const int end = piece_end(u, 0, p.tile_toks, p.causal);
-                    auto next_s = [&](int j) -> bool {
-                        const int x = n + 2 * (j - u.t0), ks = x % L::kSlots, gg = g + j - u.t0;
-                        if (!mbar_wait_warp(&full[ks], (x / L::kSlots) & 1, p.ctl, abort_flag))
-                            return false;
-                        tc_fence_after();
-                        issue_s(0, gg & 1, ks);
-                        umma_commit_el(&s_full[gg & 1]);
-                        umma_commit_el(&empty[ks]);
-                        if (j == end - 1) umma_commit_el(q_empty);
-                        return true;
-                    };
-                    if (end == u.t0) {
-                        umma_commit_el(q_empty);
-                    } else if (!next_s(u.t0)) {
-                        ok = false;
-                        break;
-                    }
-                    for (int j = u.t0; j < end; ++j) {
-                        if (j + 1 < end && !next_s(j + 1)) {  // S of the next tile ahead of PV
-                            ok = false;
-                            break;
-                        }
-                        const int x = n + 2 * (j - u.t0) + 1, vs = x % L::kSlots;
-                        const int gg = g + j - u.t0;
-                        if (!mbar_wait_warp(&full[vs], (x / L::kSlots) & 1, p.ctl, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        clear_tail(u.len, j, vs);
-                        if (!mbar_wait_warp(&p_full[gg & 1], (gg >> 1) & 1, p.ctl, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        issue_pv(0, gg & 1, vs, j > u.t0);
-                        umma_commit_el(pv_done);
-                        umma_commit_el(&empty[vs]);
-                    }
-                    if (!ok) break;
-                    n += 2 * (end - u.t0);
-                    g += end - u.t0;
-                    if (end > u.t0) umma_commit_el(&o_final[0]);
                 }
+                if (!ok) break;
+                nt += u.t1 - u.t0;
+                // O_t of this piece is final (nobody waits for a group that had no tile)
+                for (int t = 0; t < 2; ++t)
+                    if (pcnt[t] > p0[t]) umma_commit_el(&o_final[t]);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&unit_empty[e]);
             }
@@ -522,41 +588,47 @@ __global__ void __launch_bounds__(PagedLayout<D, TILES>::kThreads, 1)
             __syncwarp();
         }
     } else {
-        if constexpr (TILES == 2) regs_inc<208>();
-        // ---------------------------------------------------------------- softmax warps
+        regs_inc<208>();
+        // ---------------------------------------------------------------- softmax groups
         using T = elem_t<BF16>;
-        const int t = TILES == 2 ? (warp - L::kSoftWarp) >> 2 : 0;  // query tile
-        const int quad = warp & 3;  // a warp may touch TMEM lanes [32*(warp%4), +32)
+        const int t = (warp - 4) >> 2;  // group
+        const int quad = warp & 3;      // a warp may touch TMEM lanes [32*(warp%4), +32)
         const int row = quad * 32 + lane;
-        const int row_tok = t * p.tile_toks + row / p.rep, row_head = row % p.rep;
+        const int row_tok = row / p.rep, row_head = row % p.rep;  // within a query tile
         const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t tS = tmem + lane_base + t * 128;
         const uint32_t tO = tmem + lane_base + 256 + t * D;
         const float sl2 = p.scale_log2;
-        int scnt = 0;  // score tiles consumed
-        int nfin = 0;  // pieces with products (o_final phases)
+        int scnt = 0;          // score tiles consumed by this group
+        int nfin = 0;          // pieces in which this group had products (o_final phases)
+        int nfin1 = 0;         // first group: the same of the second
+        int npair = 0;         // merges between the groups (pair_full, pair_read phases)
+        bool owed = false;     // second group: the first has still to read what it left
         for (int k = 0;; ++k) {
             const int e = k & 1;
             if (!mbar_wait_warp(&unit_full[e], (k >> 1) & 1, p.ctl, abort_flag)) break;
             const PieceSlot u = read_slot(e);
             if (u.tok0 < 0) break;
-            const int end = piece_end(u, t, p.tile_toks, p.causal);
+            const bool pair = is_pair(u);
+            const int q = pair ? 0 : t;  // query tile
+            const int first = u.t0 + (pair ? t : 0), step = pair ? 2 : 1;
+            const int end = pair ? u.t1 : piece_end(u, t, p.tile_toks, p.causal);
             // a warp with no row of the unit only keeps the barriers going
-            const bool real = row_tok < min(u.toks, (t + 1) * p.tile_toks);
+            const int tok = q * p.tile_toks + row_tok;
+            const bool real = row_tok < p.tile_toks && tok < u.toks;
             const bool busy = __any_sync(0xffffffffu, real);
-            const int last = u.last0 + (p.causal ? row_tok : 0);  // last key this row sees
+            const int last = u.last0 + (p.causal ? tok : 0);  // last key this row sees
             float m = -INFINITY;  // running (reference) max of the scaled scores, log2 units
             float l = 0.f;        // running sum of exp2(score - m)
             bool ok = true;
-            for (int j = u.t0; j < end; ++j, ++scnt) {
-                const int buf = TILES == 2 ? t : (scnt & 1);
-                const uint32_t par = TILES == 2 ? (scnt & 1) : ((scnt >> 1) & 1);
-                if (!mbar_wait_warp(&s_full[buf], par, p.ctl, abort_flag)) {
+            for (int j = first; j < end; j += step) {
+                if (!mbar_wait_warp(&s_full[t], scnt & 1, p.ctl, abort_flag)) {
                     ok = false;
                     break;
                 }
+                ++scnt;
                 tc_fence_after();
                 if (busy) {
-                    const uint32_t tS = tmem + lane_base + buf * 128;
                     uint32_t r[128];
                     tmem_ld32(tS + 0, r + 0);
                     tmem_ld32(tS + 32, r + 32);
@@ -605,15 +677,8 @@ __global__ void __launch_bounds__(PagedLayout<D, TILES>::kThreads, 1)
                     const float2 a = fadd2(a01, a23);
                     l += a.x + a.y;
                     if (__any_sync(0xffffffffu, rescale)) {
-                        // two tiles: the previous PV into O_t completed before this S_t; one
-                        // tile: S was issued ahead of it, so wait for it
-                        if constexpr (TILES == 1) {
-                            if (!mbar_wait_warp(pv_done, (scnt - 1) & 1, p.ctl, abort_flag)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                        }
+                        // the previous PV into O_t completed before this S_t, and the next one
+                        // waits for p_full, so O_t is ours to rescale
 #pragma unroll
                         for (int cc = 0; cc < D / 32; ++cc) {
                             uint32_t o[32];
@@ -626,42 +691,94 @@ __global__ void __launch_bounds__(PagedLayout<D, TILES>::kThreads, 1)
                         }
                     }
                 }
-                mbar_arrive_warp_after_st(&p_full[buf]);
+                if (owed) {  // this arrival lets the next PV overwrite what was left in O_1
+                    if (!mbar_wait_warp(pair_read, (npair - 1) & 1, p.ctl, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    owed = false;
+                }
+                mbar_arrive_warp_after_st(&p_full[t]);
             }
             if (!ok) break;
-            if (end > u.t0) {
+            const bool had = first < end;
+            const bool both = pair && u.t1 - u.t0 > 1;  // the second group has a share
+            if (t == 1 && pair) {
+                if (both) {  // its statistics for the first group, which finds O_1 in place
+                    pair_ml[row] = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pair_full);
+                    ++npair;
+                    ++nfin;
+                    owed = true;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&unit_empty[e]);
+                continue;
+            }
+            if (had) {
                 if (!mbar_wait_warp(&o_final[t], nfin & 1, p.ctl, abort_flag)) break;
                 ++nfin;
-                tc_fence_after();
             }
+            float wa = 1.f, wb = 0.f;  // weights of O_0 and of the second group's O_1
+            if (both) {
+                if (!mbar_wait_warp(pair_full, npair & 1, p.ctl, abort_flag)) break;
+                if (!mbar_wait_warp(&o_final[1], nfin1 & 1, p.ctl, abort_flag)) break;
+                ++npair;
+                ++nfin1;
+                const float2 o = pair_ml[row];
+                const float M = fmaxf(m, o.x), mu = M == -INFINITY ? 0.f : M;
+                wa = ex2(m - mu);
+                wb = ex2(o.x - mu);
+                l = l * wa + o.y * wb;
+                m = M;
+            } else if (t == 0 && !pair && piece_end(u, 1, p.tile_toks, p.causal) > u.t0) {
+                ++nfin1;  // the second group waits for its own
+            }
+            tc_fence_after();
             if (busy) {
                 // O and LSE, or the piece's partial (m, l, O~); the tensor-memory loads are
                 // warp-wide, the stores only for real rows
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = u.dest >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
+                wa *= inv;
+                wb *= inv;
                 const int head = u.kvh * p.rep + row_head;
-                const long tok = u.tok0 + row_tok;
-                const long prow = static_cast<long>(u.dest) * p.part_rows + t * 128 + row;
+                const long otok = u.tok0 + tok;
+                const long prow = static_cast<long>(u.dest) * p.part_rows + q * 128 + row;
 #pragma unroll
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
-                    if (end > u.t0) {
+                    if (had) {
                         tmem_ld32(tO + cc * 32, o);
                         tmem_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            o[x] = __float_as_uint(__uint_as_float(o[x]) * wa);
                     } else {
 #pragma unroll
                         for (int x = 0; x < 32; ++x) o[x] = 0u;
                     }
+                    if (both) {
+                        uint32_t o1[32];
+                        tmem_ld32(tO + D + cc * 32, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            o[x] = __float_as_uint(
+                                fmaf(__uint_as_float(o1[x]), wb, __uint_as_float(o[x])));
+                    }
                     if (!real) continue;
                     if (u.dest < 0) {
                         uint4 *dst = reinterpret_cast<uint4 *>(
-                            reinterpret_cast<T *>(p.o) + tok * p.o_t + head * p.o_h + cc * 32);
+                            reinterpret_cast<T *>(p.o) + otok * p.o_t + head * p.o_h + cc * 32);
 #pragma unroll
                         for (int q4 = 0; q4 < 4; ++q4) {
                             uint32_t w[4];
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                w[x] = pack2<BF16>(__uint_as_float(o[8 * q4 + 2 * x]) * inv,
-                                                   __uint_as_float(o[8 * q4 + 2 * x + 1]) * inv);
+                                w[x] = pack2<BF16>(__uint_as_float(o[8 * q4 + 2 * x]),
+                                                   __uint_as_float(o[8 * q4 + 2 * x + 1]));
                             dst[q4] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     } else {
@@ -675,16 +792,19 @@ __global__ void __launch_bounds__(PagedLayout<D, TILES>::kThreads, 1)
                 }
                 if (real) {
                     if (u.dest < 0)
-                        p.lse[tok * p.c.H + head] = row_lse(m, l);
+                        p.lse[otok * p.c.H + head] = row_lse(m, l);
                     else
                         p.part_ml[prow] = make_float2(m, l);
                 }
             }
-            // O has been read out (the next unit's first PV waits for this warp's next p_full
-            // arrival); the unit slot is no longer needed
+            // O has been read out (the next unit's first PV into it waits for this warp's next
+            // p_full arrival, or the second group's after pair_read)
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&unit_empty[e]);
+            if (lane == 0) {
+                if (both) mbar_arrive(pair_read);
+                mbar_arrive(&unit_empty[e]);
+            }
         }
     }
 
@@ -697,70 +817,75 @@ __global__ void __launch_bounds__(PagedLayout<D, TILES>::kThreads, 1)
 }
 
 // Merge of the units that borders cut: block c does the unit whose first piece CTA c ended with,
-// one row per warp.  The pieces stand in CTA order: M = max m_s, w_s = 2^(m_s - M), l = sum w_s l_s,
-// O = sum w_s O_s / l, LSE = (M + log2 l) ln 2, in that order (deterministic).
-constexpr int kMergeWarps = 4;
+// one row per warp at a time.  The pieces stand in CTA order and are folded in in that order
+// (deterministic), a batch at a time with all its reads in flight: M = max m_s, w_s = 2^(m_s - M),
+// l = sum w_s l_s, O = sum w_s O_s / l, LSE = (M + log2 l) ln 2.
+constexpr int kMergeWarps = 8;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const PagedAttnParams p) {
     using T = elem_t<BF16>;
     constexpr int kCols = D / 32;
-    constexpr int kBatch = 8;  // pieces whose partial outputs are in flight at once
+    constexpr int kBatch = 8;
     griddep_wait();
     const int c = static_cast<int>(blockIdx.x), lane = lane_id();
     const int4 cut = p.cut[2 * c];
     const int pieces = p.cut[2 * c + 1].x;
     if (pieces < 2) return;
     const int tok0 = cut.x, toks = cut.y, kvh = cut.z;
-    auto slot = [&](int s) { return static_cast<long>(s == 0 ? 2 * c + 1 : 2 * (c + s)); };
-    for (int r = blockIdx.y * kMergeWarps + warp_id(); r < p.part_rows;
-         r += gridDim.y * kMergeWarps) {
-        const int t = r >> 7, row = r & 127;
-        const int tok = t * p.tile_toks + row / p.rep;
-        if (row >= p.tile_toks * p.rep || tok >= toks) continue;
-        float M = -INFINITY;
-        for (int s = lane; s < pieces; s += 32) M = fmaxf(M, p.part_ml[slot(s) * p.part_rows + r].x);
+    const int r = static_cast<int>(blockIdx.y) * kMergeWarps + warp_id();
+    const int row = r & 127, row_tok = row / p.rep, tok = (r >> 7) * p.tile_toks + row_tok;
+    if (r >= p.part_rows || row_tok >= p.tile_toks || tok >= toks) return;
+    float M = -INFINITY, l = 0.f, acc[kCols];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float l = 0.f, acc[kCols];
+    for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+    for (int s0 = 0; s0 < pieces; s0 += kBatch) {
+        float2 ml[kBatch];
+        float x[kBatch][kCols];
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-        for (int s0 = 0; s0 < pieces; s0 += kBatch) {
-            float2 ml[kBatch];
-            float x[kBatch][kCols];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const long pr = slot(min(s0 + i, pieces - 1)) * p.part_rows + r;
+        for (int i = 0; i < kBatch; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (s0 + i < pieces) {
+                const long slot = s0 + i == 0 ? 2 * c + 1 : 2 * (c + s0 + i);
+                const long pr = slot * p.part_rows + r;
                 ml[i] = p.part_ml[pr];
 #pragma unroll
                 for (int e = 0; e < kCols; ++e) x[i][e] = p.part_o[pr * D + lane * kCols + e];
             }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                // a piece that saw nothing (l = 0) weighs nothing; one whose scores are all NaN
-                // (m = -inf, l = NaN) passes its NaN on
-                if (s0 + i >= pieces || ml[i].y == 0.f) continue;
-                const float w = ml[i].x == -INFINITY ? 1.f : ex2(ml[i].x - M);
-                l = fmaf(w, ml[i].y, l);
-#pragma unroll
-                for (int e = 0; e < kCols; ++e) acc[e] = fmaf(w, x[i][e], acc[e]);
-            }
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int head = kvh * p.rep + row % p.rep;
-        T *dst = reinterpret_cast<T *>(p.o) + static_cast<long>(tok0 + tok) * p.o_t + head * p.o_h +
-                 lane * kCols;
+        float top = M;
 #pragma unroll
-        for (int e = 0; e < kCols; e += 2)
-            reinterpret_cast<uint32_t *>(dst + e)[0] = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
-        if (lane == 0)
-            p.lse[static_cast<long>(tok0 + tok) * p.c.H + head] = row_lse(M, l);
+        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+        const float mu = top == -INFINITY ? 0.f : top;
+        const float back = ex2(M - mu);
+        M = top;
+        l *= back;
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) acc[e] *= back;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            // a piece that saw nothing (l = 0) weighs nothing; one whose scores are all NaN
+            // (m = -inf, l = NaN) passes its NaN on
+            if (s0 + i >= pieces || ml[i].y == 0.f) continue;
+            const float w = ml[i].x == -INFINITY ? 1.f : ex2(ml[i].x - mu);
+            l = fmaf(w, ml[i].y, l);
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) acc[e] = fmaf(w, x[i][e], acc[e]);
+        }
     }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int head = kvh * p.rep + row % p.rep;
+    T *dst = reinterpret_cast<T *>(p.o) + static_cast<long>(tok0 + tok) * p.o_t + head * p.o_h +
+             lane * kCols;
+#pragma unroll
+    for (int e = 0; e < kCols; e += 2)
+        reinterpret_cast<uint32_t *>(dst + e)[0] = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0) p.lse[static_cast<long>(tok0 + tok) * p.c.H + head] = row_lse(M, l);
 }
 
-template <int D, bool BF16, int TILES>
+template <int D, bool BF16, int QT>
 cudaError_t launch_attn_t(const PagedMaps &m, const PagedAttnParams &p, cudaStream_t stream) {
-    using L = PagedLayout<D, TILES>;
-    auto kern = fa_paged_attn_kernel<D, BF16, TILES>;
+    using L = PagedLayout<D, QT>;
+    auto kern = fa_paged_attn_kernel<D, BF16, QT>;
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
@@ -768,8 +893,7 @@ cudaError_t launch_attn_t(const PagedMaps &m, const PagedAttnParams &p, cudaStre
     e = cudaGetLastError();
     if (e != cudaSuccess || p.cut == nullptr) return e;
     cudaLaunchConfig_t cfg = {};
-    const int rows = p.part_rows;  // about four rows per warp, and few blocks where rows are few
-    cfg.gridDim = dim3(kPagedCtas - 1, (rows + 4 * kMergeWarps - 1) / (4 * kMergeWarps));
+    cfg.gridDim = dim3(kPagedCtas - 1, (p.part_rows + kMergeWarps - 1) / kMergeWarps);
     cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

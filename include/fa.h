@@ -387,13 +387,13 @@ const char *fa_status_string(int code);
  *   fa_bwd_gqa over min(s, H / H_kv) dK/dV CTAs per key tile (changes the workspace size).
  *   Negative: FA_ERR_INVALID.
  * fa_debug_paged_pieces: how fa_paged_attn would spread a batch's work over `ctas` CTAs, worked out
- *   on the host from HOST copies of kv_len and q_start, with unit_toks tokens to a unit: 8 ints per
- *   piece (CTA, sequence, K/V head, first token, tokens, first and end key tile, key tiles of the
+ *   on the host from HOST copies of kv_len and q_start, with units of up to tiles (1 or 2) query tiles of
+ *   tile_toks tokens: 8 ints per piece (CTA, sequence, K/V head, first token, tokens, first and end key tile, key tiles of the
  *   unit) in order.  Returns the number of pieces (only the first max_pieces are stored) or an error.
  */
 int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, int H_kv,
-                          int page_size, int max_pages, int max_q, int unit_toks, int causal,
-                          int ctas, int *pieces, int max_pieces);
+                          int page_size, int max_pages, int max_q, int tile_toks, int tiles,
+                          int causal, int ctas, int *pieces, int max_pieces);
 int fa_debug_set_visit_log(uint8_t *buf, size_t bytes);
 int fa_debug_set_wait_limit_ns(unsigned long long ns);
 int fa_debug_set_fault(int mode);

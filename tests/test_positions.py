@@ -204,19 +204,19 @@ def test_paged_check_finds_bad_index_arrays(lib):
     assert ok(n=torch.tensor([0, 0], dtype=torch.int32))
 
 
-def pieces_of(lib, seqs, Hkv, unit, causal, ctas, pad=0, page=16, width=2000):
+def pieces_of(lib, seqs, Hkv, tile, tiles, causal, ctas, pad=0, page=16, width=2000):
     lens = torch.tensor([L for _, L in seqs], dtype=torch.int32)
     start = torch.tensor(np.cumsum([pad] + [n for n, _ in seqs]), dtype=torch.int32)
     T = max(int(start[-1]), 1) + pad
-    out = np.zeros((20000, 8), dtype=np.int32)
+    out = np.zeros((40000, 8), dtype=np.int32)
     n = lib.fa_debug_paged_pieces(lens.data_ptr(), start.data_ptr(), T, len(seqs), Hkv, page, width, T,
-                                  unit, causal, ctas, out.ctypes.data, len(out))
+                                  tile, tiles, causal, ctas, out.ctypes.data, len(out))
     assert 0 <= n <= len(out)
     return out[:n].tolist(), start.tolist()
 
 
 @pytest.mark.parametrize("causal", [0, 1])
-@pytest.mark.parametrize("seed", range(12))
+@pytest.mark.parametrize("seed", range(16))
 def test_paged_work_is_cut_into_equal_stretches_that_cover_every_unit_once(lib, seed, causal):
     rng = np.random.default_rng(seed)
     B = int(rng.integers(1, 12))
@@ -225,28 +225,37 @@ def test_paged_work_is_cut_into_equal_stretches_that_cover_every_unit_once(lib, 
         n = int(rng.choice([0, 1, 1, 2, 7, int(rng.integers(1, 900))]))
         seqs.append((n, max(0, n + int(rng.integers(-n, 3000)) if rng.random() < 0.3 else
                          n + int(rng.integers(0, 3000)))))
-    Hkv, unit = int(rng.integers(1, 9)), int(rng.choice([1, 2, 18, 32, 42, 64, 85, 256]))
-    ctas = int(rng.choice([1, 7, 152]))
-    got, start = pieces_of(lib, seqs, Hkv, unit, causal, ctas, pad=int(rng.integers(0, 3)))
-    want = []  # the line of units in order, with their weights
+    Hkv, tile = int(rng.integers(1, 9)), int(rng.choice([1, 2, 18, 32, 42, 64, 128]))
+    ctas, tiles = int(rng.choice([1, 7, 152])), int(rng.integers(1, 3))
+    got, start = pieces_of(lib, seqs, Hkv, tile, tiles, causal, ctas, pad=int(rng.integers(0, 3)))
+    want = []  # the line of units in order, with their key tiles and cost per tile
+    unit = tile * tiles
     for b, (n, L) in enumerate(seqs):
         for g in range(Hkv):
             for i in range(0, n, unit):
                 toks = min(unit, n - i)
                 end = L - n + i + toks if causal else L
                 want.append((b, g, start[b] + i, toks, max(1, -(-end // 128))))
-    at = 0
-    for cta, b, g, tok, toks, t0, t1, weight in got:
-        assert (b, g, tok, toks, weight) == want[0] and t0 == at < t1 <= weight
+    at = prev = 0
+    for cta, b, g, tok, toks, t0, t1, count in got:
+        assert (b, g, tok, toks, count) == want[0] and t0 == at < t1 <= count
+        # a unit's pieces stand in consecutive CTAs, a CTA's pieces in order
+        if t0 == 0:
+            prev = cta
+        assert cta - prev in (0, 1) and (t0 == 0 or cta == prev + 1)
+        prev = cta
         at = t1
-        if t1 == weight:
+        if t1 == count:
             want.pop(0)
             at = 0
     assert not want and at == 0
-    total = sum(x[6] - x[5] for x in got)
-    share = [sum(x[6] - x[5] for x in got if x[0] == c) for c in range(min(ctas, total))]
-    if total:
-        assert max(share) - min(share) <= 1 and sum(share) == total
+    cost = {}
+    for x in got:
+        c = 2 if x[4] > tile else 1
+        cost[x[0]] = cost.get(x[0], 0) + c * (x[6] - x[5]) + (2 if tiles == 2 and x[5] == 0 else 0)
+    if len(cost) > 1:  # shares differ by no more than a tile and a unit's cost at each border
+        share = [cost.get(c, 0) for c in range(max(cost) + 1)]
+        assert max(share) - min(share) <= 2 * (2 + 2) + 1
 
 
 def test_wrappers_refuse_cpu_tensors_and_wrong_types(lib):
