@@ -1002,7 +1002,7 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
         uint8_t *ws = static_cast<uint8_t *>(workspace);
         p.cut = reinterpret_cast<int4 *>(ws);
         p.part_ml = reinterpret_cast<float2 *>(ws + kPagedCutBytes);
-        p.part_o = reinterpret_cast<float *>(p.part_ml + kPagedSlots * tl.part_rows);
+        p.part_o = reinterpret_cast<float4 *>(p.part_ml + kPagedSlots * tl.part_rows);
     }
     if (make_ctl(p.c.status, 0, 0, &p.ctl) != FA_OK) return FA_ERR_INVALID;
     fa::PagedMaps maps;
@@ -1041,28 +1041,27 @@ int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, i
         return FA_ERR_INVALID;
     c.max_q = max_q;
     const fa::PagedWork w = {tile_toks, tiles * tile_toks, fa::paged_unit_cost(tiles), causal ? 1 : 0};
-    auto weight = [&](int b) -> long {
-        const fa::PagedSeq s = fa::paged_seq(c, b);
-        return s.n > 0 ? H_kv * fa::paged_prefix(s, w, fa::paged_units(s, w)) : 0;
-    };
+    auto weight = [&](int b) { return H_kv * fa::paged_head(fa::paged_seq(c, b), w); };
     long total = 0;
     for (int b = 0; b < B; ++b) total += weight(b);
-    const int used = fa::paged_ctas(total, ctas);
+    fa::PagedLine line;
+    line.cut(total, ctas);
     int n = 0;
-    for (int k = 0; k < used; ++k) {
-        const long at = fa::paged_border(total, used, k);
-        long room = fa::paged_border(total, used, k + 1) - at, before = 0;
+    for (int k = 0; k < line.ctas; ++k) {
+        const long at = line.border(k), end = line.border(k + 1);
+        long room = end - at, before = 0;
         int b = 0;
         while (before + weight(b) <= at) before += weight(b++);
         fa::PagedCursor cur;
         cur.start(c, w, b, at - before);
         while (room > 0) {
+            const long from = end - room;
             const fa::PagedPiece u = cur.take(c, w, room);
             if (u.t0 == u.t1) continue;
             if (n < max_pieces) {
-                int *x = pieces + 8 * n;
+                int *x = pieces + 9 * n;
                 x[0] = k, x[1] = u.b, x[2] = u.kvh, x[3] = u.tok0, x[4] = u.toks, x[5] = u.t0;
-                x[6] = u.t1, x[7] = u.tiles;
+                x[6] = u.t1, x[7] = u.tiles, x[8] = line.holder(from + u.left - 1);
             }
             ++n;
         }

@@ -51,8 +51,7 @@ struct PagedLayout {
     // pair_full, pair_read, unit_full[2], unit_empty[2], drain
     static constexpr int kNumBars = 2 + 2 * kKSlots + 2 * kVSlots + 13;
     static constexpr int kUnitOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // two unit slots
-    static constexpr int kScanOff = kUnitOff + 2 * 48;  // the plan's sums: 16 longs
-    static constexpr int kMiscOff = kScanOff + 16 * 8;  // TMEM base, abort flag
+    static constexpr int kMiscOff = kUnitOff + 2 * 32;  // TMEM base, abort flag
     static constexpr int kPairOff = kMiscOff + 8;       // the second group's (m, l): float2[128]
     static constexpr int kBytes = kPairOff + 128 * 8;
     static constexpr int kAlloc = kBytes + 1024;
@@ -79,7 +78,6 @@ struct PieceSlot {
     int len;
     int t0, t1; // key tiles, t1 not beyond what the unit sees
     int dest;   // -1: O and LSE, otherwise the slot of its partial result
-    int b;      // sequence
 };
 
 // First key tile from t0 on that query tile q of the piece does not take part in.
@@ -91,76 +89,55 @@ __device__ __forceinline__ int piece_end(const PieceSlot &u, int q, int tile_tok
     return max(u.t0, min(u.t1, end));
 }
 
-// The CTA's stretch of the line of key tiles, found by all threads together: W is the sum of the
-// sequences' weights; the border W c / G is then looked for in a running sum over the sequences.
-struct Stretch {
-    long total;     // W
-    int ctas;       // G: CTAs that get work
-    long begin, end;
-    int seq;        // sequence that holds `begin`, and the weight before it
-    long before;
-};
-template <int THREADS>
-__device__ __forceinline__ Stretch find_stretch(const PagedAttnParams &p, const PagedWork &w,
-                                                long *scan) {
-    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-    constexpr int kWarps = THREADS / 32;
-    auto weight = [&](int b) -> long {
-        if (b >= p.c.B) return 0;
-        const PagedSeq s = paged_seq(p.c, b);
-        if (s.bad && blockIdx.x == 0) paged_report(p.c);
-        return s.n > 0 ? p.c.Hkv * paged_prefix(s, w, paged_units(s, w)) : 0;
+// One warp finds its CTA's stretch of the line: the sequences' lengths are summed, 128 sequences at
+// a time with their index reads in flight together, and the border is looked for in the running
+// sum.  Returns what the CTA may take and leaves `cur` at its beginning.
+__device__ __forceinline__ long find_stretch(const PagedView &c, const PagedWork &w, bool report,
+                                             PagedLine &line, PagedCursor &cur) {
+    constexpr int kEach = 4;
+    const int lane = lane_id();
+    auto length = [&](int b) -> long {
+        if (b >= c.B) return 0;
+        const PagedSeq s = paged_seq(c, b);
+        if (s.bad && report) paged_report(c);
+        return c.Hkv * paged_head(s, w);
     };
-    long mine = 0, first = weight(tid);  // the first THREADS sequences' weights are kept
-    for (int b = tid; b < p.c.B; b += THREADS) mine += b == tid ? first : weight(b);
+    long first[kEach], sum = 0;  // the first 128 sequences' lengths are kept
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) scan[warp] = mine;
-    __syncthreads();
-    Stretch r;
-    r.total = 0;
+    for (int i = 0; i < kEach; ++i) {
+        first[i] = length(32 * i + lane);
+        sum += first[i];
+    }
+    for (int b = 32 * kEach + lane; b < c.B; b += 32) sum += length(b);
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) r.total += scan[i];
-    r.ctas = paged_ctas(r.total, static_cast<int>(gridDim.x));
-    const int c = static_cast<int>(blockIdx.x);
-    r.begin = r.end = 0;
-    r.seq = 0;
-    r.before = 0;
-    if (c >= r.ctas) return r;
-    r.begin = paged_border(r.total, r.ctas, c);
-    r.end = paged_border(r.total, r.ctas, c + 1);
-    long base = 0;
-    for (int b0 = 0; b0 < p.c.B; b0 += THREADS) {  // inclusive sums of THREADS sequences at a time
-        const long x = b0 == 0 ? first : weight(b0 + tid);
-        long sum = x;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    line.cut(sum, static_cast<int>(gridDim.x));
+    const int cta = static_cast<int>(blockIdx.x);
+    if (cta >= line.ctas) return 0;
+    const long begin = line.border(cta), room = line.border(cta + 1) - begin;
+    long before = 0;
+    for (int b0 = 0; b0 < c.B; b0 += 32) {
+        long x = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (b0 == 32 * i) x = first[i];
+        if (b0 >= 32 * kEach) x = length(b0 + lane);
+        long upto = x;  // inclusive
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
+            const long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
         }
-        __syncthreads();  // the sums read above are done with
-        if (lane == 31) scan[warp] = sum;
-        __syncthreads();
-        long all = 0;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) sum += scan[i];
-            all += scan[i];
+        const unsigned past = __ballot_sync(0xffffffffu, before + upto > begin);
+        if (past != 0) {
+            const int at = __ffs(static_cast<int>(past)) - 1;
+            const long here = before + __shfl_sync(0xffffffffu, upto - x, at);
+            cur.start(c, w, b0 + at, begin - here);
+            return room;
         }
-        if (base + all > r.begin) {
-            __syncthreads();
-            if (base + sum - x <= r.begin && r.begin < base + sum) {
-                scan[0] = b0 + tid;
-                scan[1] = base + sum - x;
-            }
-            __syncthreads();
-            r.seq = static_cast<int>(scan[0]);
-            r.before = scan[1];
-            break;
-        }
-        base += all;
+        before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    return r;
+    return 0;  // not reached: the border lies inside the line
 }
 
 // Page ids of a piece's key tiles for one load warp: 32 at a time in the lanes, the next 32 read
@@ -174,7 +151,7 @@ struct PageWindow {
         const int i = first + lane_id();
         return i < have ? row[i] : c.num_pages;
     }
-    __device__ __forceinline__ void open(const PagedView &c, const PieceSlot &u) {
+    __device__ __forceinline__ void open(const PagedView &c, const PagedPiece &u) {
         row = c.table + static_cast<long>(u.b) * c.max_pages;
         have = (u.len + (1 << c.page_shift) - 1) >> c.page_shift;
         base = ((u.t0 * kPagedKeys) >> c.page_shift) & ~31;
@@ -223,7 +200,13 @@ __global__ void __launch_bounds__(384, 1)
     const int warp = warp_id(), lane = lane_id();
     const PagedWork work = {p.tile_toks, QT * p.tile_toks, paged_unit_cost(QT), p.causal};
 
-    if (threadIdx.x == 0) {
+    // the plan is made by both load warps at once, so that V's does not wait for the other's slot
+    PagedLine line;
+    PagedCursor cur;
+    long room = 0;
+    if (warp == 0 || warp == 2)
+        room = find_stretch(p.c, work, blockIdx.x == 0 && warp == 0, line, cur);
+    if (threadIdx.x == 96) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int s = 0; s < L::kKSlots; ++s) {
@@ -239,7 +222,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&p_full[i], 4);  // one arrival per softmax warp of a group
             mbar_init(&o_final[i], 1);
             mbar_init(&unit_full[i], 1);
-            mbar_init(&unit_empty[i], 10);  // the MMA warp, the V warp and the softmax warps
+            mbar_init(&unit_empty[i], 9);  // the MMA warp and the softmax warps
         }
         mbar_init(pair_full, 4);
         mbar_init(pair_read, 4);
@@ -254,8 +237,6 @@ __global__ void __launch_bounds__(384, 1)
         tmem_alloc(tmem_slot, L::kTmemCols);
         tmem_relinquish();
     }
-    const Stretch mine =
-        find_stretch<L::kThreads>(p, work, reinterpret_cast<long *>(smem + L::kScanOff));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -265,7 +246,7 @@ __global__ void __launch_bounds__(384, 1)
 
     auto read_slot = [&](int e) {
         PieceSlot u;
-        volatile int *s = unit_slot + 12 * e;
+        volatile int *s = unit_slot + 8 * e;
         u.tok0 = s[0];
         u.toks = s[1];
         u.kvh = s[2];
@@ -274,91 +255,72 @@ __global__ void __launch_bounds__(384, 1)
         u.t0 = s[5];
         u.t1 = s[6];
         u.dest = s[7];
-        u.b = s[8];
         return u;
     };
     // both groups work on the same query tile and take alternate key tiles
-    auto is_pair = [&](const PieceSlot &u) { return QT == 1 || u.toks <= p.tile_toks; };
+    auto is_pair = [&](int toks) { return QT == 1 || toks <= p.tile_toks; };
 
     if (warp < 4) {
-        // warpgroup 0 gives registers to the softmax groups: 128 x 80 + 256 x 208 = 63488 of the
+        // warpgroup 0 gives registers to the softmax groups: 128 x 88 + 256 x 208 = 64512, all of the
         // 384 x 168 = 64512 the CTA is launched with
-        regs_dec<80>();
+        regs_dec<88>();
         const int box_rows = min(1 << p.c.page_shift, kPagedKeys);  // rows of one page in a tile
         const int boxes = kPagedKeys / box_rows;                    // pages of a tile
-        // key tile j's pages from K's or V's map into a ring slot: one lane per page
-        auto load_tile = [&](const CUtensorMap *map, const PieceSlot &u, int j, int id,
-                             uint8_t *slot, uint64_t *bar) {
-            if (lane == 0) mbar_arrive_expect_tx(bar, L::kTileBytes);
-            __syncwarp();
-            if (lane < boxes) {
-                const int y = (j * kPagedKeys) & ((1 << p.c.page_shift) - 1);
-                uint8_t *dst = slot + lane * box_rows * 128;
-                for (int b = 0; b < L::kBoxes; ++b)
-                    tma_load_4d(dst + b * L::kBoxBytes, map, b * 64, maps.rows_inner ? y : u.kvh,
-                                maps.rows_inner ? u.kvh : y, id, bar);
-            }
-        };
-        if (warp == 0) {
-            // ------------------------------------------------- units, Q and K
-            int n = 0;   // K tiles issued
+        if (warp == 0 || warp == 2) {
+            // ------------------------------------------------- loads: Q and K, or V
+            const bool is_v = warp == 2;
+            const CUtensorMap *map = is_v ? &maps.v : &maps.k;
+            uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+            uint8_t *ring = smem + (is_v ? L::kVOff : L::kKOff);
+            const int slots = is_v ? L::kVSlots : L::kKSlots;
+            int n = 0;  // tiles issued
+            int slot = 0;
+            uint32_t parity = 1;  // of the wait for the slot's last tenant
             int nq = 0;  // Q loads issued
             int k = 0;   // pieces so far
             bool ok = true;
-            PagedCursor cur;
-            long room = mine.end - mine.begin;
-            if (room > 0) cur.start(p.c, work, mine.seq, mine.begin - mine.before);
             int4 cut0 = make_int4(-1, 0, 0, 0);  // what the merge has to do for this CTA
             int cut_n = 0;
             for (;;) {
-                PieceSlot u;
-                u.tok0 = -1;
+                PagedPiece u;
+                u.t0 = u.t1 = 0;
+                const long end = line.border(static_cast<int>(blockIdx.x) + 1);
+                long from = 0;
                 while (room > 0) {
-                    const long at = mine.end - room;
-                    const PagedPiece x = cur.take(p.c, work, room);
-                    if (x.t0 == x.t1) continue;
-                    const bool whole = x.t1 - x.t0 == x.tiles;
-                    if (!whole && x.t0 == 0) {  // starts a unit that other CTAs finish
-                        const long end = at + x.unit_end;
-                        cut0 = make_int4(x.tok0, x.toks, x.kvh, 0);
-                        cut_n = static_cast<int>((end * mine.ctas + mine.total - 1) / mine.total) -
-                                static_cast<int>(blockIdx.x);
+                    from = end - room;
+                    u = cur.take(p.c, work, room);
+                    if (u.t0 < u.t1) break;
+                }
+                const bool any = u.t0 < u.t1;
+                const bool whole = u.t1 - u.t0 == u.tiles;
+                const int first_tile = u.t0;
+                // a unit that stands before its sequence sees nothing
+                if (any && u.last0 + (p.causal ? u.toks - 1 : 0) < 0) u.t1 = u.t0;
+                if (!is_v) {
+                    const int e = k & 1;
+                    if (k >= 2 && !mbar_wait_warp(&unit_empty[e], ((k >> 1) - 1) & 1, p.ctl,
+                                                  abort_flag)) {
+                        ok = false;
+                        break;
                     }
-                    u.tok0 = x.tok0;
-                    u.toks = x.toks;
-                    u.kvh = x.kvh;
-                    u.last0 = x.last0;
-                    u.len = x.len;
-                    u.t0 = x.t0;
-                    // a unit that stands before its sequence sees nothing
-                    u.t1 = x.last0 + (p.causal ? x.toks - 1 : 0) < 0 ? x.t0 : x.t1;
-                    u.dest = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (x.t0 == 0 ? 1 : 0);
-                    u.b = x.b;
-                    break;
-                }
-                const int e = k & 1;
-                if (k >= 2 && !mbar_wait_warp(&unit_empty[e], ((k >> 1) - 1) & 1, p.ctl,
-                                              abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    volatile int *s = unit_slot + 12 * e;
-                    s[0] = u.tok0;
-                    if (u.tok0 >= 0) {
-                        s[1] = u.toks;
-                        s[2] = u.kvh;
-                        s[3] = u.last0;
-                        s[4] = u.len;
-                        s[5] = u.t0;
-                        s[6] = u.t1;
-                        s[7] = u.dest;
-                        s[8] = u.b;
+                    if (lane == 0) {
+                        volatile int *s = unit_slot + 8 * e;
+                        s[0] = any ? u.tok0 : -1;
+                        if (any) {
+                            s[1] = u.toks;
+                            s[2] = u.kvh;
+                            s[3] = u.last0;
+                            s[4] = u.len;
+                            s[5] = u.t0;
+                            s[6] = u.t1;
+                            s[7] = whole ? -1
+                                         : 2 * static_cast<int>(blockIdx.x) + (first_tile == 0 ? 1 : 0);
+                        }
+                        mbar_arrive(&unit_full[e]);
                     }
-                    mbar_arrive(&unit_full[e]);
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (u.tok0 < 0) break;
+                if (!any) break;
                 ++k;
                 PageWindow win;
                 win.open(p.c, u);
@@ -366,7 +328,7 @@ __global__ void __launch_bounds__(384, 1)
                     if (nq > 0 && !mbar_wait_warp(q_empty, (nq - 1) & 1, p.ctl, abort_flag))
                         return false;
                     if (lane == 0) {
-                        const int tiles = is_pair(u) ? 1 : 2;
+                        const int tiles = is_pair(u.toks) ? 1 : 2;
                         mbar_arrive_expect_tx(
                             q_full, tiles * L::kBoxes * 128 * p.rep * p.q_box_toks);
                         for (int t = 0; t < tiles; ++t)
@@ -377,17 +339,34 @@ __global__ void __launch_bounds__(384, 1)
                     ++nq;
                     return true;
                 };
-                bool q_done = false;
-                if (nq == 0) ok = q_done = load_q();  // the first Q needs no page id
+                bool q_done = is_v;
+                if (!q_done && nq == 0) ok = q_done = load_q();  // the first Q needs no page id
+                if (!whole && first_tile == 0) {  // starts a unit that other CTAs finish
+                    cut0 = make_int4(u.tok0, u.toks, u.kvh, 0);
+                    cut_n = line.holder(from + u.left - 1) - static_cast<int>(blockIdx.x) + 1;
+                }
                 for (int j = u.t0; j < u.t1 && ok; ++j) {
-                    const int id = win.tile(p.c, j, boxes), s = n % L::kKSlots;
-                    if (!mbar_wait_warp(&k_empty[s], ((n / L::kKSlots) & 1) ^ 1, p.ctl,
-                                        abort_flag)) {
+                    const int id = win.tile(p.c, j, boxes);
+                    if (!mbar_wait_warp(&empty[slot], parity, p.ctl, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    load_tile(&maps.k, u, j, id, smem + L::kKOff + s * L::kTileBytes, &k_full[s]);
+                    // the tile's pages into its slot: one lane per page
+                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], L::kTileBytes);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const int y = (j * kPagedKeys) & ((1 << p.c.page_shift) - 1);
+                        uint8_t *dst = ring + slot * L::kTileBytes + lane * box_rows * 128;
+                        for (int b = 0; b < L::kBoxes; ++b)
+                            tma_load_4d(dst + b * L::kBoxBytes, map, b * 64,
+                                        maps.rows_inner ? y : u.kvh, maps.rows_inner ? u.kvh : y,
+                                        id, &full[slot]);
+                    }
                     ++n;
+                    if (++slot == slots) {
+                        slot = 0;
+                        parity ^= 1;
+                    }
                     // the first K goes ahead of Q: its slot frees before the Q tiles do
                     if (!q_done) {
                         ok = load_q();
@@ -397,7 +376,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (ok && !q_done) ok = load_q();  // a unit that sees nothing takes its turn
                 if (!ok) break;
             }
-            if (p.cut != nullptr && lane == 0) {
+            if (!is_v && p.cut != nullptr && lane == 0) {
                 p.cut[2 * blockIdx.x] = cut0;
                 p.cut[2 * blockIdx.x + 1] = make_int4(cut_n, 0, 0, 0);
             }
@@ -405,42 +384,9 @@ __global__ void __launch_bounds__(384, 1)
                 // let every copy still in flight land before shared memory goes away
                 if (lane == 0) {
                     if (nq > 0) drain_wait(q_full, (nq - 1) & 1, p.ctl);
-                    for (int l = n > L::kKSlots ? n - L::kKSlots : 0; l < n; ++l)
-                        drain_wait(&k_full[l % L::kKSlots], (l / L::kKSlots) & 1, p.ctl);
+                    for (int l = n > slots ? n - slots : 0; l < n; ++l)
+                        drain_wait(&full[l % slots], (l / slots) & 1, p.ctl);
                 }
-            }
-            __syncwarp();
-        } else if (warp == 2) {
-            // ------------------------------------------------- V
-            int n = 0;
-            bool ok = true;
-            for (int k = 0; ok; ++k) {
-                const int e = k & 1;
-                if (!mbar_wait_warp(&unit_full[e], (k >> 1) & 1, p.ctl, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                const PieceSlot u = read_slot(e);
-                if (u.tok0 < 0) break;
-                PageWindow win;
-                win.open(p.c, u);
-                for (int j = u.t0; j < u.t1; ++j) {
-                    const int id = win.tile(p.c, j, boxes), s = n % L::kVSlots;
-                    if (!mbar_wait_warp(&v_empty[s], ((n / L::kVSlots) & 1) ^ 1, p.ctl,
-                                        abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    load_tile(&maps.v, u, j, id, smem + L::kVOff + s * L::kTileBytes, &v_full[s]);
-                    ++n;
-                }
-                __syncwarp();
-                if (ok && lane == 0) mbar_arrive(&unit_empty[e]);
-            }
-            if (!ok || *abort_flag) {
-                if (lane == 0)
-                    for (int l = n > L::kVSlots ? n - L::kVSlots : 0; l < n; ++l)
-                        drain_wait(&v_full[l % L::kVSlots], (l / L::kVSlots) & 1, p.ctl);
             }
             __syncwarp();
         } else if (warp == 1) {
@@ -514,7 +460,7 @@ __global__ void __launch_bounds__(384, 1)
                 const int p0[2] = {pcnt[0], pcnt[1]};
                 const int n0 = nt - u.t0;  // ring index of key tile j is n0 + j
                 if (u.t1 == u.t0) umma_commit_el(q_empty);  // nothing seen: Q is free at once
-                if (is_pair(u)) {
+                if (is_pair(u.toks)) {
                     // step by step, group t takes tile j + t
                     for (int j = u.t0; ok && j - 2 < u.t1; j += 2) {
 #pragma unroll
@@ -609,7 +555,7 @@ __global__ void __launch_bounds__(384, 1)
             if (!mbar_wait_warp(&unit_full[e], (k >> 1) & 1, p.ctl, abort_flag)) break;
             const PieceSlot u = read_slot(e);
             if (u.tok0 < 0) break;
-            const bool pair = is_pair(u);
+            const bool pair = is_pair(u.toks);
             const int q = pair ? 0 : t;  // query tile
             const int first = u.t0 + (pair ? t : 0), step = pair ? 2 : 1;
             const int end = pair ? u.t1 : piece_end(u, t, p.tile_toks, p.causal);
@@ -745,10 +691,10 @@ __global__ void __launch_bounds__(384, 1)
                 wb *= inv;
                 const int head = u.kvh * p.rep + row_head;
                 const long otok = u.tok0 + tok;
-                const long prow = static_cast<long>(u.dest) * p.part_rows + q * 128 + row;
+                const int prow = q * 128 + row;
 #pragma unroll
                 for (int cc = 0; cc < D / 32; ++cc) {
-                    uint32_t o[32];
+                    uint32_t o[32], o1[32];
                     if (had) {
                         tmem_ld32(tO + cc * 32, o);
                         tmem_wait_ld();
@@ -760,7 +706,6 @@ __global__ void __launch_bounds__(384, 1)
                         for (int x = 0; x < 32; ++x) o[x] = 0u;
                     }
                     if (both) {
-                        uint32_t o1[32];
                         tmem_ld32(tO + D + cc * 32, o1);
                         tmem_wait_ld();
 #pragma unroll
@@ -782,10 +727,13 @@ __global__ void __launch_bounds__(384, 1)
                             dst[q4] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + cc * 32);
+                        // column-major in groups of four: the warp's rows side by side, 512 bytes
+                        // a store (row by row the 256 rows took 11000 cycles)
+                        float4 *dst = p.part_o +
+                                      (static_cast<long>(u.dest) * (D / 4) + cc * 8) * p.part_rows + prow;
 #pragma unroll
                         for (int q4 = 0; q4 < 8; ++q4)
-                            dst[q4] = make_float4(
+                            dst[q4 * p.part_rows] = make_float4(
                                 __uint_as_float(o[4 * q4]), __uint_as_float(o[4 * q4 + 1]),
                                 __uint_as_float(o[4 * q4 + 2]), __uint_as_float(o[4 * q4 + 3]));
                     }
@@ -794,7 +742,7 @@ __global__ void __launch_bounds__(384, 1)
                     if (u.dest < 0)
                         p.lse[otok * p.c.H + head] = row_lse(m, l);
                     else
-                        p.part_ml[prow] = make_float2(m, l);
+                        p.part_ml[static_cast<long>(u.dest) * p.part_rows + prow] = make_float2(m, l);
                 }
             }
             // O has been read out (the next unit's first PV into it waits for this warp's next
@@ -816,40 +764,41 @@ __global__ void __launch_bounds__(384, 1)
     }
 }
 
-// Merge of the units that borders cut: block c does the unit whose first piece CTA c ended with,
-// one row per warp at a time.  The pieces stand in CTA order and are folded in in that order
-// (deterministic), a batch at a time with all its reads in flight: M = max m_s, w_s = 2^(m_s - M),
-// l = sum w_s l_s, O = sum w_s O_s / l, LSE = (M + log2 l) ln 2.
+// Merge of the units that borders cut: block (c, y) does rows [32 y, 32 y + 32) of the unit whose first
+// piece CTA c ended with, a lane per row and a slice of the columns per warp.  The pieces stand in
+// CTA order and are folded in in that order (deterministic), a batch at a time with all its reads
+// in flight: M = max m_s, w_s = 2^(m_s - M), l = sum w_s l_s, O = sum w_s O_s / l, LSE = (M + log2 l) ln 2.
 constexpr int kMergeWarps = 8;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const PagedAttnParams p) {
     using T = elem_t<BF16>;
-    constexpr int kCols = D / 32;
-    constexpr int kBatch = 8;
+    constexpr int kCols = D / 4 / kMergeWarps;  // float4 columns per warp
+    constexpr int kBatch = 4;
     griddep_wait();
-    const int c = static_cast<int>(blockIdx.x), lane = lane_id();
+    const int c = static_cast<int>(blockIdx.x), warp = warp_id();
     const int4 cut = p.cut[2 * c];
     const int pieces = p.cut[2 * c + 1].x;
     if (pieces < 2) return;
     const int tok0 = cut.x, toks = cut.y, kvh = cut.z;
-    const int r = static_cast<int>(blockIdx.y) * kMergeWarps + warp_id();
+    const int r = static_cast<int>(blockIdx.y) * 32 + lane_id();
     const int row = r & 127, row_tok = row / p.rep, tok = (r >> 7) * p.tile_toks + row_tok;
     if (r >= p.part_rows || row_tok >= p.tile_toks || tok >= toks) return;
-    float M = -INFINITY, l = 0.f, acc[kCols];
+    float M = -INFINITY, l = 0.f;
+    float4 acc[kCols];
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+    for (int e = 0; e < kCols; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = 0; s0 < pieces; s0 += kBatch) {
         float2 ml[kBatch];
-        float x[kBatch][kCols];
+        float4 x[kBatch][kCols];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             ml[i] = make_float2(-INFINITY, 0.f);
             if (s0 + i < pieces) {
                 const long slot = s0 + i == 0 ? 2 * c + 1 : 2 * (c + s0 + i);
-                const long pr = slot * p.part_rows + r;
-                ml[i] = p.part_ml[pr];
+                ml[i] = p.part_ml[slot * p.part_rows + r];
+                const float4 *src = p.part_o + (slot * (D / 4) + warp * kCols) * p.part_rows + r;
 #pragma unroll
-                for (int e = 0; e < kCols; ++e) x[i][e] = p.part_o[pr * D + lane * kCols + e];
+                for (int e = 0; e < kCols; ++e) x[i][e] = src[e * p.part_rows];
             }
         }
         float top = M;
@@ -860,7 +809,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const 
         M = top;
         l *= back;
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) acc[e] *= back;
+        for (int e = 0; e < kCols; ++e)
+            acc[e] = make_float4(acc[e].x * back, acc[e].y * back, acc[e].z * back, acc[e].w * back);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             // a piece that saw nothing (l = 0) weighs nothing; one whose scores are all NaN
@@ -869,17 +819,23 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const 
             const float w = ml[i].x == -INFINITY ? 1.f : ex2(ml[i].x - mu);
             l = fmaf(w, ml[i].y, l);
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) acc[e] = fmaf(w, x[i][e], acc[e]);
+            for (int e = 0; e < kCols; ++e)
+                acc[e] = make_float4(fmaf(w, x[i][e].x, acc[e].x), fmaf(w, x[i][e].y, acc[e].y),
+                                     fmaf(w, x[i][e].z, acc[e].z), fmaf(w, x[i][e].w, acc[e].w));
         }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const int head = kvh * p.rep + row % p.rep;
-    T *dst = reinterpret_cast<T *>(p.o) + static_cast<long>(tok0 + tok) * p.o_t + head * p.o_h +
-             lane * kCols;
+    uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.o) +
+                                           static_cast<long>(tok0 + tok) * p.o_t + head * p.o_h +
+                                           warp * kCols * 4);
 #pragma unroll
     for (int e = 0; e < kCols; e += 2)
-        reinterpret_cast<uint32_t *>(dst + e)[0] = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0) p.lse[static_cast<long>(tok0 + tok) * p.c.H + head] = row_lse(M, l);
+        dst[e / 2] = make_uint4(pack2<BF16>(acc[e].x * inv, acc[e].y * inv),
+                                pack2<BF16>(acc[e].z * inv, acc[e].w * inv),
+                                pack2<BF16>(acc[e + 1].x * inv, acc[e + 1].y * inv),
+                                pack2<BF16>(acc[e + 1].z * inv, acc[e + 1].w * inv));
+    if (warp == 0) p.lse[static_cast<long>(tok0 + tok) * p.c.H + head] = row_lse(M, l);
 }
 
 template <int D, bool BF16, int QT>
@@ -893,7 +849,7 @@ cudaError_t launch_attn_t(const PagedMaps &m, const PagedAttnParams &p, cudaStre
     e = cudaGetLastError();
     if (e != cudaSuccess || p.cut == nullptr) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kPagedCtas - 1, (p.part_rows + kMergeWarps - 1) / kMergeWarps);
+    cfg.gridDim = dim3(kPagedCtas - 1, (p.part_rows + 31) / 32);
     cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

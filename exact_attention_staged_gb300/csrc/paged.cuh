@@ -52,10 +52,12 @@ __host__ __device__ inline int paged_page(const PagedView &c, int b, int pos) {
 // How the attention's work is cut.  A unit is one K/V head of one sequence with up to
 // `unit_toks` of its new tokens (all query heads of the group), walked over the key tiles that its
 // last token sees.  Units in order (sequence, K/V head, tokens) form one line; a unit takes
-// unit_cost + tile_cost * tiles of it (tiles at least 1), where tile_cost is 2 for a unit of two
-// query tiles and 1 for a unit of one.  CTA c of G takes [c W / G, (c + 1) W / G) of the line's
-// length W, so every CTA gets an equal share whatever the mixture of lengths.  A border inside a
-// unit cuts it between two key tiles; its pieces are merged afterwards.
+// unit_cost + tile_cost * keys of it (keys at least 1), where tile_cost is 2 for a unit of two
+// query tiles and 1 for a unit of one.  The line is cut into one equal stretch per CTA, whatever
+// the mixture of lengths.  A border inside a unit cuts it between two key tiles; its pieces are
+// merged afterwards.  Lengths go by keys and not by tiles because their sums over units are then
+// polynomials: a CTA finds its place with a few multiplications (with rounded tiles the search
+// took up to 13000 cycles before the first load).
 constexpr int kPagedKeys = 128;  // keys per tile
 
 struct PagedWork {
@@ -65,81 +67,76 @@ struct PagedWork {
     int causal;
 };
 
-// sum of floor((a i + b) / m) for i < n (a, b >= 0): Euclid's steps on the lattice points below
-// the line, a handful of divisions.
-__host__ __device__ inline long paged_floor_sum(long n, long m, long a, long b) {
-    long sum = 0;
-    while (n > 0) {
-        if (a >= m) {
-            sum += n * (n - 1) / 2 * (a / m);
-            a %= m;
-        }
-        if (b >= m) {
-            sum += n * (b / m);
-            b %= m;
-        }
-        const long y = a * n + b;
-        if (y < m) break;
-        n = y / m;
-        b = y % m;
-        const long t = m;
-        m = a;
-        a = t;
-    }
-    return sum;
-}
+// What a unit costs beside its keys (Q, the first loads, the epilogue), for units of up to two query
+// tiles or of one.
+__host__ __device__ inline int paged_unit_cost(int tiles) { return tiles == 2 ? 256 : 32; }
 
 __host__ __device__ inline int paged_units(const PagedSeq &s, const PagedWork &w) {
-    return (s.n + w.unit_toks - 1) / w.unit_toks;  // per K/V head
+    return s.n <= w.unit_toks ? (s.n > 0 ? 1 : 0) : (s.n - 1) / w.unit_toks + 1;  // per K/V head
 }
 __host__ __device__ inline int paged_tile_cost(const PagedWork &w, int toks) {
     return toks > w.tile_toks ? 2 : 1;
 }
-// Key tiles that the first `toks` new tokens of a sequence see.
-__host__ __device__ inline int paged_tiles(const PagedSeq &s, const PagedWork &w, int toks) {
+// Keys that the first `toks` new tokens of a sequence see.
+__host__ __device__ inline int paged_keys(const PagedSeq &s, const PagedWork &w, int toks) {
     const int end = w.causal ? s.len - s.n + toks : s.len;
-    return end > 0 ? (end + kPagedKeys - 1) / kPagedKeys : 0;
+    return end > 0 ? end : 0;
 }
 
-// Length on the line of the first i units of one K/V head.
-__host__ __device__ inline long paged_prefix(const PagedSeq &s, const PagedWork &w, long i) {
-    const long last = paged_units(s, w) - 1;
-    const long m = i < last ? i : last;  // units before the last one: whole ones
-    long tiles = 0;
-    if (m > 0) {
-        if (w.causal) {  // unit j sees len - n + (j + 1) unit_toks keys, at least a weight of 1
-            const long ctx = static_cast<long>(s.len) - s.n;
-            long none = ctx < 0 ? -ctx / w.unit_toks : 0;
+// Length on the line of the first m units of one K/V head, all but the last of which are whole.
+__host__ __device__ inline long paged_prefix(const PagedSeq &s, const PagedWork &w, long m) {
+    long keys;
+    if (w.causal) {  // unit j sees len - n + (j + 1) unit_toks keys, at least a weight of 1
+        const long ctx = static_cast<long>(s.len) - s.n;
+        long none = 0;
+        if (ctx < 0) {
+            none = -ctx / w.unit_toks;
             if (none > m) none = m;
-            tiles = none + paged_floor_sum(m - none, kPagedKeys, w.unit_toks,
-                                           ctx + (none + 1) * w.unit_toks + kPagedKeys - 1);
+        }
+        keys = none + (m - none) * ctx +
+               w.unit_toks * (m * (m + 1) / 2 - none * (none + 1) / 2);
+    } else {
+        keys = m * (s.len > 0 ? s.len : 1);
+    }
+    return m * w.unit_cost + keys * paged_tile_cost(w, w.unit_toks);
+}
+__host__ __device__ inline long paged_head(const PagedSeq &s, const PagedWork &w) {
+    const int last = paged_units(s, w) - 1;
+    if (last < 0) return 0;
+    const int keys = paged_keys(s, w, s.n);
+    return (last > 0 ? paged_prefix(s, w, last) : 0) + w.unit_cost +
+           static_cast<long>(keys > 0 ? keys : 1) *
+               paged_tile_cost(w, s.n - last * w.unit_toks);
+}
+
+// The line of length `total` cut for up to `most` CTAs: the first r of them take q + 1, the others q.
+// No stretch is shorter than two single key tiles, one step of a CTA's two softmax groups (nor
+// than a tile of two query tiles, so that every CTA between a cut unit's first and last one has a
+// piece of it).
+struct PagedLine {
+    long total, q;
+    int ctas, r;
+    __host__ __device__ void cut(long length, int most) {
+        total = length;
+        ctas = length >= most * 256l ? most : length >= 256 ? static_cast<int>(length) / 256
+                                             : length > 0 ? 1 : 0;
+        if (ctas == 0) {
+            q = r = 0;
+        } else if (length < (1l << 31)) {
+            q = static_cast<unsigned>(length) / static_cast<unsigned>(ctas);
+            r = static_cast<int>(length - q * ctas);
         } else {
-            const int t = paged_tiles(s, w, 0);
-            tiles = m * (t > 0 ? t : 1);
+            q = length / ctas;
+            r = static_cast<int>(length - q * ctas);
         }
     }
-    long sum = m * w.unit_cost + tiles * paged_tile_cost(w, w.unit_toks);
-    if (i > last) {
-        const int t = paged_tiles(s, w, s.n);
-        sum += w.unit_cost + (t > 0 ? t : 1) * paged_tile_cost(w, s.n - static_cast<int>(last) * w.unit_toks);
+    __host__ __device__ long border(int c) const { return q * c + (c < r ? c : r); }
+    // The CTA whose stretch holds position x.
+    __host__ __device__ int holder(long x) const {
+        const long wide = (q + 1) * r;
+        return static_cast<int>(x < wide ? x / (q + 1) : r + (x - wide) / q);
     }
-    return sum;
-}
-
-// What a unit costs beside its tiles (Q, the first loads, the epilogue), in single tiles; units of
-// up to two query tiles or of one.
-__host__ __device__ inline int paged_unit_cost(int tiles) { return tiles == 2 ? 2 : 0; }
-
-// CTAs that share a line of length W: no stretch shorter than two single key tiles, which is one
-// step of a CTA's two softmax groups (and no shorter than a tile of two query tiles, so that every
-// CTA between a unit's first and last one has a piece of it).
-__host__ __device__ inline int paged_ctas(long total, int most) {
-    const long g = total / 2;
-    return g >= most ? most : g > 0 ? static_cast<int>(g) : total > 0 ? 1 : 0;
-}
-__host__ __device__ inline long paged_border(long total, int ctas, int c) {
-    return total * c / ctas;
-}
+};
 
 // A stretch of one unit's key tiles, [t0, t1) of `tiles` (tiles at least 1).
 struct PagedPiece {
@@ -150,32 +147,54 @@ struct PagedPiece {
     int last0;    // last key that the first token sees (that token j sees: + j when causal)
     int len;
     int t0, t1, tiles;
-    long unit_end;  // end of the unit on the line, from the position before it was taken
+    long left;    // of the unit on the line, from where the piece was taken
 };
 
 struct PagedCursor {
     PagedSeq s;
-    int b, g, i;  // sequence, K/V head and unit
-    int at;       // place inside the unit's length
+    int b, g, i, units;  // sequence, K/V head, unit; units per head
+    long at;             // place inside the unit's length
 
-    // `pos`: length inside sequence b that lies before the position
+    // `pos`: length inside sequence b that lies before the position.  Head and unit are estimated
+    // in floating point and put right by the exact lengths.
     __host__ __device__ void start(const PagedView &c, const PagedWork &w, int seq, long pos) {
         b = seq;
         s = paged_seq(c, b);
-        const int units = paged_units(s, w);
-        const long each = paged_prefix(s, w, units);
-        g = static_cast<int>(pos / each);
+        units = paged_units(s, w);
+        const long each = paged_head(s, w);
+        g = static_cast<int>(static_cast<float>(pos) / static_cast<float>(each));
+        if (g > c.Hkv - 1) g = c.Hkv - 1;
+        while (g * each > pos) --g;
+        while (g + 1 < c.Hkv && (g + 1) * each <= pos) ++g;
         pos -= g * each;
-        int lo = 0, hi = units - 1;  // the last unit whose prefix is <= pos
-        while (lo < hi) {
-            const int mid = lo + (hi - lo + 1) / 2;
-            if (paged_prefix(s, w, mid) <= pos)
-                lo = mid;
-            else
-                hi = mid - 1;
+        i = 0;
+        if (units > 1) {
+            const int last = units - 1;
+            const long ctx = static_cast<long>(s.len) - s.n;
+            if (w.causal && ctx < 0) {
+                int lo = 0, hi = last;  // the last unit whose prefix is <= pos
+                while (lo < hi) {
+                    const int mid = lo + (hi - lo + 1) / 2;
+                    if (paged_prefix(s, w, mid) <= pos)
+                        lo = mid;
+                    else
+                        hi = mid - 1;
+                }
+                i = lo;
+            } else {  // pos = a i^2 + f i
+                const float cost = static_cast<float>(paged_tile_cost(w, w.unit_toks));
+                const float a = w.causal ? 0.5f * cost * w.unit_toks : 0.f;
+                const float f = w.unit_cost + cost * (w.causal ? ctx + 0.5f * w.unit_toks
+                                                               : static_cast<float>(s.len));
+                const float x = static_cast<float>(pos);
+                i = static_cast<int>(2.f * x / (f + sqrtf(f * f + 4.f * a * x)));
+                if (i > last) i = last;
+                while (i > 0 && paged_prefix(s, w, i) > pos) --i;
+                while (i < last && paged_prefix(s, w, i + 1) <= pos) ++i;
+            }
+            if (i > 0) pos -= paged_prefix(s, w, i);
         }
-        i = lo;
-        at = static_cast<int>(lo > 0 ? pos - paged_prefix(s, w, lo) : pos);
+        at = pos;
     }
     // The next piece, taking at most `room` of the line; `room` is lowered by what it took.  The
     // piece is empty (t0 == t1) where both borders fall before or into the same key tile.
@@ -188,22 +207,26 @@ struct PagedCursor {
         p.b = b;
         p.last0 = w.causal ? s.len - s.n + i0 : s.len - 1;
         p.len = s.len;
-        const int seen = paged_tiles(s, w, i0 + p.toks), cost = paged_tile_cost(w, p.toks);
-        p.tiles = seen > 0 ? seen : 1;
-        const int length = w.unit_cost + cost * p.tiles;
-        p.unit_end = length - at;
-        auto tile_of = [&](int x) { return x > w.unit_cost ? (x - w.unit_cost) / cost : 0; };
+        int keys = paged_keys(s, w, i0 + p.toks);
+        if (keys == 0) keys = 1;
+        const int cost = paged_tile_cost(w, p.toks);
+        p.tiles = (keys - 1) / kPagedKeys + 1;
+        const long length = w.unit_cost + static_cast<long>(cost) * keys;
+        p.left = length - at;
+        auto tile_of = [&](long x) {
+            return x > w.unit_cost ? static_cast<int>((x - w.unit_cost) >> (cost == 2 ? 8 : 7)) : 0;
+        };
         p.t0 = tile_of(at);
-        if (room < length - at) {
-            at += static_cast<int>(room);
+        if (room < p.left) {
+            at += room;
             room = 0;
             p.t1 = tile_of(at);
             return p;
         }
         p.t1 = p.tiles;
-        room -= length - at;
+        room -= p.left;
         at = 0;
-        if (++i == paged_units(s, w)) {
+        if (++i == units) {
             i = 0;
             if (++g == c.Hkv) {
                 g = 0;
@@ -211,6 +234,7 @@ struct PagedCursor {
                     if (++b >= c.B) break;
                     s = paged_seq(c, b);
                 } while (s.n == 0);
+                units = paged_units(s, w);
             }
         }
         return p;

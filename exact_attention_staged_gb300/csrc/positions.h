@@ -61,7 +61,7 @@ struct PagedAttnParams {
     int causal;
     // a unit that a border cuts: CTA c's piece that starts inside a unit goes to slot 2c, its piece
     // that starts one but does not end it to slot 2c + 1, and cut[c] says what to merge
-    float *part_o;                   // [slots][part_rows][d] unnormalised
+    float4 *part_o;                  // [slots][d / 4][part_rows] unnormalised, 4 columns each
     float2 *part_ml;                 // [slots][part_rows] running max (log2) and sum
     int4 *cut;                       // [2 * CTAs], or nullptr: no unit has more than one key tile
     Ctl ctl;

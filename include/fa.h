@@ -386,10 +386,11 @@ const char *fa_status_string(int code);
  * fa_debug_set_dkdv_splits: 0 = automatic; s > 0 splits every K/V head's query group of
  *   fa_bwd_gqa over min(s, H / H_kv) dK/dV CTAs per key tile (changes the workspace size).
  *   Negative: FA_ERR_INVALID.
- * fa_debug_paged_pieces: how fa_paged_attn would spread a batch's work over `ctas` CTAs, worked out
- *   on the host from HOST copies of kv_len and q_start, with units of up to tiles (1 or 2) query tiles of
- *   tile_toks tokens: 8 ints per piece (CTA, sequence, K/V head, first token, tokens, first and end key tile, key tiles of the
- *   unit) in order.  Returns the number of pieces (only the first max_pieces are stored) or an error.
+ * fa_debug_paged_pieces: how fa_paged_attn would spread a batch's work over up to `ctas` CTAs, worked
+ *   out on the host from HOST copies of kv_len and q_start, with units of up to `tiles` (1 or 2)
+ *   query tiles of tile_toks tokens: 9 ints per piece, in order (CTA, sequence, K/V head, first
+ *   token, tokens, first and end key tile, key tiles of the unit, the CTA that holds its last
+ *   piece).  Returns the number of pieces (only the first max_pieces are stored) or an error.
  */
 int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, int H_kv,
                           int page_size, int max_pages, int max_q, int tile_toks, int tiles,

@@ -208,7 +208,7 @@ def pieces_of(lib, seqs, Hkv, tile, tiles, causal, ctas, pad=0, page=16, width=2
     lens = torch.tensor([L for _, L in seqs], dtype=torch.int32)
     start = torch.tensor(np.cumsum([pad] + [n for n, _ in seqs]), dtype=torch.int32)
     T = max(int(start[-1]), 1) + pad
-    out = np.zeros((40000, 8), dtype=np.int32)
+    out = np.zeros((40000, 9), dtype=np.int32)
     n = lib.fa_debug_paged_pieces(lens.data_ptr(), start.data_ptr(), T, len(seqs), Hkv, page, width, T,
                                   tile, tiles, causal, ctas, out.ctypes.data, len(out))
     assert 0 <= n <= len(out)
@@ -237,15 +237,17 @@ def test_paged_work_is_cut_into_equal_stretches_that_cover_every_unit_once(lib, 
                 end = L - n + i + toks if causal else L
                 want.append((b, g, start[b] + i, toks, max(1, -(-end // 128))))
     at = prev = 0
-    for cta, b, g, tok, toks, t0, t1, count in got:
+    ends = []
+    for cta, b, g, tok, toks, t0, t1, count, holder in got:
         assert (b, g, tok, toks, count) == want[0] and t0 == at < t1 <= count
-        # a unit's pieces stand in consecutive CTAs, a CTA's pieces in order
-        if t0 == 0:
-            prev = cta
-        assert cta - prev in (0, 1) and (t0 == 0 or cta == prev + 1)
+        # a unit's pieces stand in consecutive CTAs, and each names the one that holds the last
+        assert t0 == 0 or cta == prev + 1
         prev = cta
+        ends.append(holder)
         at = t1
         if t1 == count:
+            assert set(ends) == {cta}
+            ends = []
             want.pop(0)
             at = 0
     assert not want and at == 0
@@ -253,9 +255,24 @@ def test_paged_work_is_cut_into_equal_stretches_that_cover_every_unit_once(lib, 
     for x in got:
         c = 2 if x[4] > tile else 1
         cost[x[0]] = cost.get(x[0], 0) + c * (x[6] - x[5]) + (2 if tiles == 2 and x[5] == 0 else 0)
-    if len(cost) > 1:  # shares differ by no more than a tile and a unit's cost at each border
+    if len(cost) > 2:  # shares differ by what the borders and the units' last tiles leave
         share = [cost.get(c, 0) for c in range(max(cost) + 1)]
-        assert max(share) - min(share) <= 2 * (2 + 2) + 1
+        units = max(sum(x[0] == c for x in got) for c in cost)
+        assert max(share) - min(share) <= 4 * units + 4
+
+
+@pytest.mark.parametrize("n,L,Hkv,tile,causal", [(1, 2000000000, 8, 32, 1), (9000, 9000, 3, 128, 1),
+                                                 (5000, 100000, 1, 16, 0), (3000, 1000, 2, 42, 1),
+                                                 (1 << 20, 1 << 20, 2, 128, 1)])
+def test_paged_work_of_long_sequences(lib, n, L, Hkv, tile, causal):
+    got, _ = pieces_of(lib, [(1, 5), (n, L), (0, 7), (2, 300)], Hkv, tile, 2, causal, 152, page=1024,
+                       width=2000000)
+    for b, last in ((0, 1), (1, -(-L // 128)), (3, 3)):
+        mine = [x for x in got if x[1] == b]
+        units = -(-(1, n, 0, 2)[b] // (2 * tile))
+        assert sum(x[5] == 0 for x in mine) == sum(x[6] == x[7] for x in mine) == units * Hkv
+        assert mine[-1][6] == mine[-1][7] == max(last, 1)
+    assert got[0][0] == 0 and max(x[0] for x in got) == 151
 
 
 def test_wrappers_refuse_cpu_tensors_and_wrong_types(lib):
