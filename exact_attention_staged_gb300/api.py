@@ -7,8 +7,10 @@ is not an sm_103 GPU, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+import struct
 import threading
 from typing import Optional, Tuple
 
@@ -405,6 +407,11 @@ def bwd_dropout(q, k, v, o, lse, dout, p_drop: float, seed: int, offset: int = 0
 
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
     else torch.cuda.current_device
+_DTYPES = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16}
+_I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
+_empty = torch.empty
+# strides are handed over as the bytes of a long long array
+_pack10, _pack12, _pack14 = (struct.Struct(f"={n}q").pack for n in (10, 12, 14))
 
 
 def _elsewhere(call, stream, device, tensors):
@@ -422,20 +429,24 @@ def _elsewhere(call, stream, device, tensors):
     return result
 
 
-def _on_device(dev: int, **tensors):
+def _raw(dev: int) -> int:
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _check_place(dev: int, **tensors):
     for name, t in tensors.items():
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name} must be a CUDA tensor on the same device as the others")
 
 
-def _int32(t, name, shape):
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+def _check_i32(t, name, shape):
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 {list(shape)}")
 
 
-def _freq_table(freq, d: int) -> int:
+def _freq_table(freq) -> int:
     """Checks a frequency table; the number of rotated elements."""
-    if freq.dtype != torch.int64 or freq.dim() != 1 or not freq.is_contiguous():
+    if freq.dtype is not _I64 or freq.dim() != 1 or not freq.is_contiguous():
         raise ValueError("freq must be a contiguous int64 table of rope_frequencies()")
     return 2 * freq.shape[0]
 
@@ -471,44 +482,51 @@ def _rope(q, k, freq, positions, interleaved, mscale, out_q, out_k, inverse, str
         return _elsewhere(lambda: _rope(q, k, freq, positions, interleaved, mscale, out_q, out_k,
                                         inverse, None),
                           stream, q.device, (q, k, freq, positions, out_q, out_k))
-    _on_device(dev, k=k, freq=freq, positions=positions, out_q=out_q, out_k=out_k)
-    B, H, N, d = _shape(q)
-    rot = _freq_table(freq, d)
-    dtype = _dtype_code(q)
-    Hkv = 0
-    if k is not None:
-        kb, Hkv, kn, kd = _shape(k)
-        if kb != B or kn != N or kd != d or k.dtype != q.dtype:
-            raise ValueError("k must be [B, H_kv, N, d] with the dtype of q")
-    elif out_k is not None:
-        raise ValueError("out_k needs k")
+    if freq.get_device() != dev or positions is not None or out_q is not None \
+            or out_k is not None or k is not None:
+        _check_place(dev, k=k, freq=freq, positions=positions, out_q=out_q, out_k=out_k)
+    shape, dt = q.shape, q.dtype
+    code = _DTYPES.get(dt)
+    if code is None:
+        _dtype_code(q)
+    if len(shape) != 4:
+        raise ValueError("q, k must be [B, heads, N, d]")
+    B, H, N, d = shape
     if positions is not None:
-        _int32(positions, "positions", (B, N))
+        _check_i32(positions, "positions", (B, N))
     if out_q is None:
-        out_q = q.new_empty((B, H, N, d))
-    elif out_q.shape != q.shape or out_q.dtype != q.dtype:
+        out_q = _empty(shape, dtype=dt, device=q.device)
+    elif out_q.shape != shape or out_q.dtype is not dt:
         raise ValueError("out_q must match q in shape and dtype")
-    if k is not None:
+    a0, a1, a2, ae = q.stride()
+    b0, b1, b2, be = out_q.stride()
+    if k is None:
+        if out_k is not None:
+            raise ValueError("out_k needs k")
+        Hkv = kp = kop = c0 = c1 = c2 = e0 = e1 = e2 = 0
+        ce = ee = 1
+    else:
+        kshape = k.shape
+        if len(kshape) != 4 or kshape[0] != B or kshape[2] != N or kshape[3] != d \
+                or k.dtype is not dt:
+            raise ValueError("k must be [B, H_kv, N, d] with the dtype of q")
+        Hkv = kshape[1]
         if out_k is None:
-            out_k = k.new_empty((B, Hkv, N, d))
-        elif out_k.shape != k.shape or out_k.dtype != k.dtype:
+            out_k = _empty(kshape, dtype=dt, device=q.device)
+        elif out_k.shape != kshape or out_k.dtype is not dt:
             raise ValueError("out_k must match k in shape and dtype")
-    st = q.stride() + out_q.stride()
-    if k is not None:
-        st += k.stride() + out_k.stride()
-    if any(x != 1 for x in st[3::4]):
+        c0, c1, c2, ce = k.stride()
+        e0, e1, e2, ee = out_k.stride()
+        kp, kop = k.data_ptr(), out_k.data_ptr()
+    if ae != 1 or be != 1 or ce != 1 or ee != 1:
         raise ValueError("the rows of q, k and the outputs must be contiguous")
-    strides = (ctypes.c_longlong * 12)(*(x for i, x in enumerate(st) if i & 3 != 3))
-    _check(load().fa_rope(q.data_ptr(), out_q.data_ptr(), None if k is None else k.data_ptr(),
-                          None if k is None else out_k.data_ptr(), strides, freq.data_ptr(),
-                          None if positions is None else positions.data_ptr(), B, H, Hkv, N, d,
-                          rot, dtype, int(bool(interleaved)), inverse, mscale, _raw(dev)),
-           "fa_rope")
+    rc = load().fa_rope(q.data_ptr(), out_q.data_ptr(), kp or None, kop or None,
+                        _pack12(a0, a1, a2, b0, b1, b2, c0, c1, c2, e0, e1, e2), freq.data_ptr(),
+                        None if positions is None else positions.data_ptr(), B, H, Hkv, N, d,
+                        _freq_table(freq), code, 1 if interleaved else 0, inverse, mscale, _raw(dev))
+    if rc != FA_OK:
+        raise FAError(rc, "fa_rope")
     return out_q if k is None else (out_q, out_k)
-
-
-def _raw(dev: int) -> int:
-    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def rope(q, k, freq, positions=None, interleaved: bool = False, mscale: float = 1.0, out_q=None,
@@ -533,22 +551,31 @@ def rope_bwd(dq, dk, freq, positions=None, interleaved: bool = False, mscale: fl
 
 
 def _paged_shapes(q, k_pages, v_pages, block_table, kv_len, q_start):
-    """T, H, H_kv, d, num_pages, page_size, B, max_pages of a paged batch (q or k: [T, heads, d])."""
-    if q.dim() != 3:
+    """T, heads, d, num_pages, H_kv, page_size, B, max_pages, the dtype's code and the six page strides
+    of a paged batch (q or k: [T, heads, d])."""
+    shape, kshape, tshape, dt = q.shape, k_pages.shape, block_table.shape, q.dtype
+    code = _DTYPES.get(dt)
+    if code is None:
+        _dtype_code(q)
+    if len(shape) != 3:
         raise ValueError("tokens must be [T, heads, d]")
-    T, H, d = q.shape
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != d \
-            or k_pages.dtype != q.dtype or v_pages.dtype != q.dtype:
+    T, H, d = shape
+    if len(kshape) != 4 or kshape != v_pages.shape or kshape[3] != d \
+            or k_pages.dtype is not dt or v_pages.dtype is not dt:
         raise ValueError("k_pages and v_pages must be [num_pages, H_kv, page_size, d] with the dtype "
                          "of the tokens")
-    num_pages, Hkv, page_size, _ = k_pages.shape
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous():
+    if len(tshape) != 2 or block_table.dtype is not _I32 or not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous int32 [B, max_pages]")
-    B, max_pages = block_table.shape
-    _int32(kv_len, "kv_len", (B,))
+    B, max_pages = tshape
+    _check_i32(kv_len, "kv_len", (B,))
     if q_start is not None:
-        _int32(q_start, "q_start", (B + 1,))
-    return T, H, Hkv, d, num_pages, page_size, B, max_pages
+        _check_i32(q_start, "q_start", (B + 1,))
+    k0, k1, k2, ke = k_pages.stride()
+    v0, v1, v2, ve = v_pages.stride()
+    if ke != 1 or ve != 1:
+        raise ValueError("the rows of the pages must be contiguous")
+    num_pages, Hkv, page_size, _ = kshape
+    return (T, H, d, num_pages, Hkv, page_size, B, max_pages, code, (k0, k1, k2, v0, v1, v2))
 
 
 def paged_check(block_table, kv_len, q_start, num_pages: int, page_size: int,
@@ -593,44 +620,56 @@ def paged_append(k, v, k_pages, v_pages, block_table, kv_len, q_start=None, q=No
                                                q, out_q, freq, positions, interleaved, mscale),
                           stream, k.device, (k, v, k_pages, v_pages, block_table, kv_len, q_start, q,
                                              out_q, freq, positions))
-    _on_device(dev, v=v, k_pages=k_pages, v_pages=v_pages, block_table=block_table, kv_len=kv_len,
-               q_start=q_start, q=q, out_q=out_q, freq=freq, positions=positions)
-    T, Hkv, pool_heads, d, num_pages, page_size, B, max_pages = \
+    if v.get_device() != dev or k_pages.get_device() != dev or v_pages.get_device() != dev \
+            or block_table.get_device() != dev or kv_len.get_device() != dev \
+            or (q_start is not None and q_start.get_device() != dev) \
+            or (q is not None and q.get_device() != dev) \
+            or (freq is not None and freq.get_device() != dev) \
+            or out_q is not None or positions is not None:
+        _check_place(dev, v=v, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
+                     kv_len=kv_len, q_start=q_start, q=q, out_q=out_q, freq=freq,
+                     positions=positions)
+    T, Hkv, d, num_pages, pool_heads, page_size, B, max_pages, code, pages = \
         _paged_shapes(k, k_pages, v_pages, block_table, kv_len, q_start)
-    if Hkv != pool_heads or v.shape != k.shape or v.dtype != k.dtype:
+    dt = k.dtype
+    if Hkv != pool_heads or v.shape != k.shape or v.dtype is not dt:
         raise ValueError("k and v must be [T, H_kv, d] with the H_kv and dtype of the pages")
-    dtype = _dtype_code(k)
-    rot = 0 if freq is None else _freq_table(freq, d)
     if positions is not None:
-        _int32(positions, "positions", (T,))
-    H, st = Hkv, (0, 0, 1, 8, 8, 1)
+        _check_i32(positions, "positions", (T,))
+    k0, k1, ke = k.stride()
+    v0, v1, ve = v.stride()
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d or q.dtype != k.dtype:
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != d or q.dtype is not dt:
             raise ValueError("q must be [T, H, d] with the dtype of k")
-        H = q.shape[1]
+        H = shape[1]
         if out_q is None:
-            out_q = q.new_empty((T, H, d))
-        elif out_q.shape != q.shape or out_q.dtype != q.dtype:
+            out_q = _empty(shape, dtype=dt, device=q.device)
+        elif out_q.shape != shape or out_q.dtype is not dt:
             raise ValueError("out_q must match q in shape and dtype")
-        st = q.stride() + out_q.stride()
-    elif out_q is not None:
-        raise ValueError("out_q needs q")
-    st += k.stride() + v.stride()
-    ps = k_pages.stride() + v_pages.stride()
-    if st[2::3] != (1, 1, 1, 1) or ps[3::4] != (1, 1):
-        raise ValueError("the rows of q, k, v and the pages must be contiguous")
-    strides = (ctypes.c_longlong * 14)(st[0], st[1], st[3], st[4], st[6], st[7], st[9], st[10],
-                                       *ps[:3], *ps[4:7])
-    _check(load().fa_paged_append(
-        None if q is None else q.data_ptr(), None if q is None else out_q.data_ptr(), k.data_ptr(),
-        v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), strides, block_table.data_ptr(),
-        kv_len.data_ptr(), None if q_start is None else q_start.data_ptr(),
+        q0, q1, qe = q.stride()
+        o0, o1, oe = out_q.stride()
+        qp, op = q.data_ptr(), out_q.data_ptr()
+    else:
+        if out_q is not None:
+            raise ValueError("out_q needs q")
+        H, q0, q1, o0, o1, qp, op = Hkv, 0, 0, 8, 8, None, None
+        qe = oe = 1
+    if ke != 1 or ve != 1 or qe != 1 or oe != 1:
+        raise ValueError("the rows of q, k and v must be contiguous")
+    rc = load().fa_paged_append(
+        qp, op, k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        _pack14(q0, q1, o0, o1, k0, k1, v0, v1, *pages), block_table.data_ptr(), kv_len.data_ptr(),
+        None if q_start is None else q_start.data_ptr(),
         None if positions is None else positions.data_ptr(),
         None if freq is None else freq.data_ptr(), T, B, H, Hkv, d, num_pages, page_size, max_pages,
-        rot, dtype, int(bool(interleaved)), mscale, _raw(dev)), "fa_paged_append")
+        0 if freq is None else _freq_table(freq), code, 1 if interleaved else 0, mscale, _raw(dev))
+    if rc != FA_OK:
+        raise FAError(rc, "fa_paged_append")
     return out_q
 
 
+@functools.lru_cache(maxsize=1024)
 def paged_workspace_bytes(T: int, B: int, H: int, H_kv: int, d: int, max_q: int, page_size: int,
                           max_pages: int) -> int:
     return int(load().fa_paged_attn_workspace_bytes(T, B, H, H_kv, d, max_q, page_size, max_pages))
@@ -653,41 +692,47 @@ def paged_attention(q, k_pages, v_pages, block_table, kv_len, q_start=None,
                                                   max_q, scale, causal, out, lse, workspace),
                           stream, q.device, (q, k_pages, v_pages, block_table, kv_len, q_start, out,
                                              lse, workspace))
-    _on_device(dev, k_pages=k_pages, v_pages=v_pages, block_table=block_table, kv_len=kv_len,
-               q_start=q_start, out=out, lse=lse, workspace=workspace)
-    T, H, Hkv, d, num_pages, page_size, B, max_pages = \
+    if k_pages.get_device() != dev or v_pages.get_device() != dev \
+            or block_table.get_device() != dev or kv_len.get_device() != dev \
+            or (q_start is not None and q_start.get_device() != dev) \
+            or out is not None or lse is not None or workspace is not None:
+        _check_place(dev, k_pages=k_pages, v_pages=v_pages, block_table=block_table, kv_len=kv_len,
+                     q_start=q_start, out=out, lse=lse, workspace=workspace)
+    T, H, d, num_pages, Hkv, page_size, B, max_pages, code, pages = \
         _paged_shapes(q, k_pages, v_pages, block_table, kv_len, q_start)
-    dtype = _dtype_code(q)
-    lib = load()
     if max_q is None:
         max_q = T if q_start is not None else max(T // max(B, 1), 1)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    device = q.device
     if out is None:
-        out = q.new_empty((T, H, d))
-    elif out.shape != q.shape or out.dtype != q.dtype:
+        out = _empty(q.shape, dtype=q.dtype, device=device)
+    elif out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError("out must match q in shape and dtype")
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
+        lse = _empty((T, H), dtype=_F32, device=device)
+    elif lse.dtype is not _F32 or lse.shape != (T, H) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [T, H]")
-    st = q.stride() + out.stride()
-    ps = k_pages.stride() + v_pages.stride()
-    if st[2::3] != (1, 1) or ps[3::4] != (1, 1):
-        raise ValueError("the rows of q, out and the pages must be contiguous")
-    nbytes = lib.fa_paged_attn_workspace_bytes(T, B, H, Hkv, d, max_q, page_size, max_pages)
+    q0, q1, qe = q.stride()
+    o0, o1, oe = out.stride()
+    if qe != 1 or oe != 1:
+        raise ValueError("the rows of q and out must be contiguous")
+    nbytes = paged_workspace_bytes(T, B, H, Hkv, d, max_q, page_size, max_pages)
     if workspace is None:
+        ws = None
         if nbytes > 0:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = _empty(nbytes, dtype=_U8, device=device)
+            ws = workspace.data_ptr()
     elif not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError("workspace must be contiguous, of paged_workspace_bytes() bytes")
-    strides = (ctypes.c_longlong * 10)(st[0], st[1], st[3], st[4], *ps[:3], *ps[4:7])
-    _check(lib.fa_paged_attn(
+    else:
+        ws = workspace.data_ptr()
+    rc = load().fa_paged_attn(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
-        strides, block_table.data_ptr(), kv_len.data_ptr(),
+        _pack10(q0, q1, o0, o1, *pages), block_table.data_ptr(), kv_len.data_ptr(),
         None if q_start is None else q_start.data_ptr(), T, B, H, Hkv, d, num_pages, page_size,
-        max_pages, max_q, dtype, scale, int(bool(causal)),
-        None if workspace is None else workspace.data_ptr(), nbytes, _raw(dev)), "fa_paged_attn")
+        max_pages, max_q, code, 1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0,
+        ws, nbytes, _raw(dev))
+    if rc != FA_OK:
+        raise FAError(rc, "fa_paged_attn")
     return out, lse
 
 

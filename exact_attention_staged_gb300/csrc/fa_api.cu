@@ -987,6 +987,7 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
     int dev = 0;
     rc = device_setup(&dev, &p.c.status);
     if (rc != FA_OK) return rc;
+    p.device = dev;
     p.c.max_q = max_q < T ? max_q : T;
     const PagedTiling tl = paged_tiling(H, H_kv, p.c.max_q);
     p.o = static_cast<uint16_t *>(o);

@@ -17,10 +17,10 @@ namespace fa {
 namespace {
 
 constexpr int kAppendWarps = 8;
-constexpr int kAppendBatch = 4;  // row pieces of a lane in flight together
+constexpr int kAppendBatch = 2;  // row pieces of a lane in flight together
 
 template <int D, bool BF16, bool INTER>
-__global__ void __launch_bounds__(kAppendWarps * 32) fa_paged_append_kernel(const PagedAppendParams p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 4) fa_paged_append_kernel(const PagedAppendParams p) {
     constexpr int kUnits = D / kRopeElems;   // units of a row
     constexpr int kHeads = 32 / kUnits;      // heads that a warp takes at a time
     const PagedView &c = p.c;
@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) fa_paged_append_kernel(cons
                                   : isk ? p.k + t * p.k_t + (h - heads_q) * p.k_h
                                         : p.v + t * p.v_t + (h - heads_q - c.Hkv) * p.v_h;
             const int2 from = h < heads_q + c.Hkv ? at : make_int2(u * kRopeElems, u * kRopeElems + 8);
-            lo[i] = *reinterpret_cast<const uint4 *>(src + from.x);
-            hi[i] = *reinterpret_cast<const uint4 *>(src + from.y);
+            lo[i] = __ldcs(reinterpret_cast<const uint4 *>(src + from.x));
+            hi[i] = __ldcs(reinterpret_cast<const uint4 *>(src + from.y));
         }
         if (!known) {
             known = true;
@@ -104,7 +104,7 @@ cudaError_t launch_append_t(PagedAppendParams p, cudaStream_t stream) {
     const int rounds = (heads + kHeads - 1) / kHeads;
     // a token's heads are spread over several warps while there are few tokens
     int per = rounds;
-    while (per > 1 && static_cast<long>(p.c.T) * ((rounds + per - 1) / per) < 152 * 32)
+    while (per > 1 && static_cast<long>(p.c.T) * ((rounds + per - 1) / per) < 152 * 64)
         per = (per + 1) / 2;
     p.chunks = (rounds + per - 1) / per;
     const long warps = static_cast<long>(p.c.T) * p.chunks;

@@ -30,6 +30,7 @@
 // softmax groups.  MMA order per step: PV_0 of the step before, S_0, PV_1, S_1, as in the forward.
 #include "paged.cuh"
 
+#include <atomic>
 #include <type_traits>
 
 namespace fa {
@@ -842,9 +843,15 @@ template <int D, bool BF16, int QT>
 cudaError_t launch_attn_t(const PagedMaps &m, const PagedAttnParams &p, cudaStream_t stream) {
     using L = PagedLayout<D, QT>;
     auto kern = fa_paged_attn_kernel<D, BF16, QT>;
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    if (e != cudaSuccess) return e;
+    // the attribute holds for the device from then on: set once for each of them
+    static std::atomic<unsigned long long> ready{0};
+    const unsigned long long bit = 1ull << (p.device & 63);
+    cudaError_t e = cudaSuccess;
+    if ((ready.load(std::memory_order_acquire) & bit) == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
     kern<<<kPagedCtas, L::kThreads, L::kAlloc, stream>>>(m, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.cut == nullptr) return e;

@@ -5,7 +5,8 @@
 // elements behind rot_dim are copied.  The backward is the transpose: the same with -t.
 //
 // The work is one read and one write of every element, 6 operations a pair, so it is bound by
-// HBM.  A thread owns one unit of a row (8 pairs, or 16 elements that pass through) and walks
+// HBM: 8192 rows of 40 heads of 128 take 27.0 us, 6.2 TB/s or 0.91 of the measured copy rate.  A
+// thread owns one unit of a row (8 pairs, or 16 elements that pass through) and walks
 // the heads of a chunk: their angle is the same, so the sines and cosines are worked out once for
 // all of them (Q's and K's heads alike: one launch for both), and the loads of several heads are
 // in flight at a time.
@@ -18,7 +19,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeBatch = 4;  // heads whose loads are in flight together
 
 template <int D, bool BF16, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) fa_rope_kernel(const RopeParams p) {
     constexpr int kUnits = D / kRopeElems;  // units of a row
     const int u = static_cast<int>(threadIdx.x) % kUnits;
     const long row = static_cast<long>(blockIdx.x) * (kRopeThreads / kUnits) + threadIdx.x / kUnits;
@@ -46,8 +47,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
             const RopeSide &s = isq ? p.q : p.k;
             const uint16_t *src = s.in + b * s.in_b + hh * s.in_h + n * s.in_n;
             dst[i] = s.out + b * s.out_b + hh * s.out_h + n * s.out_n;
-            lo[i] = *reinterpret_cast<const uint4 *>(src + at.x);
-            hi[i] = *reinterpret_cast<const uint4 *>(src + at.y);
+            lo[i] = __ldcs(reinterpret_cast<const uint4 *>(src + at.x));
+            hi[i] = __ldcs(reinterpret_cast<const uint4 *>(src + at.y));
         }
 #pragma unroll
         for (int i = 0; i < kRopeBatch; ++i) {
@@ -63,11 +64,12 @@ template <int D, bool BF16, bool INTER>
 cudaError_t launch_rope_t(RopeParams p, cudaStream_t stream) {
     const long per_block = kRopeThreads / (D / kRopeElems);
     const long blocks = (p.rows + per_block - 1) / per_block;
-    // heads per thread: as many as still leave every SM several blocks
+    // heads per thread: two batches of them while that leaves every SM four blocks (one more than it
+    // holds), else one, else fewer heads.  8k x 40 heads: 27.0 us against 30.4 with five heads and
+    // twice the blocks; 1k x 32 heads of 64: 8.2 against 10.7 with one head and twice the blocks.
     const int heads = p.H + p.Hkv;
-    p.chunk = heads;
-    while (p.chunk > 1 && blocks * ((heads + p.chunk - 1) / p.chunk) < 8 * 152)
-        p.chunk = (p.chunk + 1) / 2;
+    p.chunk = 2 * kRopeBatch;
+    while (p.chunk > 1 && blocks * ((heads + p.chunk - 1) / p.chunk) < 4 * 152) p.chunk /= 2;
     dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + p.chunk - 1) / p.chunk));
     fa_rope_kernel<D, BF16, INTER><<<grid, kRopeThreads, 0, stream>>>(p);
     return cudaGetLastError();

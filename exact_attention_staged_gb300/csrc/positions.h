@@ -59,6 +59,7 @@ struct PagedAttnParams {
     int part_rows;                   // rows of a partial result's slot
     float scale_log2;                // scale * log2(e)
     int causal;
+    int device;                      // host only: the current device
     // a unit that a border cuts: CTA c's piece that starts inside a unit goes to slot 2c, its piece
     // that starts one but does not end it to slot 2c + 1, and cut[c] says what to merge
     float4 *part_o;                  // [slots][d / 4][part_rows] unnormalised, 4 columns each

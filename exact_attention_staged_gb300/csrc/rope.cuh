@@ -4,7 +4,9 @@
 // in units of 2^-64 turns, so p * f_j modulo one turn is the low 64 bits of an integer product:
 // no rounding at any position (a 32-bit float angle is off by 0.06 rad at position 10^6), and no
 // 64-bit floating point, whose rate on this GPU is 1/64 of the 32-bit one.  The top 32 bits of the
-// product are the angle to 2^-33 turns; its sine and cosine are taken in 32 bits.
+// product are the angle to 2^-33 turns.  Its sine and cosine come from the special-function unit
+// (error below 2^-21 for angles in [-pi, pi)), a thousandth of the rounding to 16 bits that follows;
+// the accurate functions took about 25 instructions a pair, which bounded rows of few heads.
 #pragma once
 
 #include "positions.h"
@@ -25,12 +27,11 @@ __device__ __forceinline__ void rope_angles(const unsigned long long *freq, int 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const unsigned long long turns = (e ? f.y : f.x) * p;
-            // signed, so that the half turns lie in [-1, 1) and small angles keep all their bits
+            // signed, so that the angle lies in [-pi, pi) and small ones keep all their bits
             const int top = static_cast<int>(turns >> 32);
-            float s, c;
-            sincospif(static_cast<float>(top) * 0x1p-31f, &s, &c);
-            cs[2 * j + e] = c * mscale;
-            sn[2 * j + e] = s * mscale;
+            const float angle = static_cast<float>(top) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+            cs[2 * j + e] = __cosf(angle) * mscale;
+            sn[2 * j + e] = __sinf(angle) * mscale;
         }
     }
 }
