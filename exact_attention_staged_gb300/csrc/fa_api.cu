@@ -1046,7 +1046,7 @@ int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, i
     long total = 0;
     for (int b = 0; b < B; ++b) total += weight(b);
     fa::PagedLine line;
-    line.cut(total, ctas);
+    line.cut(total, w, ctas);
     int n = 0;
     for (int k = 0; k < line.ctas; ++k) {
         const long at = line.border(k), end = line.border(k + 1);
@@ -1054,7 +1054,8 @@ int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, i
         int b = 0;
         while (before + weight(b) <= at) before += weight(b++);
         fa::PagedCursor cur;
-        cur.start(c, w, b, at - before);
+        const fa::PagedSeq seq = fa::paged_seq(c, b);
+        cur.start(c, w, b, seq, fa::paged_head(seq, w), at - before);
         while (room > 0) {
             const long from = end - room;
             const fa::PagedPiece u = cur.take(c, w, room);

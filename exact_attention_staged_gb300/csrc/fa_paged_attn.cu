@@ -90,55 +90,57 @@ __device__ __forceinline__ int piece_end(const PieceSlot &u, int q, int tile_tok
     return max(u.t0, min(u.t1, end));
 }
 
-// One warp finds its CTA's stretch of the line: the sequences' lengths are summed, 128 sequences at
-// a time with their index reads in flight together, and the border is looked for in the running
-// sum.  Returns what the CTA may take and leaves `cur` at its beginning.
+// One warp finds its CTA's stretch of the line, a lane per sequence: the first pass sums the lengths
+// and cuts the line, the second looks for the CTA's border in the running sum (up to 32 sequences
+// it still has at hand).  Rolled up so that the code is short: it runs once, from a cold
+// instruction cache.  Returns what the CTA may take and leaves `cur` at its beginning.
 __device__ __forceinline__ long find_stretch(const PagedView &c, const PagedWork &w, bool report,
                                              PagedLine &line, PagedCursor &cur) {
-    constexpr int kEach = 4;
-    const int lane = lane_id();
-    auto length = [&](int b) -> long {
-        if (b >= c.B) return 0;
-        const PagedSeq s = paged_seq(c, b);
-        if (s.bad && report) paged_report(c);
-        return c.Hkv * paged_head(s, w);
-    };
-    long first[kEach], sum = 0;  // the first 128 sequences' lengths are kept
+    const int lane = lane_id(), cta = static_cast<int>(blockIdx.x);
+    long sum = 0, begin = 0, each = 0;
+    PagedSeq s;
+    s.tok0 = s.n = s.len = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int b0 = 0; b0 < c.B; b0 += 32) {
+            if (pass == 0 || c.B > 32) {
+                each = 0;
+                if (b0 + lane < c.B) {
+                    s = paged_seq(c, b0 + lane);
+                    if (s.bad && report) paged_report(c);
+                    each = paged_head(s, w);
+                }
+            }
+            const long x = c.Hkv * each;
+            long upto = x;  // inclusive
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        first[i] = length(32 * i + lane);
-        sum += first[i];
-    }
-    for (int b = 32 * kEach + lane; b < c.B; b += 32) sum += length(b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    line.cut(sum, static_cast<int>(gridDim.x));
-    const int cta = static_cast<int>(blockIdx.x);
-    if (cta >= line.ctas) return 0;
-    const long begin = line.border(cta), room = line.border(cta + 1) - begin;
-    long before = 0;
-    for (int b0 = 0; b0 < c.B; b0 += 32) {
-        long x = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (b0 == 32 * i) x = first[i];
-        if (b0 >= 32 * kEach) x = length(b0 + lane);
-        long upto = x;  // inclusive
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            if (pass == 1) {
+                const unsigned past = __ballot_sync(0xffffffffu, sum + upto > begin);
+                if (past != 0) {
+                    const int at = __ffs(static_cast<int>(past)) - 1;
+                    const long pos = begin - sum - __shfl_sync(0xffffffffu, upto - x, at);
+                    s.tok0 = __shfl_sync(0xffffffffu, s.tok0, at);
+                    s.n = __shfl_sync(0xffffffffu, s.n, at);
+                    s.len = __shfl_sync(0xffffffffu, s.len, at);
+                    cur.start(c, w, b0 + at, s, __shfl_sync(0xffffffffu, each, at), pos);
+                    return line.border(cta + 1) - begin;
+                }
+            }
+            sum += __shfl_sync(0xffffffffu, upto, 31);
         }
-        const unsigned past = __ballot_sync(0xffffffffu, before + upto > begin);
-        if (past != 0) {
-            const int at = __ffs(static_cast<int>(past)) - 1;
-            const long here = before + __shfl_sync(0xffffffffu, upto - x, at);
-            cur.start(c, w, b0 + at, begin - here);
-            return room;
+        if (pass == 0) {
+            line.cut(sum, w, static_cast<int>(gridDim.x));
+            if (cta >= line.ctas) break;
+            begin = line.border(cta);
+            sum = 0;
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    return 0;  // not reached: the border lies inside the line
+    return 0;
 }
 
 // Page ids of a piece's key tiles for one load warp: 32 at a time in the lanes, the next 32 read
@@ -474,6 +476,7 @@ __global__ void __launch_bounds__(384, 1)
                                 }
                                 issue_pv(t, (n0 + jp) % L::kVSlots, pcnt[t] > p0[t]);
                                 ++pcnt[t];
+                                if (jp + 2 >= u.t1) umma_commit_el(&o_final[t]);
                                 umma_commit_el(&v_empty[(n0 + jp) % L::kVSlots]);
                             }
                             if (jn < u.t1) {
@@ -512,6 +515,7 @@ __global__ void __launch_bounds__(384, 1)
                                 }
                                 issue_pv(t, vs, pcnt[t] > p0[t]);
                                 ++pcnt[t];
+                                if (j == end[t]) umma_commit_el(&o_final[t]);
                             }
                             if (j < end[t]) issue_s(t, t, (n0 + j) % L::kKSlots);
                         }
@@ -523,9 +527,6 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 if (!ok) break;
                 nt += u.t1 - u.t0;
-                // O_t of this piece is final (nobody waits for a group that had no tile)
-                for (int t = 0; t < 2; ++t)
-                    if (pcnt[t] > p0[t]) umma_commit_el(&o_final[t]);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&unit_empty[e]);
             }

@@ -69,7 +69,7 @@ struct PagedWork {
 
 // What a unit costs beside its keys (Q, the first loads, the epilogue), for units of up to two query
 // tiles or of one.
-__host__ __device__ inline int paged_unit_cost(int tiles) { return tiles == 2 ? 256 : 32; }
+__host__ __device__ inline int paged_unit_cost(int tiles) { return tiles == 2 ? 256 : 0; }
 
 __host__ __device__ inline int paged_units(const PagedSeq &s, const PagedWork &w) {
     return s.n <= w.unit_toks ? (s.n > 0 ? 1 : 0) : (s.n - 1) / w.unit_toks + 1;  // per K/V head
@@ -100,26 +100,32 @@ __host__ __device__ inline long paged_prefix(const PagedSeq &s, const PagedWork 
     }
     return m * w.unit_cost + keys * paged_tile_cost(w, w.unit_toks);
 }
+// Keys of a unit as the line counts them: at least one; a sequence's only unit (generated or drafted
+// tokens) by whole tiles, so that borders fall on tiles where there are few of them.
+__host__ __device__ inline long paged_line_keys(int keys, int units) {
+    if (units > 1) return keys > 0 ? keys : 1;
+    return keys > 0 ? (static_cast<long>(keys) + kPagedKeys - 1) / kPagedKeys * kPagedKeys : kPagedKeys;
+}
 __host__ __device__ inline long paged_head(const PagedSeq &s, const PagedWork &w) {
-    const int last = paged_units(s, w) - 1;
-    if (last < 0) return 0;
-    const int keys = paged_keys(s, w, s.n);
-    return (last > 0 ? paged_prefix(s, w, last) : 0) + w.unit_cost +
-           static_cast<long>(keys > 0 ? keys : 1) *
-               paged_tile_cost(w, s.n - last * w.unit_toks);
+    const int units = paged_units(s, w);
+    if (units == 0) return 0;
+    return (units > 1 ? paged_prefix(s, w, units - 1) : 0) + w.unit_cost +
+           paged_line_keys(paged_keys(s, w, s.n), units) *
+               paged_tile_cost(w, s.n - (units - 1) * w.unit_toks);
 }
 
 // The line of length `total` cut for up to `most` CTAs: the first r of them take q + 1, the others q.
-// No stretch is shorter than two single key tiles, one step of a CTA's two softmax groups (nor
-// than a tile of two query tiles, so that every CTA between a cut unit's first and last one has a
+// No stretch is shorter than a unit's cost and two single key tiles, one step of a CTA's two softmax
+// groups (so none is without work, and every CTA between a cut unit's first and last one has a
 // piece of it).
 struct PagedLine {
     long total, q;
     int ctas, r;
-    __host__ __device__ void cut(long length, int most) {
+    __host__ __device__ void cut(long length, const PagedWork &w, int most) {
+        const int least = w.unit_cost + 2 * kPagedKeys;
         total = length;
-        ctas = length >= most * 256l ? most : length >= 256 ? static_cast<int>(length) / 256
-                                             : length > 0 ? 1 : 0;
+        ctas = length >= static_cast<long>(most) * least ? most
+               : length >= least ? static_cast<int>(length) / least : length > 0 ? 1 : 0;
         if (ctas == 0) {
             q = r = 0;
         } else if (length < (1l << 31)) {
@@ -155,44 +161,44 @@ struct PagedCursor {
     int b, g, i, units;  // sequence, K/V head, unit; units per head
     long at;             // place inside the unit's length
 
-    // `pos`: length inside sequence b that lies before the position.  Head and unit are estimated
-    // in floating point and put right by the exact lengths.
-    __host__ __device__ void start(const PagedView &c, const PagedWork &w, int seq, long pos) {
+    // `pos`: length inside sequence seq that lies before the position; `each`: its length per
+    // K/V head.  Head and unit are estimated in floating point and put right by the exact lengths.
+    __host__ __device__ void start(const PagedView &c, const PagedWork &w, int seq,
+                                   const PagedSeq &which, long each, long pos) {
         b = seq;
-        s = paged_seq(c, b);
+        s = which;
         units = paged_units(s, w);
-        const long each = paged_head(s, w);
         g = static_cast<int>(static_cast<float>(pos) / static_cast<float>(each));
         if (g > c.Hkv - 1) g = c.Hkv - 1;
         while (g * each > pos) --g;
         while (g + 1 < c.Hkv && (g + 1) * each <= pos) ++g;
         pos -= g * each;
         i = 0;
-        if (units > 1) {
-            const int last = units - 1;
+        if (units > 1) {  // the last unit whose prefix is <= pos; pos = a i^2 + f i while ctx >= 0
             const long ctx = static_cast<long>(s.len) - s.n;
-            if (w.causal && ctx < 0) {
-                int lo = 0, hi = last;  // the last unit whose prefix is <= pos
-                while (lo < hi) {
-                    const int mid = lo + (hi - lo + 1) / 2;
-                    if (paged_prefix(s, w, mid) <= pos)
-                        lo = mid;
-                    else
-                        hi = mid - 1;
+            const float cost = static_cast<float>(paged_tile_cost(w, w.unit_toks));
+            const float a = w.causal ? 0.5f * cost * w.unit_toks : 0.f;
+            const float f = w.unit_cost + cost * (w.causal ? ctx + 0.5f * w.unit_toks
+                                                           : static_cast<float>(s.len));
+            const float x = static_cast<float>(pos);
+            int lo = 0, hi = units - 1, tries = 0;
+            int mid = ctx >= 0 ? static_cast<int>(2.f * x / (f + sqrtf(f * f + 4.f * a * x))) : hi / 2;
+            long before = 0;
+            while (lo < hi) {
+                mid = mid <= lo ? lo + 1 : mid > hi ? hi : mid;
+                const long here = paged_prefix(s, w, mid);
+                if (here <= pos) {
+                    lo = mid;
+                    before = here;
+                    ++mid;
+                } else {
+                    hi = mid - 1;
+                    mid = hi;
                 }
-                i = lo;
-            } else {  // pos = a i^2 + f i
-                const float cost = static_cast<float>(paged_tile_cost(w, w.unit_toks));
-                const float a = w.causal ? 0.5f * cost * w.unit_toks : 0.f;
-                const float f = w.unit_cost + cost * (w.causal ? ctx + 0.5f * w.unit_toks
-                                                               : static_cast<float>(s.len));
-                const float x = static_cast<float>(pos);
-                i = static_cast<int>(2.f * x / (f + sqrtf(f * f + 4.f * a * x)));
-                if (i > last) i = last;
-                while (i > 0 && paged_prefix(s, w, i) > pos) --i;
-                while (i < last && paged_prefix(s, w, i + 1) <= pos) ++i;
+                if (++tries > 4) mid = lo + (hi - lo + 1) / 2;  // the estimate was no help
             }
-            if (i > 0) pos -= paged_prefix(s, w, i);
+            i = lo;
+            pos -= before;
         }
         at = pos;
     }
@@ -207,11 +213,10 @@ struct PagedCursor {
         p.b = b;
         p.last0 = w.causal ? s.len - s.n + i0 : s.len - 1;
         p.len = s.len;
-        int keys = paged_keys(s, w, i0 + p.toks);
-        if (keys == 0) keys = 1;
         const int cost = paged_tile_cost(w, p.toks);
-        p.tiles = (keys - 1) / kPagedKeys + 1;
-        const long length = w.unit_cost + static_cast<long>(cost) * keys;
+        const long keys = paged_line_keys(paged_keys(s, w, i0 + p.toks), units);
+        p.tiles = static_cast<int>((keys - 1) / kPagedKeys) + 1;
+        const long length = w.unit_cost + cost * keys;
         p.left = length - at;
         auto tile_of = [&](long x) {
             return x > w.unit_cost ? static_cast<int>((x - w.unit_cost) >> (cost == 2 ? 8 : 7)) : 0;

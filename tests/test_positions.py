@@ -272,7 +272,7 @@ def test_paged_work_of_long_sequences(lib, n, L, Hkv, tile, causal):
         units = -(-(1, n, 0, 2)[b] // (2 * tile))
         assert sum(x[5] == 0 for x in mine) == sum(x[6] == x[7] for x in mine) == units * Hkv
         assert mine[-1][6] == mine[-1][7] == max(last, 1)
-    assert got[0][0] == 0 and max(x[0] for x in got) == 151
+    assert sorted({x[0] for x in got}) == list(range(max(x[0] for x in got) + 1))  # none idle
 
 
 def test_wrappers_refuse_cpu_tensors_and_wrong_types(lib):
