@@ -7,10 +7,8 @@ is not an sm_103 GPU, the calls raise.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
-import struct
 import threading
 from typing import Optional, Tuple
 
@@ -407,11 +405,25 @@ def bwd_dropout(q, k, v, o, lse, dout, p_drop: float, seed: int, offset: int = 0
 
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
     else torch.cuda.current_device
-_DTYPES = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16}
-_I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
-_empty = torch.empty
-# strides are handed over as the bytes of a long long array
-_pack10, _pack12, _pack14 = (struct.Struct(f"={n}q").pack for n in (10, 12, 14))
+_binding = None
+
+
+def _calls():
+    """The extension that checks and makes the short calls (csrc/binding.c), set up once."""
+    global _binding
+    if _binding is None:
+        lib = load()
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m exact_attention_staged_gb300.build`")
+        from . import _binding as ext
+        names = ("fa_rope", "fa_paged_append", "fa_paged_attn", "fa_paged_attn_workspace_bytes")
+        ext.setup(tuple(ctypes.cast(getattr(lib, n), _vp).value for n in names), torch.empty, _raw,
+                  torch.bfloat16, torch.float16, torch.int32, torch.int64, torch.float32,
+                  torch.uint8, FAError)
+        _binding = ext
+    return _binding
 
 
 def _elsewhere(call, stream, device, tensors):
@@ -430,25 +442,20 @@ def _elsewhere(call, stream, device, tensors):
 
 
 def _raw(dev: int) -> int:
-    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _check_place(dev: int, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on the same device as the others")
+if _raw_stream is not None:
+    _raw = _raw_stream  # noqa: F811 (the same, without building a Stream object)
 
 
-def _check_i32(t, name, shape):
-    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int32 {list(shape)}")
-
-
-def _freq_table(freq) -> int:
-    """Checks a frequency table; the number of rotated elements."""
-    if freq.dtype is not _I64 or freq.dim() != 1 or not freq.is_contiguous():
-        raise ValueError("freq must be a contiguous int64 table of rope_frequencies()")
-    return 2 * freq.shape[0]
+def _away(t, stream) -> bool:
+    """Whether a call on tensor t has to leave the current device or stream."""
+    if stream is not None:
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        return True
+    return t.is_cuda and t.get_device() != _current_device()
 
 
 _SCALINGS = {"plain": FA_ROPE_PLAIN, "linear": FA_ROPE_LINEAR, "ntk": FA_ROPE_NTK,
@@ -474,61 +481,6 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain"
     return table.to(device) if device is not None else table, float(mscale.value)
 
 
-def _rope(q, k, freq, positions, interleaved, mscale, out_q, out_k, inverse, stream):
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("q must be a CUDA tensor")
-    if stream is not None or dev != _current_device():
-        return _elsewhere(lambda: _rope(q, k, freq, positions, interleaved, mscale, out_q, out_k,
-                                        inverse, None),
-                          stream, q.device, (q, k, freq, positions, out_q, out_k))
-    if freq.get_device() != dev or positions is not None or out_q is not None \
-            or out_k is not None or k is not None:
-        _check_place(dev, k=k, freq=freq, positions=positions, out_q=out_q, out_k=out_k)
-    shape, dt = q.shape, q.dtype
-    code = _DTYPES.get(dt)
-    if code is None:
-        _dtype_code(q)
-    if len(shape) != 4:
-        raise ValueError("q, k must be [B, heads, N, d]")
-    B, H, N, d = shape
-    if positions is not None:
-        _check_i32(positions, "positions", (B, N))
-    if out_q is None:
-        out_q = _empty(shape, dtype=dt, device=q.device)
-    elif out_q.shape != shape or out_q.dtype is not dt:
-        raise ValueError("out_q must match q in shape and dtype")
-    a0, a1, a2, ae = q.stride()
-    b0, b1, b2, be = out_q.stride()
-    if k is None:
-        if out_k is not None:
-            raise ValueError("out_k needs k")
-        Hkv = kp = kop = c0 = c1 = c2 = e0 = e1 = e2 = 0
-        ce = ee = 1
-    else:
-        kshape = k.shape
-        if len(kshape) != 4 or kshape[0] != B or kshape[2] != N or kshape[3] != d \
-                or k.dtype is not dt:
-            raise ValueError("k must be [B, H_kv, N, d] with the dtype of q")
-        Hkv = kshape[1]
-        if out_k is None:
-            out_k = _empty(kshape, dtype=dt, device=q.device)
-        elif out_k.shape != kshape or out_k.dtype is not dt:
-            raise ValueError("out_k must match k in shape and dtype")
-        c0, c1, c2, ce = k.stride()
-        e0, e1, e2, ee = out_k.stride()
-        kp, kop = k.data_ptr(), out_k.data_ptr()
-    if ae != 1 or be != 1 or ce != 1 or ee != 1:
-        raise ValueError("the rows of q, k and the outputs must be contiguous")
-    rc = load().fa_rope(q.data_ptr(), out_q.data_ptr(), kp or None, kop or None,
-                        _pack12(a0, a1, a2, b0, b1, b2, c0, c1, c2, e0, e1, e2), freq.data_ptr(),
-                        None if positions is None else positions.data_ptr(), B, H, Hkv, N, d,
-                        _freq_table(freq), code, 1 if interleaved else 0, inverse, mscale, _raw(dev))
-    if rc != FA_OK:
-        raise FAError(rc, "fa_rope")
-    return out_q if k is None else (out_q, out_k)
-
-
 def rope(q, k, freq, positions=None, interleaved: bool = False, mscale: float = 1.0, out_q=None,
          out_k=None, stream=None):
     """q [B, H, N, d] and k [B, H_kv, N, d] turned to their positions in one launch (fa_rope).
@@ -538,7 +490,10 @@ def rope(q, k, freq, positions=None, interleaved: bool = False, mscale: float = 
     for 0 .. N - 1.  Any strides with contiguous rows will do (slices of a joint projection);
     results are dense unless out_q, out_k are given, which may be q and k themselves.
     """
-    return _rope(q, k, freq, positions, interleaved, mscale, out_q, out_k, 0, stream)
+    if _away(q, stream):
+        return _elsewhere(lambda: rope(q, k, freq, positions, interleaved, mscale, out_q, out_k),
+                          stream, q.device, (q, k, freq, positions, out_q, out_k))
+    return _calls().rope(q, k, freq, positions, interleaved, mscale, out_q, out_k, False)
 
 
 def rope_bwd(dq, dk, freq, positions=None, interleaved: bool = False, mscale: float = 1.0,
@@ -547,35 +502,11 @@ def rope_bwd(dq, dk, freq, positions=None, interleaved: bool = False, mscale: fl
 
     out_q and out_k may be slices of the joint projection's gradient.
     """
-    return _rope(dq, dk, freq, positions, interleaved, mscale, out_q, out_k, 1, stream)
-
-
-def _paged_shapes(q, k_pages, v_pages, block_table, kv_len, q_start):
-    """T, heads, d, num_pages, H_kv, page_size, B, max_pages, the dtype's code and the six page strides
-    of a paged batch (q or k: [T, heads, d])."""
-    shape, kshape, tshape, dt = q.shape, k_pages.shape, block_table.shape, q.dtype
-    code = _DTYPES.get(dt)
-    if code is None:
-        _dtype_code(q)
-    if len(shape) != 3:
-        raise ValueError("tokens must be [T, heads, d]")
-    T, H, d = shape
-    if len(kshape) != 4 or kshape != v_pages.shape or kshape[3] != d \
-            or k_pages.dtype is not dt or v_pages.dtype is not dt:
-        raise ValueError("k_pages and v_pages must be [num_pages, H_kv, page_size, d] with the dtype "
-                         "of the tokens")
-    if len(tshape) != 2 or block_table.dtype is not _I32 or not block_table.is_contiguous():
-        raise ValueError("block_table must be contiguous int32 [B, max_pages]")
-    B, max_pages = tshape
-    _check_i32(kv_len, "kv_len", (B,))
-    if q_start is not None:
-        _check_i32(q_start, "q_start", (B + 1,))
-    k0, k1, k2, ke = k_pages.stride()
-    v0, v1, v2, ve = v_pages.stride()
-    if ke != 1 or ve != 1:
-        raise ValueError("the rows of the pages must be contiguous")
-    num_pages, Hkv, page_size, _ = kshape
-    return (T, H, d, num_pages, Hkv, page_size, B, max_pages, code, (k0, k1, k2, v0, v1, v2))
+    if _away(dq, stream):
+        return _elsewhere(lambda: rope_bwd(dq, dk, freq, positions, interleaved, mscale, out_q,
+                                           out_k),
+                          stream, dq.device, (dq, dk, freq, positions, out_q, out_k))
+    return _calls().rope(dq, dk, freq, positions, interleaved, mscale, out_q, out_k, True)
 
 
 def paged_check(block_table, kv_len, q_start, num_pages: int, page_size: int,
@@ -612,64 +543,15 @@ def paged_append(k, v, k_pages, v_pages, block_table, kv_len, q_start=None, q=No
     rope_frequencies(), or None for no rotation; positions int32 [T] rotates to other positions
     than the places in the cache.
     """
-    dev = k.get_device()
-    if dev < 0:
-        raise ValueError("k must be a CUDA tensor")
-    if stream is not None or dev != _current_device():
+    if _away(k, stream):
         return _elsewhere(lambda: paged_append(k, v, k_pages, v_pages, block_table, kv_len, q_start,
                                                q, out_q, freq, positions, interleaved, mscale),
                           stream, k.device, (k, v, k_pages, v_pages, block_table, kv_len, q_start, q,
                                              out_q, freq, positions))
-    if v.get_device() != dev or k_pages.get_device() != dev or v_pages.get_device() != dev \
-            or block_table.get_device() != dev or kv_len.get_device() != dev \
-            or (q_start is not None and q_start.get_device() != dev) \
-            or (q is not None and q.get_device() != dev) \
-            or (freq is not None and freq.get_device() != dev) \
-            or out_q is not None or positions is not None:
-        _check_place(dev, v=v, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
-                     kv_len=kv_len, q_start=q_start, q=q, out_q=out_q, freq=freq,
-                     positions=positions)
-    T, Hkv, d, num_pages, pool_heads, page_size, B, max_pages, code, pages = \
-        _paged_shapes(k, k_pages, v_pages, block_table, kv_len, q_start)
-    dt = k.dtype
-    if Hkv != pool_heads or v.shape != k.shape or v.dtype is not dt:
-        raise ValueError("k and v must be [T, H_kv, d] with the H_kv and dtype of the pages")
-    if positions is not None:
-        _check_i32(positions, "positions", (T,))
-    k0, k1, ke = k.stride()
-    v0, v1, ve = v.stride()
-    if q is not None:
-        shape = q.shape
-        if len(shape) != 3 or shape[0] != T or shape[2] != d or q.dtype is not dt:
-            raise ValueError("q must be [T, H, d] with the dtype of k")
-        H = shape[1]
-        if out_q is None:
-            out_q = _empty(shape, dtype=dt, device=q.device)
-        elif out_q.shape != shape or out_q.dtype is not dt:
-            raise ValueError("out_q must match q in shape and dtype")
-        q0, q1, qe = q.stride()
-        o0, o1, oe = out_q.stride()
-        qp, op = q.data_ptr(), out_q.data_ptr()
-    else:
-        if out_q is not None:
-            raise ValueError("out_q needs q")
-        H, q0, q1, o0, o1, qp, op = Hkv, 0, 0, 8, 8, None, None
-        qe = oe = 1
-    if ke != 1 or ve != 1 or qe != 1 or oe != 1:
-        raise ValueError("the rows of q, k and v must be contiguous")
-    rc = load().fa_paged_append(
-        qp, op, k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-        _pack14(q0, q1, o0, o1, k0, k1, v0, v1, *pages), block_table.data_ptr(), kv_len.data_ptr(),
-        None if q_start is None else q_start.data_ptr(),
-        None if positions is None else positions.data_ptr(),
-        None if freq is None else freq.data_ptr(), T, B, H, Hkv, d, num_pages, page_size, max_pages,
-        0 if freq is None else _freq_table(freq), code, 1 if interleaved else 0, mscale, _raw(dev))
-    if rc != FA_OK:
-        raise FAError(rc, "fa_paged_append")
-    return out_q
+    return _calls().paged_append(k, v, k_pages, v_pages, block_table, kv_len, q_start, q, out_q, freq,
+                                 positions, interleaved, mscale)
 
 
-@functools.lru_cache(maxsize=1024)
 def paged_workspace_bytes(T: int, B: int, H: int, H_kv: int, d: int, max_q: int, page_size: int,
                           max_pages: int) -> int:
     return int(load().fa_paged_attn_workspace_bytes(T, B, H, H_kv, d, max_q, page_size, max_pages))
@@ -684,56 +566,13 @@ def paged_attention(q, k_pages, v_pages, block_table, kv_len, q_start=None,
     ones of sequence b sees keys j <= kv_len[b] - n + i, or with causal=False all kv_len[b].  max_q:
     the most new tokens that any sequence brings, when the caller knows it.  LSE is fp32 [T, H].
     """
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("q must be a CUDA tensor")
-    if stream is not None or dev != _current_device():
+    if _away(q, stream):
         return _elsewhere(lambda: paged_attention(q, k_pages, v_pages, block_table, kv_len, q_start,
                                                   max_q, scale, causal, out, lse, workspace),
                           stream, q.device, (q, k_pages, v_pages, block_table, kv_len, q_start, out,
                                              lse, workspace))
-    if k_pages.get_device() != dev or v_pages.get_device() != dev \
-            or block_table.get_device() != dev or kv_len.get_device() != dev \
-            or (q_start is not None and q_start.get_device() != dev) \
-            or out is not None or lse is not None or workspace is not None:
-        _check_place(dev, k_pages=k_pages, v_pages=v_pages, block_table=block_table, kv_len=kv_len,
-                     q_start=q_start, out=out, lse=lse, workspace=workspace)
-    T, H, d, num_pages, Hkv, page_size, B, max_pages, code, pages = \
-        _paged_shapes(q, k_pages, v_pages, block_table, kv_len, q_start)
-    if max_q is None:
-        max_q = T if q_start is not None else max(T // max(B, 1), 1)
-    device = q.device
-    if out is None:
-        out = _empty(q.shape, dtype=q.dtype, device=device)
-    elif out.shape != q.shape or out.dtype is not q.dtype:
-        raise ValueError("out must match q in shape and dtype")
-    if lse is None:
-        lse = _empty((T, H), dtype=_F32, device=device)
-    elif lse.dtype is not _F32 or lse.shape != (T, H) or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous fp32 [T, H]")
-    q0, q1, qe = q.stride()
-    o0, o1, oe = out.stride()
-    if qe != 1 or oe != 1:
-        raise ValueError("the rows of q and out must be contiguous")
-    nbytes = paged_workspace_bytes(T, B, H, Hkv, d, max_q, page_size, max_pages)
-    if workspace is None:
-        ws = None
-        if nbytes > 0:
-            workspace = _empty(nbytes, dtype=_U8, device=device)
-            ws = workspace.data_ptr()
-    elif not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
-        raise ValueError("workspace must be contiguous, of paged_workspace_bytes() bytes")
-    else:
-        ws = workspace.data_ptr()
-    rc = load().fa_paged_attn(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
-        _pack10(q0, q1, o0, o1, *pages), block_table.data_ptr(), kv_len.data_ptr(),
-        None if q_start is None else q_start.data_ptr(), T, B, H, Hkv, d, num_pages, page_size,
-        max_pages, max_q, code, 1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0,
-        ws, nbytes, _raw(dev))
-    if rc != FA_OK:
-        raise FAError(rc, "fa_paged_attn")
-    return out, lse
+    return _calls().paged_attention(q, k_pages, v_pages, block_table, kv_len, q_start, max_q, scale,
+                                    causal, out, lse, workspace)
 
 
 def sync_status(stream=None) -> int:

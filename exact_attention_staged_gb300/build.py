@@ -1,8 +1,9 @@
-"""Build libfa.so in-tree with nvcc for sm_103a (one -gencode, translation units in parallel).
+"""Build libfa.so in-tree with nvcc for sm_103a (one -gencode, translation units in parallel), and
+the Python extension beside it with the host compiler.
 
 Usage: ``python -m exact_attention_staged_gb300.build`` or ``build()`` from Python.
 Objects go to ``exact_attention_staged_gb300/_build/``; the library to
-``exact_attention_staged_gb300/libfa.so``.  Both are git-ignored.
+``exact_attention_staged_gb300/libfa.so``, the extension to ``_binding.so``.  All are git-ignored.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
+BINDING = os.path.join(PKG, "_binding.so")  # Python extension: the short calls' per-call path
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_fp8.cu", "fa_bwd.cu", "fa_decode.cu", "fa_rope.cu",
            "fa_paged.cu", "fa_paged_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,9 +39,9 @@ def _flags():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "fa.h"),
                                                                   __file__]
     return any(os.path.getmtime(p) > t for p in deps)
@@ -62,8 +65,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(res.stdout + res.stderr, file=sys.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_binding() -> None:
+        tmp = BINDING + f".tmp{os.getpid()}"
+        cmd = [shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared",
+               "-I", sysconfig.get_path("include"), "-I", INCLUDE, os.path.join(CSRC, "binding.c"),
+               "-o", tmp, "-lm"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"compiling binding.c failed:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, BINDING)
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     res = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True,
                          text=True)
