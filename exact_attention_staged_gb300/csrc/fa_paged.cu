@@ -21,6 +21,8 @@ constexpr int kAppendBatch = 2;  // row pieces of a lane in flight together
 
 template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(kAppendWarps * 32, 4) fa_paged_append_kernel(const PagedAppendParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
     constexpr int kUnits = D / kRopeElems;   // units of a row
     constexpr int kHeads = 32 / kUnits;      // heads that a warp takes at a time
     const PagedView &c = p.c;
@@ -109,9 +111,8 @@ cudaError_t launch_append_t(PagedAppendParams p, cudaStream_t stream) {
     p.chunks = (rounds + per - 1) / per;
     const long warps = static_cast<long>(p.c.T) * p.chunks;
     const long grid = (warps + kAppendWarps - 1) / kAppendWarps;
-    fa_paged_append_kernel<D, BF16, INTER>
-        <<<static_cast<unsigned>(grid), kAppendWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(fa_paged_append_kernel<D, BF16, INTER>, dim3(static_cast<unsigned>(grid)),
+                             kAppendWarps * 32, 0, stream, p);
 }
 
 template <int D>

@@ -20,6 +20,8 @@ constexpr int kRopeBatch = 4;  // heads whose loads are in flight together
 
 template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 3) fa_rope_kernel(const RopeParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
     constexpr int kUnits = D / kRopeElems;  // units of a row
     const int u = static_cast<int>(threadIdx.x) % kUnits;
     const long row = static_cast<long>(blockIdx.x) * (kRopeThreads / kUnits) + threadIdx.x / kUnits;
@@ -71,8 +73,7 @@ cudaError_t launch_rope_t(RopeParams p, cudaStream_t stream) {
     p.chunk = 2 * kRopeBatch;
     while (p.chunk > 1 && blocks * ((heads + p.chunk - 1) / p.chunk) < 4 * 152) p.chunk /= 2;
     dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + p.chunk - 1) / p.chunk));
-    fa_rope_kernel<D, BF16, INTER><<<grid, kRopeThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(fa_rope_kernel<D, BF16, INTER>, grid, kRopeThreads, 0, stream, p);
 }
 
 template <int D>

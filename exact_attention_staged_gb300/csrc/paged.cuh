@@ -67,9 +67,11 @@ struct PagedWork {
     int causal;
 };
 
-// What a unit costs beside its keys (Q, the first loads, the epilogue), for units of up to two query
-// tiles or of one.
-__host__ __device__ inline int paged_unit_cost(int tiles) { return tiles == 2 ? 256 : 0; }
+// What a unit costs beside its keys (Q, the first loads, the epilogue): for units of up to two query
+// tiles as much as 2.5 of their key tiles (a whole 8k prompt, whose first units are short, takes
+// 414 us with one tile, 391 with 1.75, 371 with 2.5, 368 with 3.5 and 372 with 5; two chunks of
+// 1k at d = 64 28.4, 28.0, 29.2, 29.5 and 30.3); units of one tile load ahead into the next.
+__host__ __device__ inline int paged_unit_cost(int tiles) { return tiles == 2 ? 640 : 0; }
 
 __host__ __device__ inline int paged_units(const PagedSeq &s, const PagedWork &w) {
     return s.n <= w.unit_toks ? (s.n > 0 ? 1 : 0) : (s.n - 1) / w.unit_toks + 1;  // per K/V head

@@ -79,6 +79,25 @@ constexpr int kPagedCtas = 152;      // one per SM
 
 constexpr int kErrIndex = -6;  // an index array on the device holds a value out of range
 
+// A launch that may overlap the end of the grid before it in the stream (programmatic stream
+// serialization): the kernel calls griddep_wait() before it touches global memory, so only its
+// launch and set-up are early, and griddep_launch_dependents() lets its own successor do the same.
+template <class... KernelArgs, class... Args>
+cudaError_t launch_overlapped(void (*kernel)(KernelArgs...), dim3 grid, unsigned threads, size_t smem,
+                              cudaStream_t stream, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_rope(const RopeParams &p, int d, bool bf16, bool inter, cudaStream_t stream);
 cudaError_t launch_paged_append(const PagedAppendParams &p, int d, bool bf16, bool inter,
                                 cudaStream_t stream);
