@@ -770,12 +770,14 @@ __global__ void __launch_bounds__(384, 1)
 // piece CTA c ended with, a lane per row and a slice of the columns per warp.  The pieces stand in
 // CTA order and are folded in in that order (deterministic), a batch at a time with all its reads
 // in flight: M = max m_s, w_s = 2^(m_s - M), l = sum w_s l_s, O = sum w_s O_s / l, LSE = (M + log2 l) ln 2.
+// A chunk's unit has 256 rows in few pieces, so its batches are small and more blocks share an SM; a
+// single token's unit has few rows in up to one piece per SM.
 constexpr int kMergeWarps = 8;
-template <int D, bool BF16>
+template <int D, bool BF16, int QT>
 __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const PagedAttnParams p) {
     using T = elem_t<BF16>;
     constexpr int kCols = D / 4 / kMergeWarps;  // float4 columns per warp
-    constexpr int kBatch = 4;
+    constexpr int kBatch = QT == 2 ? 2 : 8;
     griddep_wait();
     const int c = static_cast<int>(blockIdx.x), warp = warp_id();
     const int4 cut = p.cut[2 * c];
@@ -859,7 +861,7 @@ cudaError_t launch_attn_t(const PagedMaps &m, const PagedAttnParams &p, cudaStre
     kern<<<kPagedCtas, L::kThreads, L::kAlloc, stream>>>(m, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.cut == nullptr) return e;
-    return launch_overlapped(fa_paged_merge_kernel<D, BF16>,
+    return launch_overlapped(fa_paged_merge_kernel<D, BF16, QT>,
                              dim3(kPagedCtas - 1, (p.part_rows + 31) / 32), kMergeWarps * 32, 0,
                              stream, p);
 }
