@@ -540,6 +540,7 @@ int make_map_4d(CUtensorMap *m, const void *base, int dtype, const long long (&e
 
 // How paged attention lays its rows out: a query tile is floor(128 / rep) tokens of one head group;
 // one tile per unit while no sequence brings more tokens than that, two otherwise.
+constexpr long kClusterTiles = 24;
 struct PagedTiling {
     int rep, tile_toks, tiles, part_rows;
 };
@@ -550,6 +551,24 @@ PagedTiling paged_tiling(int H, int Hkv, int max_q) {
     t.tiles = max_q > t.tile_toks ? 2 : 1;
     t.part_rows = t.tiles == 2 ? 256 : max_q * t.rep;
     return t;
+}
+
+// CTAs of the cluster that takes a unit, or 0 for one line of all units over the chip.  Units are the
+// K/V heads of the sequences (one query tile each); a size is taken if all units' clusters are on
+// the chip at once and each CTA gets at most kClusterTiles key tiles of the longest possible cache.
+// A cluster lies inside one GPC, so larger ones leave SMs over: 15 clusters of 8, 23 of 6, 28 of 5,
+// 36 of 4, 46 of 3, 76 of 2 were on this GPU at once with one CTA per SM; kFit keeps a little below.
+// One sequence of 1000 keys (8 K/V heads of 128) takes 8.0 us so and 10.5 as a line, 8 of 1000 11.0 and
+// 16.6, 16 of 2500 30.8 and 34.4.  Beyond about 30 tiles per CTA the line is as fast where lengths
+// differ (4 of 8k to 16k: 35.6 and 34.5), and it stays so however much they do.
+int paged_cluster(const PagedTiling &t, int B, int Hkv, long capacity) {
+    if (t.tiles != 1) return 0;
+    constexpr int kSize[] = {8, 6, 5, 4, 3, 2, 1}, kFit[] = {14, 22, 26, 34, 44, 72, 148};
+    const long units = static_cast<long>(B) * Hkv;
+    const long tiles = (capacity + fa::kPagedKeys - 1) / fa::kPagedKeys;
+    for (int i = 0; i < 7; ++i)
+        if (units <= kFit[i]) return tiles <= kClusterTiles * kSize[i] ? kSize[i] : 0;
+    return 0;
 }
 
 // Scratch of paged attention: what to merge, then per slot the running statistics and O~.
@@ -952,9 +971,12 @@ size_t fa_paged_attn_workspace_bytes(int T, int B, int H, int H_kv, int d, int m
     if (max_q < 1 || check_paged(T, B, H, H_kv, d, 1, page_size, max_pages, FA_BF16, &c) != FA_OK ||
         H / H_kv > 128)
         return 0;
-    if (max_pages * page_size <= fa::kPagedKeys) return 0;  // one key tile: nothing to merge
-    return kPagedCutBytes + kPagedSlots * paged_tiling(H, H_kv, max_q < T ? max_q : T).part_rows *
-                                (sizeof(float2) + d * sizeof(float));
+    const PagedTiling t = paged_tiling(H, H_kv, max_q < T ? max_q : T);
+    // nothing to merge with one key tile, or merged inside the clusters
+    if (max_pages * page_size <= fa::kPagedKeys ||
+        paged_cluster(t, B, H_kv, static_cast<long>(max_pages) * page_size) > 0)
+        return 0;
+    return kPagedCutBytes + kPagedSlots * t.part_rows * (sizeof(float2) + d * sizeof(float));
 }
 
 int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void *o, float *lse,
@@ -1023,8 +1045,10 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
                     {tl.rep, 1, p.q_box_toks}) ||
         pages_map(&maps.k, k_pages, s + 4) || pages_map(&maps.v, v_pages, s + 7))
         return FA_ERR_CUDA;
-    cudaError_t e = fa::launch_paged_attn(maps, p, d, dtype == FA_BF16, tl.tiles,
-                                          static_cast<cudaStream_t>(stream));
+    cudaError_t e = fa::launch_paged_attn(
+        maps, p, d, dtype == FA_BF16, tl.tiles,
+        paged_cluster(tl, B, H_kv, static_cast<long>(max_pages) * page_size),
+        static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -1042,11 +1066,17 @@ int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, i
         return FA_ERR_INVALID;
     c.max_q = max_q;
     const fa::PagedWork w = {tile_toks, tiles * tile_toks, fa::paged_unit_cost(tiles), causal ? 1 : 0};
-    auto weight = [&](int b) { return H_kv * fa::paged_head(fa::paged_seq(c, b), w); };
-    long total = 0;
-    for (int b = 0; b < B; ++b) total += weight(b);
+    auto head = [&](int b) { return fa::paged_head(fa::paged_seq(c, b), w); };
+    long total = 0, longest = 0, heads = 0;
+    for (int b = 0; b < B; ++b) {
+        total += H_kv * head(b);
+        longest = head(b) > longest ? head(b) : longest;
+        heads += head(b) > 0 ? H_kv : 0;
+    }
     fa::PagedLine line;
-    line.cut(total, w, ctas);
+    line.cut(total, longest, heads, w, ctas);
+    auto each = [&](int b) -> long { return line.by_unit ? head(b) > 0 : head(b); };
+    auto weight = [&](int b) { return H_kv * each(b); };
     int n = 0;
     for (int k = 0; k < line.ctas; ++k) {
         const long at = line.border(k), end = line.border(k + 1);
@@ -1055,7 +1085,8 @@ int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, i
         while (before + weight(b) <= at) before += weight(b++);
         fa::PagedCursor cur;
         const fa::PagedSeq seq = fa::paged_seq(c, b);
-        cur.start(c, w, b, seq, fa::paged_head(seq, w), at - before);
+        cur.start(c, w, b, seq, each(b), at - before);
+        if (line.by_unit) room = head(b);
         while (room > 0) {
             const long from = end - room;
             const fa::PagedPiece u = cur.take(c, w, room);
@@ -1063,7 +1094,8 @@ int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, i
             if (n < max_pieces) {
                 int *x = pieces + 9 * n;
                 x[0] = k, x[1] = u.b, x[2] = u.kvh, x[3] = u.tok0, x[4] = u.toks, x[5] = u.t0;
-                x[6] = u.t1, x[7] = u.tiles, x[8] = line.holder(from + u.left - 1);
+                x[6] = u.t1, x[7] = u.tiles;
+                x[8] = line.by_unit ? k : line.holder(from + u.left - 1);
             }
             ++n;
         }

@@ -26,6 +26,12 @@
 // device (the host knows no lengths), so prompt chunks and single tokens of any mixture balance,
 // and a single sequence's keys spread over all SMs.
 //
+// Few units of few keys (a sequence or two, a short cache) are bound by latency: the cut line and
+// the merge in a second grid cost more than they balance.  While every unit fits one cluster and
+// all clusters fit the chip at once, a cluster of up to eight CTAs takes a unit, each CTA an equal
+// share of its key tiles, and the partial results are merged through distributed shared memory in
+// the same launch, with no workspace.
+//
 // Warps: 0 walks the units and loads Q and K, 2 loads V, 1 issues the MMAs, 4..7 and 8..11 are the
 // softmax groups.  MMA order per step: PV_0 of the step before, S_0, PV_1, S_1, as in the forward.
 #include "paged.cuh"
@@ -70,6 +76,9 @@ __device__ __forceinline__ float row_lse(float m, float l) {
     return l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : l;
 }
 
+constexpr int kDestCluster = -2;
+constexpr unsigned kMaxCluster = 8;  // the portable limit
+
 // A unit's piece as the first load warp hands it to the others (one of two slots in shared memory).
 struct PieceSlot {
     int tok0;   // first token, in the batch; -1: no more pieces
@@ -78,7 +87,7 @@ struct PieceSlot {
     int last0;  // last key that the first token sees
     int len;
     int t0, t1; // key tiles, t1 not beyond what the unit sees
-    int dest;   // -1: O and LSE, otherwise the slot of its partial result
+    int dest;   // -1: O and LSE, kDestCluster: shared memory, otherwise a partial result's slot
 };
 
 // First key tile from t0 on that query tile q of the piece does not take part in.
@@ -90,6 +99,41 @@ __device__ __forceinline__ int piece_end(const PieceSlot &u, int q, int tile_tok
     return max(u.t0, min(u.t1, end));
 }
 
+// Cluster building blocks (PTX barrier.cluster, mapa, ld.shared::cluster).
+__device__ __forceinline__ unsigned cluster_size() {
+    unsigned n;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {  // every thread of every CTA of the cluster
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, unsigned rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
 // One warp finds its CTA's stretch of the line, a lane per sequence: the first pass sums the lengths
 // and cuts the line, the second looks for the CTA's border in the running sum (up to 32 sequences
 // it still has at hand).  Rolled up so that the code is short: it runs once, from a cold
@@ -97,7 +141,8 @@ __device__ __forceinline__ int piece_end(const PieceSlot &u, int q, int tile_tok
 __device__ __forceinline__ long find_stretch(const PagedView &c, const PagedWork &w, bool report,
                                              PagedLine &line, PagedCursor &cur) {
     const int lane = lane_id(), cta = static_cast<int>(blockIdx.x);
-    long sum = 0, begin = 0, each = 0;
+    long sum = 0, begin = 0, each = 0, longest = 0;
+    int heads = 0;
     PagedSeq s;
     s.tok0 = s.n = s.len = 0;
 #pragma unroll 1
@@ -112,7 +157,9 @@ __device__ __forceinline__ long find_stretch(const PagedView &c, const PagedWork
                     each = paged_head(s, w);
                 }
             }
-            const long x = c.Hkv * each;
+            // place on the line: lengths, or units counted
+            const long step = pass == 1 && line.by_unit ? (each > 0 ? 1 : 0) : each;
+            const long x = c.Hkv * step;
             long upto = x;  // inclusive
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -127,14 +174,23 @@ __device__ __forceinline__ long find_stretch(const PagedView &c, const PagedWork
                     s.tok0 = __shfl_sync(0xffffffffu, s.tok0, at);
                     s.n = __shfl_sync(0xffffffffu, s.n, at);
                     s.len = __shfl_sync(0xffffffffu, s.len, at);
-                    cur.start(c, w, b0 + at, s, __shfl_sync(0xffffffffu, each, at), pos);
-                    return line.border(cta + 1) - begin;
+                    cur.start(c, w, b0 + at, s, __shfl_sync(0xffffffffu, step, at), pos);
+                    return line.by_unit ? __shfl_sync(0xffffffffu, each, at)
+                                        : line.border(cta + 1) - begin;
                 }
+            } else {
+                longest = max(longest, each);
+                heads += each > 0 ? c.Hkv : 0;
             }
             sum += __shfl_sync(0xffffffffu, upto, 31);
         }
         if (pass == 0) {
-            line.cut(sum, w, static_cast<int>(gridDim.x));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+                heads += __shfl_xor_sync(0xffffffffu, heads, o);
+            }
+            line.cut(sum, longest, heads, w, static_cast<int>(gridDim.x));
             if (cta >= line.ctas) break;
             begin = line.border(cta);
             sum = 0;
@@ -178,7 +234,8 @@ struct PageWindow {
     }
 };
 
-template <int D, bool BF16, int QT>
+// CL: one unit per cluster (QT is 1), its partial results merged in the cluster.
+template <int D, bool BF16, int QT, bool CL>
 __global__ void __launch_bounds__(384, 1)
     fa_paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedAttnParams p) {
     using L = PagedLayout<D, QT>;
@@ -238,8 +295,27 @@ __global__ void __launch_bounds__(384, 1)
     PagedLine line;
     PagedCursor cur;
     long room = 0;
-    if (warp == 0 || warp == 2)
-        room = find_stretch(p.c, work, blockIdx.x == 0 && warp == 0, line, cur);
+    PagedPiece own;  // CL: this CTA's share of its cluster's unit
+    own.toks = 0;
+    if (warp == 0 || warp == 2) {
+        if constexpr (CL) {
+            const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+            const int unit = static_cast<int>(blockIdx.x) / ctas;
+            own.b = unit / p.c.Hkv;
+            own.kvh = unit - own.b * p.c.Hkv;
+            const PagedSeq s = paged_seq(p.c, own.b);
+            if (s.bad && warp == 0 && lane == 0) paged_report(p.c);
+            own.tok0 = s.tok0;
+            own.toks = s.n;
+            own.len = s.len;
+            own.last0 = p.causal ? s.len - s.n : s.len - 1;
+            const int tiles = (paged_keys(s, work, s.n) + kPagedKeys - 1) / kPagedKeys;
+            own.t0 = rank * tiles / ctas;
+            own.t1 = (rank + 1) * tiles / ctas;
+        } else {
+            room = find_stretch(p.c, work, blockIdx.x == 0 && warp == 0, line, cur);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -287,15 +363,22 @@ __global__ void __launch_bounds__(384, 1)
             for (;;) {
                 PagedPiece u;
                 u.t0 = u.t1 = 0;
-                const long end = line.border(static_cast<int>(blockIdx.x) + 1);
                 long from = 0;
-                while (room > 0) {
-                    from = end - room;
-                    u = cur.take(p.c, work, room);
-                    if (u.t0 < u.t1) break;
+                bool any, whole;
+                if constexpr (CL) {
+                    u = own;
+                    any = k == 0 && own.toks > 0;  // its share may be empty: it still joins the merge
+                    whole = true;
+                } else {
+                    const long end = line.border(static_cast<int>(blockIdx.x) + 1);
+                    while (room > 0) {
+                        from = end - room;
+                        u = cur.take(p.c, work, room);
+                        if (u.t0 < u.t1) break;
+                    }
+                    any = u.t0 < u.t1;
+                    whole = u.t1 - u.t0 == u.tiles;
                 }
-                const bool any = u.t0 < u.t1;
-                const bool whole = u.t1 - u.t0 == u.tiles;
                 const int first_tile = u.t0;
                 // a unit that stands before its sequence sees nothing
                 if (any && u.last0 + (p.causal ? u.toks - 1 : 0) < 0) u.t1 = u.t0;
@@ -316,7 +399,8 @@ __global__ void __launch_bounds__(384, 1)
                             s[4] = u.len;
                             s[5] = u.t0;
                             s[6] = u.t1;
-                            s[7] = whole ? -1
+                            s[7] = CL ? kDestCluster
+                                   : whole ? -1
                                          : 2 * static_cast<int>(blockIdx.x) + (first_tile == 0 ? 1 : 0);
                         }
                         mbar_arrive(&unit_full[e]);
@@ -688,7 +772,7 @@ __global__ void __launch_bounds__(384, 1)
             if (busy) {
                 // O and LSE, or the piece's partial (m, l, O~); the tensor-memory loads are
                 // warp-wide, the stores only for real rows
-                const float inv = u.dest >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
+                const float inv = CL || u.dest >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
                 wa *= inv;
                 wb *= inv;
                 const int head = u.kvh * p.rep + row_head;
@@ -716,7 +800,14 @@ __global__ void __launch_bounds__(384, 1)
                                 fmaf(__uint_as_float(o1[x]), wb, __uint_as_float(o[x])));
                     }
                     if (!real) continue;
-                    if (u.dest < 0) {
+                    if constexpr (CL) {  // V's ring is free: every product has been read out of it
+                        float4 *dst = reinterpret_cast<float4 *>(smem + L::kVOff) + cc * 8 * 128 + row;
+#pragma unroll
+                        for (int q4 = 0; q4 < 8; ++q4)
+                            dst[q4 * 128] = make_float4(
+                                __uint_as_float(o[4 * q4]), __uint_as_float(o[4 * q4 + 1]),
+                                __uint_as_float(o[4 * q4 + 2]), __uint_as_float(o[4 * q4 + 3]));
+                    } else if (u.dest < 0) {
                         uint4 *dst = reinterpret_cast<uint4 *>(
                             reinterpret_cast<T *>(p.o) + otok * p.o_t + head * p.o_h + cc * 32);
 #pragma unroll
@@ -740,7 +831,9 @@ __global__ void __launch_bounds__(384, 1)
                                 __uint_as_float(o[4 * q4 + 2]), __uint_as_float(o[4 * q4 + 3]));
                     }
                 }
-                if (real) {
+                if (CL) {
+                    pair_ml[row] = make_float2(m, l);  // the second group's were read above
+                } else if (real) {
                     if (u.dest < 0)
                         p.lse[otok * p.c.H + head] = row_lse(m, l);
                     else
@@ -763,6 +856,50 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmemCols);
+    }
+    if constexpr (CL) {
+        // the cluster's CTAs hold (m, l, O~) of their shares; each of them merges a slice of the
+        // rows' columns, in rank order
+        const unsigned ctas = cluster_size();
+        cluster_sync();
+        const PieceSlot u = read_slot(0);
+        const int items = u.tok0 < 0 ? 0 : u.toks * p.rep * (D / 4);
+        const uint32_t ml0 = smem_u32(pair_ml), o0 = smem_u32(smem + L::kVOff);
+        for (int i = static_cast<int>(cluster_rank() * L::kThreads + threadIdx.x); i < items;
+             i += static_cast<int>(ctas * L::kThreads)) {
+            const int row = i / (D / 4), col = i % (D / 4);
+            float2 ml[kMaxCluster];
+            float4 x[kMaxCluster];
+            float M = -INFINITY;
+#pragma unroll
+            for (unsigned r = 0; r < kMaxCluster; ++r) {
+                ml[r] = make_float2(-INFINITY, 0.f);
+                if (r < ctas) {
+                    ml[r] = cluster_ld2(cluster_map(ml0 + row * 8, r));
+                    x[r] = cluster_ld4(cluster_map(o0 + (col * 128 + row) * 16, r));
+                }
+                M = fmaxf(M, ml[r].x);
+            }
+            const float mu = M == -INFINITY ? 0.f : M;
+            float l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (unsigned r = 0; r < kMaxCluster; ++r) {
+                // a share that saw nothing weighs nothing, one that is all NaN passes it on
+                if (r >= ctas || ml[r].y == 0.f) continue;
+                const float w = ml[r].x == -INFINITY ? 1.f : ex2(ml[r].x - mu);
+                l = fmaf(w, ml[r].y, l);
+                acc = make_float4(fmaf(w, x[r].x, acc.x), fmaf(w, x[r].y, acc.y),
+                                  fmaf(w, x[r].z, acc.z), fmaf(w, x[r].w, acc.w));
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const long tok = u.tok0 + row / p.rep;
+            const int head = u.kvh * p.rep + row % p.rep;
+            *reinterpret_cast<uint2 *>(p.o + tok * p.o_t + head * p.o_h + col * 4) = make_uint2(
+                pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+            if (col == 0) p.lse[tok * p.c.H + head] = row_lse(M, l);
+        }
+        cluster_sync();  // no CTA leaves while another still reads its shared memory
     }
 }
 
@@ -842,19 +979,24 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const 
     if (warp == 0) p.lse[static_cast<long>(tok0 + tok) * p.c.H + head] = row_lse(M, l);
 }
 
+// The dynamic shared memory of a kernel, allowed once per device (the attribute holds from then on).
+cudaError_t allow_smem(std::atomic<unsigned long long> &ready, const void *kernel, int bytes,
+                       int device) {
+    const unsigned long long bit = 1ull << (device & 63);
+    if ((ready.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 template <int D, bool BF16, int QT>
-cudaError_t launch_attn_t(const PagedMaps &m, const PagedAttnParams &p, cudaStream_t stream) {
+cudaError_t launch_line(const PagedMaps &m, const PagedAttnParams &p, cudaStream_t stream) {
     using L = PagedLayout<D, QT>;
-    auto kern = fa_paged_attn_kernel<D, BF16, QT>;
-    // the attribute holds for the device from then on: set once for each of them
+    auto kern = fa_paged_attn_kernel<D, BF16, QT, false>;
     static std::atomic<unsigned long long> ready{0};
-    const unsigned long long bit = 1ull << (p.device & 63);
-    cudaError_t e = cudaSuccess;
-    if ((ready.load(std::memory_order_acquire) & bit) == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(bit, std::memory_order_release);
-    }
+    cudaError_t e = allow_smem(ready, reinterpret_cast<const void *>(kern), L::kAlloc, p.device);
+    if (e != cudaSuccess) return e;
     // not launched to overlap the grid before it: its CTAs would then take the SMs in the order in
     // which they come free, prompt chunks and single tokens no longer spread over the chip (a mixed
     // batch 51.8 -> 56.6 us, a single sequence 11.0 -> 10.2)
@@ -867,19 +1009,42 @@ cudaError_t launch_attn_t(const PagedMaps &m, const PagedAttnParams &p, cudaStre
 }
 
 template <int D, bool BF16>
-cudaError_t launch_attn_d(const PagedMaps &m, const PagedAttnParams &p, int tiles,
+cudaError_t launch_clusters(const PagedMaps &m, const PagedAttnParams &p, int ctas,
+                            cudaStream_t stream) {
+    using L = PagedLayout<D, 1>;
+    auto kern = fa_paged_attn_kernel<D, BF16, 1, true>;
+    static std::atomic<unsigned long long> ready{0};
+    const cudaError_t e = allow_smem(ready, reinterpret_cast<const void *>(kern), L::kAlloc, p.device);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.c.B * p.c.Hkv * ctas));
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::kAlloc;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, m, p);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_attn_t(const PagedMaps &m, const PagedAttnParams &p, int tiles, int cluster,
                           cudaStream_t st) {
-    return tiles == 2 ? launch_attn_t<D, BF16, 2>(m, p, st) : launch_attn_t<D, BF16, 1>(m, p, st);
+    if (cluster > 0) return launch_clusters<D, BF16>(m, p, cluster, st);
+    return tiles == 2 ? launch_line<D, BF16, 2>(m, p, st) : launch_line<D, BF16, 1>(m, p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn(const PagedMaps &m, const PagedAttnParams &p, int d, bool bf16,
-                              int tiles, cudaStream_t stream) {
-    if (d == 64) return bf16 ? launch_attn_d<64, true>(m, p, tiles, stream)
-                             : launch_attn_d<64, false>(m, p, tiles, stream);
-    return bf16 ? launch_attn_d<128, true>(m, p, tiles, stream)
-                : launch_attn_d<128, false>(m, p, tiles, stream);
+                              int tiles, int cluster, cudaStream_t stream) {
+    if (d == 64) return bf16 ? launch_attn_t<64, true>(m, p, tiles, cluster, stream)
+                             : launch_attn_t<64, false>(m, p, tiles, cluster, stream);
+    return bf16 ? launch_attn_t<128, true>(m, p, tiles, cluster, stream)
+                : launch_attn_t<128, false>(m, p, tiles, cluster, stream);
 }
 
 }  // namespace fa

@@ -120,12 +120,27 @@ __host__ __device__ inline long paged_head(const PagedSeq &s, const PagedWork &w
 // No stretch is shorter than a unit's cost and two single key tiles, one step of a CTA's two softmax
 // groups (so none is without work, and every CTA between a cut unit's first and last one has a
 // piece of it).
+// Where every sequence is one unit per K/V head and there are no more units than CTAs, cutting them is
+// left out when it would not pay: a CTA takes a whole unit, nothing is merged.  By unit, the time is
+// that of the longest unit (1950 cycles a key tile) or of HBM for all of them (2570 cycles a tile
+// and 152 SMs); as a line it is HBM's plus about 9000 cycles for cutting and merging.  16 x 8 heads of
+// 8k keys: 80.3 us by unit, 85.6 as a line; of 4k to 8k keys: 72.4 and 68.2.
 struct PagedLine {
     long total, q;
     int ctas, r;
-    __host__ __device__ void cut(long length, const PagedWork &w, int most) {
+    bool by_unit;
+    // longest: length of the longest head; heads: K/V heads of sequences with new tokens
+    __host__ __device__ void cut(long length, long longest, long heads, const PagedWork &w, int most) {
         const int least = w.unit_cost + 2 * kPagedKeys;
         total = length;
+        by_unit = w.unit_toks == w.tile_toks && heads <= most && 115 * longest <= length + 68000;
+        if (by_unit) {
+            total = heads;
+            ctas = static_cast<int>(heads);
+            q = heads > 0 ? 1 : 0;
+            r = 0;
+            return;
+        }
         ctas = length >= static_cast<long>(most) * least ? most
                : length >= least ? static_cast<int>(length) / least : length > 0 ? 1 : 0;
         if (ctas == 0) {

@@ -101,8 +101,8 @@ cudaError_t launch_overlapped(void (*kernel)(KernelArgs...), dim3 grid, unsigned
 cudaError_t launch_rope(const RopeParams &p, int d, bool bf16, bool inter, cudaStream_t stream);
 cudaError_t launch_paged_append(const PagedAppendParams &p, int d, bool bf16, bool inter,
                                 cudaStream_t stream);
-// tiles: query tiles per unit, 1 or 2
+// tiles: query tiles per unit, 1 or 2; cluster: CTAs per unit, or 0 for one line over all SMs
 cudaError_t launch_paged_attn(const PagedMaps &m, const PagedAttnParams &p, int d, bool bf16,
-                              int tiles, cudaStream_t stream);
+                              int tiles, int cluster, cudaStream_t stream);
 
 }  // namespace fa

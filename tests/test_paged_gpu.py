@@ -26,7 +26,8 @@ DEV = "cuda:0"
 class Batch:
     """A paged batch: `seqs` is a list of (new tokens, cached positions with them)."""
 
-    def __init__(self, seqs, H, Hkv, d, dtype, page, rows=False, seed=0, pad=(0, 0), poison=True):
+    def __init__(self, seqs, H, Hkv, d, dtype, page, rows=False, seed=0, pad=(0, 0), poison=True,
+                 room=0):
         g = torch.Generator().manual_seed(1000 + seed)
         self.seqs, self.H, self.Hkv, self.d, self.page = seqs, H, Hkv, d, page
         B = len(seqs)
@@ -34,7 +35,8 @@ class Batch:
         pool = sum(need) + 2
         ids = torch.randperm(pool, generator=g).tolist()
         # behind a sequence's pages the table holds ids that no call may follow
-        self.table = torch.full((B, max(max(need), 1) + 1), 1 << 20, dtype=torch.int32)
+        width = max(max(need) + 1, -(-room // page))
+        self.table = torch.full((B, width), 1 << 20, dtype=torch.int32)
         at = 0
         for b, c in enumerate(need):
             self.table[b, :c] = torch.tensor(ids[at:at + c], dtype=torch.int32)
@@ -114,9 +116,12 @@ CASES = [  # sequences (new, length), H, Hkv, d, dtype, page size, token rows ou
 ]
 
 
+# room: positions that the tables could hold; batches whose tables hold few positions may be computed
+# by clusters of CTAs, the others as one line of work over the chip
+@pytest.mark.parametrize("room", [0, 9000])
 @pytest.mark.parametrize("seqs,H,Hkv,d,dtype,page,rows,causal", CASES)
-def test_attention_parity(cuda_lib, seqs, H, Hkv, d, dtype, page, rows, causal):
-    t = Batch(seqs, H, Hkv, d, dtype, page, rows, seed=len(seqs) + H + d)
+def test_attention_parity(cuda_lib, seqs, H, Hkv, d, dtype, page, rows, causal, room):
+    t = Batch(seqs, H, Hkv, d, dtype, page, rows, seed=len(seqs) + H + d, room=room)
     o, lse = attend(cuda_lib, t, causal=causal)
     assert cuda_lib.sync_status() == 0
     check(t, o, lse, d ** -0.5, causal, "parity")
@@ -125,16 +130,41 @@ def test_attention_parity(cuda_lib, seqs, H, Hkv, d, dtype, page, rows, causal):
     check(t, o2, lse2, d ** -0.5, causal, "loose bound")
 
 
+@pytest.mark.parametrize("lens", [[1], [100] * 3, [129, 500, 1, 64, 1000], [600] * 16, [40] * 40,
+                                  [4000, 20], [5100], [0, 7, 0, 300]])
+@pytest.mark.parametrize("n", [1, 3])
+def test_short_and_few_sequences(cuda_lib, lens, n):
+    # from one unit to more units than SMs, key tiles fewer and more than the CTAs that share them
+    for H, Hkv, d, dtype in ((4, 1, 128, BF), (8, 4, 64, HF), (16, 8, 128, BF)):
+        t = Batch([(min(n, L), L) if L else (0, 0) for L in lens], H, Hkv, d, dtype, 16, seed=sum(lens))
+        o, lse = attend(cuda_lib, t)
+        assert cuda_lib.sync_status() == 0
+        check(t, o, lse, d ** -0.5, True, f"few {lens} {H} {Hkv} {d}")
+        again = attend(cuda_lib, t)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("room", [0, 9000])
 @pytest.mark.parametrize("dtype", [BF, HF])
-def test_rows_that_see_nothing_and_sharp_scores(cuda_lib, dtype):
+def test_rows_that_see_nothing_and_sharp_scores(cuda_lib, dtype, room):
+    # fewer tokens than a query tile, some of them before their sequence
+    t = Batch([(5, 3), (1, 0), (6, 140), (2, 1)], 4, 2, 64, dtype, 16, seed=15, room=room)
+    o, lse = attend(cuda_lib, t)
+    assert cuda_lib.sync_status() == 0
+    check(t, o, lse, 0.125, True, "short few")
+    assert bool((o[:2] == 0).all()) and bool(torch.isneginf(lse[5]).all())
+    t = Batch([(2, 900), (1, 700)], 4, 2, 64, dtype, 32, seed=16, room=room)
+    t.q *= 5
+    o, lse = attend(cuda_lib, t, scale=1.0)
+    check(t, o, lse, 1.0, True, "sharp few")
     # more new tokens than positions: the first rows stand before the sequence and see no key
-    t = Batch([(9, 4), (150, 20), (3, 0), (1, 0), (140, 141)], 4, 2, 64, dtype, 16, seed=5)
+    t = Batch([(9, 4), (150, 20), (3, 0), (1, 0), (140, 141)], 4, 2, 64, dtype, 16, seed=5, room=room)
     o, lse = attend(cuda_lib, t)
     assert cuda_lib.sync_status() == 0
     check(t, o, lse, 0.125, True, "short")
     assert bool((o[:5] == 0).all()) and bool(torch.isneginf(lse[:5]).all())
     # scores of std 40: nearly one-hot rows, the running maximum moves by far more than 8
-    t = Batch([(40, 800), (1, 900)], 4, 2, 64, dtype, 32, seed=6)
+    t = Batch([(40, 800), (1, 900)], 4, 2, 64, dtype, 32, seed=6, room=room)
     t.q *= 5
     o, lse = attend(cuda_lib, t, scale=1.0)
     check(t, o, lse, 1.0, True, "sharp")
@@ -171,8 +201,9 @@ def test_strided_rows_uniform_batches_and_shared_pages(cuda_lib):
     assert torch.equal(a[2:4], a[:2]) or torch.allclose(a[2:4].float(), a[:2].float(), atol=2e-2)
 
 
-def test_bad_indices_are_reported_not_followed(cuda_lib):
-    t = Batch([(2, 100), (3, 50)], 4, 2, 64, BF, 16, seed=9, poison=False)
+@pytest.mark.parametrize("room", [0, 9000])
+def test_bad_indices_are_reported_not_followed(cuda_lib, room):
+    t = Batch([(2, 100), (3, 50)], 4, 2, 64, BF, 16, seed=9, poison=False, room=room)
     q, k, v, table, lens, start = t.dev()
     good = cuda_lib.paged_attention(q, k, v, table, lens, start, max_q=3)
     assert cuda_lib.sync_status() == 0
