@@ -540,7 +540,6 @@ int make_map_4d(CUtensorMap *m, const void *base, int dtype, const long long (&e
 
 // How paged attention lays its rows out: a query tile is floor(128 / rep) tokens of one head group;
 // one tile per unit while no sequence brings more tokens than that, two otherwise.
-constexpr long kClusterTiles = 24;
 struct PagedTiling {
     int rep, tile_toks, tiles, part_rows;
 };
@@ -555,19 +554,20 @@ PagedTiling paged_tiling(int H, int Hkv, int max_q) {
 
 // CTAs of the cluster that takes a unit, or 0 for one line of all units over the chip.  Units are the
 // K/V heads of the sequences (one query tile each); a size is taken if all units' clusters are on
-// the chip at once and each CTA gets at most kClusterTiles key tiles of the longest possible cache.
+// the chip at once and each CTA gets no more than so many key tiles of the longest possible cache.
 // A cluster lies inside one GPC, so larger ones leave SMs over: 15 clusters of 8, 23 of 6, 28 of 5,
 // 36 of 4, 46 of 3, 76 of 2 were on this GPU at once with one CTA per SM; kFit keeps a little below.
-// One sequence of 1000 keys (8 K/V heads of 128) takes 8.0 us so and 10.5 as a line, 8 of 1000 11.0 and
-// 16.6, 16 of 2500 30.8 and 34.4.  Beyond about 30 tiles per CTA the line is as fast where lengths
-// differ (4 of 8k to 16k: 35.6 and 34.5), and it stays so however much they do.
+// One sequence of 1000 keys (8 K/V heads of 128) takes 8.0 us so and 10.5 as a line, of 8k 14.8 and
+// 17.1, of 16k 22.9 and 22.6; 8 of 1000 11.0 and 16.6, 16 of 2500 30.8 and 34.4.  Where lengths differ
+// the line is as fast from about 30 tiles per CTA (4 of 8k to 16k: 35.6 and 34.5).
 int paged_cluster(const PagedTiling &t, int B, int Hkv, long capacity) {
     if (t.tiles != 1) return 0;
     constexpr int kSize[] = {8, 6, 5, 4, 3, 2, 1}, kFit[] = {14, 22, 26, 34, 44, 72, 148};
+    constexpr long kTiles[] = {14, 24, 24, 24, 24, 24, 24};
     const long units = static_cast<long>(B) * Hkv;
     const long tiles = (capacity + fa::kPagedKeys - 1) / fa::kPagedKeys;
     for (int i = 0; i < 7; ++i)
-        if (units <= kFit[i]) return tiles <= kClusterTiles * kSize[i] ? kSize[i] : 0;
+        if (units <= kFit[i]) return tiles <= kTiles[i] * kSize[i] ? kSize[i] : 0;
     return 0;
 }
 
