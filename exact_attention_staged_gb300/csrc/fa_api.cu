@@ -552,23 +552,30 @@ PagedTiling paged_tiling(int H, int Hkv, int max_q) {
     return t;
 }
 
-// CTAs of the cluster that takes a unit, or 0 for one line of all units over the chip.  Units are the
-// K/V heads of the sequences (one query tile each); a size is taken if all units' clusters are on
-// the chip at once and each CTA gets no more than so many key tiles of the longest possible cache.
+// CTAs of the cluster that takes a unit, or 0 for one line of all units over the chip.  A size is taken
+// if all units' clusters are on the chip at once and each CTA gets no more than so many key tiles of
+// the longest possible cache.
 // A cluster lies inside one GPC, so larger ones leave SMs over: 15 clusters of 8, 23 of 6, 28 of 5,
 // 36 of 4, 46 of 3, 76 of 2 were on this GPU at once with one CTA per SM; kFit keeps a little below.
 // One sequence of 1000 keys (8 K/V heads of 128) takes 8.0 us so and 10.5 as a line, of 8k 14.8 and
 // 17.1, of 16k 22.9 and 22.6; 8 of 1000 11.0 and 16.6, 16 of 2500 30.8 and 34.4.  Where lengths differ
-// the line is as fast from about 30 tiles per CTA (4 of 8k to 16k: 35.6 and 34.5).
-int paged_cluster(const PagedTiling &t, int B, int Hkv, long capacity) {
-    if (t.tiles != 1) return 0;
+// the line is as fast from about 30 tiles per CTA (4 of 8k to 16k: 35.6 and 34.5).  A chunk of 300 tokens
+// over 300 keys (8 K/V heads) takes 16.7 and 19.9 us, over 2000 22.4 and 23.7, over 5000 33.8 and 33.0.
+fa::PagedClusters paged_clusters(const PagedTiling &t, int T, int B, int Hkv, long capacity) {
     constexpr int kSize[] = {8, 6, 5, 4, 3, 2, 1}, kFit[] = {14, 22, 26, 34, 44, 72, 148};
     constexpr long kTiles[] = {14, 24, 24, 24, 24, 24, 24};
-    const long units = static_cast<long>(B) * Hkv;
+    // no more units than this, whatever the lengths: every sequence with tokens rounds up once
+    const long each = static_cast<long>(t.tiles) * t.tile_toks, seqs = B < T ? B : T;
+    const long units = Hkv * ((T + seqs * (each - 1)) / each);
     const long tiles = (capacity + fa::kPagedKeys - 1) / fa::kPagedKeys;
-    for (int i = 0; i < 7; ++i)
-        if (units <= kFit[i]) return tiles <= kTiles[i] * kSize[i] ? kSize[i] : 0;
-    return 0;
+    for (int i = 0; i < 7; ++i) {
+        if (units > kFit[i]) continue;
+        // of units of two query tiles: the line would give a CTA no more than 1.5 tiles fewer
+        const bool take = t.tiles == 1 ? tiles <= kTiles[i] * kSize[i]
+                                       : 2 * tiles * (152 - units * kSize[i]) <= 3 * 152 * kSize[i];
+        return {take ? kSize[i] : 0, units};
+    }
+    return {0, 0};
 }
 
 // Scratch of paged attention: what to merge, then per slot the running statistics and O~.
@@ -974,7 +981,7 @@ size_t fa_paged_attn_workspace_bytes(int T, int B, int H, int H_kv, int d, int m
     const PagedTiling t = paged_tiling(H, H_kv, max_q < T ? max_q : T);
     // nothing to merge with one key tile, or merged inside the clusters
     if (max_pages * page_size <= fa::kPagedKeys ||
-        paged_cluster(t, B, H_kv, static_cast<long>(max_pages) * page_size) > 0)
+        paged_clusters(t, T, B, H_kv, static_cast<long>(max_pages) * page_size).ctas > 0)
         return 0;
     return kPagedCutBytes + kPagedSlots * t.part_rows * (sizeof(float2) + d * sizeof(float));
 }
@@ -1047,7 +1054,7 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
         return FA_ERR_CUDA;
     cudaError_t e = fa::launch_paged_attn(
         maps, p, d, dtype == FA_BF16, tl.tiles,
-        paged_cluster(tl, B, H_kv, static_cast<long>(max_pages) * page_size),
+        paged_clusters(tl, T, B, H_kv, static_cast<long>(max_pages) * page_size),
         static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

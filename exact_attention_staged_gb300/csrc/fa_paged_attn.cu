@@ -62,6 +62,10 @@ struct PagedLayout {
     static constexpr int kPairOff = kMiscOff + 8;       // the second group's (m, l): float2[128]
     static constexpr int kBytes = kPairOff + 128 * 8;
     static constexpr int kAlloc = kBytes + 1024;
+    // CL: a row of O~ laid over the rings, padded so that neighbouring rows' pieces fall into
+    // different banks
+    static constexpr int kRowBytes = (D + 4) * 4;
+    static_assert(QT * 128 * kRowBytes <= (kKSlots + kVSlots) * kTileBytes, "O~ over the rings");
     static constexpr int kThreads = 384;
     static constexpr uint32_t kTmemCols = 512;  // S_0, S_1 (2 x 128), O_0, O_1 (2 x d)
     static_assert(kAlloc <= 232448, "shared memory per CTA");
@@ -132,6 +136,49 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t a) {
                  : "r"(a)
                  : "memory");
     return v;
+}
+
+// One warp finds unit number `unit` of the batch (CL), a lane per sequence; false: there are fewer.
+__device__ __forceinline__ bool find_unit(const PagedView &c, const PagedWork &w, int unit,
+                                          bool report, PagedPiece &own) {
+    const int lane = lane_id();
+    int before = 0;
+    bool found = false;
+#pragma unroll 1
+    for (int b0 = 0; b0 < c.B; b0 += 32) {
+        PagedSeq s;
+        s.tok0 = s.n = s.len = 0;
+        if (b0 + lane < c.B) {
+            s = paged_seq(c, b0 + lane);
+            if (s.bad && report) paged_report(c);
+        }
+        const int each = paged_units(s, w), x = each * c.Hkv;
+        int upto = x;  // inclusive
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + upto > unit);
+        if (past != 0 && !found) {
+            found = true;
+            const int at = __ffs(static_cast<int>(past)) - 1;
+            const int pos = unit - before - __shfl_sync(0xffffffffu, upto - x, at);
+            const int units = __shfl_sync(0xffffffffu, each, at);
+            const int tok0 = __shfl_sync(0xffffffffu, s.tok0, at);
+            const int n = __shfl_sync(0xffffffffu, s.n, at);
+            own.b = b0 + at;
+            own.len = __shfl_sync(0xffffffffu, s.len, at);
+            own.kvh = pos / units;
+            const int i0 = (pos - own.kvh * units) * w.unit_toks;
+            own.tok0 = tok0 + i0;
+            own.toks = min(n - i0, w.unit_toks);
+            own.last0 = w.causal ? own.len - n + i0 : own.len - 1;
+            if (!report) return true;  // block 0 goes on to look at every sequence
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return found;
 }
 
 // One warp finds its CTA's stretch of the line, a lane per sequence: the first pass sums the lengths
@@ -234,7 +281,7 @@ struct PageWindow {
     }
 };
 
-// CL: one unit per cluster (QT is 1), its partial results merged in the cluster.
+// CL: one unit per cluster, its partial results merged in the cluster.
 template <int D, bool BF16, int QT, bool CL>
 __global__ void __launch_bounds__(384, 1)
     fa_paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedAttnParams p) {
@@ -300,18 +347,13 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 0 || warp == 2) {
         if constexpr (CL) {
             const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-            const int unit = static_cast<int>(blockIdx.x) / ctas;
-            own.b = unit / p.c.Hkv;
-            own.kvh = unit - own.b * p.c.Hkv;
-            const PagedSeq s = paged_seq(p.c, own.b);
-            if (s.bad && warp == 0 && lane == 0) paged_report(p.c);
-            own.tok0 = s.tok0;
-            own.toks = s.n;
-            own.len = s.len;
-            own.last0 = p.causal ? s.len - s.n : s.len - 1;
-            const int tiles = (paged_keys(s, work, s.n) + kPagedKeys - 1) / kPagedKeys;
-            own.t0 = rank * tiles / ctas;
-            own.t1 = (rank + 1) * tiles / ctas;
+            if (find_unit(p.c, work, static_cast<int>(blockIdx.x) / ctas, blockIdx.x == 0 && warp == 0,
+                          own)) {
+                const int end = own.last0 + (p.causal ? own.toks - 1 : 0) + 1;  // keys it sees
+                const int tiles = end > 0 ? (end + kPagedKeys - 1) / kPagedKeys : 0;
+                own.t0 = rank * tiles / ctas;
+                own.t1 = (rank + 1) * tiles / ctas;
+            }
         } else {
             room = find_stretch(p.c, work, blockIdx.x == 0 && warp == 0, line, cur);
         }
@@ -426,7 +468,7 @@ __global__ void __launch_bounds__(384, 1)
                     ++nq;
                     return true;
                 };
-                bool q_done = is_v;
+                bool q_done = is_v || u.t0 == u.t1;  // a piece that sees nothing needs no Q
                 if (!q_done && nq == 0) ok = q_done = load_q();  // the first Q needs no page id
                 if (!whole && first_tile == 0) {  // starts a unit that other CTAs finish
                     cut0 = make_int4(u.tok0, u.toks, u.kvh, 0);
@@ -460,7 +502,6 @@ __global__ void __launch_bounds__(384, 1)
                         q_done = true;
                     }
                 }
-                if (ok && !q_done) ok = load_q();  // a unit that sees nothing takes its turn
                 if (!ok) break;
             }
             if (!is_v && p.cut != nullptr && lane == 0) {
@@ -523,6 +564,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 return true;
             };
+            int nq = 0;            // Q tiles used: pieces with keys
             int nt = 0;            // K and V tiles consumed
             int pcnt[2] = {0, 0};  // PV products per group (p_full phases)
             auto wait_p = [&](int t) {
@@ -539,14 +581,16 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 const PieceSlot u = read_slot(e);
                 if (u.tok0 < 0) break;
-                if (!mbar_wait_warp(q_full, k & 1, p.ctl, abort_flag)) {
-                    ok = false;
-                    break;
+                if (u.t0 < u.t1) {
+                    if (!mbar_wait_warp(q_full, nq & 1, p.ctl, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    ++nq;
+                    tc_fence_after();
                 }
-                tc_fence_after();
                 const int p0[2] = {pcnt[0], pcnt[1]};
                 const int n0 = nt - u.t0;  // ring index of key tile j is n0 + j
-                if (u.t1 == u.t0) umma_commit_el(q_empty);  // nothing seen: Q is free at once
                 if (is_pair(u.toks)) {
                     // step by step, group t takes tile j + t
                     for (int j = u.t0; ok && j - 2 < u.t1; j += 2) {
@@ -753,6 +797,13 @@ __global__ void __launch_bounds__(384, 1)
                 if (!mbar_wait_warp(&o_final[t], nfin & 1, p.ctl, abort_flag)) break;
                 ++nfin;
             }
+            if constexpr (CL && QT == 2) {
+                // the results go over the K and V rings: the other group's products are done too (a
+                // CTA has one piece, so this is that barrier's first phase)
+                if (!pair && piece_end(u, 1 - t, p.tile_toks, p.causal) > u.t0 &&
+                    !mbar_wait_warp(&o_final[1 - t], 0, p.ctl, abort_flag))
+                    break;
+            }
             float wa = 1.f, wb = 0.f;  // weights of O_0 and of the second group's O_1
             if (both) {
                 if (!mbar_wait_warp(pair_full, npair & 1, p.ctl, abort_flag)) break;
@@ -800,11 +851,12 @@ __global__ void __launch_bounds__(384, 1)
                                 fmaf(__uint_as_float(o1[x]), wb, __uint_as_float(o[x])));
                     }
                     if (!real) continue;
-                    if constexpr (CL) {  // V's ring is free: every product has been read out of it
-                        float4 *dst = reinterpret_cast<float4 *>(smem + L::kVOff) + cc * 8 * 128 + row;
+                    if constexpr (CL) {
+                        float4 *dst = reinterpret_cast<float4 *>(
+                            smem + L::kKOff + (q * 128 + row) * L::kRowBytes + cc * 128);
 #pragma unroll
                         for (int q4 = 0; q4 < 8; ++q4)
-                            dst[q4 * 128] = make_float4(
+                            dst[q4] = make_float4(
                                 __uint_as_float(o[4 * q4]), __uint_as_float(o[4 * q4 + 1]),
                                 __uint_as_float(o[4 * q4 + 2]), __uint_as_float(o[4 * q4 + 3]));
                     } else if (u.dest < 0) {
@@ -831,8 +883,8 @@ __global__ void __launch_bounds__(384, 1)
                                 __uint_as_float(o[4 * q4 + 2]), __uint_as_float(o[4 * q4 + 3]));
                     }
                 }
-                if (CL) {
-                    pair_ml[row] = make_float2(m, l);  // the second group's were read above
+                if (CL) {  // over the Q tiles
+                    reinterpret_cast<float2 *>(smem)[q * 128 + row] = make_float2(m, l);
                 } else if (real) {
                     if (u.dest < 0)
                         p.lse[otok * p.c.H + head] = row_lse(m, l);
@@ -864,10 +916,13 @@ __global__ void __launch_bounds__(384, 1)
         cluster_sync();
         const PieceSlot u = read_slot(0);
         const int items = u.tok0 < 0 ? 0 : u.toks * p.rep * (D / 4);
-        const uint32_t ml0 = smem_u32(pair_ml), o0 = smem_u32(smem + L::kVOff);
+        const uint32_t ml0 = smem_u32(smem), o0 = smem_u32(smem + L::kKOff);
         for (int i = static_cast<int>(cluster_rank() * L::kThreads + threadIdx.x); i < items;
              i += static_cast<int>(ctas * L::kThreads)) {
-            const int row = i / (D / 4), col = i % (D / 4);
+            const int col = i % (D / 4), which = i / (D / 4);  // 4 columns of one token's head
+            const int tok = which / p.rep, h = which - tok * p.rep;
+            const int q = QT == 2 && tok >= p.tile_toks ? 1 : 0;
+            const int row = q * 128 + (tok - q * p.tile_toks) * p.rep + h;
             float2 ml[kMaxCluster];
             float4 x[kMaxCluster];
             float M = -INFINITY;
@@ -876,7 +931,7 @@ __global__ void __launch_bounds__(384, 1)
                 ml[r] = make_float2(-INFINITY, 0.f);
                 if (r < ctas) {
                     ml[r] = cluster_ld2(cluster_map(ml0 + row * 8, r));
-                    x[r] = cluster_ld4(cluster_map(o0 + (col * 128 + row) * 16, r));
+                    x[r] = cluster_ld4(cluster_map(o0 + row * L::kRowBytes + col * 16, r));
                 }
                 M = fmaxf(M, ml[r].x);
             }
@@ -893,11 +948,11 @@ __global__ void __launch_bounds__(384, 1)
                                   fmaf(w, x[r].z, acc.z), fmaf(w, x[r].w, acc.w));
             }
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            const long tok = u.tok0 + row / p.rep;
-            const int head = u.kvh * p.rep + row % p.rep;
-            *reinterpret_cast<uint2 *>(p.o + tok * p.o_t + head * p.o_h + col * 4) = make_uint2(
+            const long otok = u.tok0 + tok;
+            const int head = u.kvh * p.rep + h;
+            *reinterpret_cast<uint2 *>(p.o + otok * p.o_t + head * p.o_h + col * 4) = make_uint2(
                 pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-            if (col == 0) p.lse[tok * p.c.H + head] = row_lse(M, l);
+            if (col == 0) p.lse[otok * p.c.H + head] = row_lse(M, l);
         }
         cluster_sync();  // no CTA leaves while another still reads its shared memory
     }
@@ -1008,22 +1063,22 @@ cudaError_t launch_line(const PagedMaps &m, const PagedAttnParams &p, cudaStream
                              stream, p);
 }
 
-template <int D, bool BF16>
-cudaError_t launch_clusters(const PagedMaps &m, const PagedAttnParams &p, int ctas,
+template <int D, bool BF16, int QT>
+cudaError_t launch_clusters(const PagedMaps &m, const PagedAttnParams &p, PagedClusters cl,
                             cudaStream_t stream) {
-    using L = PagedLayout<D, 1>;
-    auto kern = fa_paged_attn_kernel<D, BF16, 1, true>;
+    using L = PagedLayout<D, QT>;
+    auto kern = fa_paged_attn_kernel<D, BF16, QT, true>;
     static std::atomic<unsigned long long> ready{0};
     const cudaError_t e = allow_smem(ready, reinterpret_cast<const void *>(kern), L::kAlloc, p.device);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.c.B * p.c.Hkv * ctas));
+    cfg.gridDim = dim3(static_cast<unsigned>(cl.units * cl.ctas));
     cfg.blockDim = dim3(L::kThreads);
     cfg.dynamicSmemBytes = L::kAlloc;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cl.ctas);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -1031,20 +1086,21 @@ cudaError_t launch_clusters(const PagedMaps &m, const PagedAttnParams &p, int ct
 }
 
 template <int D, bool BF16>
-cudaError_t launch_attn_t(const PagedMaps &m, const PagedAttnParams &p, int tiles, int cluster,
+cudaError_t launch_attn_t(const PagedMaps &m, const PagedAttnParams &p, int tiles, PagedClusters cl,
                           cudaStream_t st) {
-    if (cluster > 0) return launch_clusters<D, BF16>(m, p, cluster, st);
+    if (cl.ctas > 0) return tiles == 2 ? launch_clusters<D, BF16, 2>(m, p, cl, st)
+                                       : launch_clusters<D, BF16, 1>(m, p, cl, st);
     return tiles == 2 ? launch_line<D, BF16, 2>(m, p, st) : launch_line<D, BF16, 1>(m, p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn(const PagedMaps &m, const PagedAttnParams &p, int d, bool bf16,
-                              int tiles, int cluster, cudaStream_t stream) {
-    if (d == 64) return bf16 ? launch_attn_t<64, true>(m, p, tiles, cluster, stream)
-                             : launch_attn_t<64, false>(m, p, tiles, cluster, stream);
-    return bf16 ? launch_attn_t<128, true>(m, p, tiles, cluster, stream)
-                : launch_attn_t<128, false>(m, p, tiles, cluster, stream);
+                              int tiles, PagedClusters cl, cudaStream_t stream) {
+    if (d == 64) return bf16 ? launch_attn_t<64, true>(m, p, tiles, cl, stream)
+                             : launch_attn_t<64, false>(m, p, tiles, cl, stream);
+    return bf16 ? launch_attn_t<128, true>(m, p, tiles, cl, stream)
+                : launch_attn_t<128, false>(m, p, tiles, cl, stream);
 }
 
 }  // namespace fa

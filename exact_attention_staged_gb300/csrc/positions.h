@@ -101,8 +101,13 @@ cudaError_t launch_overlapped(void (*kernel)(KernelArgs...), dim3 grid, unsigned
 cudaError_t launch_rope(const RopeParams &p, int d, bool bf16, bool inter, cudaStream_t stream);
 cudaError_t launch_paged_append(const PagedAppendParams &p, int d, bool bf16, bool inter,
                                 cudaStream_t stream);
-// tiles: query tiles per unit, 1 or 2; cluster: CTAs per unit, or 0 for one line over all SMs
+// Clusters of `ctas` CTAs, one for each of up to `units` units; ctas 0: one line of units over all SMs.
+struct PagedClusters {
+    int ctas;
+    long units;
+};
+// tiles: query tiles per unit, 1 or 2
 cudaError_t launch_paged_attn(const PagedMaps &m, const PagedAttnParams &p, int d, bool bf16,
-                              int tiles, int cluster, cudaStream_t stream);
+                              int tiles, PagedClusters cl, cudaStream_t stream);
 
 }  // namespace fa

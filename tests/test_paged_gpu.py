@@ -144,6 +144,19 @@ def test_short_and_few_sequences(cuda_lib, lens, n):
         assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("seqs", [[(50, 50)], [(300, 700)], [(200, 210), (1, 90), (64, 64)], [(33, 20)],
+                                  [(0, 5), (130, 600), (2, 2)], [(500, 500)]])
+@pytest.mark.parametrize("H,Hkv,d,dtype", [(4, 1, 128, BF), (3, 1, 64, HF), (4, 2, 64, BF), (7, 1, 128, HF)])
+def test_short_chunks(cuda_lib, seqs, H, Hkv, d, dtype):
+    # chunks whose units a cluster takes: units of one and of two query tiles, tiles of uneven reach,
+    # fewer key tiles than CTAs
+    t = Batch(seqs, H, Hkv, d, dtype, 16, seed=60 + H)
+    for causal in (True, False):
+        o, lse = attend(cuda_lib, t, causal=causal)
+        assert cuda_lib.sync_status() == 0
+        check(t, o, lse, d ** -0.5, causal, f"chunk {seqs} {H} {Hkv} {d}")
+
+
 @pytest.mark.parametrize("room", [0, 9000])
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_rows_that_see_nothing_and_sharp_scores(cuda_lib, dtype, room):
