@@ -485,7 +485,7 @@ int check_paged(int T, int B, int H, int Hkv, int d, int num_pages, int page_siz
     if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_INVALID;
     if (static_cast<long long>(T) * (H + 2ll * Hkv) >= (1ll << 31) ||
         static_cast<long long>(num_pages) * page_size >= (1ll << 31) ||
-        static_cast<long long>(max_pages) * page_size >= (1ll << 31))
+        static_cast<long long>(max_pages) * page_size > (1ll << 31) - 1024)  // rounds up to tiles
         return FA_ERR_INVALID;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
@@ -1159,7 +1159,7 @@ int fa_debug_set_dkdv_splits(int splits) {
 }
 
 int fa_debug_set_fault(int mode) {
-    if (mode < 0 || mode > 3) return FA_ERR_INVALID;
+    if (mode < 0 || mode > 4) return FA_ERR_INVALID;
     std::lock_guard<std::mutex> lk(g_mu);
     g_fault_mode = mode;
     return FA_OK;

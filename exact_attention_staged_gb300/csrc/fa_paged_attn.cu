@@ -480,10 +480,11 @@ __global__ void __launch_bounds__(384, 1)
                         ok = false;
                         break;
                     }
-                    // the tile's pages into its slot: one lane per page
-                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], L::kTileBytes);
+                    // the tile's pages into its slot: one lane per page (test hook: not the first K)
+                    const bool skip = p.ctl.fault_mode == 4 && !is_v && n == 0;
+                    if (lane == 0 && !skip) mbar_arrive_expect_tx(&full[slot], L::kTileBytes);
                     __syncwarp();
-                    if (lane < boxes) {
+                    if (lane < boxes && !skip) {
                         const int y = (j * kPagedKeys) & ((1 << p.c.page_shift) - 1);
                         uint8_t *dst = ring + slot * L::kTileBytes + lane * box_rows * 128;
                         for (int b = 0; b < L::kBoxes; ++b)
@@ -512,8 +513,10 @@ __global__ void __launch_bounds__(384, 1)
                 // let every copy still in flight land before shared memory goes away
                 if (lane == 0) {
                     if (nq > 0) drain_wait(q_full, (nq - 1) & 1, p.ctl);
-                    for (int l = n > slots ? n - slots : 0; l < n; ++l)
+                    for (int l = n > slots ? n - slots : 0; l < n; ++l) {
+                        if (p.ctl.fault_mode == 4 && !is_v && l == 0) continue;
                         drain_wait(&full[l % slots], (l / slots) & 1, p.ctl);
+                    }
                 }
             }
             __syncwarp();

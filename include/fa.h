@@ -307,9 +307,10 @@ int fa_rope(const void *q, void *q_out, const void *k, void *k_out, const long l
  *               Tokens before q_start[0] and from q_start[B] on belong to no sequence: nothing is
  *               read, written or computed for them (a padded batch).
  * The index arrays live on the device, so the call cannot refuse a bad value: lengths and offsets
- * are clamped, a page id outside [0, num_pages) is not accessed (a new token's row is not written,
- * its keys and values read as zeros), and fa_sync_status() returns FA_ERR_INDEX.
- * T (H + 2 H_kv), num_pages page_size and max_pages page_size are below 2^31.
+ * are clamped (nothing is appended to such a sequence), a page id outside [0, num_pages) is not
+ * accessed (a new token's row is not written, its keys and values read as zeros), and
+ * fa_sync_status() returns FA_ERR_INDEX.
+ * T (H + 2 H_kv) and num_pages page_size are below 2^31, max_pages page_size at most 2^31 - 1024.
  *
  * fa_paged_check applies the same rules on the host to HOST copies of the arrays, for a scheduler
  * that builds them there: FA_OK, or FA_ERR_INDEX.
@@ -381,7 +382,8 @@ const char *fa_status_string(int code);
  * fa_debug_set_wait_limit_ns: bound on every device pipeline wait (default 2 s; 0 restores it).
  * fa_debug_set_fault: 0 = none; 1 = the forward's load warp skips the first key tile of each
  *   CTA; 2 = the dK/dV pass's load warp skips its first Q tile; 3 = the dQ pass's load warp
- *   skips its first K tile.  The bounded waits then run out, the kernel returns early and
+ *   skips its first K tile; 4 = paged attention's K load warp skips the first key tile of each
+ *   CTA.  The bounded waits then run out, the kernel returns early and
  *   fa_sync_status() reports FA_ERR_TIMEOUT; other values: FA_ERR_INVALID.
  * fa_debug_set_dkdv_splits: 0 = automatic; s > 0 splits every K/V head's query group of
  *   fa_bwd_gqa over min(s, H / H_kv) dK/dV CTAs per key tile (changes the workspace size).

@@ -237,6 +237,24 @@ def test_bad_indices_are_reported_not_followed(cuda_lib, room):
     assert torch.equal(again[0], good[0]) and cuda_lib.sync_status() == 0
 
 
+@pytest.mark.parametrize("room", [0, 9000])
+@pytest.mark.parametrize("seqs", [[(1, 300), (2, 500)], [(300, 700)]])
+def test_timeout_is_reported_not_hung(cuda_lib, seqs, room):
+    t = Batch(seqs, 4, 2, 64, BF, 16, seed=17, room=room)
+    want = attend(cuda_lib, t)
+    assert cuda_lib.sync_status() == 0
+    try:
+        cuda_lib.debug_set_wait_limit_ns(20_000_000)
+        cuda_lib.debug_set_fault(4)
+        attend(cuda_lib, t)
+        assert cuda_lib.sync_status() == cuda_lib.FA_ERR_TIMEOUT
+    finally:
+        cuda_lib.debug_set_fault(0)
+        cuda_lib.debug_set_wait_limit_ns(0)
+    got = attend(cuda_lib, t)
+    assert torch.equal(got[0], want[0]) and cuda_lib.sync_status() == 0
+
+
 def test_repeats_streams_graphs_and_two_calls_at_once(cuda_lib):
     t = Batch([(1, 3000), (40, 900), (1, 70)], 8, 2, 128, BF, 16, seed=10)
     q, k, v, table, lens, start = t.dev()
@@ -383,6 +401,18 @@ def test_append_positions_in_place_and_bad_pages(cuda_lib):
         assert cuda_lib.sync_status() == cuda_lib.FA_ERR_INDEX
     # only position 17 .. 19 and 38, 39 were named, all on bad pages: nothing was written
     assert torch.equal(kp, before[0]) and torch.equal(vp, before[1])
+    # a length beyond the table, a negative one, offsets out of order or behind the tokens
+    for a in (dict(lens=[20, 1 << 20]), dict(lens=[20, -1]), dict(start=[0, 4, 3]),
+              dict(start=[0, 3, 77])):
+        n = torch.tensor(a.get("lens", [20, 40]), dtype=torch.int32, device=DEV)
+        st = torch.tensor(a.get("start", [0, 3, 5]), dtype=torch.int32, device=DEV)
+        kp.copy_(before[0])
+        cuda_lib.paged_append(k, v, kp, vp, table, n, st, freq=f)
+        assert cuda_lib.sync_status() == cuda_lib.FA_ERR_INDEX, a
+        other = torch.ones(kp.shape[0], dtype=torch.bool, device=DEV)
+        other[int(t.table[0, 1])] = False  # the good sequence's tokens may be there
+        if "lens" in a:  # the bad one wrote nowhere
+            assert torch.equal(kp[other], before[0][other])
 
 
 def test_prompt_then_tokens_equals_one_long_sequence(cuda_lib):
