@@ -214,6 +214,87 @@ def test_strided_rows_uniform_batches_and_shared_pages(cuda_lib):
     assert torch.equal(a[2:4], a[:2]) or torch.allclose(a[2:4].float(), a[:2].float(), atol=2e-2)
 
 
+@pytest.mark.parametrize("rows", [False, True])
+def test_pools_with_padding_between_rows_heads_and_pages(cuda_lib, rows):
+    # no stride is a multiple of the one inside it
+    t = Batch([(2, 70), (40, 300)], 4, 2, 64, BF, 16, seed=18, rows=rows)
+    q, k, v, table, lens, start = t.dev()
+    want = cuda_lib.paged_attention(q, k, v, table, lens, start, max_q=40)
+    P, H, S, d = k.shape
+    row, head, page = (2 * 72 + 8, 72, 16 * 152 + 40) if rows else (72, 16 * 72 + 24, 2 * 1176 + 56)
+    pad = []
+    for x in (k, v):
+        room = torch.full((P * page,), 9.0, dtype=BF, device=DEV)
+        y = torch.as_strided(room, (P, H, S, d), (page, head, row, 1))
+        y.copy_(x)
+        pad.append(y)
+    got = cuda_lib.paged_attention(q, pad[0], pad[1], table, lens, start, max_q=40)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    new = torch.randn(t.T, 2, 64, device=DEV).to(BF)
+    cuda_lib.paged_append(new, new, k, v, table, lens, start)
+    cuda_lib.paged_append(new, new, pad[0], pad[1], table, lens, start)
+    assert torch.equal(pad[0].nan_to_num(), k.nan_to_num())
+    assert torch.equal(pad[1].nan_to_num(), v.nan_to_num())
+    assert cuda_lib.sync_status() == 0
+    with pytest.raises(cuda_lib.FAError):  # K and V order heads and rows differently
+        other = v.transpose(1, 2).contiguous().transpose(1, 2) if not rows else v.contiguous()
+        cuda_lib.paged_attention(q, k, other, table, lens, start)
+    with pytest.raises(cuda_lib.FAError):  # a broadcast Q
+        cuda_lib.paged_attention(q[:1].expand(t.T, 4, 64), k, v, table, lens, start)
+
+
+def test_refusals_on_device(cuda_lib):
+    t = Batch([(2, 70)], 4, 2, 64, BF, 16, seed=19)
+    q, k, v, table, lens, start = t.dev()
+    good = dict(q=q, k_pages=k, v_pages=v, block_table=table, kv_len=lens, q_start=start)
+    for bad in (dict(q=q.half()), dict(q=q[0]), dict(k_pages=k[:1]), dict(block_table=table.long()),
+                dict(block_table=table[:, ::2]), dict(kv_len=lens.cpu()), dict(kv_len=lens.float()),
+                dict(q_start=start[:1]), dict(out=q[:1]), dict(out=q.half()),
+                dict(lse=torch.zeros(2, 4, dtype=torch.float64, device=DEV)), dict(k_pages=None),
+                dict(lse=torch.zeros(4, 2, device=DEV).t())):
+        with pytest.raises((ValueError, TypeError, AttributeError)):
+            cuda_lib.paged_attention(**{**good, **bad})
+    wide = torch.zeros(1, 1000, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError):  # too small a workspace
+        cuda_lib.paged_attention(**{**good, "block_table": wide},
+                                 workspace=torch.zeros(64, dtype=torch.uint8, device=DEV))
+    for bad in (dict(max_q=0), dict(scale=0.0), dict(scale=float("inf"))):
+        with pytest.raises(cuda_lib.FAError):
+            cuda_lib.paged_attention(**{**good, **bad})
+    x = q[:, :2]
+    good = dict(k=x, v=x, k_pages=k, v_pages=v, block_table=table, kv_len=lens, q_start=start)
+    f, _ = cuda_lib.rope_frequencies(64, device=DEV)
+    for bad in (dict(k=q), dict(v=x[:1]), dict(q=q[:, :, :32]), dict(out_q=q), dict(freq=f.int()),
+                dict(positions=lens), dict(q=q, out_q=q[:1]), dict(freq=f.cpu())):
+        with pytest.raises((ValueError, TypeError)):
+            cuda_lib.paged_append(**{**good, **bad})
+    assert cuda_lib.sync_status() == 0
+
+
+def test_calls_from_several_threads(cuda_lib):
+    import threading
+    batches = [Batch([(1, 900 + 100 * i), (60, 400)], 4, 2, 64, BF, 16, seed=70 + i, room=9000 * (i % 2))
+               for i in range(4)]
+    dev = [b.dev() for b in batches]
+    want = [cuda_lib.paged_attention(*x, max_q=60) for x in dev]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        side = torch.cuda.Stream()
+        for _ in range(30):
+            o, lse = cuda_lib.paged_attention(*dev[i], max_q=60, stream=side)
+        side.synchronize()
+        if not (torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])):
+            bad.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not bad and cuda_lib.sync_status() == 0
+
+
 @pytest.mark.parametrize("room", [0, 9000])
 def test_bad_indices_are_reported_not_followed(cuda_lib, room):
     t = Batch([(2, 100), (3, 50)], 4, 2, 64, BF, 16, seed=9, poison=False, room=room)
