@@ -470,10 +470,6 @@ __global__ void __launch_bounds__(384, 1)
                 };
                 bool q_done = is_v || u.t0 == u.t1;  // a piece that sees nothing needs no Q
                 if (!q_done && nq == 0) ok = q_done = load_q();  // the first Q needs no page id
-                if (!whole && first_tile == 0) {  // starts a unit that other CTAs finish
-                    cut0 = make_int4(u.tok0, u.toks, u.kvh, 0);
-                    cut_n = line.holder(from + u.left - 1) - static_cast<int>(blockIdx.x) + 1;
-                }
                 for (int j = u.t0; j < u.t1 && ok; ++j) {
                     const int id = win.tile(p.c, j, boxes);
                     if (!mbar_wait_warp(&empty[slot], parity, p.ctl, abort_flag)) {
@@ -504,8 +500,12 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
                 if (!ok) break;
+                if (!CL && !is_v && !whole && first_tile == 0) {  // a unit that other CTAs finish
+                    cut0 = make_int4(u.tok0, u.toks, u.kvh, 0);
+                    cut_n = line.holder(from + u.left - 1) - static_cast<int>(blockIdx.x) + 1;
+                }
             }
-            if (!is_v && p.cut != nullptr && lane == 0) {
+            if (!CL && !is_v && p.cut != nullptr && lane == 0) {
                 p.cut[2 * blockIdx.x] = cut0;
                 p.cut[2 * blockIdx.x + 1] = make_int4(cut_n, 0, 0, 0);
             }
