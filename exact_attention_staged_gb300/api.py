@@ -1,4 +1,5 @@
-"""Python binding of libfa.so: argument marshalling only (ctypes).
+"""Python binding of libfa.so: argument marshalling only (ctypes; the short calls of rotary positions
+and the paged cache through the extension csrc/binding.c, whose checks cost less time).
 
 Every step of the attention path runs in the library's CUDA kernels; PyTorch supplies device
 memory and the current stream.  There is no fallback: when libfa.so is missing or the device

@@ -530,3 +530,50 @@ def test_prompt_then_tokens_equals_one_long_sequence(cuda_lib):
     # both sides round P and O to bf16 once; their O differ by no more than the sum of the two bounds
     rel = float((got.transpose(1, 2).float() - want.float()).norm() / want.float().norm())
     assert rel <= 2 * 5e-3 and float((lse.transpose(1, 2) - want_lse).abs().max()) <= 2e-3
+
+
+def test_captured_decode_steps_of_two_layers(cuda_lib):
+    """One step (a position more, then append and attention of two layers) captured once and replayed
+    token by token gives the eager steps' bits, and these the definition's values."""
+    H, Hkv, d, page, steps, lens0 = 6, 2, 64, 16, 5, (12, 300, 0, 127)
+    B = len(lens0)
+    f, _ = cuda_lib.rope_frequencies(d, device=DEV)
+    g = torch.Generator().manual_seed(60)
+    x = torch.randn((steps, 2, B, H + 2 * Hkv, d), generator=g).to(HF).to(DEV)
+    layers = [Batch([(1, L + steps) for L in lens0], H, Hkv, d, HF, page, seed=61 + i, poison=False)
+              for i in range(2)]
+
+    def run(graph):
+        caches = [tuple(y.to(DEV) for y in (t.k, t.v, t.table)) for t in layers]
+        now = torch.empty_like(x[0])
+        lens = torch.tensor(lens0, dtype=torch.int32, device=DEV)
+        bufs = [(torch.empty(B, H, d, dtype=HF, device=DEV), torch.empty(B, H, device=DEV),
+                 torch.empty(B, H, d, dtype=HF, device=DEV)) for _ in range(2)]
+
+        def step():
+            lens.add_(1)
+            for (kp, vp, table), (o, l, qr), y in zip(caches, bufs, now):
+                q, k, v = y[:, :H], y[:, H:H + Hkv], y[:, H + Hkv:]
+                cuda_lib.paged_append(k, v, kp, vp, table, lens, q=q, out_q=qr, freq=f)
+                cuda_lib.paged_attention(qr, kp, vp, table, lens, max_q=1, out=o, lse=l)
+
+        if graph:
+            captured = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(captured):
+                step()
+            step = captured.replay
+        seen = []
+        for i in range(steps):
+            now.copy_(x[i])
+            step()
+            seen += [y.clone() for b in bufs for y in b]
+        return seen, caches
+
+    want, caches = run(False)
+    got, caches2 = run(True)
+    assert cuda_lib.sync_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for t, a, b, at in zip(layers, caches, caches2, (-6, -3)):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        t.k, t.v, t.q = a[0].cpu(), a[1].cpu(), want[at + 2].cpu()
+        check(t, want[at], want[at + 1], d ** -0.5, True, "last step")
