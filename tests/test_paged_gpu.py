@@ -577,3 +577,25 @@ def test_captured_decode_steps_of_two_layers(cuda_lib):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
         t.k, t.v, t.q = a[0].cpu(), a[1].cpu(), want[at + 2].cpu()
         check(t, want[at], want[at + 1], d ** -0.5, True, "last step")
+
+
+def test_many_sequences(cuda_lib):
+    """More sequences than a warp finds in two reads, most of them short, many without a new token."""
+    g = torch.Generator().manual_seed(70)
+    lens = torch.randint(0, 40, (1500,), generator=g).tolist()
+    seqs = [(min(L, i % 4), L) for i, L in enumerate(lens)]
+    seqs[700] = (90, 900)
+    H, Hkv, d = 4, 2, 64
+    t = Batch(seqs, H, Hkv, d, BF, 8, seed=71, pad=(2, 5), poison=False)
+    _, kp, vp, table, lens, start = t.dev()
+    kv = torch.randn((2, t.T, Hkv, d), generator=g).to(BF)
+    cuda_lib.paged_append(kv[0].to(DEV), kv[1].to(DEV), kp, vp, table, lens, start)
+    for b, (n, L) in enumerate(seqs):
+        for i in range(n):
+            p, r = int(t.table[b, (L - n + i) // 8]), (L - n + i) % 8
+            t.k[p, :, r], t.v[p, :, r] = kv[0, int(t.start[b]) + i], kv[1, int(t.start[b]) + i]
+    assert torch.equal(kp.cpu(), t.k) and torch.equal(vp.cpu(), t.v)
+    for causal in (True, False):
+        o, lse = attend(cuda_lib, t, causal=causal)
+        check(t, o, lse, d ** -0.5, causal, "many")
+    assert cuda_lib.sync_status() == 0
