@@ -1025,6 +1025,7 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
     p.rep = tl.rep;
     p.tile_toks = tl.tile_toks;
     p.q_box_toks = p.c.max_q < tl.tile_toks ? p.c.max_q : tl.tile_toks;
+    p.q_bufs = p.q_box_toks * tl.rep <= 64 ? 2 : 1;
     p.part_rows = tl.part_rows;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.causal = causal ? 1 : 0;

@@ -54,11 +54,12 @@ struct PagedLayout {
     static constexpr int kKOff = QT * kTileBytes;  // after the Q tiles
     static constexpr int kVOff = kKOff + kKSlots * kTileBytes;
     static constexpr int kBarOff = kVOff + kVSlots * kTileBytes;
-    // q_full, q_empty, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_final[2],
-    // pair_full, pair_read, unit_full[2], unit_empty[2], drain
-    static constexpr int kNumBars = 2 + 2 * kKSlots + 2 * kVSlots + 13;
-    static constexpr int kUnitOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // two unit slots
-    static constexpr int kMiscOff = kUnitOff + 2 * 32;  // TMEM base, abort flag
+    static constexpr int kUnits = 4;  // unit slots: the loads run up to three units ahead
+    // q_full[2], q_empty[2], k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2],
+    // o_final[2], pair_full, pair_read, unit_full[], unit_empty[], drain
+    static constexpr int kNumBars = 4 + 2 * kKSlots + 2 * kVSlots + 8 + 2 * kUnits + 1;
+    static constexpr int kUnitOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;
+    static constexpr int kMiscOff = kUnitOff + kUnits * 32;  // TMEM base, abort flag
     static constexpr int kPairOff = kMiscOff + 8;       // the second group's (m, l): float2[128]
     static constexpr int kBytes = kPairOff + 128 * 8;
     static constexpr int kAlloc = kBytes + 1024;
@@ -80,10 +81,14 @@ __device__ __forceinline__ float row_lse(float m, float l) {
     return l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : l;
 }
 
+// Where units have no more than 64 rows, two of them share the Q tile: rows 64 to 127 of its boxes
+// are the second buffer.  A product's rows behind the unit's are whatever stands there, and unused.
+constexpr int kQBufBytes = 64 * 128;
+
 constexpr int kDestCluster = -2;
 constexpr unsigned kMaxCluster = 8;  // the portable limit
 
-// A unit's piece as the first load warp hands it to the others (one of two slots in shared memory).
+// A unit's piece as the first load warp hands it to the others (a slot in shared memory).
 struct PieceSlot {
     int tok0;   // first token, in the batch; -1: no more pieces
     int toks;
@@ -291,15 +296,15 @@ __global__ void __launch_bounds__(384, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
-    uint64_t *q_full = bars, *q_empty = bars + 1;
-    uint64_t *k_full = bars + 2, *k_empty = k_full + L::kKSlots;
+    uint64_t *q_full = bars, *q_empty = bars + 2;  // [2]: per Q buffer
+    uint64_t *k_full = bars + 4, *k_empty = k_full + L::kKSlots;
     uint64_t *v_full = k_empty + L::kKSlots, *v_empty = v_full + L::kVSlots;
     uint64_t *s_full = v_empty + L::kVSlots;  // [2]: per softmax group, as the next three
     uint64_t *p_full = s_full + 2;
     uint64_t *o_final = p_full + 2;
     uint64_t *pair_full = o_final + 2, *pair_read = pair_full + 1;
-    uint64_t *unit_full = pair_read + 1, *unit_empty = unit_full + 2;  // [2]: per unit slot
-    uint64_t *drain = unit_empty + 2;
+    uint64_t *unit_full = pair_read + 1, *unit_empty = unit_full + L::kUnits;
+    uint64_t *drain = unit_empty + L::kUnits;
     volatile int *unit_slot = reinterpret_cast<volatile int *>(smem + L::kUnitOff);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMiscOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMiscOff + 4);
@@ -308,8 +313,6 @@ __global__ void __launch_bounds__(384, 1)
     const PagedWork work = {p.tile_toks, QT * p.tile_toks, paged_unit_cost(QT), p.causal};
 
     if (threadIdx.x == 96) {
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
         for (int s = 0; s < L::kKSlots; ++s) {
             mbar_init(&k_full[s], 1);
             mbar_init(&k_empty[s], 1);
@@ -319,9 +322,13 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&v_empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);  // one arrival per softmax warp of a group
             mbar_init(&o_final[i], 1);
+        }
+        for (int i = 0; i < L::kUnits; ++i) {
             mbar_init(&unit_full[i], 1);
             mbar_init(&unit_empty[i], 9);  // the MMA warp and the softmax warps
         }
@@ -380,6 +387,9 @@ __global__ void __launch_bounds__(384, 1)
     };
     // both groups work on the same query tile and take alternate key tiles
     auto is_pair = [&](int toks) { return QT == 1 || toks <= p.tile_toks; };
+    // Q buffer of the nq-th piece with keys, and that buffer's tenants before it
+    auto q_buf = [&](int nq) { return QT == 1 && p.q_bufs == 2 ? nq & 1 : 0; };
+    auto q_use = [&](int nq) { return QT == 1 && p.q_bufs == 2 ? nq >> 1 : nq; };
 
     if (warp < 4) {
         // warpgroup 0 gives registers to the softmax groups: 128 x 88 + 256 x 208 = 64512, all of the
@@ -425,9 +435,9 @@ __global__ void __launch_bounds__(384, 1)
                 // a unit that stands before its sequence sees nothing
                 if (any && u.last0 + (p.causal ? u.toks - 1 : 0) < 0) u.t1 = u.t0;
                 if (!is_v) {
-                    const int e = k & 1;
-                    if (k >= 2 && !mbar_wait_warp(&unit_empty[e], ((k >> 1) - 1) & 1, p.ctl,
-                                                  abort_flag)) {
+                    const int e = k % L::kUnits;
+                    if (k >= L::kUnits && !mbar_wait_warp(&unit_empty[e], (k / L::kUnits - 1) & 1,
+                                                          p.ctl, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -453,17 +463,20 @@ __global__ void __launch_bounds__(384, 1)
                 ++k;
                 PageWindow win;
                 win.open(p.c, u);
-                auto load_q = [&]() {  // the Q tiles are free once the last unit's last S is done
-                    if (nq > 0 && !mbar_wait_warp(q_empty, (nq - 1) & 1, p.ctl, abort_flag))
+                auto load_q = [&]() {  // a Q buffer is free once its last unit's last S is done
+                    const int buf = q_buf(nq), use = q_use(nq);
+                    if (use > 0 && !mbar_wait_warp(&q_empty[buf], (use - 1) & 1, p.ctl, abort_flag))
                         return false;
                     if (lane == 0) {
                         const int tiles = is_pair(u.toks) ? 1 : 2;
                         mbar_arrive_expect_tx(
-                            q_full, tiles * L::kBoxes * 128 * p.rep * p.q_box_toks);
+                            &q_full[buf], tiles * L::kBoxes * 128 * p.rep * p.q_box_toks);
                         for (int t = 0; t < tiles; ++t)
                             for (int b = 0; b < L::kBoxes; ++b)
-                                tma_load_4d(smem + t * L::kTileBytes + b * L::kBoxBytes, &maps.q,
-                                            b * 64, 0, u.kvh, u.tok0 + t * p.tile_toks, q_full);
+                                tma_load_4d(smem + buf * kQBufBytes + t * L::kTileBytes +
+                                                b * L::kBoxBytes,
+                                            &maps.q, b * 64, 0, u.kvh, u.tok0 + t * p.tile_toks,
+                                            &q_full[buf]);
                     }
                     ++nq;
                     return true;
@@ -512,7 +525,8 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok || *abort_flag) {
                 // let every copy still in flight land before shared memory goes away
                 if (lane == 0) {
-                    if (nq > 0) drain_wait(q_full, (nq - 1) & 1, p.ctl);
+                    for (int l = max(nq - (QT == 1 ? p.q_bufs : 1), 0); l < nq; ++l)
+                        drain_wait(&q_full[q_buf(l)], q_use(l) & 1, p.ctl);
                     for (int l = n > slots ? n - slots : 0; l < n; ++l) {
                         if (p.ctl.fault_mode == 4 && !is_v && l == 0) continue;
                         drain_wait(&full[l % slots], (l / slots) & 1, p.ctl);
@@ -526,8 +540,8 @@ __global__ void __launch_bounds__(384, 1)
             const SDesc dk0 = sdesc_make(smem_u32(smem + L::kKOff), 16, 1024);   // K: K-major
             const SDesc dv0 = sdesc_make(smem_u32(smem + L::kVOff), L::kBoxBytes,
                                          1024);                                   // V: MN-major
-            auto issue_s = [&](int q, int t, int ks) {
-                const SDesc a = sdesc_add(dq0, q * L::kTileBytes);
+            auto issue_s = [&](int q, int t, int ks) {  // q: where Q starts
+                const SDesc a = sdesc_add(dq0, q);
                 const SDesc b = sdesc_add(dk0, ks * L::kTileBytes);
                 if constexpr (D == 128)
                     mma_ss_chain_k128(tmem + t * 128, a, b, kIdescS, 0u);
@@ -575,15 +589,67 @@ __global__ void __launch_bounds__(384, 1)
                 tc_fence_after();
                 return true;
             };
+            // QT == 1: the key tiles of all pieces are one sequence, tile x for group x & 1, and PV
+            // of tile x - 2 is issued before S of tile x, whichever piece they belong to: the next
+            // piece's scores are under way while the last one's probabilities are.
+            struct Tile {
+                int x, j, len;   // place in the sequence (-1: none), key tile, the sequence's end
+                bool add, last;  // not the first, the last of its group in the piece
+            };
+            Tile old = {-1, 0, 0, false, false}, mid = old;  // tiles x - 2 and x - 1
+            auto finish = [&](const Tile &w) {
+                if (w.x < 0) return true;
+                const int g = w.x & 1, vs = w.x % L::kVSlots;
+                if (!wait_v(w.x, w.j, w.len)) return false;
+                if (!mbar_wait_warp(&p_full[g], (w.x >> 1) & 1, p.ctl, abort_flag)) return false;
+                tc_fence_after();
+                issue_pv(g, vs, w.add);
+                if (w.last) umma_commit_el(&o_final[g]);
+                umma_commit_el(&v_empty[vs]);
+                return true;
+            };
             bool ok = true;
             for (int k = 0; ok; ++k) {
-                const int e = k & 1;
-                if (!mbar_wait_warp(&unit_full[e], (k >> 1) & 1, p.ctl, abort_flag)) {
+                const int e = k % L::kUnits;
+                if (!mbar_wait_warp(&unit_full[e], (k / L::kUnits) & 1, p.ctl, abort_flag)) {
                     ok = false;
                     break;
                 }
                 const PieceSlot u = read_slot(e);
+                if (QT == 1 && (u.tok0 < 0 || u.t0 == u.t1)) {
+                    // the end, or a piece that sees nothing: the slot after next is free only when
+                    // the tiles still open are done
+                    if (!finish(old) || !finish(mid)) {
+                        ok = false;
+                        break;
+                    }
+                    old.x = mid.x = -1;
+                }
                 if (u.tok0 < 0) break;
+                if constexpr (QT == 1) {
+                    const int buf = q_buf(nq);
+                    for (int j = u.t0; j < u.t1; ++j) {
+                        const int g = nt & 1, ks = nt % L::kKSlots;
+                        if (!finish(old) ||
+                            (j == u.t0 && !mbar_wait_warp(&q_full[buf], q_use(nq) & 1, p.ctl,
+                                                          abort_flag)) ||
+                            !wait_k(nt)) {
+                            ok = false;
+                            break;
+                        }
+                        issue_s(buf * kQBufBytes, g, ks);
+                        umma_commit_el(&k_empty[ks]);
+                        if (j == u.t1 - 1) umma_commit_el(&q_empty[buf]);
+                        old = mid;
+                        mid = {nt, j, u.len, j - u.t0 >= 2, j + 2 >= u.t1};
+                        ++nt;
+                    }
+                    if (!ok) break;
+                    if (u.t0 < u.t1) ++nq;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&unit_empty[e]);
+                    continue;
+                }
                 if (u.t0 < u.t1) {
                     if (!mbar_wait_warp(q_full, nq & 1, p.ctl, abort_flag)) {
                         ok = false;
@@ -648,7 +714,7 @@ __global__ void __launch_bounds__(384, 1)
                                 ++pcnt[t];
                                 if (j == end[t]) umma_commit_el(&o_final[t]);
                             }
-                            if (j < end[t]) issue_s(t, t, (n0 + j) % L::kKSlots);
+                            if (j < end[t]) issue_s(t * L::kTileBytes, t, (n0 + j) % L::kKSlots);
                         }
                         if (!ok) break;
                         if (j == u.t1 - 1) umma_commit_el(q_empty);
@@ -680,17 +746,21 @@ __global__ void __launch_bounds__(384, 1)
         const float sl2 = p.scale_log2;
         int scnt = 0;          // score tiles consumed by this group
         int nfin = 0;          // pieces in which this group had products (o_final phases)
-        int nfin1 = 0;         // first group: the same of the second
+        int nfin1 = 0;         // the same of the other group
         int npair = 0;         // merges between the groups (pair_full, pair_read phases)
-        bool owed = false;     // second group: the first has still to read what it left
+        bool owed = false;     // the other group has still to read what this one left in O_t
+        int lead = 0;          // the group that has a pair's first key tile, and merges
         for (int k = 0;; ++k) {
-            const int e = k & 1;
-            if (!mbar_wait_warp(&unit_full[e], (k >> 1) & 1, p.ctl, abort_flag)) break;
+            const int e = k % L::kUnits;
+            if (!mbar_wait_warp(&unit_full[e], (k / L::kUnits) & 1, p.ctl, abort_flag)) break;
             const PieceSlot u = read_slot(e);
             if (u.tok0 < 0) break;
             const bool pair = is_pair(u.toks);
             const int q = pair ? 0 : t;  // query tile
-            const int first = u.t0 + (pair ? t : 0), step = pair ? 2 : 1;
+            const bool leads = t == lead;
+            // QT == 1: key tiles alternate between the groups across pieces too
+            if (QT == 1) lead ^= (u.t1 - u.t0) & 1;
+            const int first = u.t0 + (pair && !leads ? 1 : 0), step = pair ? 2 : 1;
             const int end = pair ? u.t1 : piece_end(u, t, p.tile_toks, p.causal);
             // a warp with no row of the unit only keeps the barriers going
             const int tok = q * p.tile_toks + row_tok;
@@ -770,7 +840,7 @@ __global__ void __launch_bounds__(384, 1)
                         }
                     }
                 }
-                if (owed) {  // this arrival lets the next PV overwrite what was left in O_1
+                if (owed) {  // this arrival lets the next PV overwrite what was left in O_t
                     if (!mbar_wait_warp(pair_read, (npair - 1) & 1, p.ctl, abort_flag)) {
                         ok = false;
                         break;
@@ -782,8 +852,8 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             const bool had = first < end;
             const bool both = pair && u.t1 - u.t0 > 1;  // the second group has a share
-            if (t == 1 && pair) {
-                if (both) {  // its statistics for the first group, which finds O_1 in place
+            if (pair && !leads) {
+                if (both) {  // its statistics for the leading group, which finds O_t in place
                     pair_ml[row] = make_float2(m, l);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(pair_full);
@@ -791,6 +861,7 @@ __global__ void __launch_bounds__(384, 1)
                     ++nfin;
                     owed = true;
                 }
+                if (u.t0 < u.t1) ++nfin1;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&unit_empty[e]);
@@ -807,10 +878,10 @@ __global__ void __launch_bounds__(384, 1)
                     !mbar_wait_warp(&o_final[1 - t], 0, p.ctl, abort_flag))
                     break;
             }
-            float wa = 1.f, wb = 0.f;  // weights of O_0 and of the second group's O_1
+            float wa = 1.f, wb = 0.f;  // weights of this group's O and of the other's
             if (both) {
                 if (!mbar_wait_warp(pair_full, npair & 1, p.ctl, abort_flag)) break;
-                if (!mbar_wait_warp(&o_final[1], nfin1 & 1, p.ctl, abort_flag)) break;
+                if (!mbar_wait_warp(&o_final[1 - t], nfin1 & 1, p.ctl, abort_flag)) break;
                 ++npair;
                 ++nfin1;
                 const float2 o = pair_ml[row];
@@ -819,8 +890,8 @@ __global__ void __launch_bounds__(384, 1)
                 wb = ex2(o.x - mu);
                 l = l * wa + o.y * wb;
                 m = M;
-            } else if (t == 0 && !pair && piece_end(u, 1, p.tile_toks, p.causal) > u.t0) {
-                ++nfin1;  // the second group waits for its own
+            } else if (!pair && piece_end(u, 1 - t, p.tile_toks, p.causal) > u.t0) {
+                ++nfin1;  // the other group waits for its own
             }
             tc_fence_after();
             if (busy) {
@@ -846,7 +917,7 @@ __global__ void __launch_bounds__(384, 1)
                         for (int x = 0; x < 32; ++x) o[x] = 0u;
                     }
                     if (both) {
-                        tmem_ld32(tO + D + cc * 32, o1);
+                        tmem_ld32(tO + (t == 0 ? D : -D) + cc * 32, o1);  // the other's
                         tmem_wait_ld();
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
@@ -896,7 +967,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
             }
             // O has been read out (the next unit's first PV into it waits for this warp's next
-            // p_full arrival, or the second group's after pair_read)
+            // p_full arrival, or the other group's after pair_read)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {

@@ -56,6 +56,7 @@ struct PagedAttnParams {
     int rep;                         // query heads per K/V head
     int tile_toks;                   // tokens per query tile: floor(128 / rep)
     int q_box_toks;                  // tokens per Q box of the tensor map
+    int q_bufs;                      // Q buffers where a unit has one query tile: 2 up to 64 rows
     int part_rows;                   // rows of a partial result's slot
     float scale_log2;                // scale * log2(e)
     int causal;
