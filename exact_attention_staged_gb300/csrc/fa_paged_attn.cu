@@ -55,6 +55,7 @@ struct PagedLayout {
     static constexpr int kVOff = kKOff + kKSlots * kTileBytes;
     static constexpr int kBarOff = kVOff + kVSlots * kTileBytes;
     static constexpr int kUnits = 4;  // unit slots: the loads run up to three units ahead
+    static_assert(kUnits >= 3, "a unit's last products are issued after the next one is known");
     // q_full[2], q_empty[2], k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2],
     // o_final[2], pair_full, pair_read, unit_full[], unit_empty[], drain
     static constexpr int kNumBars = 4 + 2 * kKSlots + 2 * kVSlots + 8 + 2 * kUnits + 1;
@@ -84,6 +85,12 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // Where units have no more than 64 rows, two of them share the Q tile: rows 64 to 127 of its boxes
 // are the second buffer.  A product's rows behind the unit's are whatever stands there, and unused.
 constexpr int kQBufBytes = 64 * 128;
+
+// Pieces of no more key tiles than this are softmaxed by the rolled-up code: what runs once or twice and
+// then makes place for other code costs its fetch.  1024 sequences of up to 500 keys take 341 us without
+// it, 356 with 2, 324 with 4 and 325 with 8; a tile of a long piece takes a quarter longer in it
+// (16 x 8k at d = 64 50.1 -> 57.3).
+constexpr int kShortPiece = 4;
 
 constexpr int kDestCluster = -2;
 constexpr unsigned kMaxCluster = 8;  // the portable limit
@@ -554,25 +561,24 @@ __global__ void __launch_bounds__(384, 1)
                                   sdesc_add(dv0, vs * L::kTileBytes), kIdescPV,
                                   accumulate ? 1u : 0u);
             };
-            auto wait_k = [&](int x) {
-                if (!mbar_wait_warp(&k_full[x % L::kKSlots], (x / L::kKSlots) & 1, p.ctl,
-                                    abort_flag))
-                    return false;
+            auto wait_ks = [&](int ks, uint32_t parity) {
+                if (!mbar_wait_warp(&k_full[ks], parity, p.ctl, abort_flag)) return false;
                 tc_fence_after();
                 return true;
             };
+            auto wait_k = [&](int x) { return wait_ks(x % L::kKSlots, (x / L::kKSlots) & 1); };
             // V tile x of the ring (key tile j) has landed; its rows from the sequence's end to
             // the end of that page become zeros (pages behind it were loaded as zeros)
-            auto wait_v = [&](int x, int j, int len) {
-                const int vs = x % L::kVSlots;
-                if (!mbar_wait_warp(&v_full[vs], (x / L::kVSlots) & 1, p.ctl, abort_flag))
-                    return false;
+            auto wait_vs = [&](int vs, uint32_t parity, int j, int len) {
+                if (!mbar_wait_warp(&v_full[vs], parity, p.ctl, abort_flag)) return false;
                 const int r0 = len - j * kPagedKeys;
                 if (r0 < kPagedKeys) {
                     const int size = 1 << p.c.page_shift;
                     const int r1 = min(kPagedKeys, (r0 + size - 1) & ~(size - 1));
                     uint8_t *tile = smem + L::kVOff + vs * L::kTileBytes;
+#pragma unroll 1
                     for (int b = 0; b < L::kBoxes; ++b)
+#pragma unroll 1
                         for (int a = r0 * 128 + lane * 16; a < r1 * 128; a += 512)
                             *reinterpret_cast<uint4 *>(tile + b * L::kBoxBytes + a) =
                                 make_uint4(0, 0, 0, 0);
@@ -580,6 +586,9 @@ __global__ void __launch_bounds__(384, 1)
                     __syncwarp();
                 }
                 return true;
+            };
+            auto wait_v = [&](int x, int j, int len) {
+                return wait_vs(x % L::kVSlots, (x / L::kVSlots) & 1, j, len);
             };
             int nq = 0;            // Q tiles used: pieces with keys
             int nt = 0;            // K and V tiles consumed
@@ -593,19 +602,26 @@ __global__ void __launch_bounds__(384, 1)
             // of tile x - 2 is issued before S of tile x, whichever piece they belong to: the next
             // piece's scores are under way while the last one's probabilities are.
             struct Tile {
-                int x, j, len;   // place in the sequence (-1: none), key tile, the sequence's end
+                int j, len;      // key tile (-1: none), the sequence's end
                 bool add, last;  // not the first, the last of its group in the piece
             };
-            Tile old = {-1, 0, 0, false, false}, mid = old;  // tiles x - 2 and x - 1
-            auto finish = [&](const Tile &w) {
-                if (w.x < 0) return true;
-                const int g = w.x & 1, vs = w.x % L::kVSlots;
-                if (!wait_v(w.x, w.j, w.len)) return false;
-                if (!mbar_wait_warp(&p_full[g], (w.x >> 1) & 1, p.ctl, abort_flag)) return false;
+            Tile old = {-1, 0, false, false}, mid = old;  // tiles x - 2 and x - 1
+            int ks = 0, vs = 0;                           // ring slots of tile x and of `old`
+            uint32_t kpar = 0, vpar = 0, ppar = 0;        // parities of their barriers, and p_full's
+            // PV of `old`, for group g
+            auto finish = [&](int g) {
+                if (old.j < 0) return true;
+                if (!wait_vs(vs, vpar, old.j, old.len)) return false;
+                if (!mbar_wait_warp(&p_full[g], ppar, p.ctl, abort_flag)) return false;
                 tc_fence_after();
-                issue_pv(g, vs, w.add);
-                if (w.last) umma_commit_el(&o_final[g]);
+                issue_pv(g, vs, old.add);
+                if (old.last) umma_commit_el(&o_final[g]);
                 umma_commit_el(&v_empty[vs]);
+                if (++vs == L::kVSlots) {
+                    vs = 0;
+                    vpar ^= 1;
+                }
+                ppar ^= g;  // the groups take turns
                 return true;
             };
             bool ok = true;
@@ -616,40 +632,44 @@ __global__ void __launch_bounds__(384, 1)
                     break;
                 }
                 const PieceSlot u = read_slot(e);
-                if (QT == 1 && (u.tok0 < 0 || u.t0 == u.t1)) {
-                    // the end, or a piece that sees nothing: the slot after next is free only when
-                    // the tiles still open are done
-                    if (!finish(old) || !finish(mid)) {
-                        ok = false;
-                        break;
-                    }
-                    old.x = mid.x = -1;
-                }
-                if (u.tok0 < 0) break;
                 if constexpr (QT == 1) {
                     const int buf = q_buf(nq);
-                    for (int j = u.t0; j < u.t1; ++j) {
-                        const int g = nt & 1, ks = nt % L::kKSlots;
-                        if (!finish(old) ||
-                            (j == u.t0 && !mbar_wait_warp(&q_full[buf], q_use(nq) & 1, p.ctl,
-                                                          abort_flag)) ||
-                            !wait_k(nt)) {
+                    // at the end, and at a piece that sees nothing, the open tiles are finished (the
+                    // slot after next is free only then)
+                    const int tiles = u.tok0 < 0 ? 0 : u.t1 - u.t0, steps = tiles > 0 ? tiles : 2;
+#pragma unroll 1
+                    for (int i = 0; i < steps; ++i) {
+                        const int g = (nt + (tiles > 0 ? 0 : i)) & 1;
+                        if (!finish(g)) {
+                            ok = false;
+                            break;
+                        }
+                        old = mid;
+                        mid.j = -1;
+                        if (tiles == 0) continue;
+                        if ((i == 0 &&
+                             !mbar_wait_warp(&q_full[buf], q_use(nq) & 1, p.ctl, abort_flag)) ||
+                            !wait_ks(ks, kpar)) {
                             ok = false;
                             break;
                         }
                         issue_s(buf * kQBufBytes, g, ks);
                         umma_commit_el(&k_empty[ks]);
-                        if (j == u.t1 - 1) umma_commit_el(&q_empty[buf]);
-                        old = mid;
-                        mid = {nt, j, u.len, j - u.t0 >= 2, j + 2 >= u.t1};
+                        if (++ks == L::kKSlots) {
+                            ks = 0;
+                            kpar ^= 1;
+                        }
+                        if (i == tiles - 1) umma_commit_el(&q_empty[buf]);
+                        mid = {u.t0 + i, u.len, i >= 2, i + 2 >= tiles};
                         ++nt;
                     }
-                    if (!ok) break;
-                    if (u.t0 < u.t1) ++nq;
+                    if (!ok || u.tok0 < 0) break;
+                    if (tiles > 0) ++nq;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&unit_empty[e]);
                     continue;
                 }
+                if (u.tok0 < 0) break;
                 if (u.t0 < u.t1) {
                     if (!mbar_wait_warp(q_full, nq & 1, p.ctl, abort_flag)) {
                         ok = false;
@@ -777,7 +797,83 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 ++scnt;
                 tc_fence_after();
-                if (busy) {
+                if (QT == 1 && !CL && busy && u.t1 - u.t0 <= kShortPiece) {
+                    // as below, in steps of 32 keys
+                    const int lim = last - j * kPagedKeys;  // columns above lim are masked
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t r[32];
+                        tmem_ld32(tS + 32 * h, r);
+                        tmem_wait_ld();
+                        const int limh = lim - 32 * h;
+                        if (limh < 31) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (c > limh) r[c] = __float_as_uint(-INFINITY);
+                        }
+                        float mx[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            mx[c] = fmaxf(fmax3(__uint_as_float(r[c]), __uint_as_float(r[4 + c]),
+                                                __uint_as_float(r[8 + c])),
+                                          fmax3(fmaxf(__uint_as_float(r[12 + c]),
+                                                      __uint_as_float(r[16 + c])),
+                                                fmaxf(__uint_as_float(r[20 + c]),
+                                                      __uint_as_float(r[24 + c])),
+                                                __uint_as_float(r[28 + c])));
+                        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    }
+                    const float m_new = fmaxf(m, top * sl2);
+                    bool rescale = false;
+                    float alpha = 1.f;
+                    if (m_new > m + 8.0f) {
+                        rescale = m != -INFINITY;
+                        if (rescale) alpha = ex2(m - m_new);
+                        l *= alpha;
+                        m = m_new;
+                    }
+                    const float mu = m == -INFINITY ? 0.f : m;  // nothing unmasked yet
+                    float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                     make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const float2 sc2 = make_float2(sl2, sl2), mu2 = make_float2(-mu, -mu);
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t r[32], pk[16];
+                        tmem_ld32(tS + 32 * h, r);
+                        tmem_wait_ld();
+                        const int limh = lim - 32 * h;
+                        if (limh < 31) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (c > limh) r[c] = __float_as_uint(-INFINITY);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float2 x = ffma2(make_float2(__uint_as_float(r[2 * c]),
+                                                               __uint_as_float(r[2 * c + 1])),
+                                                   sc2, mu2);
+                            const float2 ev = make_float2(ex2(x.x), ex2(x.y));
+                            acc[c & 3] = fadd2(acc[c & 3], ev);
+                            pk[c] = pack2<BF16>(ev.x, ev.y);
+                        }
+                        tmem_st16(tS + 16 * h, pk);  // over scores that are done with
+                    }
+                    const float2 a = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+                    l += a.x + a.y;
+                    if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+                        for (int cc = 0; cc < D / 32; ++cc) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + cc * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                            tmem_st32(tO + cc * 32, o);
+                        }
+                    }
+                } else if (busy) {
                     uint32_t r[128];
                     tmem_ld32(tS + 0, r + 0);
                     tmem_ld32(tS + 32, r + 32);
@@ -828,7 +924,7 @@ __global__ void __launch_bounds__(384, 1)
                     if (__any_sync(0xffffffffu, rescale)) {
                         // the previous PV into O_t completed before this S_t, and the next one
                         // waits for p_full, so O_t is ours to rescale
-#pragma unroll
+#pragma unroll 1
                         for (int cc = 0; cc < D / 32; ++cc) {
                             uint32_t o[32];
                             tmem_ld32(tO + cc * 32, o);
@@ -903,7 +999,9 @@ __global__ void __launch_bounds__(384, 1)
                 const int head = u.kvh * p.rep + row_head;
                 const long otok = u.tok0 + tok;
                 const int prow = q * 128 + row;
-#pragma unroll
+                // (rolled up, as what else runs once a unit: unrolled, a mixed batch took 50.0 us and
+                // not 48.8, 1024 sequences of up to 500 keys 341 and not 324)
+#pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32], o1[32];
                     if (had) {
