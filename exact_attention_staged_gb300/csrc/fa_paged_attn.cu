@@ -193,69 +193,82 @@ __device__ __forceinline__ bool find_unit(const PagedView &c, const PagedWork &w
     return found;
 }
 
-// One warp finds its CTA's stretch of the line, a lane per sequence: the first pass sums the lengths
-// and cuts the line, the second looks for the CTA's border in the running sum (up to 32 sequences
-// it still has at hand).  Rolled up so that the code is short: it runs once, from a cold
-// instruction cache.  Returns what the CTA may take and leaves `cur` at its beginning.
+// One warp finds its CTA's stretch of the line: the sequences are dealt out to the lanes in equal
+// runs (their numbers come from L1 after a run's first read; 32 at a time over the whole batch, 1024
+// sequences took 50000 cycles), the sums cut the line, and the lane with the CTA's border has its run looked
+// through by all.  Rolled up so that the code is short: it runs once, from a cold instruction cache.
+// Returns what the CTA may take and leaves `cur` at its beginning.
 __device__ __forceinline__ long find_stretch(const PagedView &c, const PagedWork &w, bool report,
                                              PagedLine &line, PagedCursor &cur) {
     const int lane = lane_id(), cta = static_cast<int>(blockIdx.x);
-    long sum = 0, begin = 0, each = 0, longest = 0;
+    const int run = (c.B - 1) / 32 + 1;
+    long length = 0, longest = 0, each = 0;
     int heads = 0;
     PagedSeq s;
     s.tok0 = s.n = s.len = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int i = 0; i < run && lane * static_cast<long>(run) + i < c.B; ++i) {
+        const int b = lane * run + i;
+        s = paged_seq(c, b);
+        if (s.bad && report) paged_report(c);
+        each = paged_head(s, w);
+        length += c.Hkv * each;
+        longest = max(longest, each);
+        heads += each > 0 ? c.Hkv : 0;
+    }
+    long total = length;
+    int all = heads;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    line.cut(total, longest, all, w, static_cast<int>(gridDim.x));
+    if (cta >= line.ctas) return 0;
+    const long begin = line.border(cta);
+    // place on the line: lengths, or units counted
+    long x = line.by_unit ? heads : length, before = 0;
+    int b0 = 0, end = 1;  // (of the runs: one step)
 #pragma unroll 1
-        for (int b0 = 0; b0 < c.B; b0 += 32) {
-            if (pass == 0 || c.B > 32) {
+    for (bool runs = run > 1;; runs = false) {  // over the runs, then over the sequences of one
+#pragma unroll 1
+        for (; b0 < end; b0 += 32) {
+            if (!runs && run > 1) {
                 each = 0;
-                if (b0 + lane < c.B) {
+                if (b0 + lane < end) {
                     s = paged_seq(c, b0 + lane);
-                    if (s.bad && report) paged_report(c);
                     each = paged_head(s, w);
                 }
+                x = c.Hkv * (line.by_unit ? (each > 0 ? 1 : 0) : each);
             }
-            // place on the line: lengths, or units counted
-            const long step = pass == 1 && line.by_unit ? (each > 0 ? 1 : 0) : each;
-            const long x = c.Hkv * step;
             long upto = x;  // inclusive
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long y = __shfl_up_sync(0xffffffffu, upto, o);
                 if (lane >= o) upto += y;
             }
-            if (pass == 1) {
-                const unsigned past = __ballot_sync(0xffffffffu, sum + upto > begin);
-                if (past != 0) {
-                    const int at = __ffs(static_cast<int>(past)) - 1;
-                    const long pos = begin - sum - __shfl_sync(0xffffffffu, upto - x, at);
-                    s.tok0 = __shfl_sync(0xffffffffu, s.tok0, at);
-                    s.n = __shfl_sync(0xffffffffu, s.n, at);
-                    s.len = __shfl_sync(0xffffffffu, s.len, at);
-                    cur.start(c, w, b0 + at, s, __shfl_sync(0xffffffffu, step, at), pos);
-                    return line.by_unit ? __shfl_sync(0xffffffffu, each, at)
-                                        : line.border(cta + 1) - begin;
-                }
-            } else {
-                longest = max(longest, each);
-                heads += each > 0 ? c.Hkv : 0;
+            const unsigned past = __ballot_sync(0xffffffffu, before + upto > begin);
+            if (past == 0) {
+                before += __shfl_sync(0xffffffffu, upto, 31);
+                continue;
             }
-            sum += __shfl_sync(0xffffffffu, upto, 31);
-        }
-        if (pass == 0) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-                heads += __shfl_xor_sync(0xffffffffu, heads, o);
+            const int at = __ffs(static_cast<int>(past)) - 1;
+            before += __shfl_sync(0xffffffffu, upto - x, at);
+            if (runs) {
+                b0 = at * run;
+                end = min(b0 + run, c.B);
+                break;
             }
-            line.cut(sum, longest, heads, w, static_cast<int>(gridDim.x));
-            if (cta >= line.ctas) break;
-            begin = line.border(cta);
-            sum = 0;
+            s.tok0 = __shfl_sync(0xffffffffu, s.tok0, at);
+            s.n = __shfl_sync(0xffffffffu, s.n, at);
+            s.len = __shfl_sync(0xffffffffu, s.len, at);
+            each = __shfl_sync(0xffffffffu, each, at);
+            cur.start(c, w, b0 + at, s, line.by_unit ? 1 : each, begin - before);
+            return line.by_unit ? each : line.border(cta + 1) - begin;
         }
+        if (!runs) return 0;  // (the border lies in one of them)
     }
-    return 0;
 }
 
 // Page ids of a piece's key tiles for one load warp: 32 at a time in the lanes, the next 32 read
