@@ -11,15 +11,17 @@
 // K/V tile (256 rows per tile read from L2, as in the forward).  A unit of no more tokens than one
 // tile (single tokens, drafted ones) gives both groups the same query tile and alternate key
 // tiles: the chain from a score tile to its probabilities takes longer than HBM needs to bring the
-// next tile, and two of them in flight hide it.  At the end the second group's statistics and
-// accumulator (the same tensor-memory lanes) are merged into the first's.
+// next tile, and two of them in flight hide it.  At the end one group's statistics and accumulator
+// (the same tensor-memory lanes) are merged into those of the other, which had the first tile.  Where no unit
+// has two query tiles the groups go on taking turns from unit to unit and a unit's first scores are
+// issued before the last one's products: 1024 sequences of up to 500 keys 465 -> 399 us.
 //
 // Keys.  A tile is 128 positions, whatever the page size: its pages are loaded by one TMA box each
 // into their rows of the 128-byte-swizzled tile (a page of 8 rows or more starts on a swizzle
-// atom); pages behind the sequence's end are loaded from an index outside the pool, which TMA
-// fills with zeros.  Scores behind the end are masked, and V's rows between the end and the end of
-// its page are zeroed in shared memory before the product, so that whatever the cache holds there
-// (NaN included) meets a probability of zero as a zero.  K and V have a ring and a load warp each:
+// atom).  Scores behind the sequence's end are masked, whatever K's rows hold there.  V's pages behind the
+// end are loaded from an index outside the pool, which TMA fills with zeros, and its rows between
+// the end and the end of its page are zeroed in shared memory before the product, so that whatever
+// the cache holds there (NaN included) meets a probability of zero as a zero.  K and V have a ring and a load warp each:
 // a page of 16 rows is a box of 2 KB, and one warp alone issued them no faster than 5.6 TB/s.
 //
 // Work.  paged.cuh cuts the line of all units' key tiles into one equal stretch per CTA, on the
@@ -31,6 +33,10 @@
 // all clusters fit the chip at once, a cluster of up to eight CTAs takes a unit, each CTA an equal
 // share of its key tiles, and the partial results are merged through distributed shared memory in
 // the same launch, with no workspace.
+//
+// Code.  The loops over key tiles are unrolled, what runs once or a few times a unit is rolled up: with
+// short sequences every part of the kernel runs from a cold instruction cache, and fetching it was
+// most of the time (1024 sequences of up to 500 keys 399 -> 326 us, of up to 100 195 -> 150).
 //
 // Warps: 0 walks the units and loads Q and K, 2 loads V, 1 issues the MMAs, 4..7 and 8..11 are the
 // softmax groups.  MMA order per step: PV_0 of the step before, S_0, PV_1, S_1, as in the forward.
@@ -88,7 +94,7 @@ constexpr int kQBufBytes = 64 * 128;
 
 // Pieces of no more key tiles than this are softmaxed by the rolled-up code: what runs once or twice and
 // then makes place for other code costs its fetch.  1024 sequences of up to 500 keys take 341 us without
-// it, 356 with 2, 324 with 4 and 325 with 8; a tile of a long piece takes a quarter longer in it
+// it, 324 with 4 and 325 with 8; a tile of a long piece takes a quarter longer in it
 // (16 x 8k at d = 64 50.1 -> 57.3).
 constexpr int kShortPiece = 4;
 
@@ -288,6 +294,10 @@ struct PageWindow {
         base = ((u.t0 * kPagedKeys) >> c.page_shift) & ~31;
         now = read(c, base);
         next = read(c, base + 32);
+    }
+    // pages of the sequence from tile j on
+    __device__ __forceinline__ int left(const PagedView &c, int j) const {
+        return have - ((j * kPagedKeys) >> c.page_shift);
     }
     __device__ __forceinline__ int tile(const PagedView &c, int j, int boxes) {
         const int page0 = (j * kPagedKeys) >> c.page_shift;
@@ -511,9 +521,12 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     // the tile's pages into its slot: one lane per page (test hook: not the first K)
                     const bool skip = p.ctl.fault_mode == 4 && !is_v && n == 0;
-                    if (lane == 0 && !skip) mbar_arrive_expect_tx(&full[slot], L::kTileBytes);
+                    // K's rows behind the sequence's pages stay what they are: their scores are masked
+                    const int used = is_v ? boxes : min(boxes, win.left(p.c, j));
+                    if (lane == 0 && !skip)
+                        mbar_arrive_expect_tx(&full[slot], used * box_rows * 128 * L::kBoxes);
                     __syncwarp();
-                    if (lane < boxes && !skip) {
+                    if (lane < used && !skip) {
                         const int y = (j * kPagedKeys) & ((1 << p.c.page_shift) - 1);
                         uint8_t *dst = ring + slot * L::kTileBytes + lane * box_rows * 128;
                         for (int b = 0; b < L::kBoxes; ++b)
