@@ -599,3 +599,15 @@ def test_many_sequences(cuda_lib):
         o, lse = attend(cuda_lib, t, causal=causal)
         check(t, o, lse, d ** -0.5, causal, "many")
     assert cuda_lib.sync_status() == 0
+
+
+@pytest.mark.parametrize("H,Hkv,d,dtype", [(4, 2, 128, BF), (6, 3, 64, HF)])
+def test_short_sequences_between_ones_that_see_nothing(cuda_lib, H, Hkv, d, dtype):
+    """Units of one to three key tiles and units without any, many to a CTA, in every order."""
+    g = torch.Generator().manual_seed(75)
+    lens = torch.randint(-150, 300, (400,), generator=g).clamp(min=0).tolist()
+    t = Batch([(1 + i % 3, L) for i, L in enumerate(lens)], H, Hkv, d, dtype, 16, seed=76, room=9000)
+    for causal in (True, False):
+        o, lse = attend(cuda_lib, t, causal=causal)
+        assert cuda_lib.sync_status() == 0
+        check(t, o, lse, d ** -0.5, causal, "short")
