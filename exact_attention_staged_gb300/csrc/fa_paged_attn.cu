@@ -49,7 +49,7 @@ namespace fa {
 namespace {
 
 // QT: query tiles that a unit may have (1: no sequence brings more tokens than one tile holds).
-template <int D, int QT>
+template <int D, int QT, bool CL>
 struct PagedLayout {
     static constexpr int kTileBytes = 128 * D * 2;  // one 128 x d tile of 16-bit values
     static constexpr int kBoxes = D / 64;
@@ -61,10 +61,17 @@ struct PagedLayout {
     static constexpr int kVOff = kKOff + kKSlots * kTileBytes;
     static constexpr int kBarOff = kVOff + kVSlots * kTileBytes;
     static constexpr int kUnits = 4;  // unit slots: the loads run up to three units ahead
-    static_assert(kUnits >= 3, "a unit's last products are issued after the next one is known");
-    // q_full[2], q_empty[2], k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2],
+    // Score buffers in tensor memory, 128 columns each, before O_0 and O_1.  A third one, where it
+    // fits, has a group's next scores ready before its last product is issued.  Clusters, bound by the
+    // chain of their few tiles, gain (8 x 4 tokens 10.05 -> 9.7 us, 30 x 2 12.2 -> 11.9); the line, whose
+    // units end a tile later for it, lost (64 tokens over up to 2000 keys 30.8 -> 31.4).
+    static constexpr int kBufs = D == 64 && QT == 1 && CL ? 3 : 2;
+    static_assert(kUnits > kBufs, "a unit's last products wait for the units after it");
+    static constexpr int kOCol = kBufs * 128;
+    // q_full[2], q_empty[2], k_full[], k_empty[], v_full[], v_empty[], s_full[], p_full[],
     // o_final[2], pair_full, pair_read, unit_full[], unit_empty[], drain
-    static constexpr int kNumBars = 4 + 2 * kKSlots + 2 * kVSlots + 8 + 2 * kUnits + 1;
+    static constexpr int kNumBars =
+        4 + 2 * kKSlots + 2 * kVSlots + 2 * kBufs + 4 + 2 * kUnits + 1;
     static constexpr int kUnitOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;
     static constexpr int kMiscOff = kUnitOff + kUnits * 32;  // TMEM base, abort flag
     static constexpr int kPairOff = kMiscOff + 8;       // the second group's (m, l): float2[128]
@@ -75,7 +82,8 @@ struct PagedLayout {
     static constexpr int kRowBytes = (D + 4) * 4;
     static_assert(QT * 128 * kRowBytes <= (kKSlots + kVSlots) * kTileBytes, "O~ over the rings");
     static constexpr int kThreads = 384;
-    static constexpr uint32_t kTmemCols = 512;  // S_0, S_1 (2 x 128), O_0, O_1 (2 x d)
+    static constexpr uint32_t kTmemCols = 512;  // the score buffers, O_0, O_1 (2 x d)
+    static_assert(kOCol + 2 * D <= 512, "tensor memory");
     static_assert(kAlloc <= 232448, "shared memory per CTA");
 };
 
@@ -320,7 +328,7 @@ struct PageWindow {
 template <int D, bool BF16, int QT, bool CL>
 __global__ void __launch_bounds__(384, 1)
     fa_paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedAttnParams p) {
-    using L = PagedLayout<D, QT>;
+    using L = PagedLayout<D, QT, CL>;
     constexpr uint32_t kIdescS = idesc_f16(128, 128, BF16, false);
     constexpr uint32_t kIdescPV = idesc_f16(128, D, BF16, true);
     extern __shared__ uint8_t smem_raw[];
@@ -329,9 +337,9 @@ __global__ void __launch_bounds__(384, 1)
     uint64_t *q_full = bars, *q_empty = bars + 2;  // [2]: per Q buffer
     uint64_t *k_full = bars + 4, *k_empty = k_full + L::kKSlots;
     uint64_t *v_full = k_empty + L::kKSlots, *v_empty = v_full + L::kVSlots;
-    uint64_t *s_full = v_empty + L::kVSlots;  // [2]: per softmax group, as the next three
-    uint64_t *p_full = s_full + 2;
-    uint64_t *o_final = p_full + 2;
+    uint64_t *s_full = v_empty + L::kVSlots;  // per score buffer, as the next
+    uint64_t *p_full = s_full + L::kBufs;
+    uint64_t *o_final = p_full + L::kBufs;  // [2]: per softmax group
     uint64_t *pair_full = o_final + 2, *pair_read = pair_full + 1;
     uint64_t *unit_full = pair_read + 1, *unit_empty = unit_full + L::kUnits;
     uint64_t *drain = unit_empty + L::kUnits;
@@ -354,9 +362,11 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
+            mbar_init(&o_final[i], 1);
+        }
+        for (int i = 0; i < L::kBufs; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);  // one arrival per softmax warp of a group
-            mbar_init(&o_final[i], 1);
         }
         for (int i = 0; i < L::kUnits; ++i) {
             mbar_init(&unit_full[i], 1);
@@ -573,17 +583,17 @@ __global__ void __launch_bounds__(384, 1)
             const SDesc dk0 = sdesc_make(smem_u32(smem + L::kKOff), 16, 1024);   // K: K-major
             const SDesc dv0 = sdesc_make(smem_u32(smem + L::kVOff), L::kBoxBytes,
                                          1024);                                   // V: MN-major
-            auto issue_s = [&](int q, int t, int ks) {  // q: where Q starts
+            auto issue_s = [&](int q, int buf, int ks) {  // q: where Q starts
                 const SDesc a = sdesc_add(dq0, q);
                 const SDesc b = sdesc_add(dk0, ks * L::kTileBytes);
                 if constexpr (D == 128)
-                    mma_ss_chain_k128(tmem + t * 128, a, b, kIdescS, 0u);
+                    mma_ss_chain_k128(tmem + buf * 128, a, b, kIdescS, 0u);
                 else
-                    mma_ss_chain_k64(tmem + t * 128, a, b, kIdescS, 0u);
-                umma_commit_el(&s_full[t]);
+                    mma_ss_chain_k64(tmem + buf * 128, a, b, kIdescS, 0u);
+                umma_commit_el(&s_full[buf]);
             };
-            auto issue_pv = [&](int t, int vs, bool accumulate) {
-                mma_ts_chain_k128(tmem + 256 + t * D, tmem + t * 128,
+            auto issue_pv = [&](int t, int buf, int vs, bool accumulate) {
+                mma_ts_chain_k128(tmem + L::kOCol + t * D, tmem + buf * 128,
                                   sdesc_add(dv0, vs * L::kTileBytes), kIdescPV,
                                   accumulate ? 1u : 0u);
             };
@@ -624,30 +634,39 @@ __global__ void __launch_bounds__(384, 1)
                 tc_fence_after();
                 return true;
             };
-            // QT == 1: the key tiles of all pieces are one sequence, tile x for group x & 1, and PV
-            // of tile x - 2 is issued before S of tile x, whichever piece they belong to: the next
-            // piece's scores are under way while the last one's probabilities are.
+            // QT == 1: the key tiles of all pieces are one sequence, tile x for group x & 1 and score
+            // buffer x mod kBufs, and PV of tile x - kBufs is issued before S of tile x, whichever
+            // piece they belong to: the next piece's scores are under way while the last one's
+            // probabilities are.
             struct Tile {
                 int j, len;      // key tile (-1: none), the sequence's end
                 bool add, last;  // not the first, the last of its group in the piece
             };
-            Tile old = {-1, 0, false, false}, mid = old;  // tiles x - 2 and x - 1
-            int ks = 0, vs = 0;                           // ring slots of tile x and of `old`
-            uint32_t kpar = 0, vpar = 0, ppar = 0;        // parities of their barriers, and p_full's
-            // PV of `old`, for group g
-            auto finish = [&](int g) {
-                if (old.j < 0) return true;
-                if (!wait_vs(vs, vpar, old.j, old.len)) return false;
-                if (!mbar_wait_warp(&p_full[g], ppar, p.ctl, abort_flag)) return false;
-                tc_fence_after();
-                issue_pv(g, vs, old.add);
-                if (old.last) umma_commit_el(&o_final[g]);
-                umma_commit_el(&v_empty[vs]);
-                if (++vs == L::kVSlots) {
-                    vs = 0;
-                    vpar ^= 1;
+            Tile open[L::kBufs];  // tiles x - kBufs .. x - 1
+#pragma unroll
+            for (int i = 0; i < L::kBufs; ++i) open[i].j = -1;
+            int nf = 0;                   // tiles finished: the number of open[0]
+            int ks = 0, vs = 0;           // ring slots of tile x and of open[0]
+            uint32_t kpar = 0, vpar = 0;  // parities of their barriers
+            auto finish = [&]() {  // PV of open[0]
+                if (open[0].j >= 0) {
+                    const int g = nf & 1, buf = nf % L::kBufs;
+                    if (!wait_vs(vs, vpar, open[0].j, open[0].len)) return false;
+                    if (!mbar_wait_warp(&p_full[buf], (nf / L::kBufs) & 1, p.ctl, abort_flag))
+                        return false;
+                    tc_fence_after();
+                    issue_pv(g, buf, vs, open[0].add);
+                    if (open[0].last) umma_commit_el(&o_final[g]);
+                    umma_commit_el(&v_empty[vs]);
+                    if (++vs == L::kVSlots) {
+                        vs = 0;
+                        vpar ^= 1;
+                    }
+                    ++nf;
                 }
-                ppar ^= g;  // the groups take turns
+#pragma unroll
+                for (int i = 1; i < L::kBufs; ++i) open[i - 1] = open[i];
+                open[L::kBufs - 1].j = -1;
                 return true;
             };
             bool ok = true;
@@ -662,16 +681,14 @@ __global__ void __launch_bounds__(384, 1)
                     const int buf = q_buf(nq);
                     // at the end, and at a piece that sees nothing, the open tiles are finished (the
                     // slot after next is free only then)
-                    const int tiles = u.tok0 < 0 ? 0 : u.t1 - u.t0, steps = tiles > 0 ? tiles : 2;
+                    const int tiles = u.tok0 < 0 ? 0 : u.t1 - u.t0;
+                    const int steps = tiles > 0 ? tiles : L::kBufs;
 #pragma unroll 1
                     for (int i = 0; i < steps; ++i) {
-                        const int g = (nt + (tiles > 0 ? 0 : i)) & 1;
-                        if (!finish(g)) {
+                        if (!finish()) {
                             ok = false;
                             break;
                         }
-                        old = mid;
-                        mid.j = -1;
                         if (tiles == 0) continue;
                         if ((i == 0 &&
                              !mbar_wait_warp(&q_full[buf], q_use(nq) & 1, p.ctl, abort_flag)) ||
@@ -679,14 +696,14 @@ __global__ void __launch_bounds__(384, 1)
                             ok = false;
                             break;
                         }
-                        issue_s(buf * kQBufBytes, g, ks);
+                        issue_s(buf * kQBufBytes, nt % L::kBufs, ks);
                         umma_commit_el(&k_empty[ks]);
                         if (++ks == L::kKSlots) {
                             ks = 0;
                             kpar ^= 1;
                         }
                         if (i == tiles - 1) umma_commit_el(&q_empty[buf]);
-                        mid = {u.t0 + i, u.len, i >= 2, i + 2 >= tiles};
+                        open[L::kBufs - 1] = {u.t0 + i, u.len, i >= 2, i + 2 >= tiles};
                         ++nt;
                     }
                     if (!ok || u.tok0 < 0) break;
@@ -717,7 +734,7 @@ __global__ void __launch_bounds__(384, 1)
                                     ok = false;
                                     break;
                                 }
-                                issue_pv(t, (n0 + jp) % L::kVSlots, pcnt[t] > p0[t]);
+                                issue_pv(t, t, (n0 + jp) % L::kVSlots, pcnt[t] > p0[t]);
                                 ++pcnt[t];
                                 if (jp + 2 >= u.t1) umma_commit_el(&o_final[t]);
                                 umma_commit_el(&v_empty[(n0 + jp) % L::kVSlots]);
@@ -756,7 +773,7 @@ __global__ void __launch_bounds__(384, 1)
                                     ok = false;
                                     break;
                                 }
-                                issue_pv(t, vs, pcnt[t] > p0[t]);
+                                issue_pv(t, t, vs, pcnt[t] > p0[t]);
                                 ++pcnt[t];
                                 if (j == end[t]) umma_commit_el(&o_final[t]);
                             }
@@ -787,8 +804,7 @@ __global__ void __launch_bounds__(384, 1)
         const int row = quad * 32 + lane;
         const int row_tok = row / p.rep, row_head = row % p.rep;  // within a query tile
         const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t tS = tmem + lane_base + t * 128;
-        const uint32_t tO = tmem + lane_base + 256 + t * D;
+        const uint32_t tO = tmem + lane_base + L::kOCol + t * D;
         const float sl2 = p.scale_log2;
         int scnt = 0;          // score tiles consumed by this group
         int nfin = 0;          // pieces in which this group had products (o_final phases)
@@ -817,12 +833,22 @@ __global__ void __launch_bounds__(384, 1)
             float l = 0.f;        // running sum of exp2(score - m)
             bool ok = true;
             for (int j = first; j < end; j += step) {
-                if (!mbar_wait_warp(&s_full[t], scnt & 1, p.ctl, abort_flag)) {
+                const int x = 2 * scnt + t, buf = L::kBufs == 2 ? t : x % L::kBufs;
+                const uint32_t tS = tmem + lane_base + buf * 128;
+                if (!mbar_wait_warp(&s_full[buf], (x / L::kBufs) & 1, p.ctl, abort_flag)) {
                     ok = false;
                     break;
                 }
                 ++scnt;
                 tc_fence_after();
+                // PV of this group's last tile, into O_t, is complete when its V slot is empty again
+                auto o_ready = [&]() {
+                    const int y = x - 2;
+                    const bool in_time = mbar_wait_warp(&v_empty[y % L::kVSlots],
+                                                        (y / L::kVSlots) & 1, p.ctl, abort_flag);
+                    tc_fence_after();
+                    return in_time;
+                };
                 if (QT == 1 && !CL && busy && u.t1 - u.t0 <= kShortPiece) {
                     // as below, in steps of 32 keys
                     const int lim = last - j * kPagedKeys;  // columns above lim are masked
@@ -948,8 +974,12 @@ __global__ void __launch_bounds__(384, 1)
                     const float2 a = fadd2(a01, a23);
                     l += a.x + a.y;
                     if (__any_sync(0xffffffffu, rescale)) {
-                        // the previous PV into O_t completed before this S_t, and the next one
-                        // waits for p_full, so O_t is ours to rescale
+                        // the previous PV into O_t is complete (with two score buffers it was before
+                        // this S_t), and the next one waits for p_full, so O_t is ours to rescale
+                        if (L::kBufs == 3 && !o_ready()) {
+                            ok = false;
+                            break;
+                        }
 #pragma unroll 1
                         for (int cc = 0; cc < D / 32; ++cc) {
                             uint32_t o[32];
@@ -969,7 +999,7 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     owed = false;
                 }
-                mbar_arrive_warp_after_st(&p_full[t]);
+                mbar_arrive_warp_after_st(&p_full[buf]);
             }
             if (!ok) break;
             const bool had = first < end;
@@ -1245,7 +1275,7 @@ cudaError_t allow_smem(std::atomic<unsigned long long> &ready, const void *kerne
 
 template <int D, bool BF16, int QT>
 cudaError_t launch_line(const PagedMaps &m, const PagedAttnParams &p, cudaStream_t stream) {
-    using L = PagedLayout<D, QT>;
+    using L = PagedLayout<D, QT, false>;
     auto kern = fa_paged_attn_kernel<D, BF16, QT, false>;
     static std::atomic<unsigned long long> ready{0};
     cudaError_t e = allow_smem(ready, reinterpret_cast<const void *>(kern), L::kAlloc, p.device);
@@ -1264,7 +1294,7 @@ cudaError_t launch_line(const PagedMaps &m, const PagedAttnParams &p, cudaStream
 template <int D, bool BF16, int QT>
 cudaError_t launch_clusters(const PagedMaps &m, const PagedAttnParams &p, PagedClusters cl,
                             cudaStream_t stream) {
-    using L = PagedLayout<D, QT>;
+    using L = PagedLayout<D, QT, true>;
     auto kern = fa_paged_attn_kernel<D, BF16, QT, true>;
     static std::atomic<unsigned long long> ready{0};
     const cudaError_t e = allow_smem(ready, reinterpret_cast<const void *>(kern), L::kAlloc, p.device);
