@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) fa_paged_append_kernel(c
             const int i = t - s.tok0;
             if (s.bad && lane_id() == 0) paged_report(c);
             if (i < 0 || i >= s.n) return;
-            pos = s.len - s.n + i;
+            pos = s.ctx + i;
             // before the sequence a token has no row in the cache; a length or offset out of range
             // was clamped, so the rows that it would name are not the sequence's
             skip = pos < 0 || s.bad;

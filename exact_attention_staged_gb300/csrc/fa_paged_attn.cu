@@ -173,7 +173,7 @@ __device__ __forceinline__ bool find_unit(const PagedView &c, const PagedWork &w
 #pragma unroll 1
     for (int b0 = 0; b0 < c.B; b0 += 32) {
         PagedSeq s;
-        s.tok0 = s.n = s.len = 0;
+        s.tok0 = s.n = s.len = s.ctx = 0;
         if (b0 + lane < c.B) {
             s = paged_seq(c, b0 + lane);
             if (s.bad && report) paged_report(c);
@@ -199,7 +199,8 @@ __device__ __forceinline__ bool find_unit(const PagedView &c, const PagedWork &w
             const int i0 = (pos - own.kvh * units) * w.unit_toks;
             own.tok0 = tok0 + i0;
             own.toks = min(n - i0, w.unit_toks);
-            own.last0 = w.causal ? own.len - n + i0 : own.len - 1;
+            const int ctx = __shfl_sync(0xffffffffu, s.ctx, at);
+            own.last0 = w.causal ? ctx + i0 : own.len - 1;
             if (!report) return true;  // block 0 goes on to look at every sequence
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
@@ -219,7 +220,7 @@ __device__ __forceinline__ long find_stretch(const PagedView &c, const PagedWork
     long length = 0, longest = 0, each = 0;
     int heads = 0;
     PagedSeq s;
-    s.tok0 = s.n = s.len = 0;
+    s.tok0 = s.n = s.len = s.ctx = 0;
 #pragma unroll 1
     for (int i = 0; i < run && lane * static_cast<long>(run) + i < c.B; ++i) {
         const int b = lane * run + i;
@@ -277,6 +278,7 @@ __device__ __forceinline__ long find_stretch(const PagedView &c, const PagedWork
             s.tok0 = __shfl_sync(0xffffffffu, s.tok0, at);
             s.n = __shfl_sync(0xffffffffu, s.n, at);
             s.len = __shfl_sync(0xffffffffu, s.len, at);
+            s.ctx = __shfl_sync(0xffffffffu, s.ctx, at);
             each = __shfl_sync(0xffffffffu, each, at);
             cur.start(c, w, b0 + at, s, line.by_unit ? 1 : each, begin - before);
             return line.by_unit ? each : line.border(cta + 1) - begin;

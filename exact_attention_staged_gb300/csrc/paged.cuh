@@ -10,8 +10,9 @@ namespace fa {
 // One sequence's share of the batch.  `bad`: a stored value was out of range (and was clamped).
 struct PagedSeq {
     int tok0;  // its first token in the batch
-    int n;     // its new tokens
+    int n;     // its new tokens, no more than max_q
     int len;   // its cached positions, the new tokens included
+    int ctx;   // place of its first new token (below 0: before the sequence), whatever max_q cuts off
     bool bad;
 };
 
@@ -28,6 +29,7 @@ __host__ __device__ inline PagedSeq paged_seq_of(int first, int next, int len, i
     const long end = clamp(next, s.tok0, T);
     s.n = static_cast<int>(clamp(end - s.tok0, 0, max_q));
     s.len = static_cast<int>(clamp(len, 0, cap));
+    s.ctx = s.len - static_cast<int>(end - s.tok0);
     return s;
 }
 
@@ -81,15 +83,15 @@ __host__ __device__ inline int paged_tile_cost(const PagedWork &w, int toks) {
 }
 // Keys that the first `toks` new tokens of a sequence see.
 __host__ __device__ inline int paged_keys(const PagedSeq &s, const PagedWork &w, int toks) {
-    const int end = w.causal ? s.len - s.n + toks : s.len;
+    const int end = w.causal ? s.ctx + toks : s.len;
     return end > 0 ? end : 0;
 }
 
 // Length on the line of the first m units of one K/V head, all but the last of which are whole.
 __host__ __device__ inline long paged_prefix(const PagedSeq &s, const PagedWork &w, long m) {
     long keys;
-    if (w.causal) {  // unit j sees len - n + (j + 1) unit_toks keys, at least a weight of 1
-        const long ctx = static_cast<long>(s.len) - s.n;
+    if (w.causal) {  // unit j sees ctx + (j + 1) unit_toks keys, at least a weight of 1
+        const long ctx = s.ctx;
         long none = 0;
         if (ctx < 0) {
             none = -ctx / w.unit_toks;
@@ -192,7 +194,7 @@ struct PagedCursor {
         pos -= g * each;
         i = 0;
         if (units > 1) {  // the last unit whose prefix is <= pos; pos = a i^2 + f i while ctx >= 0
-            const long ctx = static_cast<long>(s.len) - s.n;
+            const long ctx = s.ctx;
             const float cost = static_cast<float>(paged_tile_cost(w, w.unit_toks));
             const float a = w.causal ? 0.5f * cost * w.unit_toks : 0.f;
             const float f = w.unit_cost + cost * (w.causal ? ctx + 0.5f * w.unit_toks
@@ -228,7 +230,7 @@ struct PagedCursor {
         p.toks = s.n - i0 < w.unit_toks ? s.n - i0 : w.unit_toks;
         p.kvh = g;
         p.b = b;
-        p.last0 = w.causal ? s.len - s.n + i0 : s.len - 1;
+        p.last0 = w.causal ? s.ctx + i0 : s.len - 1;
         p.len = s.len;
         const int cost = paged_tile_cost(w, p.toks);
         const long keys = paged_line_keys(paged_keys(s, w, i0 + p.toks), units);

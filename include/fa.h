@@ -345,7 +345,9 @@ int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, vo
  *               and row of k_pages and v_pages; NULL for dense tensors; limits as for the outputs
  *               in fa_rope.  k_pages and v_pages order heads and rows the same way.
  *   max_q     : no sequence brings more new tokens than this (T is always safe, the true maximum is
- *               faster); tokens beyond it are left out and reported as FA_ERR_INDEX.
+ *               faster); of a sequence that does, the tokens beyond the first max_q are left out
+ *               (their rows of o and lse stay as they were) and FA_ERR_INDEX is reported; the first
+ *               max_q see the keys that they see without the bound.
  *   causal    : != 0: row i of sequence b sees keys j <= kv_len[b] - n + i; 0: all kv_len[b] keys.
  *               A row that sees no key gets O = 0 and LSE = -inf.  Whatever the cache holds behind
  *               kv_len[b] (NaN included) has no influence.

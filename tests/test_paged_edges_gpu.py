@@ -1,0 +1,41 @@
+"""Paged cache: what the bounds of a call, its index arrays and values that are not finite may and may
+not change.  Attention is compared with the fp64 definition under the bounds that test_paged_gpu
+derives; what has to be left alone, or is promised exactly, is compared bit by bit."""
+import copy
+
+import pytest
+import torch
+
+from test_paged_gpu import BF, DEV, HF, Batch, attend, check
+
+pytestmark = pytest.mark.gpu
+
+
+# tokens beyond max_q are left out; those before them stay where they stand in the sequence
+@pytest.mark.parametrize("room", [0, 9000])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("seqs,max_q,H,Hkv,d,dtype", [
+    ([(5, 50), (1, 300)], 2, 4, 2, 64, BF),
+    ([(2, 129), (4, 130), (3, 700)], 1, 8, 2, 128, HF),
+    ([(40, 1000), (9, 20)], 30, 6, 2, 64, HF),
+    ([(300, 700), (5, 64), (1, 90)], 140, 4, 2, 128, BF),
+    ([(20, 12), (3, 2000)], 11, 4, 1, 64, BF),  # some of the first tokens see nothing
+])
+def test_tokens_beyond_max_q_leave_the_others_right(cuda_lib, seqs, max_q, H, Hkv, d, dtype, causal, room):
+    t = Batch(seqs, H, Hkv, d, dtype, 16, seed=80 + max_q, room=room)
+    out = torch.full((t.T, H, d), 3.0, dtype=dtype, device=DEV)
+    lse = torch.full((t.T, H), 3.0, device=DEV)
+    attend(cuda_lib, t, causal=causal, max_q=max_q, out=out, lse=lse)
+    assert cuda_lib.sync_status() == cuda_lib.FA_ERR_INDEX
+    kept = copy.copy(t)
+    kept.seqs = [(min(n, max_q), L - n + min(n, max_q) if causal else L) for n, L in seqs]
+    if causal:  # (a sequence that ends before its kept tokens: they see nothing, checked below)
+        kept.seqs = [(n, L) if L > 0 else (0, 0) for n, L in kept.seqs]
+    check(kept, out, lse, d ** -0.5, causal, "kept")
+    for b, (n, L) in enumerate(seqs):
+        at = int(t.start[b])
+        if causal and L - n < 0:
+            none = slice(at, at + min(n - L, max_q))
+            assert bool((out[none] == 0).all()) and bool(torch.isneginf(lse[none]).all())
+        left = slice(at + min(n, max_q), at + n)
+        assert bool((out[left] == 3.0).all()) and bool((lse[left] == 3.0).all())
