@@ -1094,11 +1094,14 @@ __global__ void __launch_bounds__(384, 1)
                             reinterpret_cast<T *>(p.o) + otok * p.o_t + head * p.o_h + cc * 32);
 #pragma unroll
                         for (int q4 = 0; q4 < 4; ++q4) {
+                            // a row that sees no key is zero, though a zero probability met the
+                            // values that the unit's other rows see and one of them is not finite
                             uint32_t w[4];
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                w[x] = pack2<BF16>(__uint_as_float(o[8 * q4 + 2 * x]),
-                                                   __uint_as_float(o[8 * q4 + 2 * x + 1]));
+                                w[x] = l == 0.f ? 0u
+                                                : pack2<BF16>(__uint_as_float(o[8 * q4 + 2 * x]),
+                                                              __uint_as_float(o[8 * q4 + 2 * x + 1]));
                             dst[q4] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     } else {

@@ -39,3 +39,26 @@ def test_tokens_beyond_max_q_leave_the_others_right(cuda_lib, seqs, max_q, H, Hk
             assert bool((out[none] == 0).all()) and bool(torch.isneginf(lse[none]).all())
         left = slice(at + min(n, max_q), at + n)
         assert bool((out[left] == 3.0).all()) and bool((lse[left] == 3.0).all())
+
+
+@pytest.mark.parametrize("room", [0, 9000])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("seqs,H,Hkv,d,dtype", [
+    ([(6, 3), (1, 50)], 4, 2, 64, BF),
+    ([(150, 20), (2, 1)], 4, 1, 128, HF),
+    ([(300, 290), (1, 40)], 4, 2, 128, BF),
+    ([(1, 700)] * 200 + [(5, 2)] * 30, 2, 1, 64, BF),
+])
+def test_rows_that_see_nothing_are_zero_whatever_others_see(cuda_lib, seqs, H, Hkv, d, dtype, value, room):
+    t = Batch(seqs, H, Hkv, d, dtype, 16, seed=90, room=room)
+    for b, (n, L) in enumerate(seqs):  # the values that the later rows of such a sequence see
+        if L < n:
+            for pos in range(L):
+                t.v[int(t.table[b, pos // 16]), :, pos % 16] = value
+    out, lse = attend(cuda_lib, t)
+    assert cuda_lib.sync_status() == 0
+    for b, (n, L) in enumerate(seqs):
+        if L < n:
+            rows = slice(int(t.start[b]), int(t.start[b]) + n - L)
+            assert bool((out[rows] == 0).all()), f"sequence {b}"
+            assert bool(torch.isneginf(lse[rows]).all()), f"sequence {b}"
