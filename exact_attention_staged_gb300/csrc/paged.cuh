@@ -276,8 +276,9 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *m
         : "memory");
 }
 
+// A wait that ran out leaves outputs undefined and a bad index does not: it keeps the status word.
 __device__ __forceinline__ void paged_report(const PagedView &c) {
-    atomicExch(c.status, kErrIndex);
+    atomicCAS(c.status, 0, kErrIndex);
 }
 
 // Sequence of token t: the b with q_start[b] <= t < q_start[b + 1], or -1 (a token before the

@@ -367,7 +367,8 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
  * Synchronises `stream`, then returns and clears the current device's status word:
  * FA_OK, FA_ERR_TIMEOUT (a kernel gave up on a pipeline wait and returned early; its outputs
  * are undefined), FA_ERR_INTERNAL (a kernel refused to run on a misaligned shared-memory base;
- * its outputs are undefined) or FA_ERR_CUDA (the stream reported an error).
+ * its outputs are undefined), FA_ERR_INDEX (a paged call met an index out of range; reported only
+ * where neither of the other two is) or FA_ERR_CUDA (the stream reported an error).
  */
 int fa_sync_status(void *stream);
 

@@ -62,3 +62,24 @@ def test_rows_that_see_nothing_are_zero_whatever_others_see(cuda_lib, seqs, H, H
             rows = slice(int(t.start[b]), int(t.start[b]) + n - L)
             assert bool((out[rows] == 0).all()), f"sequence {b}"
             assert bool(torch.isneginf(lse[rows]).all()), f"sequence {b}"
+
+
+def test_a_bad_index_does_not_hide_a_wait_that_ran_out(cuda_lib):
+    t = Batch([(1, 300), (2, 500)], 4, 2, 64, BF, 16, seed=17, poison=False)
+    q, k, v, table, lens, start = t.dev()
+    bad = table.clone()
+    bad[0, 18] = -1  # of position 299, to which the first sequence's token goes
+    new = torch.zeros(t.T, 2, 64, dtype=BF, device=DEV)
+    try:
+        cuda_lib.debug_set_wait_limit_ns(20_000_000)
+        cuda_lib.debug_set_fault(4)
+        cuda_lib.paged_attention(q, k, v, table, lens, start, max_q=2)
+        cuda_lib.paged_append(new, new, k, v, bad, lens, start)
+        assert cuda_lib.sync_status() == cuda_lib.FA_ERR_TIMEOUT
+    finally:
+        cuda_lib.debug_set_fault(0)
+        cuda_lib.debug_set_wait_limit_ns(0)
+    cuda_lib.paged_append(new, new, k, v, bad, lens, start)
+    assert cuda_lib.sync_status() == cuda_lib.FA_ERR_INDEX
+    cuda_lib.paged_append(new, new, k, v, table, lens, start)
+    assert cuda_lib.sync_status() == 0
