@@ -45,6 +45,7 @@ struct PagedAppendParams {
     const int *positions;            // [T] for the rotation, or nullptr: the places in the cache
     int rot;
     int chunks;                      // warps per token (set by the launcher)
+    unsigned blocks;                 // that move data (set by the launcher)
     float mscale;
 };
 

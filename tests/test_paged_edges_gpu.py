@@ -83,3 +83,32 @@ def test_a_bad_index_does_not_hide_a_wait_that_ran_out(cuda_lib):
     assert cuda_lib.sync_status() == cuda_lib.FA_ERR_INDEX
     cuda_lib.paged_append(new, new, k, v, table, lens, start)
     assert cuda_lib.sync_status() == 0
+
+
+@pytest.mark.parametrize("lens,start", [([20, 1 << 20, 40], [0, 3, 3, 5]), ([20, -7, 40], [0, 3, 3, 5]),
+                                        ([20, 30, 1 << 30], [0, 3, 5, 5]), ([20, 30, 40], [5, 3, 3, 3]),
+                                        ([20, 30, 40], [9, 9, 9, 9]), ([20, 30, 40], [5, 5, 5, 4])])
+def test_append_reports_bad_entries_of_sequences_without_a_token(cuda_lib, lens, start):
+    t = Batch([(3, 20), (0, 30), (2, 40)], 4, 2, 64, BF, 16, seed=41, poison=False)
+    _, k, v, table, _, _ = t.dev()
+    new = torch.zeros(5, 2, 64, dtype=BF, device=DEV)
+    cuda_lib.paged_append(new, new, k, v, table, torch.tensor(lens, dtype=torch.int32, device=DEV),
+                          torch.tensor(start, dtype=torch.int32, device=DEV))
+    assert cuda_lib.sync_status() == cuda_lib.FA_ERR_INDEX
+
+
+def test_append_reports_the_last_of_many_sequences(cuda_lib):
+    # one token, more sequences than the threads of a block, the last one's length out of range
+    B = 3000
+    k, v = (torch.zeros(4, 2, 16, 64, dtype=BF, device=DEV) for _ in range(2))
+    table = torch.zeros(B, 1, dtype=torch.int32, device=DEV)
+    lens = torch.ones(B, dtype=torch.int32, device=DEV)
+    start = torch.ones(B + 1, dtype=torch.int32, device=DEV)
+    start[0] = 0
+    new = torch.ones(1, 2, 64, dtype=BF, device=DEV)
+    cuda_lib.paged_append(new, new, k, v, table, lens, start)
+    assert cuda_lib.sync_status() == 0
+    assert bool((k[0, :, 0] == 1).all()) and float(k.float().sum()) == 2 * 64
+    lens[-1] = 17
+    cuda_lib.paged_append(new, new, k, v, table, lens, start)
+    assert cuda_lib.sync_status() == cuda_lib.FA_ERR_INDEX
