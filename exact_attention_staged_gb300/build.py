@@ -38,19 +38,25 @@ def _flags():
             "-I", INCLUDE, "-I", CSRC]
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _stale(target: str, sources) -> bool:
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "fa.h"),
-                                                                  __file__]
+    t = os.path.getmtime(target)
+    deps = [os.path.join(CSRC, f) for f in sources] + [os.path.join(INCLUDE, "fa.h"), __file__]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    """Build what is out of date; returns the library's path.
+
+    The library does not depend on the extension: where that does not compile (no Python headers, no
+    host compiler), its error is printed and the calls that need it raise.
+    """
+    need_lib = force or _stale(LIB, [f for f in os.listdir(CSRC) if f != "binding.c"])
+    need_binding = force or _stale(BINDING, ["binding.c"])
+    if not need_lib and not need_binding:
         return LIB
-    nvcc = _nvcc()
+    nvcc = _nvcc() if need_lib else ""
     os.makedirs(BUILD, exist_ok=True)
 
     def compile_one(src: str) -> str:
@@ -70,21 +76,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared",
                "-I", sysconfig.get_path("include"), "-I", INCLUDE, os.path.join(CSRC, "binding.c"),
                "-o", tmp, "-lm"]
-        res = subprocess.run(cmd, capture_output=True, text=True)
+        try:
+            res = subprocess.run(cmd, capture_output=True, text=True)
+            error = f"{res.stdout}\n{res.stderr}" if res.returncode != 0 else None
+        except OSError as e:
+            error = str(e)
+        if error is None:
+            os.replace(tmp, BINDING)
+            return
+        if os.path.exists(BINDING):  # of older sources
+            os.remove(BINDING)
+        print(f"compiling binding.c failed, the calls that need it will raise:\n{error}",
+              file=sys.stderr)
+
+    def link(objs) -> None:
+        tmp = LIB + f".tmp{os.getpid()}"
+        res = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True,
+                             text=True)
         if res.returncode != 0:
-            raise RuntimeError(f"compiling binding.c failed:\n{res.stdout}\n{res.stderr}")
-        os.replace(tmp, BINDING)
+            raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, LIB)
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(compile_binding)
-        objs = list(ex.map(compile_one, SOURCES))
-        binding.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    res = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True,
-                         text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, LIB)
+        binding = ex.submit(compile_binding) if need_binding else None
+        if need_lib:
+            link(list(ex.map(compile_one, SOURCES)))
+        if binding is not None:
+            binding.result()
     return LIB
 
 
