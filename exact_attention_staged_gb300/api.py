@@ -10,12 +10,16 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import sysconfig
 import threading
 from typing import Optional, Tuple
 
 import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
+# with the suffix of this interpreter's extensions: one built for another Python is not loaded
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
+                            "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 FA_FP16, FA_BF16 = 0, 1
 FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, -1, -2, -3, -4
@@ -414,9 +418,8 @@ def _calls():
     global _binding
     if _binding is None:
         lib = load()
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with "
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
                                "`python -m exact_attention_staged_gb300.build`")
         from . import _binding as ext
         names = ("fa_rope", "fa_paged_append", "fa_paged_attn", "fa_paged_attn_workspace_bytes")

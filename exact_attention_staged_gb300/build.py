@@ -3,7 +3,8 @@ the Python extension beside it with the host compiler.
 
 Usage: ``python -m exact_attention_staged_gb300.build`` or ``build()`` from Python.
 Objects go to ``exact_attention_staged_gb300/_build/``; the library to
-``exact_attention_staged_gb300/libfa.so``, the extension to ``_binding.so``.  All are git-ignored.
+``exact_attention_staged_gb300/libfa.so``, the extension to ``_binding`` with the interpreter's own
+suffix, so that no other Python version loads it.  All are git-ignored.
 """
 from __future__ import annotations
 
@@ -20,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
-BINDING = os.path.join(PKG, "_binding.so")  # Python extension: the short calls' per-call path
+# Python extension: the short calls' per-call path
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_fp8.cu", "fa_bwd.cu", "fa_decode.cu", "fa_rope.cu",
            "fa_paged.cu", "fa_paged_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -51,3 +51,12 @@ def test_calls_that_need_the_extension_raise_without_it(monkeypatch):
     monkeypatch.setattr(os.path, "exists", lambda p: "_binding" not in str(p) and exists(p))
     with pytest.raises(RuntimeError, match="missing"):
         api._calls()
+
+
+def test_the_extension_carries_this_interpreters_suffix():
+    build.build()
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert suffix != ".so" and build.BINDING == api.BINDING_PATH
+    assert build.BINDING.endswith(f"{os.sep}_binding{suffix}")
+    api.load()
+    assert os.path.samefile(api._calls().__file__, build.BINDING)
