@@ -526,7 +526,8 @@ def paged_check(block_table, kv_len, q_start, num_pages: int, page_size: int,
     if kv_len.shape != (B,) or (q_start is not None and q_start.shape != (B + 1,)):
         raise ValueError("kv_len must be [B] and q_start [B + 1]")
     if tokens is None:
-        tokens = B if q_start is None else int(q_start[-1])
+        # at least one, as in a call: offsets that end below it are what is looked for
+        tokens = B if q_start is None else max(int(q_start[-1]), 1)
     rc = load().fa_paged_check(block_table.data_ptr(), kv_len.data_ptr(),
                                None if q_start is None else q_start.data_ptr(), tokens, B,
                                num_pages, page_size, max_pages, tokens if max_q is None else max_q)

@@ -36,3 +36,17 @@ def test_tokens_beyond_max_q_do_not_move_the_others(lib, seqs, max_q, tiles, cau
     for x in out[:n].tolist():
         got[tuple(x[1:5])] = x[7]
     assert got == want
+
+
+def test_check_of_a_batch_whose_offsets_end_at_or_below_zero(lib):
+    table = torch.tensor([[0], [1]], dtype=torch.int32)
+    lens = torch.tensor([3, 4], dtype=torch.int32)
+
+    def ok(*start, **kw):
+        return api.paged_check(table, lens, torch.tensor(start, dtype=torch.int32), 2, 16, **kw)
+    assert ok(0, 0, 0)          # no sequence brings a token
+    assert not ok(0, 0, -3)     # offsets below zero are found, not refused
+    assert not ok(-1, 0, 0)
+    assert not ok(0, -2, -2)
+    assert not ok(-4, -4, -4)
+    assert ok(0, 1, 3, max_q=2)
