@@ -112,3 +112,52 @@ def test_append_reports_the_last_of_many_sequences(cuda_lib):
     lens[-1] = 17
     cuda_lib.paged_append(new, new, k, v, table, lens, start)
     assert cuda_lib.sync_status() == cuda_lib.FA_ERR_INDEX
+
+
+@pytest.mark.parametrize("what", [dict(lens=[20, 1 << 20, 9]), dict(lens=[20, -1, 9]),
+                                  dict(lens=[49, 40, 9]), dict(page=(1, 2, -1)), dict(page=(1, 2, 9)),
+                                  dict(page=(0, 1, 1 << 30)), dict(start=[0, 3, 5, 77]),
+                                  dict(start=[-2, 3, 5, 6])])
+@pytest.mark.parametrize("H", [0, 4])
+def test_append_to_bad_sequences_changes_nothing_and_to_good_ones_all(cuda_lib, what, H):
+    """Both pools, bit by bit, against pools built from the good sequences' tokens alone."""
+    seqs = [(3, 20), (2, 40), (1, 9)]
+    t = Batch(seqs, 4, 2, 64, HF, 16, seed=42, poison=False)
+    g = torch.Generator().manual_seed(43)
+    q, k, v = (torch.randn((6, h, 64), generator=g).to(HF) for h in (4, 2, 2))
+    lens, start, table = [L for _, L in seqs], [0, 3, 5, 6], t.table[:, :3].clone()
+    lens, start = what.get("lens", lens), what.get("start", start)
+    cap, pool = 3 * 16, t.k.shape[0]
+    if "page" in what:
+        b, i, entry = what["page"]
+        table[b, i] = pool if entry == 9 else entry
+    want_k, want_v = t.k.clone(), t.v.clone()
+    for b in range(3):
+        first, end = start[b], start[b + 1]
+        if not (0 <= first <= end <= 6 and 0 <= lens[b] <= cap):
+            continue
+        for tok in range(first, end):
+            pos = lens[b] - (end - tok)
+            page = int(table[b, pos // 16])
+            if 0 <= page < pool:
+                want_k[page, :, pos % 16], want_v[page, :, pos % 16] = k[tok], v[tok]
+    kp, vp = t.k.to(DEV), t.v.to(DEV)
+    got = cuda_lib.paged_append(k.to(DEV), v.to(DEV), kp, vp, table.to(DEV),
+                                torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                torch.tensor(start, dtype=torch.int32, device=DEV),
+                                q=q.to(DEV) if H else None)
+    assert cuda_lib.sync_status() == cuda_lib.FA_ERR_INDEX
+    assert torch.equal(kp.cpu(), want_k) and torch.equal(vp.cpu(), want_v)
+    if H:  # without a rotation Q is copied, that of bad sequences too (the last token of
+        # start [.., 77] and the first of [-2, ..] belong to clamped ranges)
+        assert torch.equal(got.cpu(), q)
+
+
+@pytest.mark.parametrize("room", [0, 9000])
+def test_sequences_that_share_their_pages(cuda_lib, room):
+    t = Batch([(2, 50)] * 3, 4, 2, 64, BF, 16, seed=8, room=room)
+    t.table[1:] = t.table[0]
+    t.q[2:] = t.q[:2].repeat(2, 1, 1)
+    out, lse = attend(cuda_lib, t)
+    assert cuda_lib.sync_status() == 0
+    check(t, out, lse, 64 ** -0.5, True, "shared")
