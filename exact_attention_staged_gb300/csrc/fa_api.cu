@@ -554,11 +554,11 @@ PagedTiling paged_tiling(int H, int Hkv, int max_q) {
 
 // CTAs of the cluster that takes a unit, or 0 for one line of all units over the chip.  A size is taken
 // if all units' clusters are on the chip at once and each CTA gets no more than so many key tiles of
-// the longest possible cache.
+// the longest possible cache, which is the tables' width: the lengths are on the device.
 // A cluster lies inside one GPC, so larger ones leave SMs over: 15 clusters of 8, 23 of 6, 28 of 5,
 // 36 of 4, 46 of 3, 76 of 2 were on this GPU at once with one CTA per SM; kFit keeps a little below.
-// One sequence of 1000 keys (8 K/V heads of 128) takes 8.0 us so and 10.5 as a line, of 8k 14.8 and
-// 17.1, of 16k 22.9 and 22.6; 8 of 1000 11.0 and 16.6, 16 of 2500 30.8 and 34.4.  Where lengths differ
+// One sequence of 1000 keys (8 K/V heads of 128) takes 7.8 us so and 10.7 as a line, of 8k 14.3 and
+// 16.3, of 16k 22.9 and 22.6; 8 of 1000 11.0 and 16.6, 16 of 2500 30.8 and 34.4.  Where lengths differ
 // the line is as fast from about 30 tiles per CTA (4 of 8k to 16k: 35.6 and 34.5).  A chunk of 300 tokens
 // over 300 keys (8 K/V heads) takes 16.7 and 19.9 us, over 2000 22.4 and 23.7, over 5000 33.8 and 33.0.
 fa::PagedClusters paged_clusters(const PagedTiling &t, int T, int B, int Hkv, long capacity) {

@@ -14,7 +14,8 @@
 // next tile, and two of them in flight hide it.  At the end one group's statistics and accumulator
 // (the same tensor-memory lanes) are merged into those of the other, which had the first tile.  Where no unit
 // has two query tiles the groups go on taking turns from unit to unit and a unit's first scores are
-// issued before the last one's products: 1024 sequences of up to 500 keys 465 -> 399 us.
+// issued before the last one's products: built, that took 1024 sequences of up to 500 keys from 465 to
+// 399 us.
 //
 // Keys.  A tile is 128 positions, whatever the page size: its pages are loaded by one TMA box each
 // into their rows of the 128-byte-swizzled tile (a page of 8 rows or more starts on a swizzle
@@ -36,7 +37,8 @@
 //
 // Code.  The loops over key tiles are unrolled, what runs once or a few times a unit is rolled up: with
 // short sequences every part of the kernel runs from a cold instruction cache, and fetching it was
-// most of the time (1024 sequences of up to 500 keys 399 -> 326 us, of up to 100 195 -> 150).
+// most of the time (1024 sequences of up to 500 keys take 306 us, of up to 100 125; with the epilogue
+// alone unrolled 314 and 147).
 //
 // Warps: 0 walks the units and loads Q and K, 2 loads V, 1 issues the MMAs, 4..7 and 8..11 are the
 // softmax groups.  MMA order per step: PV_0 of the step before, S_0, PV_1, S_1, as in the forward.
@@ -101,9 +103,9 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 constexpr int kQBufBytes = 64 * 128;
 
 // Pieces of no more key tiles than this are softmaxed by the rolled-up code: what runs once or twice and
-// then makes place for other code costs its fetch.  1024 sequences of up to 500 keys take 341 us without
-// it, 324 with 4 and 325 with 8; a tile of a long piece takes a quarter longer in it
-// (16 x 8k at d = 64 50.1 -> 57.3).
+// then makes place for other code costs its fetch.  1024 sequences of up to 500 keys take 323 us without
+// it and 306 with 4 or with 8, of up to 100 145 and 125; a tile of a long piece takes a quarter longer in
+// it (16 x 8k at d = 64 50.1 -> 57.3).
 constexpr int kShortPiece = 4;
 
 constexpr int kDestCluster = -2;
@@ -1057,8 +1059,8 @@ __global__ void __launch_bounds__(384, 1)
                 const int head = u.kvh * p.rep + row_head;
                 const long otok = u.tok0 + tok;
                 const int prow = q * 128 + row;
-                // (rolled up, as what else runs once a unit: unrolled, a mixed batch took 50.0 us and
-                // not 48.8, 1024 sequences of up to 500 keys 341 and not 324)
+                // (rolled up, as what else runs once a unit: unrolled, a mixed batch takes 50.7 us and
+                // not 48.8, 1024 sequences of up to 500 keys 314 and not 306)
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32], o1[32];
@@ -1286,11 +1288,12 @@ cudaError_t launch_line(const PagedMaps &m, const PagedAttnParams &p, cudaStream
     cudaError_t e = allow_smem(ready, reinterpret_cast<const void *>(kern), L::kAlloc, p.device);
     if (e != cudaSuccess) return e;
     // not launched to overlap the grid before it: its CTAs would then take the SMs in the order in
-    // which they come free, prompt chunks and single tokens no longer spread over the chip (a mixed
-    // batch 51.8 -> 56.6 us, a single sequence 11.0 -> 10.2)
+    // which they come free, prompt chunks and single tokens no longer spread over the chip (when tried, a
+    // mixed batch 51.8 -> 56.6 us, a single sequence 11.0 -> 10.2)
     kern<<<kPagedCtas, L::kThreads, L::kAlloc, stream>>>(m, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.cut == nullptr) return e;
+    // (the host does not know whether a unit was cut: where none was, this grid costs 0.6 us)
     return launch_overlapped(fa_paged_merge_kernel<D, BF16, QT>,
                              dim3(kPagedCtas - 1, (p.part_rows + 31) / 32), kMergeWarps * 32, 0,
                              stream, p);

@@ -5,7 +5,7 @@
 // elements behind rot_dim are copied.  The backward is the transpose: the same with -t.
 //
 // The work is one read and one write of every element, 6 operations a pair, so it is bound by
-// HBM: 8192 rows of 40 heads of 128 take 27.0 us, 6.2 TB/s or 0.91 of the measured copy rate.  A
+// HBM: 8192 rows of 40 heads of 128 take 27.1 us, 6.2 TB/s or 0.91 of the measured copy rate.  A
 // thread owns one unit of a row (8 pairs, or 16 elements that pass through) and walks
 // the heads of a chunk: their angle is the same, so the sines and cosines are worked out once for
 // all of them (Q's and K's heads alike: one launch for both), and the loads of several heads are
@@ -68,7 +68,8 @@ cudaError_t launch_rope_t(RopeParams p, cudaStream_t stream) {
     const long blocks = (p.rows + per_block - 1) / per_block;
     // heads per thread: two batches of them while that leaves every SM four blocks (one more than it
     // holds), else one, else fewer heads.  8k x 40 heads: 27.0 us against 30.4 with five heads and
-    // twice the blocks; 1k x 32 heads of 64: 8.2 against 10.7 with one head and twice the blocks.
+    // twice the blocks; 1k x 32 heads of 64: 8.2 against 10.7 with one head and twice the blocks.  It does
+    // not look at waves: 4092 rows of 32 heads of 64 are 1024 blocks, 2.25 times the 456 that fit.
     const int heads = p.H + p.Hkv;
     p.chunk = 2 * kRopeBatch;
     while (p.chunk > 1 && blocks * ((heads + p.chunk - 1) / p.chunk) < 4 * 152) p.chunk /= 2;

@@ -126,7 +126,9 @@ __host__ __device__ inline long paged_head(const PagedSeq &s, const PagedWork &w
 // left out when it would not pay: a CTA takes a whole unit, nothing is merged.  By unit, the time is
 // that of the longest unit (1950 cycles a key tile) or of HBM for all of them (2570 cycles a tile
 // and 152 SMs); as a line it is HBM's plus about 9000 cycles for cutting and merging.  16 x 8 heads of
-// 8k keys: 80.3 us by unit, 85.6 as a line; of 4k to 8k keys: 72.4 and 68.2.
+// 8k keys: 83.4 us by unit, 88.4 as a line; of 4k to 8k keys: 74.3 and 69.8.  The cycles are those of
+// d = 128; a tile of d = 64 has half the bytes, and there the rule takes whole units too often: 14 x 8
+// heads of 8k keys 49.3 us by unit, 45.0 as a line, 16 x 8 50.7 and 50.2, 18 x 8 52.8 and 57.0.
 struct PagedLine {
     long total, q;
     int ctas, r;

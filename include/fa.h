@@ -279,7 +279,7 @@ int fa_decode(const void *q, const void *k, const void *v, void *o, float *lse,
  *               which takes the gradients of q_out and k_out to those of q and k.
  * d is 64 or 128; rot_dim is a multiple of 16, at most d (otherwise FA_ERR_UNSUPPORTED); mscale is
  * finite and > 0.  Products and sums are fp32, rounded once; sines and cosines are off by less than
- * 2^-20 in absolute terms, sines of angles below 1/4 by less than 2^-22 relative plus 2^-29.
+ * 2^-20 in absolute terms, sines of angles below 1/4 by less than 2^-21 relative plus 2^-29.
  *
  * fa_rope_frequencies fills freq (HOST memory, rot_dim / 2 values; rot_dim >= 2 and even) from
  * f_j = base^(-2 j / rot_dim) radians per position, stretched as `scaling` (FA_ROPE_*) says, and
@@ -305,8 +305,9 @@ int fa_rope(const void *q, void *q_out, const void *k, void *k_out, const long l
  *               position are not read.  Sequences may share pages that they only read.
  *   kv_len    : device int32 [B], at most max_pages * page_size.
  *   q_start   : device int32 [B + 1], not decreasing, or NULL: T / B tokens each (B divides T).
- *               Tokens before q_start[0] and from q_start[B] on belong to no sequence: nothing is
- *               read, written or computed for them (a padded batch).
+ *               Tokens before q_start[0] and from q_start[B] on belong to no sequence (a padded
+ *               batch): nothing is written or computed for them, and what their rows hold has no
+ *               influence; like all T rows they have to be readable.
  * The index arrays live on the device, so the call cannot refuse a bad value: lengths and offsets
  * are clamped (nothing is appended to such a sequence), a page id outside [0, num_pages) is not
  * accessed (a new token's row is not written, its keys and values read as zeros), and
@@ -351,7 +352,11 @@ int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, vo
  *               max_q see the keys that they see without the bound.
  *   causal    : != 0: row i of sequence b sees keys j <= kv_len[b] - n + i; 0: all kv_len[b] keys.
  *               A row that sees no key gets O = 0 and LSE = -inf.  Whatever the cache holds behind
- *               kv_len[b] (NaN included) has no influence.
+ *               kv_len[b] (NaN included) has no influence.  Inside it, keys that a row does not see
+ *               have none either, but a value there that is not finite may make O of that row (if
+ *               it sees any key) NaN: its probability is a zero that may still be multiplied with it.
+ * Scores, statistics and sums are fp32; the probabilities are rounded to the inputs' 16-bit type
+ * before they are multiplied with V, as in the other attention calls, and O once at the end.
  *   workspace, workspace_bytes : device scratch of fa_paged_attn_workspace_bytes() bytes, 16-byte
  *               aligned (may be NULL when that is 0); it needs no initialisation and keeps nothing
  *               from call to call, but calls that may overlap on the GPU need one each.

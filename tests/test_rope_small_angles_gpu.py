@@ -8,6 +8,10 @@ pi / 2: the angle is cut to 2^-32 turns, 2 pi 2^-32 in absolute terms, and then 
 by t^6 / 5040 < 2^-24 relative and four roundings of 2^-24; from 1/4 on the special-function unit's
 2^-21.4 is 2^-19.4 of a sine of at least 0.247.  Two roundings follow (mscale, the product).  All of
 it is below 2^-19 relative; the rounding to 16 bits adds eps / 2 (fp16 below 2^-14: 2^-25).
+
+At any angle, sine and cosine from the special-function unit are off by up to 2^-21.2, and the angle's
+rounding (2^-24 twice, of up to pi: 2^-22.3) comes on top: together 2^-20.6 of |a| + |c|, with the three
+fp32 roundings of a product and a sum (2^-24 each) below 2^-20 (|a| + |c|), the bound of test_rope_gpu.
 """
 import numpy as np
 import pytest
