@@ -1,5 +1,5 @@
-"""Python binding of libfa.so: argument marshalling only (ctypes; the short calls of rotary positions
-and the paged cache through the extension csrc/binding.c, whose checks cost less time).
+"""Python binding of libfa.so: argument marshalling only (ctypes; the short calls of rotary positions,
+the paged cache and beam selection through the extension csrc/binding.c, whose checks cost less time).
 
 Every step of the attention path runs in the library's CUDA kernels; PyTorch supplies device
 memory and the current stream.  There is no fallback: when libfa.so is missing or the device
@@ -21,9 +21,9 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
 BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
                             "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
-FA_FP16, FA_BF16 = 0, 1
+FA_FP16, FA_BF16, FA_FP32 = 0, 1, 2  # FA_FP32: beam_select's logits only
 FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, -1, -2, -3, -4
-FA_ERR_INTERNAL, FA_ERR_INDEX = -5, -6
+FA_ERR_INTERNAL, FA_ERR_INDEX, FA_ERR_FULL = -5, -6, -7
 FA_ROPE_PLAIN, FA_ROPE_LINEAR, FA_ROPE_NTK, FA_ROPE_BY_PARTS, FA_ROPE_BANDS = 0, 1, 2, 3, 4
 FA_NOALLOC_MAX_ROWS = 1 << 20  # B*H*N limit of fa_bwd_noalloc
 
@@ -65,6 +65,16 @@ SIGNATURES = {
     "fa_paged_attn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
     "fa_paged_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                            _i, _i, _i, _f, _i, _vp, _sz, _vp]),
+    "fa_paged_reserve_workspace_bytes": (_sz, [_i, _i, _i]),
+    "fa_paged_reserve": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "fa_paged_fork": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp]),
+    "fa_paged_free": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp]),
+    "fa_paged_compact_workspace_bytes": (_sz, [_i]),
+    "fa_paged_compact": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _sz, _vp]),
+    "fa_paged_copy": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
+    "fa_beam_select_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "fa_beam_select": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz,
+                            _vp]),
     "fa_sync_status": (_i, [_vp]),
     "fa_status_string": (ctypes.c_char_p, [_i]),
     "fa_debug_paged_pieces": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _i]),
@@ -422,7 +432,10 @@ def _calls():
             raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
                                "`python -m exact_attention_staged_gb300.build`")
         from . import _binding as ext
-        names = ("fa_rope", "fa_paged_append", "fa_paged_attn", "fa_paged_attn_workspace_bytes")
+        names = ("fa_rope", "fa_paged_append", "fa_paged_attn", "fa_paged_attn_workspace_bytes",
+                 "fa_paged_reserve", "fa_paged_reserve_workspace_bytes", "fa_paged_fork", "fa_paged_free",
+                 "fa_paged_compact", "fa_paged_compact_workspace_bytes", "fa_paged_copy",
+                 "fa_beam_select", "fa_beam_select_workspace_bytes")
         ext.setup(tuple(ctypes.cast(getattr(lib, n), _vp).value for n in names), torch.empty, _raw,
                   torch.bfloat16, torch.float16, torch.int32, torch.int64, torch.float32,
                   torch.uint8, FAError)
@@ -578,6 +591,97 @@ def paged_attention(q, k_pages, v_pages, block_table, kv_len, q_start=None,
                                              lse, workspace))
     return _calls().paged_attention(q, k_pages, v_pages, block_table, kv_len, q_start, max_q, scale,
                                     causal, out, lse, workspace)
+
+
+def paged_reserve(block_table, kv_len, refs, page_size: int, q_start=None, tokens: Optional[int] = None,
+                  copies=None, workspace=None, stream=None):
+    """Pages of their own for a batch's new tokens (fa_paged_reserve).
+
+    block_table int32 [B, max_pages] (-1: no page) and refs int32 [num_pages] (holders of each page) are
+    updated.  kv_len and q_start as in paged_append; tokens: the batch's tokens (needed with q_start;
+    None: one for each sequence).  Returns copies, int32 [3, B]: paged_copy's src, dst and rows for the
+    pages that were shared and are partly filled.
+    """
+    if _away(block_table, stream):
+        return _elsewhere(lambda: paged_reserve(block_table, kv_len, refs, page_size, q_start, tokens,
+                                                copies, workspace),
+                          stream, block_table.device, (block_table, kv_len, refs, q_start, copies,
+                                                       workspace))
+    return _calls().paged_reserve(block_table, kv_len, refs, page_size, q_start, tokens, copies, workspace)
+
+
+def paged_reserve_workspace_bytes(tokens: int, B: int, page_size: int) -> int:
+    return int(load().fa_paged_reserve_workspace_bytes(tokens, B, page_size))
+
+
+def paged_fork(block_table, parents, refs, kv_len=None, stream=None):
+    """Row b of block_table (and kv_len) becomes what row parents[b] was; -1: empty (fa_paged_fork).
+
+    parents: int32 [B], as beam_select returns them (flattened).  refs follows.
+    """
+    if _away(block_table, stream):
+        return _elsewhere(lambda: paged_fork(block_table, parents, refs, kv_len), stream,
+                          block_table.device, (block_table, parents, refs, kv_len))
+    return _calls().paged_fork(block_table, parents, refs, kv_len)
+
+
+def paged_free(block_table, keep_len, refs, page_size: int, stream=None):
+    """Sequence b keeps the pages of its first keep_len[b] positions (int32 [B]; fa_paged_free)."""
+    if _away(block_table, stream):
+        return _elsewhere(lambda: paged_free(block_table, keep_len, refs, page_size), stream,
+                          block_table.device, (block_table, keep_len, refs))
+    return _calls().paged_free(block_table, keep_len, refs, page_size)
+
+
+def paged_compact(block_table, refs, moves=None, count=None, workspace=None, stream=None):
+    """Moves the live pages to the front of the pool (fa_paged_compact).
+
+    Returns moves, int32 [2, num_pages // 2 or more], and count, int32 [1]: paged_copy's src, dst and
+    count, which move the data.  block_table and refs are updated.
+    """
+    if _away(block_table, stream):
+        return _elsewhere(lambda: paged_compact(block_table, refs, moves, count, workspace), stream,
+                          block_table.device, (block_table, refs, moves, count, workspace))
+    return _calls().paged_compact(block_table, refs, moves, count, workspace)
+
+
+def paged_compact_workspace_bytes(num_pages: int) -> int:
+    return int(load().fa_paged_compact_workspace_bytes(num_pages))
+
+
+def paged_copy(k_pages, v_pages, src, dst, rows=None, count=None, stream=None):
+    """The first rows[i] rows (None: all) of page src[i] to page dst[i], int32 [n] (fa_paged_copy).
+
+    k_pages, v_pages: one layer's [num_pages, H_kv, page_size, d], or all layers' [L, num_pages, H_kv,
+    page_size, d].  Pairs with a negative page are left out, and those from count (int32 [1]) on.
+    """
+    if _away(k_pages, stream):
+        return _elsewhere(lambda: paged_copy(k_pages, v_pages, src, dst, rows, count), stream,
+                          k_pages.device, (k_pages, v_pages, src, dst, rows, count))
+    return _calls().paged_copy(k_pages, v_pages, src, dst, rows, count)
+
+
+def beam_select(logits, scores, k: Optional[int] = None, finished=None, end_token: Optional[int] = None,
+                out_scores=None, out_parents=None, out_tokens=None, out_finished=None, workspace=None,
+                stream=None):
+    """The k best continuations (None: as many as beams) of each request's beams (fa_beam_select).
+
+    logits [B, W, V] of bf16, fp16 or fp32, any strides with contiguous rows; scores fp32 [B, W].
+    finished: uint8 [B, W], beams that have ended: they offer end_token at their own score.  Returns
+    scores (fp32), parents (int32, b * W + beam; -1: no candidate was left), tokens (int32) and finished
+    (uint8), each [B, k], best first.
+    """
+    if _away(logits, stream):
+        return _elsewhere(lambda: beam_select(logits, scores, k, finished, end_token, out_scores,
+                                              out_parents, out_tokens, out_finished, workspace),
+                          stream, logits.device, (logits, scores, finished, out_scores, out_parents,
+                                                  out_tokens, out_finished, workspace))
+    return _calls().beam_select(logits, scores, k, finished, end_token, out_scores, out_parents,
+                                out_tokens, out_finished, workspace)
+
+
+def beam_select_workspace_bytes(B: int, W: int, V: int, k: int) -> int:
+    return int(load().fa_beam_select_workspace_bytes(B, W, V, k))
 
 
 def sync_status(stream=None) -> int:

@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libfa.so")
 # Python extension: the short calls' per-call path
 BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_fp8.cu", "fa_bwd.cu", "fa_decode.cu", "fa_rope.cu",
-           "fa_paged.cu", "fa_paged_attn.cu"]
+           "fa_paged.cu", "fa_paged_attn.cu", "fa_pages.cu", "fa_beam.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

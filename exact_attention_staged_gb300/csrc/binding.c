@@ -1,5 +1,5 @@
 /* binding.c - the per-call path of the Python binding for the calls that are short on the GPU (rotary
- * positions and the paged cache): argument checks, result allocation and the call into libfa.so.
+ * positions, the paged cache and its tables, beam selection): argument checks, result allocation and the call into libfa.so.
  *
  * A single token's append or attention takes 3 to 10 us on the GPU; the same checks in Python and
  * ctypes took 15 to 22 us on the host, this module takes about half.  It knows nothing of torch but
@@ -24,16 +24,37 @@ typedef int (*attn_fn)(const void *, const void *, const void *, void *, float *
                        const long long *, const int *, const int *, const int *, int, int, int, int,
                        int, int, int, int, int, int, float, int, void *, size_t, void *);
 typedef size_t (*attn_bytes_fn)(int, int, int, int, int, int, int, int);
+typedef int (*reserve_fn)(int *, const int *, const int *, int *, int *, int, int, int, int, int, void *,
+                          size_t, void *);
+typedef size_t (*reserve_bytes_fn)(int, int, int);
+typedef int (*fork_fn)(int *, int *, const int *, int *, int, int, int, void *);
+typedef int (*free_fn)(int *, const int *, int *, int, int, int, int, void *);
+typedef int (*compact_fn)(int *, int *, int *, int *, int *, int, int, int, void *, size_t, void *);
+typedef size_t (*compact_bytes_fn)(int);
+typedef int (*copy_fn)(void *, void *, const long long *, const int *, const int *, const int *,
+                       const int *, int, int, int, int, int, int, void *);
+typedef int (*beam_fn)(const void *, const long long *, const float *, const uint8_t *, float *, int *,
+                       int *, uint8_t *, int, int, int, int, int, int, void *, size_t, void *);
+typedef size_t (*beam_bytes_fn)(int, int, int, int);
 
 static rope_fn g_rope;
 static append_fn g_append;
 static attn_fn g_attn;
 static attn_bytes_fn g_attn_bytes;
+static reserve_fn g_reserve;
+static reserve_bytes_fn g_reserve_bytes;
+static fork_fn g_fork;
+static free_fn g_free;
+static compact_fn g_compact;
+static compact_bytes_fn g_compact_bytes;
+static copy_fn g_copy;
+static beam_fn g_beam;
+static beam_bytes_fn g_beam_bytes;
 /* torch.empty, the current raw stream of a device, the dtypes, the error class: set by setup() */
 static PyObject *g_empty, *g_stream, *g_bf16, *g_fp16, *g_i32, *g_i64, *g_f32, *g_u8, *g_error;
 static PyObject *s_get_device, *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_device, *s_kwnames;
 
-#define MAX_DIMS 4
+#define MAX_DIMS 5
 typedef struct {
     PyObject *obj; /* borrowed; NULL where the caller gave None */
     const char *name;
@@ -60,7 +81,7 @@ static int ints_of(PyObject *tuple, long long *out) {
     if (!PyTuple_Check(tuple)) {
         fail(PyExc_TypeError, "expected a tensor");
     } else if (PyTuple_GET_SIZE(tuple) > MAX_DIMS) {
-        fail(PyExc_ValueError, "tensors have at most four axes");
+        fail(PyExc_ValueError, "tensors have at most five axes");
     } else {
         n = (int)PyTuple_GET_SIZE(tuple);
         for (int i = 0; i < n; ++i) {
@@ -294,7 +315,7 @@ static PyObject *py_rope(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     if (fits(ext, 6)) return NULL;
     PyObject *device = PyObject_GetAttr(q.obj, s_device), *rq = NULL, *rk = NULL, *out = NULL;
     void *pq, *pk = NULL, *stream;
-    long long sq[4], sk[4] = {0, 0, 0, 0};
+    long long sq[MAX_DIMS], sk[MAX_DIMS] = {0};
     if (device == NULL) return NULL;
     if ((rq = result(&oq, &q, device, &pq, sq)) == NULL) goto done;
     if (k.obj != NULL && (rk = result(&ok, &k, device, &pk, sk)) == NULL) goto done;
@@ -396,7 +417,7 @@ static PyObject *py_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     if (rot < 0 || fits(ext, 2)) return NULL;
     PyObject *rq = NULL;
     void *pq = NULL, *stream;
-    long long sq[4] = {8, 8, 1, 0};
+    long long sq[MAX_DIMS] = {8, 8, 1};
     if (q.obj != NULL) {
         PyObject *device = PyObject_GetAttr(q.obj, s_device);
         if (device == NULL) return NULL;
@@ -465,7 +486,7 @@ static PyObject *py_attention(PyObject *self, PyObject *const *a, Py_ssize_t n) 
                                                  (int)max_q, (int)b.page_size, (int)b.max_pages);
     PyObject *device = PyObject_GetAttr(q.obj, s_device), *ro = NULL, *rl = NULL, *rw = NULL, *res = NULL;
     void *po, *pl = lse.ptr, *pw = ws.ptr, *stream;
-    long long so[4];
+    long long so[MAX_DIMS];
     if (device == NULL) return NULL;
     if ((ro = result(&out, &q, device, &po, so)) == NULL) goto done;
     if (lse.obj != NULL) {
@@ -511,19 +532,329 @@ done:
     return res;
 }
 
-/* setup((fa_rope, fa_paged_append, fa_paged_attn, fa_paged_attn_workspace_bytes addresses), torch.empty,
- *       raw stream of a device, bfloat16, float16, int32, int64, float32, uint8, error class) */
+/* An integer argument that the library takes as an int. */
+static int int_arg(PyObject *obj, const char *name, long long *out) {
+    *out = PyLong_AsLongLong(obj);
+    if (*out == -1 && PyErr_Occurred()) return -1;
+    if (*out < -0x7fffffffLL || *out > 0x7fffffffLL) {
+        PyErr_Format(PyExc_ValueError, "%s is out of range", name);
+        return -1;
+    }
+    return 0;
+}
+
+/* The caller's workspace of at least `need` bytes, or a new one (*made: to be released). */
+static int workspace(const Tensor *given, size_t need, PyObject *like, void **ptr, PyObject **made) {
+    *made = NULL;
+    if (given->obj != NULL) {
+        if (!is_dense(given)) return fail(PyExc_ValueError, "workspace must be contiguous");
+        PyObject *bytes = PyObject_GetAttrString(given->obj, "nbytes");
+        const long long have = bytes ? PyLong_AsLongLong(bytes) : -1;
+        Py_XDECREF(bytes);
+        if (have < 0) return -1;
+        if ((size_t)have < need)
+            return fail(PyExc_ValueError, "workspace is smaller than its *_workspace_bytes()");
+        *ptr = given->ptr;
+        return 0;
+    }
+    const long long shape[1] = {need > 16 ? (long long)need : 16};
+    PyObject *device = PyObject_GetAttr(like, s_device);
+    if (device == NULL) return -1;
+    *made = new_tensor(shape, 1, g_u8, device, ptr);
+    Py_DECREF(device);
+    return *made == NULL ? -1 : 0;
+}
+
+/* A result of the given shape: the caller's, which has to be contiguous, or a new one. */
+static PyObject *dense_result(const Tensor *given, PyObject *dtype, const long long *shape, int dims,
+                              PyObject *device, void **ptr) {
+    if (given->obj == NULL) return new_tensor(shape, dims, dtype, device, ptr);
+    int same = given->dtype == dtype && given->dims == dims && is_dense(given);
+    for (int i = 0; same && i < dims; ++i) same = given->shape[i] == shape[i];
+    if (!same) {
+        PyErr_Format(PyExc_ValueError, "%s has the wrong shape or type, or is not contiguous", given->name);
+        return NULL;
+    }
+    *ptr = given->ptr;
+    Py_INCREF(given->obj);
+    return given->obj;
+}
+
+/* block_table [B, max_pages] and refs [num_pages]. */
+static int take_tables(PyObject *table, PyObject *refs, long *dev, Tensor *t, Tensor *r) {
+    if (first_device(table, "block_table", dev) || take(table, "block_table", *dev, t) ||
+        take(refs, "refs", *dev, r))
+        return -1;
+    if (t->dims != 2 || t->dtype != g_i32 || !is_dense(t))
+        return fail(PyExc_ValueError, "block_table must be contiguous int32 [B, max_pages]");
+    if (r->obj == NULL || r->dims != 1 || r->dtype != g_i32 || !is_dense(r))
+        return fail(PyExc_ValueError, "refs must be contiguous int32 [num_pages]");
+    const long long ext[3] = {t->shape[0], t->shape[1], r->shape[0]};
+    return fits(ext, 3);
+}
+
+/* An index array that has to be there. */
+static int need_index(const Tensor *t, long long n) {
+    if (t->obj == NULL) {
+        PyErr_Format(PyExc_ValueError, "%s must be contiguous int32 [%lld]", t->name, n);
+        return -1;
+    }
+    return check_index(t, n, -1);
+}
+
+/* paged_reserve(block_table, kv_len, refs, page_size, q_start, tokens, copies, workspace) */
+static PyObject *py_reserve(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Tensor table, refs, len, start, copies, ws;
+    long dev;
+    long long page, T;
+    if (count_args(n, 8) || take_tables(a[0], a[2], &dev, &table, &refs) ||
+        take(a[1], "kv_len", dev, &len) || take(a[4], "q_start", dev, &start) ||
+        take(a[6], "copies", dev, &copies) || take(a[7], "workspace", dev, &ws) ||
+        int_arg(a[3], "page_size", &page))
+        return NULL;
+    const long long B = table.shape[0];
+    if (need_index(&len, B) || check_index(&start, B + 1, -1)) return NULL;
+    if (a[5] != Py_None) {
+        if (int_arg(a[5], "tokens", &T)) return NULL;
+    } else if (start.obj != NULL) {
+        fail(PyExc_ValueError, "q_start needs tokens, the number of the batch's tokens");
+        return NULL;
+    } else {
+        T = B;
+    }
+    PyObject *device = PyObject_GetAttr(table.obj, s_device), *rc = NULL, *rw = NULL;
+    void *pc, *pw, *stream;
+    if (device == NULL) return NULL;
+    const long long shape[2] = {3, B};
+    rc = dense_result(&copies, g_i32, shape, 2, device, &pc);
+    Py_DECREF(device);
+    if (rc == NULL) return NULL;
+    const size_t need = T < 1 || page < 1 ? 0 : g_reserve_bytes((int)T, (int)B, (int)page);
+    if (workspace(&ws, need, table.obj, &pw, &rw) || stream_of(dev, &stream)) goto fail;
+    {
+        int code;
+        Py_BEGIN_ALLOW_THREADS
+        code = g_reserve(table.ptr, len.ptr, start.ptr, refs.ptr, pc, (int)T, (int)B, (int)refs.shape[0],
+                         (int)page, (int)table.shape[1], pw, need, stream);
+        Py_END_ALLOW_THREADS
+        if (check_rc(code, "fa_paged_reserve")) goto fail;
+    }
+    Py_XDECREF(rw);
+    return rc;
+fail:
+    Py_XDECREF(rc);
+    Py_XDECREF(rw);
+    return NULL;
+}
+
+/* paged_fork(block_table, parents, refs, kv_len) */
+static PyObject *py_fork(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Tensor table, refs, parents, len;
+    long dev;
+    void *stream;
+    if (count_args(n, 4) || take_tables(a[0], a[2], &dev, &table, &refs) ||
+        take(a[1], "parents", dev, &parents) || take(a[3], "kv_len", dev, &len) ||
+        need_index(&parents, table.shape[0]) || check_index(&len, table.shape[0], -1) ||
+        stream_of(dev, &stream))
+        return NULL;
+    int code;
+    Py_BEGIN_ALLOW_THREADS
+    code = g_fork(table.ptr, len.ptr, parents.ptr, refs.ptr, (int)table.shape[0], (int)refs.shape[0],
+                  (int)table.shape[1], stream);
+    Py_END_ALLOW_THREADS
+    if (check_rc(code, "fa_paged_fork")) return NULL;
+    Py_RETURN_NONE;
+}
+
+/* paged_free(block_table, keep_len, refs, page_size) */
+static PyObject *py_free(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Tensor table, refs, keep;
+    long dev;
+    long long page;
+    void *stream;
+    if (count_args(n, 4) || take_tables(a[0], a[2], &dev, &table, &refs) ||
+        take(a[1], "keep_len", dev, &keep) || need_index(&keep, table.shape[0]) ||
+        int_arg(a[3], "page_size", &page) || stream_of(dev, &stream))
+        return NULL;
+    int code;
+    Py_BEGIN_ALLOW_THREADS
+    code = g_free(table.ptr, keep.ptr, refs.ptr, (int)table.shape[0], (int)refs.shape[0], (int)page,
+                  (int)table.shape[1], stream);
+    Py_END_ALLOW_THREADS
+    if (check_rc(code, "fa_paged_free")) return NULL;
+    Py_RETURN_NONE;
+}
+
+/* paged_compact(block_table, refs, moves, count, workspace) */
+static PyObject *py_compact(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Tensor table, refs, moves, count, ws;
+    long dev;
+    if (count_args(n, 5) || take_tables(a[0], a[1], &dev, &table, &refs) ||
+        take(a[2], "moves", dev, &moves) || take(a[3], "count", dev, &count) ||
+        take(a[4], "workspace", dev, &ws))
+        return NULL;
+    const long long pages = refs.shape[0], one[1] = {1};
+    long long shape[2] = {2, pages > 1 ? pages / 2 : 1};
+    if (moves.obj != NULL && moves.dims == 2 && moves.shape[1] > shape[1]) shape[1] = moves.shape[1];
+    PyObject *device = PyObject_GetAttr(table.obj, s_device), *rm = NULL, *rc = NULL, *rw = NULL, *out = NULL;
+    void *pm, *pc, *pw, *stream;
+    if (device == NULL) return NULL;
+    if ((rm = dense_result(&moves, g_i32, shape, 2, device, &pm)) == NULL ||
+        (rc = dense_result(&count, g_i32, one, 1, device, &pc)) == NULL)
+        goto done;
+    const size_t need = g_compact_bytes((int)pages);
+    if (workspace(&ws, need, table.obj, &pw, &rw) || stream_of(dev, &stream)) goto done;
+    {
+        int code;
+        Py_BEGIN_ALLOW_THREADS
+        code = g_compact(table.ptr, refs.ptr, pm, (int *)pm + shape[1], pc, (int)table.shape[0], (int)pages,
+                         (int)table.shape[1], pw, need, stream);
+        Py_END_ALLOW_THREADS
+        if (check_rc(code, "fa_paged_compact")) goto done;
+    }
+    out = PyTuple_Pack(2, rm, rc);
+done:
+    Py_DECREF(device);
+    Py_XDECREF(rm);
+    Py_XDECREF(rc);
+    Py_XDECREF(rw);
+    return out;
+}
+
+/* paged_copy(k_pages, v_pages, src, dst, rows, count) */
+static PyObject *py_copy(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Tensor k, v, src, dst, rows, count;
+    long dev;
+    void *stream;
+    if (count_args(n, 6) || first_device(a[0], "k_pages", &dev) || take(a[0], "k_pages", dev, &k) ||
+        take(a[1], "v_pages", dev, &v) || take(a[2], "src", dev, &src) || take(a[3], "dst", dev, &dst) ||
+        take(a[4], "rows", dev, &rows) || take(a[5], "count", dev, &count))
+        return NULL;
+    if (v.obj == NULL || (k.dims != 4 && k.dims != 5) || !same_shape(&k, &v) || k.dtype != v.dtype) {
+        fail(PyExc_ValueError, "k_pages and v_pages must be [num_pages, H_kv, page_size, d] or [L, num_pages, "
+                               "H_kv, page_size, d] of one type");
+        return NULL;
+    }
+    if (dtype_code(&k) < 0) return NULL;
+    if (src.obj == NULL || src.dims != 1) {
+        fail(PyExc_ValueError, "src must be contiguous int32 [n]");
+        return NULL;
+    }
+    if (need_index(&src, src.shape[0]) || need_index(&dst, src.shape[0]) ||
+        check_index(&rows, src.shape[0], -1) || check_index(&count, 1, -1))
+        return NULL;
+    const int at = k.dims - 4; /* the axis of pages */
+    const long long L = at ? k.shape[0] : 1;
+    const long long ext[6] = {src.shape[0], L, k.shape[at + 1], k.shape[at + 3], k.shape[at],
+                              k.shape[at + 2]};
+    if (fits(ext, 6) || stream_of(dev, &stream)) return NULL;
+    const long long st[8] = {at ? k.stride[0] : 8, k.stride[at], k.stride[at + 1], k.stride[at + 2],
+                             at ? v.stride[0] : 8, v.stride[at], v.stride[at + 1], v.stride[at + 2]};
+    int code;
+    Py_BEGIN_ALLOW_THREADS
+    code = g_copy(k.ptr, v.ptr, st, src.ptr, dst.ptr, rows.ptr, count.ptr, (int)ext[0], (int)ext[1],
+                  (int)ext[2], (int)ext[3], (int)ext[4], (int)ext[5], stream);
+    Py_END_ALLOW_THREADS
+    if (check_rc(code, "fa_paged_copy")) return NULL;
+    Py_RETURN_NONE;
+}
+
+/* beam_select(logits, scores, k, finished, end_token, out_scores, out_parents, out_tokens, out_finished,
+ *             workspace) */
+static PyObject *py_beam(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Tensor x, scores, fin, out[4], ws;
+    static const char *names[4] = {"out_scores", "out_parents", "out_tokens", "out_finished"};
+    long dev;
+    if (count_args(n, 10) || first_device(a[0], "logits", &dev) || take(a[0], "logits", dev, &x) ||
+        take(a[1], "scores", dev, &scores) || take(a[3], "finished", dev, &fin) ||
+        take(a[9], "workspace", dev, &ws))
+        return NULL;
+    for (int i = 0; i < 4; ++i)
+        if (take(a[5 + i], names[i], dev, &out[i])) return NULL;
+    if (x.dims != 3) {
+        fail(PyExc_ValueError, "logits must be [B, W, V]");
+        return NULL;
+    }
+    int code = x.dtype == g_f32 ? FA_FP32 : x.dtype == g_bf16 ? FA_BF16 : x.dtype == g_fp16 ? FA_FP16 : -1;
+    if (code < 0) {
+        PyErr_Format(PyExc_TypeError,
+                     "unsupported dtype %R: use torch.bfloat16, torch.float16 or torch.float32", x.dtype);
+        return NULL;
+    }
+    const long long B = x.shape[0], W = x.shape[1], V = x.shape[2];
+    const Tensor *small[2] = {&scores, &fin};
+    for (int i = 0; i < 2; ++i) {
+        const Tensor *s = small[i];
+        if (i == 1 && s->obj == NULL) continue;
+        if (s->obj == NULL || s->dims != 2 || s->shape[0] != B || s->shape[1] != W || !is_dense(s) ||
+            s->dtype != (i ? g_u8 : g_f32)) {
+            fail(PyExc_ValueError, i ? "finished must be contiguous uint8 [B, W]"
+                                     : "scores must be contiguous fp32 [B, W]");
+            return NULL;
+        }
+    }
+    long long K = W, end = -1;
+    if ((a[2] != Py_None && int_arg(a[2], "k", &K)) || (a[4] != Py_None && int_arg(a[4], "end_token", &end)))
+        return NULL;
+    if (K < 1) {
+        fail(PyExc_ValueError, "k must be at least 1");
+        return NULL;
+    }
+    const long long ext[4] = {B, W, V, K}, shape[2] = {B, K};
+    if (fits(ext, 4)) return NULL;
+    PyObject *types[4] = {g_f32, g_i32, g_i32, g_u8}, *made[4] = {NULL, NULL, NULL, NULL}, *rw = NULL;
+    PyObject *device = PyObject_GetAttr(x.obj, s_device), *res = NULL;
+    void *ptr[4], *pw, *stream;
+    if (device == NULL) return NULL;
+    for (int i = 0; i < 4; ++i)
+        if ((made[i] = dense_result(&out[i], types[i], shape, 2, device, &ptr[i])) == NULL) goto done;
+    const size_t need = g_beam_bytes((int)B, (int)W, (int)V, (int)K);
+    if (workspace(&ws, need, x.obj, &pw, &rw) || stream_of(dev, &stream)) goto done;
+    {
+        const long long st[2] = {x.stride[0], x.stride[1]};
+        Py_BEGIN_ALLOW_THREADS
+        code = g_beam(x.ptr, st, scores.ptr, fin.ptr, ptr[0], ptr[1], ptr[2], ptr[3], (int)B, (int)W, (int)V,
+                      (int)K, code, (int)end, pw, need, stream);
+        Py_END_ALLOW_THREADS
+        if (check_rc(code, "fa_beam_select")) goto done;
+    }
+    res = PyTuple_Pack(4, made[0], made[1], made[2], made[3]);
+done:
+    Py_DECREF(device);
+    for (int i = 0; i < 4; ++i) Py_XDECREF(made[i]);
+    Py_XDECREF(rw);
+    return res;
+}
+
+/* setup(addresses of the entry points in the order below, torch.empty, raw stream of a device, bfloat16,
+ *       float16, int32, int64, float32, uint8, error class) */
 static PyObject *py_setup(PyObject *self, PyObject *args) {
     (void)self;
-    unsigned long long rope, append, attn, bytes;
+    unsigned long long f[13];
     PyObject *o[9];
-    if (!PyArg_ParseTuple(args, "(KKKK)OOOOOOOOO", &rope, &append, &attn, &bytes, &o[0], &o[1], &o[2],
-                          &o[3], &o[4], &o[5], &o[6], &o[7], &o[8]))
+    if (!PyArg_ParseTuple(args, "(KKKKKKKKKKKKK)OOOOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6],
+                          &f[7], &f[8], &f[9], &f[10], &f[11], &f[12], &o[0], &o[1], &o[2], &o[3], &o[4],
+                          &o[5], &o[6], &o[7], &o[8]))
         return NULL;
-    g_rope = (rope_fn)(uintptr_t)rope;
-    g_append = (append_fn)(uintptr_t)append;
-    g_attn = (attn_fn)(uintptr_t)attn;
-    g_attn_bytes = (attn_bytes_fn)(uintptr_t)bytes;
+    g_rope = (rope_fn)(uintptr_t)f[0];
+    g_append = (append_fn)(uintptr_t)f[1];
+    g_attn = (attn_fn)(uintptr_t)f[2];
+    g_attn_bytes = (attn_bytes_fn)(uintptr_t)f[3];
+    g_reserve = (reserve_fn)(uintptr_t)f[4];
+    g_reserve_bytes = (reserve_bytes_fn)(uintptr_t)f[5];
+    g_fork = (fork_fn)(uintptr_t)f[6];
+    g_free = (free_fn)(uintptr_t)f[7];
+    g_compact = (compact_fn)(uintptr_t)f[8];
+    g_compact_bytes = (compact_bytes_fn)(uintptr_t)f[9];
+    g_copy = (copy_fn)(uintptr_t)f[10];
+    g_beam = (beam_fn)(uintptr_t)f[11];
+    g_beam_bytes = (beam_bytes_fn)(uintptr_t)f[12];
     PyObject **slots[9] = {&g_empty, &g_stream, &g_bf16, &g_fp16, &g_i32, &g_i64, &g_f32, &g_u8, &g_error};
     for (int i = 0; i < 9; ++i) {
         Py_INCREF(o[i]);
@@ -537,6 +868,12 @@ static PyMethodDef kMethods[] = {
     {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, NULL},
     {"paged_append", (PyCFunction)(void (*)(void))py_append, METH_FASTCALL, NULL},
     {"paged_attention", (PyCFunction)(void (*)(void))py_attention, METH_FASTCALL, NULL},
+    {"paged_reserve", (PyCFunction)(void (*)(void))py_reserve, METH_FASTCALL, NULL},
+    {"paged_fork", (PyCFunction)(void (*)(void))py_fork, METH_FASTCALL, NULL},
+    {"paged_free", (PyCFunction)(void (*)(void))py_free, METH_FASTCALL, NULL},
+    {"paged_compact", (PyCFunction)(void (*)(void))py_compact, METH_FASTCALL, NULL},
+    {"paged_copy", (PyCFunction)(void (*)(void))py_copy, METH_FASTCALL, NULL},
+    {"beam_select", (PyCFunction)(void (*)(void))py_beam, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, kMethods,

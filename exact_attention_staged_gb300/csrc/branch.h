@@ -1,0 +1,90 @@
+// branch.h - parameter blocks and launchers of decoding with branches: the page tables' upkeep
+// (fa_pages.cu) and beam selection (fa_beam.cu).
+#pragma once
+
+#include "positions.h"
+
+namespace fa {
+
+constexpr int kErrFull = -7;  // too few free pages
+
+// A page is free where refs is 0; a table's entry is a page id, or below 0 for none.
+struct PageTables {
+    int *table;               // [B, max_pages]
+    int *refs;                // [num_pages] holders of each page
+    int B, num_pages, max_pages, page_shift;
+    int *status;              // device status word
+};
+
+struct PagedReserveParams {
+    PagedView c;              // the batch; c.table is t.table
+    PageTables t;
+    int *copies;              // [3, B]: page to copy from, page to copy to, rows; or nullptr
+    int *fresh;               // workspace: the pages given out, in order
+};
+
+struct PagedForkParams {
+    PageTables t;
+    int *kv_len;              // [B] or nullptr
+    const int *parents;       // [B]
+    int cols;                 // columns of the table per block (set by the launcher)
+};
+
+struct PagedFreeParams {
+    PageTables t;
+    const int *keep_len;      // [B]
+};
+
+struct PagedCompactParams {
+    PageTables t;
+    int *src, *dst;           // [num_pages / 2]
+    int *count;
+    int *live;                // workspace: live pages
+    int *rank;                // workspace [num_pages]: which move a page behind the live ones makes
+};
+
+struct PagedCopySide {
+    uint16_t *base;
+    long layer, page, outer, inner;  // strides in elements
+};
+struct PagedCopyParams {
+    PagedCopySide k, v;
+    const int *src, *dst, *rows, *count;
+    int n, L, num_pages;
+    // a page is `outers` runs of `inners` pieces of 16 * (1 << piece_shift) bytes; rows are the outer
+    // index or the inner one
+    int heads, page_size, rows_inner;
+    int piece_shift;
+    int *status;
+};
+
+struct BeamParams {
+    const void *logits;
+    long stride_b, stride_w;         // elements
+    const float *scores;             // [B, W]
+    const uint8_t *finished;         // [B, W] or nullptr
+    float *out_scores;               // [B, K]
+    int *parents, *tokens;           // [B, K]
+    uint8_t *out_finished;           // [B, K]
+    int B, W, V, K, end_token;
+    int chunks;                      // pieces of a row
+    unsigned long long *keys;        // workspace [B * W][chunks][K]
+    float2 *stats;                   // workspace [B * W][chunks]: maximum, sum of e^(x - maximum)
+};
+
+cudaError_t launch_paged_reserve(const PagedReserveParams &p, cudaStream_t stream);
+cudaError_t launch_paged_fork(PagedForkParams p, cudaStream_t stream);
+cudaError_t launch_paged_free(const PagedFreeParams &p, cudaStream_t stream);
+cudaError_t launch_paged_compact(const PagedCompactParams &p, cudaStream_t stream);
+cudaError_t launch_paged_copy(const PagedCopyParams &p, cudaStream_t stream);
+
+// Sequences that one call may have: their places are kept in shared memory.
+constexpr int kBranchMaxSeqs = 32768;
+
+enum BeamType { kBeamF16 = 0, kBeamBF16 = 1, kBeamF32 = 2 };
+constexpr int kBeamChunk = 8192;   // logits of one piece of a row
+constexpr int kBeamMaxK = 128;
+constexpr int kBeamMaxWidth = 2048;     // beams of a request
+cudaError_t launch_beam_select(const BeamParams &p, int type, cudaStream_t stream);
+
+}  // namespace fa

@@ -1,6 +1,7 @@
 // fa_api.cu - the C ABI of libfa.so: argument validation, TMA tensor maps, launches, and the
 // per-device status word that bounded pipeline waits report into.  See include/fa.h.
 #include "fa.h"
+#include "branch.h"
 #include "fa_internal.h"
 #include "paged.cuh"
 
@@ -514,6 +515,41 @@ int check_paged_index(const int *table, const int *kv_len, const int *q_start, f
     c->kv_len = kv_len;
     c->q_start = q_start;
     return FA_OK;
+}
+
+// Sizes and arrays of the calls that keep a paged cache's tables.
+int check_tables(int *table, int *refs, int B, int num_pages, int page_size, int max_pages,
+                 fa::PageTables *t) {
+    fa::PagedView c = {};
+    int rc = check_paged(1, B, 1, 1, 64, num_pages, page_size, max_pages, FA_BF16, &c);
+    if (rc != FA_OK) return rc;
+    rc = check_ptrs({refs});
+    if (rc != FA_OK) return rc;
+    if (table == nullptr || (reinterpret_cast<uintptr_t>(table) & 3u) != 0) return FA_ERR_INVALID;
+    if (B > fa::kBranchMaxSeqs) return FA_ERR_UNSUPPORTED;
+    t->table = table;
+    t->refs = refs;
+    t->B = B;
+    t->num_pages = num_pages;
+    t->max_pages = max_pages;
+    t->page_shift = c.page_shift;
+    int dev = 0;
+    return device_setup(&dev, &t->status);
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+long reserve_items(int T, int B, int page_size) { return static_cast<long>(T) / page_size + 2l * B; }
+
+long beam_chunks(int V) { return (static_cast<long>(V) + fa::kBeamChunk - 1) / fa::kBeamChunk; }
+int check_beam(int B, int W, int V, int K, int dtype) {
+    if (B < 1 || W < 1 || V < 1 || K < 1) return FA_ERR_INVALID;
+    if (dtype != FA_FP16 && dtype != FA_BF16 && dtype != FA_FP32) return FA_ERR_INVALID;
+    if (static_cast<long long>(W) * V >= (1ll << 31) || static_cast<long long>(B) * W >= (1ll << 31) ||
+        static_cast<long long>(B) * W * beam_chunks(V) >= (1ll << 31) ||
+        static_cast<long long>(B) * K >= (1ll << 31))
+        return FA_ERR_INVALID;
+    return K > fa::kBeamMaxK || W > fa::kBeamMaxWidth ? FA_ERR_UNSUPPORTED : FA_OK;
 }
 
 // 4-D 16-bit tensor map, x contiguous: extents and (for y, z, w) strides in elements, boxes of 64
@@ -1111,6 +1147,183 @@ int fa_debug_paged_pieces(const int *kv_len, const int *q_start, int T, int B, i
     return n;
 }
 
+int fa_paged_free(int *block_table, const int *keep_len, int *refs, int B, int num_pages, int page_size,
+                  int max_pages, void *stream) {
+    if (keep_len == nullptr || !aligned4(keep_len)) return FA_ERR_INVALID;
+    fa::PagedFreeParams p = {};
+    int rc = check_tables(block_table, refs, B, num_pages, page_size, max_pages, &p.t);
+    if (rc != FA_OK) return rc;
+    p.keep_len = keep_len;
+    cudaError_t e = fa::launch_paged_free(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_paged_fork(int *block_table, int *kv_len, const int *parents, int *refs, int B, int num_pages,
+                  int max_pages, void *stream) {
+    if (parents == nullptr || !aligned4(parents) || !aligned4(kv_len)) return FA_ERR_INVALID;
+    fa::PagedForkParams p = {};
+    int rc = check_tables(block_table, refs, B, num_pages, 8, max_pages, &p.t);
+    if (rc != FA_OK) return rc;
+    p.kv_len = kv_len;
+    p.parents = parents;
+    cudaError_t e = fa::launch_paged_fork(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_paged_reserve_workspace_bytes(int T, int B, int page_size) {
+    fa::PagedView c = {};
+    if (check_paged(T, B, 1, 1, 64, 1, page_size, 1, FA_BF16, &c) != FA_OK) return 0;
+    return round256(sizeof(int) * static_cast<size_t>(reserve_items(T, B, page_size)));
+}
+
+int fa_paged_reserve(int *block_table, const int *kv_len, const int *q_start, int *refs, int *copies, int T,
+                     int B, int num_pages, int page_size, int max_pages, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+    fa::PagedReserveParams p = {};
+    int rc = check_paged(T, B, 1, 1, 64, num_pages, page_size, max_pages, FA_BF16, &p.c);
+    if (rc != FA_OK) return rc;
+    rc = check_paged_index(block_table, kv_len, q_start, &p.c);
+    if (rc != FA_OK) return rc;
+    rc = check_ptrs({workspace});
+    if (rc != FA_OK) return rc;
+    if (!aligned4(copies) || reserve_items(T, B, page_size) >= (1l << 31) ||
+        workspace_bytes < fa_paged_reserve_workspace_bytes(T, B, page_size))
+        return FA_ERR_INVALID;
+    rc = check_tables(block_table, refs, B, num_pages, page_size, max_pages, &p.t);
+    if (rc != FA_OK) return rc;
+    p.c.status = p.t.status;
+    p.copies = copies;
+    p.fresh = static_cast<int *>(workspace);
+    cudaError_t e = fa::launch_paged_reserve(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_paged_compact_workspace_bytes(int num_pages) {
+    return num_pages < 1 ? 0 : round256(sizeof(int) * (static_cast<size_t>(num_pages) + 4));
+}
+
+int fa_paged_compact(int *block_table, int *refs, int *src, int *dst, int *count, int B, int num_pages,
+                     int max_pages, void *workspace, size_t workspace_bytes, void *stream) {
+    if (src == nullptr || dst == nullptr || count == nullptr || !aligned4(src) || !aligned4(dst) ||
+        !aligned4(count))
+        return FA_ERR_INVALID;
+    int rc = check_ptrs({workspace});
+    if (rc != FA_OK) return rc;
+    if (workspace_bytes < fa_paged_compact_workspace_bytes(num_pages)) return FA_ERR_INVALID;
+    fa::PagedCompactParams p = {};
+    rc = check_tables(block_table, refs, B, num_pages, 8, max_pages, &p.t);
+    if (rc != FA_OK) return rc;
+    p.src = src;
+    p.dst = dst;
+    p.count = count;
+    p.live = static_cast<int *>(workspace);
+    p.rank = p.live + 4;
+    cudaError_t e = fa::launch_paged_compact(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_paged_copy(void *k_pages, void *v_pages, const long long *strides, const int *src, const int *dst,
+                  const int *rows, const int *count, int n, int L, int H_kv, int d, int num_pages,
+                  int page_size, void *stream) {
+    fa::PagedView c = {};
+    int rc = check_paged(1, 1, H_kv, H_kv, d, num_pages, page_size, 1, FA_BF16, &c);
+    if (rc != FA_OK) return rc;
+    if (n < 1 || L < 1) return FA_ERR_INVALID;
+    rc = check_ptrs({k_pages, v_pages});
+    if (rc != FA_OK) return rc;
+    if (src == nullptr || dst == nullptr) return FA_ERR_INVALID;
+    for (const int *x : {src, dst, rows, count})
+        if (!aligned4(x)) return FA_ERR_INVALID;
+    const long long row = d, slab = static_cast<long long>(page_size) * d, page = H_kv * slab;
+    const long long dense[8] = {num_pages * page, page, slab, row, num_pages * page, page, slab, row};
+    const long long *given = strides != nullptr ? strides : dense;
+    long long s[8] = {};
+    for (int i = 0; i < 8; i += 4) {
+        rc = take_strides(given + i, {L, num_pages, H_kv, page_size}, true, s + i);
+        if (rc != FA_OK) return rc;
+    }
+    fa::PagedCopyParams p = {};
+    int dev = 0;
+    rc = device_setup(&dev, &p.status);
+    if (rc != FA_OK) return rc;
+    // runs along the axis whose pieces lie closer together (an axis of extent 1 is never that)
+    p.rows_inner = H_kv == 1 || (page_size > 1 && s[3] <= s[2]) ? 1 : 0;
+    auto side = [&](fa::PagedCopySide *x, void *base, const long long *t) {
+        x->base = static_cast<uint16_t *>(base);
+        x->layer = t[0];
+        x->page = t[1];
+        x->outer = p.rows_inner ? t[2] : t[3];
+        x->inner = p.rows_inner ? t[3] : t[2];
+    };
+    side(&p.k, k_pages, s);
+    side(&p.v, v_pages, s + 4);
+    p.src = src;
+    p.dst = dst;
+    p.rows = rows;
+    p.count = count;
+    p.n = n;
+    p.L = L;
+    p.num_pages = num_pages;
+    p.heads = H_kv;
+    p.page_size = page_size;
+    p.piece_shift = d == 64 ? 3 : 4;
+    cudaError_t e = fa::launch_paged_copy(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_beam_select_workspace_bytes(int B, int W, int V, int K) {
+    if (check_beam(B, W, V, K, FA_FP32) != FA_OK) return 0;
+    const size_t pieces = static_cast<size_t>(B) * W * beam_chunks(V);
+    return round256(pieces * K * sizeof(unsigned long long)) + round256(pieces * sizeof(float2));
+}
+
+int fa_beam_select(const void *logits, const long long *strides, const float *scores,
+                   const uint8_t *finished, float *out_scores, int *parents, int *tokens,
+                   uint8_t *out_finished, int B, int W, int V, int K, int dtype, int end_token,
+                   void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_beam(B, W, V, K, dtype);
+    if (rc != FA_OK) return rc;
+    const uintptr_t size = dtype == FA_FP32 ? 4 : 2;
+    if (logits == nullptr || reinterpret_cast<uintptr_t>(logits) % size != 0) return FA_ERR_INVALID;
+    for (const void *x : {static_cast<const void *>(scores), static_cast<const void *>(out_scores),
+                          static_cast<const void *>(parents), static_cast<const void *>(tokens)})
+        if (x == nullptr || !aligned4(x)) return FA_ERR_INVALID;
+    if (out_finished == nullptr) return FA_ERR_INVALID;
+    if (end_token < -1 || end_token >= V || (finished != nullptr && end_token < 0)) return FA_ERR_INVALID;
+    rc = check_ptrs({workspace});
+    if (rc != FA_OK) return rc;
+    if (workspace_bytes < fa_beam_select_workspace_bytes(B, W, V, K)) return FA_ERR_INVALID;
+    fa::BeamParams p = {};
+    p.stride_b = B == 1 ? 0 : strides != nullptr ? strides[0] : static_cast<long long>(W) * V;
+    p.stride_w = W == 1 ? 0 : strides != nullptr ? strides[1] : V;
+    for (const long x : {p.stride_b, p.stride_w})
+        if (x < 0 || x >= (1l << 39)) return FA_ERR_INVALID;
+    int dev = 0, *status = nullptr;
+    rc = device_setup(&dev, &status);
+    if (rc != FA_OK) return rc;
+    p.logits = logits;
+    p.scores = scores;
+    p.finished = finished;
+    p.out_scores = out_scores;
+    p.parents = parents;
+    p.tokens = tokens;
+    p.out_finished = out_finished;
+    p.B = B;
+    p.W = W;
+    p.V = V;
+    p.K = K;
+    p.end_token = end_token;
+    p.chunks = static_cast<int>(beam_chunks(V));
+    p.keys = static_cast<unsigned long long *>(workspace);
+    p.stats = reinterpret_cast<float2 *>(
+        static_cast<uint8_t *>(workspace) +
+        round256(static_cast<size_t>(B) * W * p.chunks * K * sizeof(unsigned long long)));
+    cudaError_t e = fa::launch_beam_select(
+        p, dtype == FA_FP32 ? fa::kBeamF32 : dtype == FA_BF16 ? fa::kBeamBF16 : fa::kBeamF16,
+        static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 int fa_sync_status(void *stream) {
     int dev = 0, *status = nullptr;
     int rc = device_setup(&dev, &status);
@@ -1132,6 +1345,7 @@ const char *fa_status_string(int code) {
         case FA_ERR_CUDA: return "CUDA runtime error";
         case FA_ERR_TIMEOUT: return "device pipeline wait timed out";
         case FA_ERR_INDEX: return "page id, token offset or length out of range";
+        case FA_ERR_FULL: return "too few free pages";
         case FA_ERR_INTERNAL: return "kernel found its shared memory misaligned";
         default: return "unknown status";
     }

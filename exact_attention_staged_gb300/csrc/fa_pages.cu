@@ -1,0 +1,514 @@
+// fa_pages.cu - the upkeep of paged-cache tables: giving pages to new tokens, forking and freeing
+// sequences, moving the live pages together, copying pages.
+//
+// Sequences may hold the same page; refs counts the table entries (and whatever else the caller
+// counts) that hold each page, and a page is free where it is 0.  There is no other state: pages are
+// given out lowest id first, so the same calls give the same tables, whatever the order in which
+// blocks and atomics run.  Nothing is read back by the host.
+//
+// The index work is a few bytes per page, bound by the latency of a handful of dependent reads and
+// of the launch; copying is bound by HBM.
+#include "branch.h"
+#include "paged.cuh"
+
+#include <algorithm>
+#include <climits>
+#include <cooperative_groups.h>
+
+namespace fa {
+namespace {
+
+namespace cg = cooperative_groups;
+
+__device__ __forceinline__ void page_report(int *status, int code = kErrIndex) {
+    atomicCAS(status, 0, code);
+}
+
+// ------------------------------------------------------------------------------------------ free
+// Sequence b keeps the pages of its first keep_len[b] positions.  Every entry behind them is looked
+// at (pages may have been reserved ahead), a thread each.
+constexpr int kFreeThreads = 256;
+constexpr int kFreeCols = 1024;
+
+__global__ void __launch_bounds__(kFreeThreads) fa_paged_free_kernel(const PagedFreeParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const PageTables &t = p.t;
+    const int b = blockIdx.y;
+    const long cap = static_cast<long>(t.max_pages) << t.page_shift;
+    long keep = p.keep_len[b];
+    if (keep < 0 || keep > cap) {
+        if (threadIdx.x == 0) page_report(t.status);
+        keep = keep < 0 ? 0 : cap;
+    }
+    const int first = static_cast<int>((keep + (1l << t.page_shift) - 1) >> t.page_shift);
+    const long end = min(static_cast<long>(t.max_pages), (blockIdx.x + 1l) * kFreeCols);
+    for (long i = blockIdx.x * static_cast<long>(kFreeCols) + threadIdx.x; i < end; i += kFreeThreads) {
+        if (i < first) continue;
+        int *at = t.table + static_cast<long>(b) * t.max_pages + i;
+        const int e = *at;
+        if (e == -1) continue;
+        *at = -1;
+        if (e < 0 || e >= t.num_pages) {
+            page_report(t.status);
+        } else if (atomicSub(&t.refs[e], 1) <= 0) {  // held by more entries than were counted
+            atomicAdd(&t.refs[e], 1);
+            page_report(t.status);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------ fork
+// Row b becomes row parents[b].  A block takes `cols` columns of all rows, which are independent of
+// the others, into shared memory and writes them back permuted: in place, without a second table.  A
+// page's count changes by the row's new holders less one.
+constexpr int kForkThreads = 256;
+
+__global__ void __launch_bounds__(kForkThreads) fa_paged_fork_kernel(const PagedForkParams p) {
+    extern __shared__ int fork_smem[];
+    const PageTables &t = p.t;
+    const int B = t.B, cols = p.cols;
+    int *parent = fork_smem, *children = fork_smem + B, *tile = fork_smem + 2 * B;
+    for (int b = threadIdx.x; b < B; b += kForkThreads) children[b] = 0;
+    griddep_launch_dependents();
+    griddep_wait();
+    __syncthreads();
+    for (int b = threadIdx.x; b < B; b += kForkThreads) {
+        int q = p.parents[b];
+        if (q < -1 || q >= B) {
+            if (blockIdx.x == 0) page_report(t.status);
+            q = b;
+        }
+        parent[b] = q;
+        if (q >= 0) atomicAdd(&children[q], 1);
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && p.kv_len != nullptr) {
+        int *len = tile;  // before the columns use it
+        for (int b = threadIdx.x; b < B; b += kForkThreads) len[b] = p.kv_len[b];
+        __syncthreads();
+        for (int b = threadIdx.x; b < B; b += kForkThreads)
+            if (parent[b] != b) p.kv_len[b] = parent[b] >= 0 ? len[parent[b]] : 0;
+        __syncthreads();
+    }
+    const int c0 = blockIdx.x * cols, width = min(cols, t.max_pages - c0);
+    for (int x = threadIdx.x; x < B * cols; x += kForkThreads) {
+        const int b = x / cols, c = x - b * cols;
+        if (c >= width || (parent[b] == b && children[b] == 1)) continue;
+        tile[x] = t.table[static_cast<long>(b) * t.max_pages + c0 + c];
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < B * cols; x += kForkThreads) {
+        const int b = x / cols, c = x - b * cols;
+        if (c >= width || (parent[b] == b && children[b] == 1)) continue;
+        const int e = tile[x], more = children[b] - 1;
+        if (e >= 0 && more != 0) {
+            if (e >= t.num_pages) {
+                page_report(t.status);
+            } else if (atomicAdd(&t.refs[e], more) + more < 0) {
+                page_report(t.status);
+            }
+        }
+        if (parent[b] == b) continue;
+        const int now = parent[b] >= 0 ? tile[parent[b] * cols + c] : -1;
+        if (now != e) t.table[static_cast<long>(b) * t.max_pages + c0 + c] = now;
+    }
+}
+
+// --------------------------------------------------------------------------------------- reserve
+// One cluster does all of it (a CTA where there is little), in steps with a barrier between them.
+// An item is a page place that a sequence's new tokens write to; items are numbered by sequence,
+// then place, and so are the pages that they get.
+//   1  every item that has a page gives its hold back: refs becomes the holders that do not write
+//   2  where none is left, the items that had the page compete for it with their numbers
+//   3  the lowest keeps it; all other items, and those that had none, are left with -1; needs and
+//      free pages are counted
+//   4  the free pages are listed by rank, as far as they are needed
+//   5  item after item takes the page of its rank
+constexpr int kReserveThreads = 1024;
+constexpr int kReserveCtas = 8;  // the portable cluster size
+
+// Exclusive prefix of x over the CTA's threads, and the sum; `scratch` holds 33 ints.
+__device__ __forceinline__ int block_scan(int x, int *scratch, int *sum) {
+    const int lane = lane_id(), w = warp_id();
+    int upto = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    __syncthreads();  // the scratch of the call before has been read
+    if (lane == 31) scratch[w] = upto;
+    __syncthreads();
+    if (w == 0) {
+        const int n = static_cast<int>(blockDim.x >> 5);
+        int v = lane < n ? scratch[lane] : 0, s = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        if (lane < n) scratch[lane] = s - v;
+        if (lane == 31) scratch[32] = s;
+    }
+    __syncthreads();
+    *sum = scratch[32];
+    return scratch[w] + upto - x;
+}
+
+// Whether refs of the four pages from i on (0 behind the end) make them free, as bits.
+__device__ __forceinline__ int free_bits(const int *refs, long i, long end) {
+    if (i >= end) return 0;
+    int r[4] = {1, 1, 1, 1};
+    if (i + 4 <= end) {
+        const int4 v = __ldcg(reinterpret_cast<const int4 *>(refs + i));
+        r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+    } else {
+        for (int k = 0; i + k < end; ++k) r[k] = __ldcg(refs + i + k);
+    }
+    return (r[0] == 0) | (r[1] == 0) << 1 | (r[2] == 0) << 2 | (r[3] == 0) << 3;
+}
+
+__global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const PagedReserveParams p) {
+    extern __shared__ int before[];  // [B + 1] items before each sequence's
+    __shared__ int scratch[33];
+    __shared__ int counts[2];        // this CTA's needs and free pages
+    griddep_launch_dependents();
+    griddep_wait();
+    cg::cluster_group cluster = cg::this_cluster();
+    const PageTables &t = p.t;
+    const int B = t.B, tid = threadIdx.x;
+    const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
+
+    // a sequence's first place, and how many its tokens write to
+    auto places = [&](int b, int *first, int *ctx) {
+        const PagedSeq s = paged_seq(p.c, b);
+        *ctx = max(s.ctx, 0);
+        *first = *ctx >> t.page_shift;
+        if (s.bad && cta == 0) page_report(t.status);
+        if (s.bad || s.n == 0 || s.len == 0) return 0;
+        return ((s.len - 1) >> t.page_shift) + 1 - *first;
+    };
+    // offsets in order are what bounds the items by the batch's tokens: others reserve nothing
+    bool ordered = true;
+    for (int b = tid; b < B; b += kReserveThreads) {
+        if (p.c.q_start != nullptr && p.c.q_start[b + 1] < p.c.q_start[b]) ordered = false;
+        if (p.copies != nullptr && cta == 0) {
+            p.copies[b] = p.copies[B + b] = -1;
+            p.copies[2 * B + b] = 0;
+        }
+    }
+    if (__syncthreads_and(ordered) == 0) {
+        if (tid == 0 && cta == 0) page_report(t.status);
+        return;
+    }
+    int items = 0;
+    for (int b0 = 0; b0 < B; b0 += kReserveThreads) {
+        const int b = b0 + tid;
+        int first, ctx, sum;
+        const int n = b < B ? places(b, &first, &ctx) : 0;
+        const int x = block_scan(n, scratch, &sum);
+        if (b < B) before[b] = items + x;
+        items += sum;
+    }
+    if (tid == 0) before[B] = items;
+    __syncthreads();
+    const int per = (items + ctas - 1) / ctas;
+    const int lo = min(items, cta * per), hi = min(items, lo + per);
+    // the sequence of item g, and its entry
+    auto find = [&](int g, int *b) {
+        int l = 0, r = B;  // before[l] <= g < before[r]
+        while (r - l > 1) {
+            const int m = (l + r) / 2;
+            if (before[m] <= g) l = m;
+            else r = m;
+        }
+        *b = l;
+        const PagedSeq s = paged_seq(p.c, l);
+        return t.table + static_cast<long>(l) * t.max_pages + (max(s.ctx, 0) >> t.page_shift) + g - before[l];
+    };
+
+    for (int g = lo + tid; g < hi; g += kReserveThreads) {
+        int b;
+        const int e = *find(g, &b);
+        if (e >= 0 && e < t.num_pages) atomicSub(&t.refs[e], 1);
+        else if (e != -1) page_report(t.status);
+    }
+    cluster.sync();
+    for (int g = lo + tid; g < hi; g += kReserveThreads) {
+        int b;
+        const int e = *find(g, &b);
+        if (e >= 0 && e < t.num_pages && __ldcg(&t.refs[e]) <= 0) atomicMin(&t.refs[e], INT_MIN + g);
+    }
+    cluster.sync();
+    int needs = 0;
+    for (int g = lo + tid; g < hi; g += kReserveThreads) {
+        int b;
+        int *at = find(g, &b);
+        const int e = *at;
+        const bool had = e >= 0 && e < t.num_pages;
+        if (had && __ldcg(&t.refs[e]) == INT_MIN + g) {
+            t.refs[e] = 1;
+            continue;
+        }
+        ++needs;
+        *at = -1;
+        if (had && p.copies != nullptr && g == before[b]) {
+            const int rows = max(paged_seq(p.c, b).ctx, 0) & ((1 << t.page_shift) - 1);
+            if (rows > 0) {
+                p.copies[b] = e;
+                p.copies[2 * B + b] = rows;
+            }
+        }
+    }
+    // this CTA's share of the pool, in whole groups of four pages
+    const long share = ((t.num_pages + 3l) / 4 + ctas - 1) / ctas * 4;
+    const long from = min(static_cast<long>(t.num_pages), cta * share);
+    const long to = min(static_cast<long>(t.num_pages), from + share);
+    int frees = 0;
+    for (long i = from + 4 * tid; i < to; i += 4 * kReserveThreads) frees += __popc(free_bits(t.refs, i, to));
+    int sum;
+    block_scan(needs, scratch, &sum);
+    if (tid == 0) counts[0] = sum;
+    block_scan(frees, scratch, &sum);
+    if (tid == 0) counts[1] = sum;
+    cluster.sync();
+    int need_before = 0, need_all = 0, free_before = 0, free_all = 0;
+    for (int c = 0; c < ctas; ++c) {
+        const int *other = cluster.map_shared_rank(counts, c);
+        if (c < cta) need_before += other[0], free_before += other[1];
+        need_all += other[0], free_all += other[1];
+    }
+    for (long i0 = from; i0 < to && free_before < need_all; i0 += 4 * kReserveThreads) {
+        const long i = i0 + 4 * tid;
+        const int bits = free_bits(t.refs, i, to);
+        int rank = free_before + block_scan(__popc(bits), scratch, &sum);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (bits >> k & 1) {
+                if (rank < need_all) p.fresh[rank] = static_cast<int>(i + k);
+                ++rank;
+            }
+        free_before += sum;
+    }
+    cluster.sync();  // also: nobody's counts are read any more
+    for (int g0 = lo; g0 < hi; g0 += kReserveThreads) {
+        const int g = g0 + tid;
+        int b = 0, *at = nullptr;
+        if (g < hi) at = find(g, &b);
+        const bool need = at != nullptr && *at == -1;
+        const int rank = need_before + block_scan(need, scratch, &sum);
+        need_before += sum;
+        if (!need) continue;
+        const int page = rank < free_all ? __ldcg(&p.fresh[rank]) : -1;
+        const bool copied = p.copies != nullptr && g == before[b] && __ldcg(&p.copies[b]) >= 0;
+        if (page >= 0) {
+            *at = page;
+            t.refs[page] = 1;
+            if (copied) p.copies[B + b] = page;
+        } else {
+            page_report(t.status, kErrFull);
+            if (copied) {
+                p.copies[b] = -1;
+                p.copies[2 * B + b] = 0;
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------------------------------------- compact
+// n live pages; the k-th live page at or behind n moves to the k-th free page before n.  With
+// live(i) the live pages before i, a free page i < n is number i - live(i) of the free ones, and a
+// live page i >= n makes move live(i) - live(n).
+__global__ void __launch_bounds__(kReserveThreads) fa_paged_plan_kernel(const PagedCompactParams p) {
+    __shared__ int scratch[33];
+    __shared__ int counts[2];  // this CTA's live pages; those of them before n
+    griddep_launch_dependents();
+    griddep_wait();
+    cg::cluster_group cluster = cg::this_cluster();
+    const PageTables &t = p.t;
+    const int tid = threadIdx.x;
+    const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
+    const long share = ((t.num_pages + 3l) / 4 + ctas - 1) / ctas * 4;
+    const long from = min(static_cast<long>(t.num_pages), cta * share);
+    const long to = min(static_cast<long>(t.num_pages), from + share);
+    auto live_of = [&](long i, long end) {
+        const int there = static_cast<int>(max(0l, min(4l, end - i)));
+        return there - __popc(free_bits(t.refs, i, end));
+    };
+    int sum, mine = 0;
+    for (long i = from + 4 * tid; i < to; i += 4 * kReserveThreads) mine += live_of(i, to);
+    block_scan(mine, scratch, &sum);
+    if (tid == 0) counts[0] = sum;
+    cluster.sync();
+    int n = 0, live = 0;  // live pages in all, and before this CTA's share
+    for (int c = 0; c < ctas; ++c) {
+        const int x = cluster.map_shared_rank(counts, c)[0];
+        n += x;
+        if (c < cta) live += x;
+    }
+    mine = 0;
+    const long border = min(to, static_cast<long>(n));
+    for (long i = from + 4 * tid; i < border; i += 4 * kReserveThreads) mine += live_of(i, border);
+    block_scan(mine, scratch, &sum);
+    if (tid == 0) counts[1] = sum;
+    cluster.sync();
+    int front = 0;  // live pages before n
+    for (int c = 0; c < ctas; ++c) front += cluster.map_shared_rank(counts, c)[1];
+    if (cta == 0 && tid == 0) {
+        *p.count = n - front;
+        *p.live = n;
+    }
+    for (long i0 = from; i0 < to; i0 += 4 * kReserveThreads) {
+        const long i = i0 + 4 * tid;
+        const int bits = free_bits(t.refs, i, to);
+        int at = live + block_scan(live_of(i, to), scratch, &sum);
+        for (int k = 0; k < 4 && i + k < to; ++k) {
+            const int id = static_cast<int>(i + k);
+            const bool is_free = bits >> k & 1;
+            if (id < n && is_free) p.dst[id - at] = id;
+            if (id >= n) p.rank[id] = is_free ? -1 : at - front;
+            if (id >= n && !is_free) p.src[at - front] = id;
+            if (!is_free) ++at;
+        }
+        live += sum;
+    }
+    cluster.sync();  // nobody's counts are read any more
+}
+
+__global__ void __launch_bounds__(256) fa_paged_apply_kernel(const PagedCompactParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const PageTables &t = p.t;
+    const int n = *p.live, moves = *p.count;
+    const long threads = static_cast<long>(gridDim.x) * 256, me = blockIdx.x * 256l + threadIdx.x;
+    for (long i = me; i < moves; i += threads) {
+        t.refs[p.dst[i]] = t.refs[p.src[i]];
+        t.refs[p.src[i]] = 0;
+    }
+    const long entries = static_cast<long>(t.B) * t.max_pages;
+    for (long i = me; i < entries; i += threads) {
+        const int e = t.table[i];
+        if (e < n && e >= -1) continue;
+        const int r = e >= 0 && e < t.num_pages ? p.rank[e] : -1;
+        if (r >= 0) t.table[i] = p.dst[r];
+        else page_report(t.status);  // no page, or one that nobody holds
+    }
+}
+
+// ------------------------------------------------------------------------------------------ copy
+// A warp copies a run: consecutive 16-byte pieces of one page of one layer.  Runs are a head's rows
+// or, where the heads of a token lie side by side, a row's heads.
+constexpr int kCopyWarps = 8;
+constexpr int kCopyBatch = 8;  // pieces of a lane in flight together
+
+__global__ void __launch_bounds__(kCopyWarps * 32) fa_paged_copy_kernel(const PagedCopyParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int n = p.count != nullptr ? min(max(*p.count, 0), p.n) : p.n;
+    const int runs = p.rows_inner ? p.heads : p.page_size;  // of a page
+    const long units = static_cast<long>(n) * p.L * 2 * runs;
+    const long warps = static_cast<long>(gridDim.x) * kCopyWarps;
+    for (long u = blockIdx.x * static_cast<long>(kCopyWarps) + warp_id(); u < units; u += warps) {
+        long x = u / runs;
+        const int run = static_cast<int>(u - x * runs);
+        const bool isv = x & 1;
+        x >>= 1;
+        const int e = static_cast<int>(x / p.L), layer = static_cast<int>(x - static_cast<long>(e) * p.L);
+        const int src = p.src[e], dst = p.dst[e];
+        int rows = p.rows != nullptr ? p.rows[e] : p.page_size;
+        if (src < 0 || dst < 0) continue;
+        if (src >= p.num_pages || dst >= p.num_pages || rows < 0 || rows > p.page_size) {
+            if (lane_id() == 0) page_report(p.status);
+            continue;
+        }
+        if (!p.rows_inner && run >= rows) continue;
+        const int inners = p.rows_inner ? rows : p.heads;
+        const PagedCopySide &s = isv ? p.v : p.k;
+        const uint16_t *from = s.base + layer * s.layer + src * s.page + run * s.outer;
+        uint16_t *to = s.base + layer * s.layer + dst * s.page + run * s.outer;
+        const int pieces = inners << p.piece_shift;
+        for (int i0 = lane_id(); i0 < pieces; i0 += 32 * kCopyBatch) {
+            uint4 v[kCopyBatch];
+            long off[kCopyBatch];
+#pragma unroll
+            for (int k = 0; k < kCopyBatch; ++k) {
+                const int i = i0 + 32 * k;
+                off[k] = (i >> p.piece_shift) * s.inner + (i & ((1 << p.piece_shift) - 1)) * 8;
+                if (i < pieces) v[k] = *reinterpret_cast<const uint4 *>(from + off[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kCopyBatch; ++k)
+                if (i0 + 32 * k < pieces) *reinterpret_cast<uint4 *>(to + off[k]) = v[k];
+        }
+    }
+}
+
+// A launch of one cluster that may overlap the end of the grid before it.
+template <class Params>
+cudaError_t launch_cluster(void (*kernel)(Params), int ctas, size_t smem, cudaStream_t stream,
+                           const Params &p) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kReserveThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_free(const PagedFreeParams &p, cudaStream_t stream) {
+    const dim3 grid((p.t.max_pages - 1) / kFreeCols + 1, p.t.B);
+    return launch_overlapped(fa_paged_free_kernel, grid, kFreeThreads, 0, stream, p);
+}
+
+cudaError_t launch_paged_fork(PagedForkParams p, cudaStream_t stream) {
+    p.cols = 32;
+    auto bytes = [&] { return sizeof(int) * p.t.B * (2 + static_cast<size_t>(p.cols)); };
+    while (p.cols > 1 && bytes() > 100 * 1024) p.cols /= 2;
+    if (bytes() > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            fa_paged_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes()));
+        if (e != cudaSuccess) return e;
+    }
+    return launch_overlapped(fa_paged_fork_kernel, dim3((p.t.max_pages - 1) / p.cols + 1), kForkThreads,
+                             bytes(), stream, p);
+}
+
+cudaError_t launch_paged_reserve(const PagedReserveParams &p, cudaStream_t stream) {
+    const long items = (static_cast<long>(p.c.T) >> p.t.page_shift) + 2l * p.t.B;
+    const int ctas = items <= kReserveThreads && p.t.num_pages <= 8 * kReserveThreads ? 1 : kReserveCtas;
+    return launch_cluster(fa_paged_reserve_kernel, ctas, sizeof(int) * (p.t.B + 1), stream, p);
+}
+
+cudaError_t launch_paged_compact(const PagedCompactParams &p, cudaStream_t stream) {
+    const int ctas = p.t.num_pages <= 8 * kReserveThreads ? 1 : kReserveCtas;
+    const cudaError_t e = launch_cluster(fa_paged_plan_kernel, ctas, 0, stream, p);
+    if (e != cudaSuccess) return e;
+    const long work = std::max(static_cast<long>(p.t.B) * p.t.max_pages, static_cast<long>(p.t.num_pages) / 2);
+    const long blocks = std::min((work + 255) / 256, 152l * 8);
+    return launch_overlapped(fa_paged_apply_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, p);
+}
+
+cudaError_t launch_paged_copy(const PagedCopyParams &p, cudaStream_t stream) {
+    const long units = static_cast<long>(p.n) * p.L * 2 * (p.rows_inner ? p.heads : p.page_size);
+    const long blocks = std::min((units + kCopyWarps - 1) / kCopyWarps, 152l * 8);
+    return launch_overlapped(fa_paged_copy_kernel, dim3(static_cast<unsigned>(blocks)), kCopyWarps * 32, 0,
+                             stream, p);
+}
+
+}  // namespace fa

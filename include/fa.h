@@ -47,7 +47,7 @@
 extern "C" {
 #endif
 
-typedef enum { FA_FP16 = 0, FA_BF16 = 1 } fa_dtype;
+typedef enum { FA_FP16 = 0, FA_BF16 = 1, FA_FP32 = 2 /* fa_beam_select's logits only */ } fa_dtype;
 
 enum {
     FA_OK = 0,
@@ -58,6 +58,7 @@ enum {
     FA_ERR_INTERNAL = -5,     /* a kernel found its shared memory misplaced (its base not
                                  1024-byte aligned) and returned without computing; never
                                  expected (from fa_sync_status) */
+    FA_ERR_FULL = -7,         /* fa_paged_reserve found too few free pages (from fa_sync_status) */
     FA_ERR_INDEX = -6         /* an index array on the device (page ids, token offsets, lengths)
                                  holds a value out of range; what it named was not accessed
                                  (from fa_sync_status), or fa_paged_check found it on the host */
@@ -370,11 +371,108 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
                   void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Keeping a paged cache's tables.  Everything below happens on the device, in the order of the stream:
+ * a serving step that branches, grows and drops sequences reads nothing back, and can be captured.
+ *   block_table : device int32 [B, max_pages] as above, written by these calls.  An entry is a page id,
+ *               or -1 for none; a table starts out as -1 everywhere.  Every entry of a row counts,
+ *               those behind the sequence's length too (pages reserved ahead).
+ *   refs      : device int32 [num_pages], 16-byte aligned: how many entries hold each page, plus whatever
+ *               the caller adds for holds of its own (a prefix to be kept).  A page is free where refs
+ *               is 0; refs starts out as zeros.
+ * These two are the whole state; the calls leave them consistent, give pages out lowest id first, and
+ * so always come to the same tables.  At most 32768 sequences (otherwise FA_ERR_UNSUPPORTED); calls on
+ * one table or one refs array have to be ordered by the caller.  Values out of range are not
+ * followed and reported as FA_ERR_INDEX by fa_sync_status(), as is a count that would fall below
+ * zero or an entry that names a free page.
+ *
+ * fa_paged_reserve: after it, every page that the batch's new tokens (kv_len, q_start, T as in
+ * fa_paged_append) will be written to is held by their sequence alone.  In order of sequence and
+ * position: a place without a page gets a free one; a place whose page others hold too gets a free one in
+ * its stead, unless all its holders are places of this call: then the first of them keeps the page.
+ *   copies    : device int32 [3, B], or NULL: row 0 names the page to copy from, row 1 the one to copy to
+ *               and row 2 the rows to copy, for every sequence whose first new token goes behind tokens
+ *               on a page that it shared (-1, -1, 0 for the others): arguments for fa_paged_copy.
+ *   Sequences with a length or offset out of range get nothing, and none does where offsets decrease.
+ *   Where the free pages run out, the places that are left get -1 (FA_ERR_FULL from fa_sync_status): a shared page's hold is given
+ *   back, nobody else's pages are touched, and appending there is refused as usual.
+ *   workspace : at least fa_paged_reserve_workspace_bytes() bytes, 16-byte aligned, as in fa_paged_attn.
+ *
+ * fa_paged_fork: row b becomes what row parents[b] was; both hold its pages from then on.
+ *   parents   : device int32 [B]: -1 leaves row b empty, parents[b] = b as it is; any row may have many
+ *               children or none (its pages are given back).
+ *   kv_len    : device int32 [B], permuted likewise (0 for an empty row), or NULL.
+ *
+ * fa_paged_free: sequence b keeps the pages of its first keep_len[b] positions (device int32 [B]; 0: a
+ * sequence that ends, less than its length: drafted tokens that were refused) and gives the others back.
+ *
+ * fa_paged_compact: moves the live pages to the front of the pool: with n of them, the k-th of those with
+ * ids from n on takes the place of the k-th free page before n.  Table and refs follow; the data has to be
+ * moved by fa_paged_copy with the lists that it leaves:
+ *   src, dst  : device int32 [num_pages / 2], of which the first *count are written (the others stay).
+ *   count     : device int32, how many pages move.
+ *   workspace : at least fa_paged_compact_workspace_bytes() bytes, 16-byte aligned.
+ * fa_paged_compact and fa_paged_fork need no page size: max_pages is below 2^28.
+ *
+ * fa_paged_copy: the first rows[i] rows (rows NULL: all) of page src[i] to page dst[i], of all heads, of K
+ * and of V, in all layers, for i < n.
+ *   k_pages, v_pages : L layers of pages, as in fa_paged_append; written.
+ *   strides   : host array of 8 strides in elements: layer, page, head and row of k_pages and of v_pages;
+ *               NULL for dense tensors [L, num_pages, H_kv, page_size, d]; limits as for the outputs in
+ *               fa_rope.
+ *   src, dst, rows : device int32 [n].  Pairs with a negative page are left out.  A page may be copied to
+ *               many; one that is copied to must not occur otherwise.
+ *   count     : device int32: no more than that many pairs, or NULL.
+ */
+size_t fa_paged_reserve_workspace_bytes(int T, int B, int page_size);
+int fa_paged_reserve(int *block_table, const int *kv_len, const int *q_start, int *refs, int *copies,
+                     int T, int B, int num_pages, int page_size, int max_pages, void *workspace,
+                     size_t workspace_bytes, void *stream);
+int fa_paged_fork(int *block_table, int *kv_len, const int *parents, int *refs, int B, int num_pages,
+                  int max_pages, void *stream);
+int fa_paged_free(int *block_table, const int *keep_len, int *refs, int B, int num_pages,
+                  int page_size, int max_pages, void *stream);
+size_t fa_paged_compact_workspace_bytes(int num_pages);
+int fa_paged_compact(int *block_table, int *refs, int *src, int *dst, int *count, int B, int num_pages,
+                     int max_pages, void *workspace, size_t workspace_bytes, void *stream);
+int fa_paged_copy(void *k_pages, void *v_pages, const long long *strides, const int *src,
+                  const int *dst, const int *rows, const int *count, int n, int L, int H_kv, int d,
+                  int num_pages, int page_size, void *stream);
+
+/*
+ * Beam search's selection.  Each of B requests has W beams; candidate (w, v) continues beam w with token v
+ * and scores scores[b][w] + logits[b][w][v] - ln sum_u e^logits[b][w][u].  The K best candidates of a
+ * request are returned, best first, equal ones by the lowest w V + v; scores are compared before they
+ * are rounded to fp32.
+ *   logits    : device [B, W, V] of FA_FP16, FA_BF16 or FA_FP32 (dtype), aligned to an element.
+ *   strides   : host array of 2 strides in elements (request, beam), at least 0 and below 2^39; NULL for a
+ *               dense tensor.
+ *   scores    : device fp32 [B, W].
+ *   finished  : device uint8 [B, W], or NULL.  A beam that has ended (not 0) has one candidate: end_token,
+ *               with the beam's score.  Its logits are not read.
+ *   end_token : -1 for none (only without finished).
+ *   out_scores, parents, tokens, out_finished : device [B, K]; parents (int32) are places in the batch,
+ *               b W + w, as fa_paged_fork wants them where K = W; out_finished (uint8) is 1 where the
+ *               token is end_token or the parent had ended.
+ * Only finite scores are candidates: a token of logit -inf is none, nor is any of a beam whose score or
+ * whose logits' sum is not finite (a NaN or +inf among them).  Where a request has fewer than K, the
+ * places left have score -inf, parent and token -1 and out_finished 1.
+ * W V, B K and B W ceil(V / 8192) are below 2^31; K is at most 128 and W at most 2048 (otherwise
+ * FA_ERR_UNSUPPORTED).  Sums are fp32.
+ *   workspace : at least fa_beam_select_workspace_bytes() bytes, 16-byte aligned, as in fa_paged_attn.
+ */
+size_t fa_beam_select_workspace_bytes(int B, int W, int V, int K);
+int fa_beam_select(const void *logits, const long long *strides, const float *scores,
+                   const uint8_t *finished, float *out_scores, int *parents, int *tokens,
+                   uint8_t *out_finished, int B, int W, int V, int K, int dtype, int end_token,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronises `stream`, then returns and clears the current device's status word:
  * FA_OK, FA_ERR_TIMEOUT (a kernel gave up on a pipeline wait and returned early; its outputs
  * are undefined), FA_ERR_INTERNAL (a kernel refused to run on a misaligned shared-memory base;
- * its outputs are undefined), FA_ERR_INDEX (a paged call met an index out of range; reported only
- * where neither of the other two is) or FA_ERR_CUDA (the stream reported an error).
+ * its outputs are undefined), FA_ERR_INDEX (a paged call met an index out of range), FA_ERR_FULL (a cache
+ * ran out of pages; the first of these two that was met is reported, where neither of the other two
+ * is) or FA_ERR_CUDA (the stream reported an error).
  */
 int fa_sync_status(void *stream);
 
