@@ -67,9 +67,9 @@ struct BeamParams {
     int *parents, *tokens;           // [B, K]
     uint8_t *out_finished;           // [B, K]
     int B, W, V, K, end_token;
-    int chunks;                      // pieces of a row
-    unsigned long long *keys;        // workspace [B * W][chunks][K]
-    float2 *stats;                   // workspace [B * W][chunks]: maximum, sum of e^(x - maximum)
+    int pieces, piece_len;           // pieces of a row, and their logits (whole tiles)
+    unsigned long long *keys;        // workspace [B * W][pieces][K]
+    float2 *stats;                   // workspace [B * W][pieces]: maximum, sum of e^(x - maximum)
 };
 
 cudaError_t launch_paged_reserve(const PagedReserveParams &p, cudaStream_t stream);
@@ -82,7 +82,17 @@ cudaError_t launch_paged_copy(const PagedCopyParams &p, cudaStream_t stream);
 constexpr int kBranchMaxSeqs = 32768;
 
 enum BeamType { kBeamF16 = 0, kBeamBF16 = 1, kBeamF32 = 2 };
-constexpr int kBeamChunk = 8192;   // logits of one piece of a row
+constexpr int kBeamThreads = 256;
+constexpr int kBeamTiles = 16;         // tiles of a piece, at most
+// Logits per load, 16 bytes or what the rows' starts are aligned to.
+inline int beam_vec(const void *logits, long stride_b, long stride_w, int type) {
+    const long size = type == kBeamF32 ? 4 : 2, most = 16 / size;
+    const long bits = static_cast<long>(reinterpret_cast<uintptr_t>(logits)) / size | stride_b | stride_w;
+    const long align = bits & -bits;  // 0: every row starts at address 0, as it were
+    return static_cast<int>(align == 0 || align > most ? most : align);
+}
+// A thread's logits of a tile: twice as many where a load brings several 16-bit ones.
+constexpr int beam_elems(int type, int vec) { return type != kBeamF32 && vec >= 4 ? 32 : 16; }
 constexpr int kBeamMaxK = 128;
 constexpr int kBeamMaxWidth = 2048;     // beams of a request
 cudaError_t launch_beam_select(const BeamParams &p, int type, cudaStream_t stream);

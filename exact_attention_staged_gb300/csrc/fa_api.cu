@@ -5,6 +5,7 @@
 #include "fa_internal.h"
 #include "paged.cuh"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cudaTypedefs.h>
@@ -541,12 +542,23 @@ bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 long reserve_items(int T, int B, int page_size) { return static_cast<long>(T) / page_size + 2l * B; }
 
-long beam_chunks(int V) { return (static_cast<long>(V) + fa::kBeamChunk - 1) / fa::kBeamChunk; }
+// Pieces of a beam's logits: whole tiles of `tile`, so many that all rows' pieces just find places at
+// once, four CTAs per SM (256 rows of 131072 bf16 logits take XX us in two pieces, XX in three).
+struct BeamPieces {
+    int pieces, len;
+};
+BeamPieces beam_pieces(int B, int W, int V, int tile) {
+    const long rows = static_cast<long>(B) * W;
+    const long tiles = (static_cast<long>(V) + tile - 1) / tile;
+    const long want = std::min(tiles, std::max(1l, 4l * 152 / rows));
+    const long each = std::min((tiles + want - 1) / want, static_cast<long>(fa::kBeamTiles));
+    return {static_cast<int>((tiles + each - 1) / each), static_cast<int>(each * tile)};
+}
 int check_beam(int B, int W, int V, int K, int dtype) {
     if (B < 1 || W < 1 || V < 1 || K < 1) return FA_ERR_INVALID;
     if (dtype != FA_FP16 && dtype != FA_BF16 && dtype != FA_FP32) return FA_ERR_INVALID;
     if (static_cast<long long>(W) * V >= (1ll << 31) || static_cast<long long>(B) * W >= (1ll << 31) ||
-        static_cast<long long>(B) * W * beam_chunks(V) >= (1ll << 31) ||
+        static_cast<long long>(B) * W * (V / 4096 + 1ll) >= (1ll << 31) ||
         static_cast<long long>(B) * K >= (1ll << 31))
         return FA_ERR_INVALID;
     return K > fa::kBeamMaxK || W > fa::kBeamMaxWidth ? FA_ERR_UNSUPPORTED : FA_OK;
@@ -1273,7 +1285,9 @@ int fa_paged_copy(void *k_pages, void *v_pages, const long long *strides, const 
 
 size_t fa_beam_select_workspace_bytes(int B, int W, int V, int K) {
     if (check_beam(B, W, V, K, FA_FP32) != FA_OK) return 0;
-    const size_t pieces = static_cast<size_t>(B) * W * beam_chunks(V);
+    int most = 0;  // whatever the logits' type and alignment
+    for (const int elems : {16, 32}) most = std::max(most, beam_pieces(B, W, V, elems * fa::kBeamThreads).pieces);
+    const size_t pieces = static_cast<size_t>(B) * W * most;
     return round256(pieces * K * sizeof(unsigned long long)) + round256(pieces * sizeof(float2));
 }
 
@@ -1313,14 +1327,16 @@ int fa_beam_select(const void *logits, const long long *strides, const float *sc
     p.V = V;
     p.K = K;
     p.end_token = end_token;
-    p.chunks = static_cast<int>(beam_chunks(V));
+    const int type = dtype == FA_FP32 ? fa::kBeamF32 : dtype == FA_BF16 ? fa::kBeamBF16 : fa::kBeamF16;
+    const int vec = fa::beam_vec(logits, p.stride_b, p.stride_w, type);
+    const BeamPieces pieces = beam_pieces(B, W, V, fa::kBeamThreads * fa::beam_elems(type, vec));
+    p.pieces = pieces.pieces;
+    p.piece_len = pieces.len;
     p.keys = static_cast<unsigned long long *>(workspace);
     p.stats = reinterpret_cast<float2 *>(
         static_cast<uint8_t *>(workspace) +
-        round256(static_cast<size_t>(B) * W * p.chunks * K * sizeof(unsigned long long)));
-    cudaError_t e = fa::launch_beam_select(
-        p, dtype == FA_FP32 ? fa::kBeamF32 : dtype == FA_BF16 ? fa::kBeamBF16 : fa::kBeamF16,
-        static_cast<cudaStream_t>(stream));
+        round256(static_cast<size_t>(B) * W * p.pieces * K * sizeof(unsigned long long)));
+    cudaError_t e = fa::launch_beam_select(p, type, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

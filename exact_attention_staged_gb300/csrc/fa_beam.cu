@@ -3,28 +3,34 @@
 // Candidate (w, v) of a request continues beam w with token v and scores
 //   s(w, v) = score_w + x_wv - L_w,   L_w = ln sum_v e^x_wv,
 // and the K best of the W V candidates are wanted, equal ones by the lowest w V + v.  Within a row the
-// order of s is that of x, so a row's logits are read once: a CTA takes a piece of a row into
-// registers, finds its maximum m and sum of e^(x - m) (fp32; the maximum is known before the first
-// exponential) and its K largest x; a second, small grid joins the pieces' statistics and candidates of
-// a request.  Bound by reading the logits from HBM.
+// order of s is that of x, so a row's logits are read once: a CTA streams a piece of a row, tile after
+// tile with the next one's loads in flight, and keeps the sum of e^(x - m) with a running maximum m per
+// thread (fp32); a second, small grid joins the pieces' statistics and candidates of a request.  Bound by
+// reading the logits from HBM.
 //
-// The K largest of a piece: the K-th largest of the maxima of 64 (or 256) groups of its logits is a
-// bound that at least K logits reach and, the groups being a random partition as it were, not many
-// more.  Those that reach it are collected and ranked by counting.  Where too many do (a piece of
-// equal logits), the K-th largest is found by bisection, first on the value, then on the place.
+// The K largest of a piece: while streaming, a thread only notes the maximum of its logits of each tile.
+// The K-th largest maximum of groups of threads is then a bound that at least K logits reach and, the
+// groups being a random partition as it were, not many more; they stand where the noted maxima reach it, and
+// those few places are read again.  The loop has neither barriers nor shared counters (collecting
+// candidates in it took 34 us for 256 rows of 131072 bf16 logits, of which streaming alone is 14.4).
+// Where more logits reach the bound than there is room for (long runs of rising or equal logits), the
+// K-th largest is found by bisection over them.
 //
-// s is formed in 64 bits from the fp32 sums, so candidates of different beams are told apart well below
-// the fp32 spacing of the scores, to which the result is rounded once.
+// s is formed as an unevaluated sum of two fp32 numbers, so candidates of different beams are told apart
+// well below the fp32 spacing of the scores, to which the result is rounded once.
 #include "branch.h"
 
+#include <cstring>
 #include <type_traits>
 
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kElems = kBeamChunk / kThreads;  // logits of a thread
-constexpr int kCap = 1024;                     // candidates that are ranked by counting
+constexpr int kThreads = kBeamThreads;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCap = 512;                     // candidates that there is room for
+constexpr int kJoinThreads = 1024;
+constexpr int kJoinOwn = 4;                   // a thread's candidates that stay in registers
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -36,30 +42,57 @@ __device__ __forceinline__ unsigned order_of(float x) {
 __device__ __forceinline__ float value_of(unsigned u) {
     return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
-__device__ __forceinline__ unsigned long long order_of(double x) {
-    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
-    return u >> 63 ? ~u : u | 1ull << 63;
-}
-__device__ __forceinline__ double value_of(unsigned long long u) {
-    return __longlong_as_double(static_cast<long long>(u >> 63 ? u ^ 1ull << 63 : ~u));
+// The CTA's K-th largest of values[0 .. n), n a multiple of 4 no more than the threads, by counting; every
+// thread calls it and gets the result, which `out` passes on.
+__device__ __forceinline__ unsigned kth_largest(const unsigned *values, int n, int k, unsigned *out) {
+    const int tid = threadIdx.x;
+    if (tid < n) {
+        const unsigned mine = values[tid];
+        int rank = 0;
+        const uint4 *all = reinterpret_cast<const uint4 *>(values);
+#pragma unroll 4
+        for (int j = 0; j < n / 4; ++j) {
+            const uint4 x = all[j];
+            const int i = 4 * j;  // equal ones in order
+            rank += x.x > mine || (x.x == mine && i < tid);
+            rank += x.y > mine || (x.y == mine && i + 1 < tid);
+            rank += x.z > mine || (x.z == mine && i + 2 < tid);
+            rank += x.w > mine || (x.w == mine && i + 3 < tid);
+        }
+        if (rank == k - 1) *out = mine;
+    }
+    __syncthreads();
+    return *out;
 }
 
-// The k-th largest of the warp's 32 * N values (k at most that many), by bits from the top.
-template <int N>
-__device__ __forceinline__ unsigned kth_largest(const unsigned (&v)[N], int k) {
-    unsigned found = 0;
-#pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
-        const unsigned want = found | 1u << bit;
-        int n = 0;
+// The CTA keeps the k largest of n distinct keys (k < n <= kCap), largest first; `least` gets the last.
+// Ends without a barrier.
+__device__ __forceinline__ void keep_largest(unsigned long long *key, int n, int k,
+                                             unsigned long long *least) {
+    constexpr int kOwn = kCap / kThreads;
+    unsigned long long mine[kOwn];
+    int rank[kOwn];
 #pragma unroll
-        for (int i = 0; i < N; ++i) n += __popc(__ballot_sync(kAll, v[i] >= want));
-        if (n >= k) found = want;
+    for (int i = 0; i < kOwn; ++i) {
+        const int at = static_cast<int>(threadIdx.x) + i * kThreads;
+        rank[i] = k;
+        if (at < n) {
+            mine[i] = key[at];
+            rank[i] = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) rank[i] += key[j] > mine[i];
+        }
     }
-    return found;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        if (rank[i] < k) key[rank[i]] = mine[i];
+        if (rank[i] == k - 1) *least = mine[i];
+    }
 }
 
 // The sum of x over the CTA's threads, the same in each; `scratch` holds a word per warp.
+template <int THREADS = kThreads>
 __device__ __forceinline__ int block_sum(int x, int *scratch) {
     x = __reduce_add_sync(kAll, x);
     __syncthreads();
@@ -67,7 +100,7 @@ __device__ __forceinline__ int block_sum(int x, int *scratch) {
     __syncthreads();
     int s = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) s += scratch[w];
+    for (int w = 0; w < THREADS / 32; ++w) s += scratch[w];
     return s;
 }
 
@@ -90,316 +123,420 @@ __device__ __forceinline__ float beam_float(beam_elem<TYPE> x) {
     else return __half2float(x);
 }
 
-// VEC: logits per load, what the rows' alignment allows.
+// A thread's logits of a tile as they were loaded.  Logit i * VEC + k of the thread is number
+// (i * kThreads + tid) * VEC + k of the tile; behind the row's end they are -inf.
 template <int TYPE, int VEC>
-__global__ void __launch_bounds__(kThreads) fa_beam_piece_kernel(const BeamParams p) {
+struct BeamTile {
     using Elem = beam_elem<TYPE>;
     using Vec = typename VecOf<VEC * sizeof(Elem)>::type;
-    __shared__ unsigned groups[kThreads];
+    static constexpr int kElems = beam_elems(TYPE, VEC), kSize = kElems * kThreads;
+    Vec raw[kElems / VEC];
+
+    static __device__ __forceinline__ int place(int e) {
+        return (e / VEC * kThreads + static_cast<int>(threadIdx.x)) * VEC + e % VEC;
+    }
+    // x: the tile's first logit; left: how many there are to the end
+    __device__ __forceinline__ void load(const Elem *x, int left) {
+        if (left >= kSize) {
+#pragma unroll
+            for (int i = 0; i < kElems / VEC; ++i)
+                raw[i] = __ldcs(reinterpret_cast<const Vec *>(x + place(i * VEC)));
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kElems / VEC; ++i) {
+            const int at = place(i * VEC);
+            Elem e[VEC];
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                if (at + k < left) e[k] = x[at + k];
+                else if constexpr (TYPE == kBeamF32) e[k] = -INFINITY;
+                else if constexpr (TYPE == kBeamBF16) e[k] = __ushort_as_bfloat16(0xff80);
+                else e[k] = __ushort_as_half(0xfc00);
+            }
+            memcpy(&raw[i], e, sizeof(Vec));
+        }
+    }
+    __device__ __forceinline__ void floats(float (&v)[kElems]) const {
+        const Elem *e = reinterpret_cast<const Elem *>(raw);
+#pragma unroll
+        for (int k = 0; k < kElems; ++k) v[k] = beam_float<TYPE>(e[k]);
+    }
+};
+
+// VEC: logits per load, what the rows' alignment allows.
+template <int TYPE, int VEC>
+__global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamParams p) {
+    using Tile = BeamTile<TYPE, VEC>;
+    using Elem = typename Tile::Elem;
+    constexpr int kElems = Tile::kElems;
+    __shared__ float tops[kBeamTiles][kThreads];  // of each thread's logits of each tile
+    __shared__ __align__(16) unsigned groups[kThreads];
     __shared__ unsigned bound;
     __shared__ int found;
-    __shared__ int scratch[kThreads / 32];
-    __shared__ float sums[kThreads / 32];
-    __shared__ unsigned long long cand[kCap];
+    __shared__ int scratch[kWarps];
+    __shared__ float sums[kWarps];
+    __shared__ unsigned long long cand[kCap], last;
     griddep_launch_dependents();
     griddep_wait();
-    const int row = blockIdx.x / p.chunks, piece = blockIdx.x - row * p.chunks;
+    const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
     const int tid = threadIdx.x, lane = lane_id();
     if (p.finished != nullptr && p.finished[row] != 0) return;
     const int b = row / p.W, w = row - b * p.W;
-    const int v0 = piece * kBeamChunk, left = p.V - v0;
+    const int v0 = piece * p.piece_len, len = min(p.V - v0, p.piece_len);
     const Elem *x = static_cast<const Elem *>(p.logits) + b * p.stride_b + w * p.stride_w + v0;
-
-    // logit i * VEC + k of the thread is number (i * kThreads + tid) * VEC + k of the piece
-    float v[kElems];
-    auto place = [&](int e) { return (e / VEC * kThreads + tid) * VEC + e % VEC; };
-    Vec raw[kElems / VEC];
+    const int K = p.K;
+    const int tiles = (len - 1) / Tile::kSize + 1;
+    float m = -INFINITY, s = 0.f;  // this thread's maximum, and sum of e^(x - m)
+    Tile next;
+    next.load(x, len);
+#pragma unroll 1
+    for (int t = 0; t < tiles; ++t) {
+        float v[kElems];
+        next.floats(v);
+        const int after = (t + 1) * Tile::kSize;
+        if (t + 1 < tiles) next.load(x + after, len - after);
+        float a = fmax3(v[0], v[1], v[2]), c = fmax3(v[3], v[4], v[5]);
 #pragma unroll
-    for (int i = 0; i < kElems / VEC; ++i) {
-        if ((i * kThreads + tid) * VEC + VEC <= left)
-            raw[i] = __ldcs(reinterpret_cast<const Vec *>(x) + i * kThreads + tid);
-    }
-#pragma unroll
-    for (int i = 0; i < kElems / VEC; ++i) {
-        const int at = (i * kThreads + tid) * VEC;
-        const Elem *e = reinterpret_cast<const Elem *>(&raw[i]);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            if (at + VEC <= left) v[i * VEC + k] = beam_float<TYPE>(e[k]);
-            else v[i * VEC + k] = at + k < left ? beam_float<TYPE>(x[at + k]) : -INFINITY;
+        for (int e = 6; e + 3 < kElems; e += 4) {
+            a = fmax3(a, v[e], v[e + 1]);
+            c = fmax3(c, v[e + 2], v[e + 3]);
         }
-    }
-    float top = v[0];
+        const float top = fmax3(fmaxf(a, c), v[kElems - 2], v[kElems - 1]);
+        tops[t][tid] = top;
+        if (top > m) {
+            s *= ex2((m - top) * kLog2e);
+            m = top;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;  // nothing but -inf so far sums to 0
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                         make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int e = 1; e < kElems; ++e) top = fmaxf(top, v[e]);
-    // groups of four threads up to K = 64, of one behind that
-    const bool wide = p.K > 64;
-    const float four = fmaxf(fmaxf(top, __shfl_xor_sync(kAll, top, 1)),
-                             __shfl_xor_sync(kAll, fmaxf(top, __shfl_xor_sync(kAll, top, 1)), 2));
-    if (wide) groups[tid] = order_of(top);
-    else if ((lane & 3) == 0) groups[tid / 4] = order_of(four);
+        for (int e = 0; e < kElems; e += 2) {
+            // the difference first: its rounding is relative to itself, and 0 for the largest
+            const float2 y = fmul2(fsub2(make_float2(v[e], v[e + 1]), make_float2(ref, ref)),
+                                   make_float2(kLog2e, kLog2e));
+            acc[e / 2 & 3] = fadd2(acc[e / 2 & 3], make_float2(ex2(y.x), ex2(y.y)));
+        }
+        const float2 q = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+        s += q.x + q.y;
+    }
+
+    // groups of 8 threads, of 2 or of 1: about four times as many as wanted
+    const int width = K <= 16 ? 8 : K <= 64 ? 2 : 1;
+    float g = m;
+    for (int o = 1; o < width; o *= 2) g = fmaxf(g, __shfl_xor_sync(kAll, g, o));
+    if (tid % width == 0) groups[tid / width] = order_of(g);
     if (tid == 0) found = 0;
     __syncthreads();
-    unsigned most = 0;
-    if (wide) {
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) most = max(most, groups[lane + 32 * i]);
-    } else {
-        most = max(groups[lane], groups[lane + 32]);
-    }
-    most = __reduce_max_sync(kAll, most);
-    if (warp_id() == 0) {
-        unsigned t;
-        if (wide) {
-            unsigned g[kThreads / 32];
-#pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i) g[i] = groups[lane + 32 * i];
-            t = kth_largest(g, p.K);
-        } else {
-            const unsigned g[2] = {groups[lane], groups[lane + 32]};
-            t = kth_largest(g, p.K);
-        }
-        if (lane == 0) bound = t;
-    }
-    const float m = value_of(most);
-    const float ref = m == -INFINITY ? 0.f : m;  // a piece of nothing but -inf sums to 0
-    float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                     make_float2(0.f, 0.f)};
-#pragma unroll
-    for (int e = 0; e < kElems; e += 2) {
-        // the difference first: its rounding is relative to itself, and 0 for the largest
-        const float2 y = fmul2(fsub2(make_float2(v[e], v[e + 1]), make_float2(ref, ref)),
-                               make_float2(kLog2e, kLog2e));
-        acc[e / 2 & 3] = fadd2(acc[e / 2 & 3], make_float2(ex2(y.x), ex2(y.y)));
-    }
-    const float2 a = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
-    float sum = a.x + a.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (lane == 0) sums[warp_id()] = sum;
-    __syncthreads();
-    const float t = value_of(bound);
-    auto key = [&](int e) {
-        return static_cast<unsigned long long>(order_of(v[e])) << 32 | ~static_cast<unsigned>(v0 + place(e));
-    };
-    if (top >= t) {
-#pragma unroll
-        for (int e = 0; e < kElems; ++e)
-            if (v[e] >= t && v[e] > -INFINITY) {
-                const int at = atomicAdd(&found, 1);
-                if (at < kCap) cand[at] = key(e);
+    const unsigned least = kth_largest(groups, kThreads / width, K, &bound);
+    const float bar = value_of(least);
+    // f(logit, its place in the piece) for this thread's logits of the tiles whose maximum is at least bar
+    auto each = [&](auto f) {
+        for (int t = 0; t < tiles; ++t) {
+            if (!(tops[t][tid] >= bar)) continue;
+#pragma unroll 1
+            for (int i = 0; i < kElems / VEC; ++i) {
+                const int at = t * Tile::kSize + Tile::place(i * VEC);
+                for (int k = 0; k < VEC && at + k < len; ++k) f(beam_float<TYPE>(x[at + k]), at + k);
             }
-    }
+        }
+    };
+    auto key_of = [&](float v, int place) {  // larger: a larger logit, or the first of equal ones
+        return static_cast<unsigned long long>(order_of(v)) << 32 | ~static_cast<unsigned>(v0 + place);
+    };
+    auto take = [&](float v, int place) {
+        const int at = atomicAdd(&found, 1);
+        if (at < kCap) cand[at] = key_of(v, place);
+    };
+    if (m >= bar && m > -INFINITY)
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) {
+            if (!(tops[t][tid] >= bar)) continue;
+            next.load(x + t * Tile::kSize, len - t * Tile::kSize);
+            float v[kElems];
+            next.floats(v);
+            unsigned hits = 0;
+#pragma unroll
+            for (int e = 0; e < kElems; ++e) hits |= (v[e] >= bar && v[e] > -INFINITY ? 1u : 0u) << e;
+            for (; hits != 0; hits &= hits - 1) {
+                const int at = t * Tile::kSize + Tile::place(__ffs(static_cast<int>(hits)) - 1);
+                take(beam_float<TYPE>(x[at]), at);
+            }
+        }
     __syncthreads();
     int n = found;
     if (n > kCap) {
-        // rare: the K-th largest by bisection on the value, then on the place of its equals
-        unsigned lo = 0;
-#pragma unroll 1
-        for (int bit = 31; bit >= 0; --bit) {
-            const unsigned want = lo | 1u << bit;
+        // the K-th largest logit `lo` is the bound, or above it
+        unsigned lo = least;
+        auto reach = [&](unsigned want) {
             int c = 0;
-#pragma unroll
-            for (int e = 0; e < kElems; ++e) c += v[e] > -INFINITY && order_of(v[e]) >= want;
-            if (block_sum(c, scratch) >= p.K) lo = want;
+            each([&](float v, int) { c += v > -INFINITY && order_of(v) >= want; });
+            return block_sum(c, scratch);
+        };
+        if (reach(lo + 1) >= K) {
+            unsigned hi = ~0u;
+            while (hi - lo > 1) {
+                const unsigned mid = lo + (hi - lo) / 2;
+                if (reach(mid) >= K) lo = mid;
+                else hi = mid;
+            }
         }
-        int above = 0;
-#pragma unroll
-        for (int e = 0; e < kElems; ++e) above += v[e] > -INFINITY && order_of(v[e]) > lo;
-        const int room = p.K - block_sum(above, scratch);
-        int end = 0;  // the first places up to which fewer than `room` of the equals lie
-#pragma unroll 1
-        for (int bit = kBeamChunk / 2; bit > 0; bit /= 2) {
+        // of its equals, the first that make K: those before place `end`
+        const int room = K - reach(lo + 1);
+        const float equal = value_of(lo);
+        int end = 0, before = 0;
+        for (int span = 1 << (31 - __clz(len)); span > 0; span /= 2) {
             int c = 0;
-#pragma unroll
-            for (int e = 0; e < kElems; ++e) c += order_of(v[e]) == lo && place(e) < end + bit;
-            if (block_sum(c, scratch) < room) end += bit;
+            for (int i = end + tid; i < min(end + span, len); i += kThreads) c += beam_float<TYPE>(x[i]) == equal;
+            c = block_sum(c, scratch);
+            if (before + c < room) before += c, end += span;
         }
         if (tid == 0) found = 0;
         __syncthreads();
-#pragma unroll
-        for (int e = 0; e < kElems; ++e) {
-            const unsigned o = order_of(v[e]);
-            if (v[e] > -INFINITY && (o > lo || (o == lo && place(e) <= end)))
-                cand[atomicAdd(&found, 1)] = key(e);
-        }
+        each([&](float v, int place) {
+            if (v > equal || (v == equal && place <= end)) take(v, place);
+        });
         __syncthreads();
         n = found;
     }
-    const long out = static_cast<long>(row) * p.chunks + piece;
-    unsigned long long *keys = p.keys + out * p.K;
-    for (int i = tid; i < n; i += kThreads) {
-        const unsigned long long mine = cand[i];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += cand[j] > mine;
-        if (rank < p.K) keys[rank] = mine;
+    if (n > K) {
+        keep_largest(cand, n, K, &last);
+        n = K;
     }
-    for (int i = n + tid; i < p.K; i += kThreads) keys[i] = 0;
-    if (tid == 0) {
-        float s = sums[0];
+    // the threads' sums, to the CTA's maximum
+    const unsigned all = __reduce_max_sync(kAll, order_of(m));
+    if (lane == 0) groups[warp_id()] = all;
+    __syncthreads();
+    unsigned most = groups[0];
 #pragma unroll
-        for (int i = 1; i < kThreads / 32; ++i) s += sums[i];
-        p.stats[out] = make_float2(m, s);
+    for (int i = 1; i < kWarps; ++i) most = max(most, groups[i]);
+    const float top = value_of(most);
+    if (m != -INFINITY) s *= ex2((m - top) * kLog2e);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    if (lane == 0) sums[warp_id()] = s;
+    const long out = static_cast<long>(row) * p.pieces + piece;
+    for (int i = tid; i < K; i += kThreads) p.keys[out * K + i] = i < n ? cand[i] : 0;
+    __syncthreads();
+    if (tid == 0) {
+        float sum = sums[0];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) sum += sums[i];
+        p.stats[out] = make_float2(top, sum);
     }
 }
 
-// ln s in 64 bits: the exponent's share is exact to them, that of the mantissa off by an fp32 rounding
-// of a value below 0.7.
-__device__ __forceinline__ double wide_log(float s) {
+// hi + lo, in order as unsigned integers: lo is what hi's rounding left.  0 where it is not finite.
+__device__ __forceinline__ unsigned long long pair_order(float hi, float lo) {
+    return fabsf(hi) < INFINITY ? static_cast<unsigned long long>(order_of(hi)) << 32 | order_of(lo) : 0;
+}
+// a + b and what its rounding left.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
+}
+
+// ln s as a pair: the exponent's share is exact to 2^-36 (the first term of ln 2 has 12 bits), that of the
+// mantissa off by a rounding of a value below 0.7.
+__device__ __forceinline__ float2 pair_log(float s) {
     int e;
     const float f = frexpf(s, &e);
-    return e * 0.693147180559945309417 + static_cast<double>(logf(f));
+    const float2 r = two_sum(e * 0.693115234375f, logf(f));
+    return make_float2(r.x, fmaf(static_cast<float>(e), 3.1946184945309417e-05f, r.y));
 }
 
-// One CTA per request joins its rows' pieces.
-__global__ void __launch_bounds__(kThreads) fa_beam_join_kernel(const BeamParams p) {
-    // [W] of each beam: score - ln of its sum (NaN for none), and the maximum that the sum refers to.  The
-    // two are kept apart: x less the maximum is exact, whatever their size.
-    extern __shared__ double base[];
-    float *ref = reinterpret_cast<float *>(base + p.W);
-    __shared__ unsigned groups[kThreads];
+// What a request's beams add to a logit: (hi, lo) of score - ln of the beam's sum (NaN: it offers nothing),
+// and the maximum that the sum refers to.  They are kept apart: x less the maximum is exact as a pair,
+// whatever their size.
+struct BeamBase {
+    float hi, lo, ref;
+};
+
+// Lanes that share the work on one of n things (a power of two up to 32).
+__device__ __forceinline__ int lanes_each(int n) {
+    int p = 32;
+    while (p > 1 && n * p > kJoinThreads) p /= 2;
+    return p;
+}
+__device__ __forceinline__ int sum_lanes(int x, int p) {
+    for (int o = p / 2; o > 0; o /= 2) x += __shfl_xor_sync(kAll, x, o);
+    return x;
+}
+
+// One CTA per request joins its rows' pieces: the sums, then the K best candidates, by a bound and counting as
+// for the pieces.  A request has a few hundred to a few thousand candidates and the time is that of the
+// chain of steps, so many threads share each count.
+__global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamParams p) {
+    extern __shared__ BeamBase base[];  // [W]
+    __shared__ unsigned groups[256];
     __shared__ unsigned bound;
     __shared__ int found;
-    __shared__ int scratch[kThreads / 32];
-    __shared__ unsigned long long cand[kCap];
-    __shared__ int where[kCap];
+    __shared__ int scratch[kJoinThreads / 32];
+    __shared__ unsigned long long cand[kJoinThreads];
+    __shared__ int where[kJoinThreads];
     griddep_launch_dependents();
     griddep_wait();
     const int b = blockIdx.x, tid = threadIdx.x, lane = lane_id();
-    const int W = p.W, K = p.K, S = p.chunks, V = p.V;
-    for (int w = warp_id(); w < W; w += kThreads / 32) {
-        const int row = b * W + w;
-        const double score = static_cast<double>(p.scores[row]);
-        if (p.finished != nullptr && p.finished[row] != 0) {
-            if (lane == 0) base[w] = score, ref[w] = 0.f;
+    const int W = p.W, K = p.K, S = p.pieces, V = p.V;
+    const int list = S * K, total = W * list;
+    const unsigned long long *keys = p.keys + static_cast<long>(b) * total;
+    const uint8_t *finished = p.finished != nullptr ? p.finished + static_cast<long>(b) * W : nullptr;
+    unsigned long long own[kJoinOwn];
+#pragma unroll
+    for (int r = 0; r < kJoinOwn; ++r) {
+        const int i = tid + r * kJoinThreads;
+        own[r] = i < total ? keys[i] : 0;
+    }
+    for (int w = warp_id(); w < W; w += kJoinThreads / 32) {
+        const float score = p.scores[static_cast<long>(b) * W + w];
+        if (finished != nullptr && finished[w] != 0) {
+            if (lane == 0) base[w] = {score, 0.f, 0.f};
             continue;
         }
-        const float2 *st = p.stats + static_cast<long>(row) * S;
+        const float2 *st = p.stats + (static_cast<long>(b) * W + w) * S;
         float m = -INFINITY;
         for (int i = lane; i < S; i += 32) m = fmaxf(m, st[i].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
         float s = 0.f;
         for (int i = lane; i < S; i += 32)
-            if (st[i].x != -INFINITY) s += st[i].y * ex2((st[i].x - m) * kLog2e);
+            s += st[i].x == -INFINITY ? st[i].y : st[i].y * ex2((st[i].x - m) * kLog2e);  // y: 0 or NaN
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
         if (lane == 0) {
+            const float2 l = pair_log(s), r = two_sum(score, -l.x);
             // nothing to choose from, or a logit that is no number
-            base[w] = m > -INFINITY && s < INFINITY ? score - wide_log(s) : __longlong_as_double(-1ll);
-            ref[w] = m;
+            const bool none = !(m > -INFINITY && s < INFINITY);
+            base[w] = {none ? NAN : r.x, r.y - l.y, m};
         }
     }
     if (tid == 0) found = 0;
     __syncthreads();
-    // candidate i of the request: its order (0: none) and w V + v
-    const int list = S * K, total = W * list;
-    auto get = [&](int i, int *at) -> unsigned long long {
-        const int w = i / list, j = i - w * list, row = b * W + w;
-        double s;
-        if (p.finished != nullptr && p.finished[row] != 0) {
-            if (j != 0) return 0;
+    // the order (0: none) of candidate i of the request, whose key is k, and its place w V + v
+    auto order = [&](int i, unsigned long long k, int *at) -> unsigned long long {
+        const int w = i / list;
+        const BeamBase c = base[w];
+        if (finished != nullptr && finished[w] != 0) {
             *at = w * V + p.end_token;
-            s = base[w];
-        } else {
-            const unsigned long long k = p.keys[static_cast<long>(row) * list + j];
-            if (k == 0) return 0;
-            *at = w * V + static_cast<int>(~static_cast<unsigned>(k));
-            s = base[w] + (static_cast<double>(value_of(static_cast<unsigned>(k >> 32))) -
-                           static_cast<double>(ref[w]));
+            return i == w * list ? pair_order(c.hi, 0.f) : 0;
         }
-        return isfinite(s) ? order_of(s) : 0;
+        if (k == 0) return 0;
+        *at = w * V + static_cast<int>(~static_cast<unsigned>(k));
+        const float2 d = two_sum(value_of(static_cast<unsigned>(k >> 32)), -c.ref);
+        const float2 s = two_sum(d.x, c.hi);
+        const float2 r = two_sum(s.x, s.y + (d.y + c.lo));
+        return pair_order(r.x, r.y);
     };
-    int at = 0;
-    unsigned long long most = 0;
-    for (int i = tid; i < total; i += kThreads) most = max(most, get(i, &at));
-    groups[tid] = static_cast<unsigned>(most >> 32);
-    __syncthreads();
-    if (warp_id() == 0) {
-        unsigned g[kThreads / 32];
+    int place[kJoinOwn];
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) g[i] = groups[lane + 32 * i];
-        const unsigned t = kth_largest(g, K);
-        if (lane == 0) bound = t;
+    for (int r = 0; r < kJoinOwn; ++r) {
+        const int i = tid + r * kJoinThreads;
+        place[r] = 0;
+        own[r] = i < total ? order(i, own[r], &place[r]) : 0;
+    }
+    // f(order, place) for this thread's candidates
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int r = 0; r < kJoinOwn; ++r) f(own[r], place[r]);
+        for (int i = tid + kJoinOwn * kJoinThreads; i < total; i += kJoinThreads) {
+            int at = 0;
+            const unsigned long long k = order(i, keys[i], &at);
+            f(k, at);
+        }
+    };
+    auto take = [&](unsigned long long k, int at) {
+        const int n = atomicAdd(&found, 1);
+        if (n < kJoinThreads) cand[n] = k, where[n] = at;
+    };
+    // K candidates at least reach the K-th largest of the best ones of groups of threads
+    unsigned long long most = 0;
+    each([&](unsigned long long k, int) { most = max(most, k); });
+    const int width = K <= 8 ? 32 : K <= 32 ? 8 : 4, count = kJoinThreads / width;
+    unsigned best = static_cast<unsigned>(most >> 32);
+    for (int o = 1; o < width; o *= 2) best = max(best, __shfl_xor_sync(kAll, best, o));
+    if (lane % width == 0) groups[tid / width] = best;
+    __syncthreads();
+    {
+        const int i = tid / width, part = tid % width;
+        const unsigned mine = groups[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = part; j < count; j += width) rank += groups[j] > mine || (groups[j] == mine && j < i);
+        rank = sum_lanes(rank, width);
+        if (part == 0 && rank == K - 1) bound = mine;
     }
     __syncthreads();
-    unsigned long long t = static_cast<unsigned long long>(bound) << 32;
-    for (int i = tid; i < total; i += kThreads) {
-        const unsigned long long k = get(i, &at);
-        if (k != 0 && k >= t) {
-            const int n = atomicAdd(&found, 1);
-            if (n < kCap) cand[n] = k, where[n] = at;
-        }
-    }
+    const unsigned long long t = max(static_cast<unsigned long long>(bound) << 32, 1ull);
+    if (most >= t)
+        each([&](unsigned long long k, int at) {
+            if (k >= t) take(k, at);
+        });
     __syncthreads();
     int n = found;
-    if (n > kCap) {
-        // rare: the K-th best by bisection on the score, then on the place of its equals
-        unsigned long long lo = 0;
-#pragma unroll 1
-        for (int bit = 63; bit >= 0; --bit) {
-            const unsigned long long want = lo | 1ull << bit;
+    if (n > kJoinThreads) {
+        // The K-th best by bisection on the score, then on the place of its equals.
+        unsigned long long lo = t, hi = ~0ull;  // lo is reached by K or more
+        auto reach = [&](auto test) {
             int c = 0;
-            for (int i = tid; i < total; i += kThreads) c += get(i, &at) >= want;
-            if (block_sum(c, scratch) >= K) lo = want;
+            each([&](unsigned long long k, int at) { c += test(k, at); });
+            return block_sum<kJoinThreads>(c, scratch);
+        };
+        while (hi - lo > 1) {
+            const unsigned long long mid = lo + (hi - lo) / 2;
+            if (reach([&](unsigned long long k, int) { return k >= mid; }) >= K) lo = mid;
+            else hi = mid;
         }
-        int above = 0;
-        for (int i = tid; i < total; i += kThreads) above += get(i, &at) > lo;
-        const int room = K - block_sum(above, scratch);
-        int end = 0;
+        const int room = K - reach([&](unsigned long long k, int) { return k > lo; });
+        int end = 0;  // the place of the last of the equals that are taken
 #pragma unroll 1
         for (int bit = 30; bit >= 0; --bit) {
-            int c = 0;
-            for (int i = tid; i < total; i += kThreads) c += get(i, &at) == lo && at < end + (1 << bit);
-            if (block_sum(c, scratch) < room) end += 1 << bit;
+            const int to = end | 1 << bit;
+            if (reach([&](unsigned long long k, int at) { return k == lo && at < to; }) < room) end = to;
         }
         if (tid == 0) found = 0;
         __syncthreads();
-        for (int i = tid; i < total; i += kThreads) {
-            const unsigned long long k = get(i, &at);
-            if (k > lo || (k == lo && k != 0 && at <= end)) {
-                const int j = atomicAdd(&found, 1);
-                cand[j] = k, where[j] = at;
-            }
-        }
+        each([&](unsigned long long k, int at) {
+            if (k > lo || (k == lo && at <= end)) take(k, at);
+        });
         __syncthreads();
         n = found;
     }
     const long out = static_cast<long>(b) * K;
-    for (int i = tid; i < n; i += kThreads) {
-        const unsigned long long mine = cand[i];
-        const int spot = where[i];
+    const int lanes = lanes_each(n), i = tid / lanes, part = tid % lanes;
+    if (i - lane / lanes < n) {  // some lane of the warp has a candidate
+        const bool there = i < n;
+        const unsigned long long mine = there ? cand[i] : 0;
+        const int spot = there ? where[i] : 0;
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += cand[j] > mine || (cand[j] == mine && where[j] < spot);
-        if (rank >= K) continue;
-        const int w = spot / V, v = spot - w * V;
-        p.out_scores[out + rank] = static_cast<float>(value_of(mine));
-        p.parents[out + rank] = b * W + w;
-        p.tokens[out + rank] = v;
-        p.out_finished[out + rank] =
-            v == p.end_token || (p.finished != nullptr && p.finished[b * W + w] != 0);
+#pragma unroll 4
+        for (int j = part; j < n; j += lanes) rank += cand[j] > mine || (cand[j] == mine && where[j] < spot);
+        rank = sum_lanes(rank, lanes);
+        if (there && part == 0 && rank < K) {
+            const int w = spot / V, v = spot - w * V;
+            p.out_scores[out + rank] = value_of(static_cast<unsigned>(mine >> 32));
+            p.parents[out + rank] = b * W + w;
+            p.tokens[out + rank] = v;
+            p.out_finished[out + rank] = v == p.end_token || (finished != nullptr && finished[w] != 0);
+        }
     }
-    for (int i = n + tid; i < K; i += kThreads) {
-        p.out_scores[out + i] = -INFINITY;
-        p.parents[out + i] = p.tokens[out + i] = -1;
-        p.out_finished[out + i] = 1;
+    for (int k = n + tid; k < K; k += kJoinThreads) {
+        p.out_scores[out + k] = -INFINITY;
+        p.parents[out + k] = p.tokens[out + k] = -1;
+        p.out_finished[out + k] = 1;
     }
 }
 
 template <int TYPE, int VEC>
 cudaError_t launch_piece(const BeamParams &p, cudaStream_t stream) {
-    return launch_overlapped(fa_beam_piece_kernel<TYPE, VEC>, dim3(p.chunks * p.B * p.W), kThreads, 0, stream,
+    return launch_overlapped(fa_beam_piece_kernel<TYPE, VEC>, dim3(p.pieces * p.B * p.W), kThreads, 0, stream,
                              p);
 }
 
 }  // namespace
 
 cudaError_t launch_beam_select(const BeamParams &p, int type, cudaStream_t stream) {
-    const long bits = static_cast<long>(reinterpret_cast<uintptr_t>(p.logits)) /
-                          (type == kBeamF32 ? 4 : 2) | p.stride_b | p.stride_w;
-    const long align = bits & -bits & 15;  // logits that every row's start is a multiple of
-    const int vec = align == 0 || align >= (type == kBeamF32 ? 4 : 8) ? (type == kBeamF32 ? 4 : 8)
-                                                                     : static_cast<int>(align);
+    const int vec = beam_vec(p.logits, p.stride_b, p.stride_w, type);
     cudaError_t e;
     if (type == kBeamF32) {
         e = vec == 4 ? launch_piece<kBeamF32, 4>(p, stream) : vec == 2 ? launch_piece<kBeamF32, 2>(p, stream)
@@ -416,8 +553,8 @@ cudaError_t launch_beam_select(const BeamParams &p, int type, cudaStream_t strea
                        : launch_piece<kBeamF16, 1>(p, stream);
     }
     if (e != cudaSuccess) return e;
-    return launch_overlapped(fa_beam_join_kernel, dim3(p.B), kThreads,
-                            (sizeof(double) + sizeof(float)) * p.W, stream, p);
+    return launch_overlapped(fa_beam_join_kernel, dim3(p.B), kJoinThreads, sizeof(BeamBase) * p.W,
+                            stream, p);
 }
 
 }  // namespace fa
