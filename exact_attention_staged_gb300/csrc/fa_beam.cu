@@ -42,8 +42,25 @@ __device__ __forceinline__ unsigned order_of(float x) {
 __device__ __forceinline__ float value_of(unsigned u) {
     return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
-// The CTA's K-th largest of values[0 .. n), n a multiple of 4 no more than the threads, by counting; every
-// thread calls it and gets the result, which `out` passes on.
+// The k-th largest of values[0 .. 32), which every lane of the warp gets.
+__device__ __forceinline__ unsigned kth_of_32(const unsigned *values, int k) {
+    const uint4 *all = reinterpret_cast<const uint4 *>(values);
+    const int lane = lane_id();
+    const unsigned mine = values[lane];
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {  // equal ones in order
+        const uint4 x = all[j];
+        rank += x.x > mine || (x.x == mine && 4 * j < lane);
+        rank += x.y > mine || (x.y == mine && 4 * j + 1 < lane);
+        rank += x.z > mine || (x.z == mine && 4 * j + 2 < lane);
+        rank += x.w > mine || (x.w == mine && 4 * j + 3 < lane);
+    }
+    return __shfl_sync(kAll, mine, __ffs(static_cast<int>(__ballot_sync(kAll, rank == k - 1))) - 1);
+}
+
+// The CTA's k-th largest of values[0 .. n), n a multiple of 4 no more than the threads; every thread calls
+// it and gets the result, which `out` passes on.
 __device__ __forceinline__ unsigned kth_largest(const unsigned *values, int n, int k, unsigned *out) {
     const int tid = threadIdx.x;
     if (tid < n) {
@@ -53,7 +70,7 @@ __device__ __forceinline__ unsigned kth_largest(const unsigned *values, int n, i
 #pragma unroll 4
         for (int j = 0; j < n / 4; ++j) {
             const uint4 x = all[j];
-            const int i = 4 * j;  // equal ones in order
+            const int i = 4 * j;
             rank += x.x > mine || (x.x == mine && i < tid);
             rank += x.y > mine || (x.y == mine && i + 1 < tid);
             rank += x.z > mine || (x.z == mine && i + 2 < tid);
@@ -63,32 +80,6 @@ __device__ __forceinline__ unsigned kth_largest(const unsigned *values, int n, i
     }
     __syncthreads();
     return *out;
-}
-
-// The CTA keeps the k largest of n distinct keys (k < n <= kCap), largest first; `least` gets the last.
-// Ends without a barrier.
-__device__ __forceinline__ void keep_largest(unsigned long long *key, int n, int k,
-                                             unsigned long long *least) {
-    constexpr int kOwn = kCap / kThreads;
-    unsigned long long mine[kOwn];
-    int rank[kOwn];
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-        const int at = static_cast<int>(threadIdx.x) + i * kThreads;
-        rank[i] = k;
-        if (at < n) {
-            mine[i] = key[at];
-            rank[i] = 0;
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) rank[i] += key[j] > mine[i];
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-        if (rank[i] < k) key[rank[i]] = mine[i];
-        if (rank[i] == k - 1) *least = mine[i];
-    }
 }
 
 // The sum of x over the CTA's threads, the same in each; `scratch` holds a word per warp.
@@ -132,8 +123,8 @@ struct BeamTile {
     static constexpr int kElems = beam_elems(TYPE, VEC), kSize = kElems * kThreads;
     Vec raw[kElems / VEC];
 
-    static __device__ __forceinline__ int place(int e) {
-        return (e / VEC * kThreads + static_cast<int>(threadIdx.x)) * VEC + e % VEC;
+    static __device__ __forceinline__ int place(int e, int tid = threadIdx.x) {
+        return (e / VEC * kThreads + tid) * VEC + e % VEC;
     }
     // x: the tile's first logit; left: how many there are to the end
     __device__ __forceinline__ void load(const Elem *x, int left) {
@@ -158,9 +149,19 @@ struct BeamTile {
         }
     }
     __device__ __forceinline__ void floats(float (&v)[kElems]) const {
-        const Elem *e = reinterpret_cast<const Elem *>(raw);
+        if constexpr (TYPE != kBeamF32 && VEC > 1) {
+            uint32_t word[kElems / 2];
+            memcpy(word, raw, sizeof(raw));
 #pragma unroll
-        for (int k = 0; k < kElems; ++k) v[k] = beam_float<TYPE>(e[k]);
+            for (int k = 0; k < kElems / 2; ++k) {
+                const float2 f = unpack2<TYPE == kBeamBF16>(word[k]);
+                v[2 * k] = f.x, v[2 * k + 1] = f.y;
+            }
+        } else {
+            const Elem *e = reinterpret_cast<const Elem *>(raw);
+#pragma unroll
+            for (int k = 0; k < kElems; ++k) v[k] = beam_float<TYPE>(e[k]);
+        }
     }
 };
 
@@ -175,8 +176,9 @@ __global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamPa
     __shared__ unsigned bound;
     __shared__ int found;
     __shared__ int scratch[kWarps];
+    __shared__ unsigned tops_of[kWarps];  // each warp's maximum
     __shared__ float sums[kWarps];
-    __shared__ unsigned long long cand[kCap], last;
+    __shared__ unsigned long long cand[kCap];
     griddep_launch_dependents();
     griddep_wait();
     const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
@@ -227,9 +229,20 @@ __global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamPa
     float g = m;
     for (int o = 1; o < width; o *= 2) g = fmaxf(g, __shfl_xor_sync(kAll, g, o));
     if (tid % width == 0) groups[tid / width] = order_of(g);
+    const unsigned mine = __reduce_max_sync(kAll, order_of(m));
+    if (lane == 0) tops_of[warp_id()] = mine;
     if (tid == 0) found = 0;
     __syncthreads();
-    const unsigned least = kth_largest(groups, kThreads / width, K, &bound);
+    const unsigned least = width == 8 ? kth_of_32(groups, K)
+                                      : kth_largest(groups, kThreads / width, K, &bound);
+    unsigned most = tops_of[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) most = max(most, tops_of[i]);
+    const float top = value_of(most);
+    if (m != -INFINITY) s *= ex2((m - top) * kLog2e);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    if (lane == 0) sums[warp_id()] = s;
     const float bar = value_of(least);
     // f(logit, its place in the piece) for this thread's logits of the tiles whose maximum is at least bar
     auto each = [&](auto f) {
@@ -249,21 +262,18 @@ __global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamPa
         const int at = atomicAdd(&found, 1);
         if (at < kCap) cand[at] = key_of(v, place);
     };
-    if (m >= bar && m > -INFINITY)
+    // a warp reads each of its threads' places again together, a logit per lane
+    if (__any_sync(kAll, m >= bar && m > -INFINITY))
 #pragma unroll 1
-        for (int t = 0; t < tiles; ++t) {
-            if (!(tops[t][tid] >= bar)) continue;
-            next.load(x + t * Tile::kSize, len - t * Tile::kSize);
-            float v[kElems];
-            next.floats(v);
-            unsigned hits = 0;
-#pragma unroll
-            for (int e = 0; e < kElems; ++e) hits |= (v[e] >= bar && v[e] > -INFINITY ? 1u : 0u) << e;
-            for (; hits != 0; hits &= hits - 1) {
-                const int at = t * Tile::kSize + Tile::place(__ffs(static_cast<int>(hits)) - 1);
-                take(beam_float<TYPE>(x[at]), at);
+        for (int t = 0; t < tiles; ++t)
+            for (unsigned who = __ballot_sync(kAll, tops[t][tid] >= bar); who != 0; who &= who - 1) {
+                const int owner = (tid & ~31) + __ffs(static_cast<int>(who)) - 1;
+                if (lane >= kElems) continue;
+                const int at = t * Tile::kSize + Tile::place(lane, owner);
+                if (at >= len) continue;
+                const float v = beam_float<TYPE>(x[at]);
+                if (v >= bar && v > -INFINITY) take(v, at);
             }
-        }
     __syncthreads();
     int n = found;
     if (n > kCap) {
@@ -300,26 +310,18 @@ __global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamPa
         __syncthreads();
         n = found;
     }
-    if (n > K) {
-        keep_largest(cand, n, K, &last);
-        n = K;
-    }
-    // the threads' sums, to the CTA's maximum
-    const unsigned all = __reduce_max_sync(kAll, order_of(m));
-    if (lane == 0) groups[warp_id()] = all;
-    __syncthreads();
-    unsigned most = groups[0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) most = max(most, groups[i]);
-    const float top = value_of(most);
-    if (m != -INFINITY) s *= ex2((m - top) * kLog2e);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-    if (lane == 0) sums[warp_id()] = s;
+    // the K largest, largest first, by counting
     const long out = static_cast<long>(row) * p.pieces + piece;
-    for (int i = tid; i < K; i += kThreads) p.keys[out * K + i] = i < n ? cand[i] : 0;
-    __syncthreads();
-    if (tid == 0) {
+    unsigned long long *keys = p.keys + out * K;
+    for (int i = tid; i < n; i += kThreads) {
+        const unsigned long long k = cand[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) rank += cand[j] > k;
+        if (rank < K) keys[rank] = k;
+    }
+    for (int i = n + tid; i < K; i += kThreads) keys[i] = 0;
+    if (tid == kThreads - 1) {
         float sum = sums[0];
 #pragma unroll
         for (int i = 1; i < kWarps; ++i) sum += sums[i];
@@ -382,11 +384,18 @@ __global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamPa
     const int list = S * K, total = W * list;
     const unsigned long long *keys = p.keys + static_cast<long>(b) * total;
     const uint8_t *finished = p.finished != nullptr ? p.finished + static_cast<long>(b) * W : nullptr;
+    // Candidate i is one of list i / K.  The lists are sorted, and each is turned by a step of its own, so that
+    // the good ones fall to different threads.
+    const int step = K * 5 / 8 + 1;
+    auto key_at = [&](int i) {
+        const int l = i / K;
+        return keys[l * K + (i - l * K + l % K * step) % K];
+    };
     unsigned long long own[kJoinOwn];
 #pragma unroll
     for (int r = 0; r < kJoinOwn; ++r) {
         const int i = tid + r * kJoinThreads;
-        own[r] = i < total ? keys[i] : 0;
+        own[r] = i < total ? key_at(i) : 0;
     }
     for (int w = warp_id(); w < W; w += kJoinThreads / 32) {
         const float score = p.scores[static_cast<long>(b) * W + w];
@@ -412,6 +421,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamPa
         }
     }
     if (tid == 0) found = 0;
+    if (tid < 256) groups[tid] = 0;
     __syncthreads();
     // the order (0: none) of candidate i of the request, whose key is k, and its place w V + v
     auto order = [&](int i, unsigned long long k, int *at) -> unsigned long long {
@@ -441,7 +451,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamPa
         for (int r = 0; r < kJoinOwn; ++r) f(own[r], place[r]);
         for (int i = tid + kJoinOwn * kJoinThreads; i < total; i += kJoinThreads) {
             int at = 0;
-            const unsigned long long k = order(i, keys[i], &at);
+            const unsigned long long k = order(i, key_at(i), &at);
             f(k, at);
         }
     };
@@ -452,10 +462,8 @@ __global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamPa
     // K candidates at least reach the K-th largest of the best ones of groups of threads
     unsigned long long most = 0;
     each([&](unsigned long long k, int) { most = max(most, k); });
-    const int width = K <= 8 ? 32 : K <= 32 ? 8 : 4, count = kJoinThreads / width;
-    unsigned best = static_cast<unsigned>(most >> 32);
-    for (int o = 1; o < width; o *= 2) best = max(best, __shfl_xor_sync(kAll, best, o));
-    if (lane % width == 0) groups[tid / width] = best;
+    const int count = K <= 8 ? 32 : K <= 32 ? 128 : 256, width = kJoinThreads / count;
+    if (most != 0) atomicMax(&groups[tid % count], static_cast<unsigned>(most >> 32));
     __syncthreads();
     {
         const int i = tid / width, part = tid % width;
