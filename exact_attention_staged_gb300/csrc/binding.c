@@ -557,7 +557,9 @@ static int workspace(const Tensor *given, size_t need, PyObject *like, void **pt
         *ptr = given->ptr;
         return 0;
     }
-    const long long shape[1] = {need > 16 ? (long long)need : 16};
+    *ptr = NULL;
+    if (need == 0) return 0;
+    const long long shape[1] = {(long long)need};
     PyObject *device = PyObject_GetAttr(like, s_device);
     if (device == NULL) return -1;
     *made = new_tensor(shape, 1, g_u8, device, ptr);

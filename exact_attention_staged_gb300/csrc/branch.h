@@ -68,6 +68,7 @@ struct BeamParams {
     uint8_t *out_finished;           // [B, K]
     int B, W, V, K, end_token;
     int pieces, piece_len;           // pieces of a row, and their logits (whole tiles)
+    int ctas;                        // per request, or 0: a grid over all pieces, and one that joins them
     unsigned long long *keys;        // workspace [B * W][pieces][K]
     float2 *stats;                   // workspace [B * W][pieces]: maximum, sum of e^(x - maximum)
 };
@@ -83,7 +84,7 @@ constexpr int kBranchMaxSeqs = 32768;
 
 enum BeamType { kBeamF16 = 0, kBeamBF16 = 1, kBeamF32 = 2 };
 constexpr int kBeamThreads = 256;
-constexpr int kBeamTiles = 16;         // tiles of a piece, at most
+constexpr int kBeamNoted = 4096;        // maxima that a CTA notes: a piece has as many times its threads in tiles
 // Logits per load, 16 bytes or what the rows' starts are aligned to.
 inline int beam_vec(const void *logits, long stride_b, long stride_w, int type) {
     const long size = type == kBeamF32 ? 4 : 2, most = 16 / size;
@@ -95,6 +96,35 @@ inline int beam_vec(const void *logits, long stride_b, long stride_w, int type) 
 constexpr int beam_elems(int type, int vec) { return type != kBeamF32 && vec >= 4 ? 32 : 16; }
 constexpr int kBeamMaxK = 128;
 constexpr int kBeamMaxWidth = 2048;     // beams of a request
-cudaError_t launch_beam_select(const BeamParams &p, int type, cudaStream_t stream);
+cudaError_t launch_beam_select(const BeamParams &p, int type, int vec, cudaStream_t stream);
+
+// A launch of `clusters` clusters of `ctas` CTAs that may overlap the end of the grid before it.
+template <class Params>
+cudaError_t launch_clusters(void (*kernel)(Params), int clusters, int ctas, int threads, size_t smem,
+                            cudaStream_t stream, const Params &p) {
+    if (ctas > 8) {  // more than every device has to allow
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    if (smem > 8 * 1024) {  // beside the static part
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(clusters * ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 }  // namespace fa

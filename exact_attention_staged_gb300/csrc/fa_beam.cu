@@ -20,16 +20,19 @@
 // well below the fp32 spacing of the scores, to which the result is rounded once.
 #include "branch.h"
 
+#include <cooperative_groups.h>
 #include <cstring>
 #include <type_traits>
 
 namespace fa {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kThreads = kBeamThreads;
-constexpr int kWarps = kThreads / 32;
 constexpr int kCap = 512;                     // candidates that there is room for
 constexpr int kJoinThreads = 1024;
+constexpr int kJoinCap = 1024;
 constexpr int kJoinOwn = 4;                   // a thread's candidates that stay in registers
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kAll = 0xffffffffu;
@@ -115,16 +118,16 @@ __device__ __forceinline__ float beam_float(beam_elem<TYPE> x) {
 }
 
 // A thread's logits of a tile as they were loaded.  Logit i * VEC + k of the thread is number
-// (i * kThreads + tid) * VEC + k of the tile; behind the row's end they are -inf.
-template <int TYPE, int VEC>
+// (i * THREADS + tid) * VEC + k of the tile; behind the row's end they are -inf.
+template <int TYPE, int VEC, int THREADS>
 struct BeamTile {
     using Elem = beam_elem<TYPE>;
     using Vec = typename VecOf<VEC * sizeof(Elem)>::type;
-    static constexpr int kElems = beam_elems(TYPE, VEC), kSize = kElems * kThreads;
+    static constexpr int kElems = beam_elems(TYPE, VEC), kSize = kElems * THREADS;
     Vec raw[kElems / VEC];
 
     static __device__ __forceinline__ int place(int e, int tid = threadIdx.x) {
-        return (e / VEC * kThreads + tid) * VEC + e % VEC;
+        return (e / VEC * THREADS + tid) * VEC + e % VEC;
     }
     // x: the tile's first logit; left: how many there are to the end
     __device__ __forceinline__ void load(const Elem *x, int left) {
@@ -165,25 +168,22 @@ struct BeamTile {
     }
 };
 
-// VEC: logits per load, what the rows' alignment allows.
-template <int TYPE, int VEC>
-__global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamParams p) {
-    using Tile = BeamTile<TYPE, VEC>;
+// The CTA's work on one piece of a row: its K best into keys, its sum into *stats.
+template <int TYPE, int VEC, int THREADS>
+__device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int piece,
+                                           unsigned long long *keys, float2 *stats) {
+    using Tile = BeamTile<TYPE, VEC, THREADS>;
     using Elem = typename Tile::Elem;
     constexpr int kElems = Tile::kElems;
-    __shared__ float tops[kBeamTiles][kThreads];  // of each thread's logits of each tile
-    __shared__ __align__(16) unsigned groups[kThreads];
+    __shared__ float tops[kBeamNoted / THREADS][THREADS];  // of each thread's logits of each tile
+    __shared__ __align__(16) unsigned groups[256];
     __shared__ unsigned bound;
     __shared__ int found;
-    __shared__ int scratch[kWarps];
-    __shared__ unsigned tops_of[kWarps];  // each warp's maximum
-    __shared__ float sums[kWarps];
+    __shared__ int scratch[THREADS / 32];
+    __shared__ unsigned tops_of[THREADS / 32];  // each warp's maximum
+    __shared__ float sums[THREADS / 32];
     __shared__ unsigned long long cand[kCap];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
     const int tid = threadIdx.x, lane = lane_id();
-    if (p.finished != nullptr && p.finished[row] != 0) return;
     const int b = row / p.W, w = row - b * p.W;
     const int v0 = piece * p.piece_len, len = min(p.V - v0, p.piece_len);
     const Elem *x = static_cast<const Elem *>(p.logits) + b * p.stride_b + w * p.stride_w + v0;
@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamPa
         s += q.x + q.y;
     }
 
-    // groups of 8 threads, of 2 or of 1: about four times as many as wanted
-    const int width = K <= 16 ? 8 : K <= 64 ? 2 : 1;
+    // groups of threads: about four times as many as wanted
+    const int count = K <= 16 ? 32 : K <= 64 ? 128 : 256, width = THREADS / count;
     float g = m;
     for (int o = 1; o < width; o *= 2) g = fmaxf(g, __shfl_xor_sync(kAll, g, o));
     if (tid % width == 0) groups[tid / width] = order_of(g);
@@ -233,11 +233,10 @@ __global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamPa
     if (lane == 0) tops_of[warp_id()] = mine;
     if (tid == 0) found = 0;
     __syncthreads();
-    const unsigned least = width == 8 ? kth_of_32(groups, K)
-                                      : kth_largest(groups, kThreads / width, K, &bound);
+    const unsigned least = count == 32 ? kth_of_32(groups, K) : kth_largest(groups, count, K, &bound);
     unsigned most = tops_of[0];
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i) most = max(most, tops_of[i]);
+    for (int i = 1; i < THREADS / 32; ++i) most = max(most, tops_of[i]);
     const float top = value_of(most);
     if (m != -INFINITY) s *= ex2((m - top) * kLog2e);
 #pragma unroll
@@ -282,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamPa
         auto reach = [&](unsigned want) {
             int c = 0;
             each([&](float v, int) { c += v > -INFINITY && order_of(v) >= want; });
-            return block_sum(c, scratch);
+            return block_sum<THREADS>(c, scratch);
         };
         if (reach(lo + 1) >= K) {
             unsigned hi = ~0u;
@@ -298,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamPa
         int end = 0, before = 0;
         for (int span = 1 << (31 - __clz(len)); span > 0; span /= 2) {
             int c = 0;
-            for (int i = end + tid; i < min(end + span, len); i += kThreads) c += beam_float<TYPE>(x[i]) == equal;
-            c = block_sum(c, scratch);
+            for (int i = end + tid; i < min(end + span, len); i += THREADS) c += beam_float<TYPE>(x[i]) == equal;
+            c = block_sum<THREADS>(c, scratch);
             if (before + c < room) before += c, end += span;
         }
         if (tid == 0) found = 0;
@@ -311,22 +310,31 @@ __global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamPa
         n = found;
     }
     // the K largest, largest first, by counting
-    const long out = static_cast<long>(row) * p.pieces + piece;
-    unsigned long long *keys = p.keys + out * K;
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < n; i += THREADS) {
         const unsigned long long k = cand[i];
         int rank = 0;
 #pragma unroll 4
         for (int j = 0; j < n; ++j) rank += cand[j] > k;
         if (rank < K) keys[rank] = k;
     }
-    for (int i = n + tid; i < K; i += kThreads) keys[i] = 0;
-    if (tid == kThreads - 1) {
+    for (int i = n + tid; i < K; i += THREADS) keys[i] = 0;
+    if (tid == THREADS - 1) {
         float sum = sums[0];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) sum += sums[i];
-        p.stats[out] = make_float2(top, sum);
+        for (int i = 1; i < THREADS / 32; ++i) sum += sums[i];
+        *stats = make_float2(top, sum);
     }
+}
+
+// VEC: logits per load, what the rows' alignment allows.
+template <int TYPE, int VEC>
+__global__ void __launch_bounds__(kThreads, 4) fa_beam_piece_kernel(const BeamParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int row = blockIdx.x / p.pieces, piece = blockIdx.x - row * p.pieces;
+    if (p.finished != nullptr && p.finished[row] != 0) return;
+    const long out = static_cast<long>(row) * p.pieces + piece;
+    beam_piece<TYPE, VEC, kThreads>(p, row, piece, p.keys + out * p.K, p.stats + out);
 }
 
 // hi + lo, in order as unsigned integers: lo is what hi's rounding left.  0 where it is not finite.
@@ -356,9 +364,10 @@ struct BeamBase {
 };
 
 // Lanes that share the work on one of n things (a power of two up to 32).
+template <int THREADS>
 __device__ __forceinline__ int lanes_each(int n) {
     int p = 32;
-    while (p > 1 && n * p > kJoinThreads) p /= 2;
+    while (p > 1 && n * p > THREADS) p /= 2;
     return p;
 }
 __device__ __forceinline__ int sum_lanes(int x, int p) {
@@ -366,51 +375,51 @@ __device__ __forceinline__ int sum_lanes(int x, int p) {
     return x;
 }
 
-// One CTA per request joins its rows' pieces: the sums, then the K best candidates, by a bound and counting as
-// for the pieces.  A request has a few hundred to a few thousand candidates and the time is that of the
-// chain of steps, so many threads share each count.
-__global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamParams p) {
-    extern __shared__ BeamBase base[];  // [W]
+// One CTA joins the pieces of request b: the sums, then the K best candidates, by a bound and counting as for
+// the pieces.  A request has up to a few thousand candidates and the time is that of the chain of steps,
+// so many threads share each count.  list_of(l) and stats_of(l): the candidates and the sum of
+// piece l % pieces of beam l / pieces.
+template <int THREADS, class Lists, class Stats>
+__device__ __forceinline__ void beam_join(const BeamParams &p, int b, BeamBase *base, Lists list_of,
+                                          Stats stats_of) {
     __shared__ unsigned groups[256];
     __shared__ unsigned bound;
     __shared__ int found;
-    __shared__ int scratch[kJoinThreads / 32];
-    __shared__ unsigned long long cand[kJoinThreads];
-    __shared__ int where[kJoinThreads];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int b = blockIdx.x, tid = threadIdx.x, lane = lane_id();
+    __shared__ int scratch[THREADS / 32];
+    __shared__ unsigned long long cand[kJoinCap];
+    __shared__ int where[kJoinCap];
+    const int tid = threadIdx.x, lane = lane_id();
     const int W = p.W, K = p.K, S = p.pieces, V = p.V;
     const int list = S * K, total = W * list;
-    const unsigned long long *keys = p.keys + static_cast<long>(b) * total;
     const uint8_t *finished = p.finished != nullptr ? p.finished + static_cast<long>(b) * W : nullptr;
     // Candidate i is one of list i / K.  The lists are sorted, and each is turned by a step of its own, so that
     // the good ones fall to different threads.
     const int step = K * 5 / 8 + 1;
     auto key_at = [&](int i) {
         const int l = i / K;
-        return keys[l * K + (i - l * K + l % K * step) % K];
+        return list_of(l)[(i - l * K + l % K * step) % K];
     };
     unsigned long long own[kJoinOwn];
 #pragma unroll
     for (int r = 0; r < kJoinOwn; ++r) {
-        const int i = tid + r * kJoinThreads;
-        own[r] = i < total ? key_at(i) : 0;
+        const int i = tid + r * THREADS;
+        own[r] = i < total && (finished == nullptr || finished[i / list] == 0) ? key_at(i) : 0;
     }
-    for (int w = warp_id(); w < W; w += kJoinThreads / 32) {
+    for (int w = warp_id(); w < W; w += THREADS / 32) {
         const float score = p.scores[static_cast<long>(b) * W + w];
         if (finished != nullptr && finished[w] != 0) {
             if (lane == 0) base[w] = {score, 0.f, 0.f};
             continue;
         }
-        const float2 *st = p.stats + (static_cast<long>(b) * W + w) * S;
         float m = -INFINITY;
-        for (int i = lane; i < S; i += 32) m = fmaxf(m, st[i].x);
+        for (int i = lane; i < S; i += 32) m = fmaxf(m, stats_of(w * S + i).x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
         float s = 0.f;
-        for (int i = lane; i < S; i += 32)
-            s += st[i].x == -INFINITY ? st[i].y : st[i].y * ex2((st[i].x - m) * kLog2e);  // y: 0 or NaN
+        for (int i = lane; i < S; i += 32) {
+            const float2 st = stats_of(w * S + i);
+            s += st.x == -INFINITY ? st.y : st.y * ex2((st.x - m) * kLog2e);  // y: 0 or NaN
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
         if (lane == 0) {
@@ -441,7 +450,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamPa
     int place[kJoinOwn];
 #pragma unroll
     for (int r = 0; r < kJoinOwn; ++r) {
-        const int i = tid + r * kJoinThreads;
+        const int i = tid + r * THREADS;
         place[r] = 0;
         own[r] = i < total ? order(i, own[r], &place[r]) : 0;
     }
@@ -449,7 +458,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamPa
     auto each = [&](auto f) {
 #pragma unroll
         for (int r = 0; r < kJoinOwn; ++r) f(own[r], place[r]);
-        for (int i = tid + kJoinOwn * kJoinThreads; i < total; i += kJoinThreads) {
+        for (int i = tid + kJoinOwn * THREADS; i < total; i += THREADS) {
             int at = 0;
             const unsigned long long k = order(i, key_at(i), &at);
             f(k, at);
@@ -457,12 +466,12 @@ __global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamPa
     };
     auto take = [&](unsigned long long k, int at) {
         const int n = atomicAdd(&found, 1);
-        if (n < kJoinThreads) cand[n] = k, where[n] = at;
+        if (n < kJoinCap) cand[n] = k, where[n] = at;
     };
     // K candidates at least reach the K-th largest of the best ones of groups of threads
     unsigned long long most = 0;
     each([&](unsigned long long k, int) { most = max(most, k); });
-    const int count = K <= 8 ? 32 : K <= 32 ? 128 : 256, width = kJoinThreads / count;
+    const int count = K <= 8 ? 32 : K <= 32 ? 128 : 256, width = THREADS / count;
     if (most != 0) atomicMax(&groups[tid % count], static_cast<unsigned>(most >> 32));
     __syncthreads();
     {
@@ -482,13 +491,13 @@ __global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamPa
         });
     __syncthreads();
     int n = found;
-    if (n > kJoinThreads) {
+    if (n > kJoinCap) {
         // The K-th best by bisection on the score, then on the place of its equals.
         unsigned long long lo = t, hi = ~0ull;  // lo is reached by K or more
         auto reach = [&](auto test) {
             int c = 0;
             each([&](unsigned long long k, int at) { c += test(k, at); });
-            return block_sum<kJoinThreads>(c, scratch);
+            return block_sum<THREADS>(c, scratch);
         };
         while (hi - lo > 1) {
             const unsigned long long mid = lo + (hi - lo) / 2;
@@ -511,9 +520,11 @@ __global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamPa
         n = found;
     }
     const long out = static_cast<long>(b) * K;
-    const int lanes = lanes_each(n), i = tid / lanes, part = tid % lanes;
-    if (i - lane / lanes < n) {  // some lane of the warp has a candidate
+    const int lanes = lanes_each<THREADS>(n), part = tid % lanes;
+    for (int i0 = 0; i0 < n; i0 += THREADS / lanes) {
+        const int i = i0 + tid / lanes;
         const bool there = i < n;
+        if (!__any_sync(kAll, there)) continue;
         const unsigned long long mine = there ? cand[i] : 0;
         const int spot = there ? where[i] : 0;
         int rank = 0;
@@ -528,41 +539,80 @@ __global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamPa
             p.out_finished[out + rank] = v == p.end_token || (finished != nullptr && finished[w] != 0);
         }
     }
-    for (int k = n + tid; k < K; k += kJoinThreads) {
+    for (int k = n + tid; k < K; k += THREADS) {
         p.out_scores[out + k] = -INFINITY;
         p.parents[out + k] = p.tokens[out + k] = -1;
         p.out_finished[out + k] = 1;
     }
 }
 
+__global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamParams p) {
+    extern __shared__ BeamBase base[];  // [W]
+    griddep_launch_dependents();
+    griddep_wait();
+    const long first = static_cast<long>(blockIdx.x) * p.W * p.pieces;  // of the request's pieces
+    beam_join<kJoinThreads>(
+        p, blockIdx.x, base, [&](int l) { return p.keys + (first + l) * p.K; },
+        [&](int l) { return p.stats[first + l]; });
+}
+
+// Small requests in one launch, without a workspace: a cluster per request, whose CTAs take pieces in turns
+// and leave lists and sums in their shared memory, where the first CTA reads them.
 template <int TYPE, int VEC>
-cudaError_t launch_piece(const BeamParams &p, cudaStream_t stream) {
-    return launch_overlapped(fa_beam_piece_kernel<TYPE, VEC>, dim3(p.pieces * p.B * p.W), kThreads, 0, stream,
-                             p);
+__global__ void __launch_bounds__(kThreads) fa_beam_cluster_kernel(const BeamParams p) {
+    extern __shared__ __align__(16) unsigned char beam_smem[];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
+    const int units = p.W * p.pieces, slots = (units + ctas - 1) / ctas;
+    unsigned long long *lists = reinterpret_cast<unsigned long long *>(beam_smem);  // [slots][K]
+    float2 *stats = reinterpret_cast<float2 *>(lists + slots * p.K);                // [slots]
+    BeamBase *base = reinterpret_cast<BeamBase *>(stats + slots);                   // [W]
+    griddep_launch_dependents();
+    griddep_wait();
+    const int b = blockIdx.x / ctas;
+    for (int u = cta, slot = 0; u < units; u += ctas, ++slot) {
+        const int w = u / p.pieces, row = b * p.W + w;
+        if (p.finished != nullptr && p.finished[row] != 0) continue;
+        if (slot > 0) __syncthreads();  // the piece before is out of the way
+        beam_piece<TYPE, VEC, kThreads>(p, row, u - w * p.pieces, lists + slot * p.K, stats + slot);
+    }
+    cluster.sync();
+    if (cta == 0)
+        beam_join<kThreads>(
+            p, b, base, [&](int l) { return cluster.map_shared_rank(lists, l % ctas) + l / ctas * p.K; },
+            [&](int l) { return cluster.map_shared_rank(stats, l % ctas)[l / ctas]; });
+    cluster.sync();  // the lists have been read
+}
+
+template <int TYPE, int VEC>
+cudaError_t launch_vec(const BeamParams &p, cudaStream_t stream) {
+    if (p.ctas == 0) {
+        const cudaError_t e = launch_overlapped(fa_beam_piece_kernel<TYPE, VEC>, dim3(p.pieces * p.B * p.W),
+                                                kThreads, 0, stream, p);
+        return e != cudaSuccess ? e
+                                : launch_overlapped(fa_beam_join_kernel, dim3(p.B), kJoinThreads,
+                                                    sizeof(BeamBase) * p.W, stream, p);
+    }
+    const int slots = (p.W * p.pieces + p.ctas - 1) / p.ctas;
+    const size_t smem = slots * (p.K * sizeof(unsigned long long) + sizeof(float2)) + p.W * sizeof(BeamBase);
+    return launch_clusters(fa_beam_cluster_kernel<TYPE, VEC>, p.B, p.ctas, kThreads, smem, stream, p);
+}
+
+template <int TYPE>
+cudaError_t launch_type(const BeamParams &p, int vec, cudaStream_t stream) {
+    if constexpr (TYPE != kBeamF32)
+        if (vec == 8) return launch_vec<TYPE, 8>(p, stream);
+    return vec == 4 ? launch_vec<TYPE, 4>(p, stream)
+           : vec == 2 ? launch_vec<TYPE, 2>(p, stream)
+                      : launch_vec<TYPE, 1>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_beam_select(const BeamParams &p, int type, cudaStream_t stream) {
-    const int vec = beam_vec(p.logits, p.stride_b, p.stride_w, type);
-    cudaError_t e;
-    if (type == kBeamF32) {
-        e = vec == 4 ? launch_piece<kBeamF32, 4>(p, stream) : vec == 2 ? launch_piece<kBeamF32, 2>(p, stream)
-                                                                       : launch_piece<kBeamF32, 1>(p, stream);
-    } else if (type == kBeamBF16) {
-        e = vec == 8   ? launch_piece<kBeamBF16, 8>(p, stream)
-            : vec == 4 ? launch_piece<kBeamBF16, 4>(p, stream)
-            : vec == 2 ? launch_piece<kBeamBF16, 2>(p, stream)
-                       : launch_piece<kBeamBF16, 1>(p, stream);
-    } else {
-        e = vec == 8   ? launch_piece<kBeamF16, 8>(p, stream)
-            : vec == 4 ? launch_piece<kBeamF16, 4>(p, stream)
-            : vec == 2 ? launch_piece<kBeamF16, 2>(p, stream)
-                       : launch_piece<kBeamF16, 1>(p, stream);
-    }
-    if (e != cudaSuccess) return e;
-    return launch_overlapped(fa_beam_join_kernel, dim3(p.B), kJoinThreads, sizeof(BeamBase) * p.W,
-                            stream, p);
+cudaError_t launch_beam_select(const BeamParams &p, int type, int vec, cudaStream_t stream) {
+    return type == kBeamF32    ? launch_type<kBeamF32>(p, vec, stream)
+           : type == kBeamBF16 ? launch_type<kBeamBF16>(p, vec, stream)
+                               : launch_type<kBeamF16>(p, vec, stream);
 }
 
 }  // namespace fa

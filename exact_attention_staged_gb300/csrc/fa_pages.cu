@@ -444,31 +444,6 @@ __global__ void __launch_bounds__(kCopyWarps * 32) fa_paged_copy_kernel(const Pa
     }
 }
 
-// A launch of one cluster that may overlap the end of the grid before it.
-template <class Params>
-cudaError_t launch_cluster(void (*kernel)(Params), int ctas, size_t smem, cudaStream_t stream,
-                           const Params &p) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kReserveThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 }  // namespace
 
 cudaError_t launch_paged_free(const PagedFreeParams &p, cudaStream_t stream) {
@@ -492,12 +467,13 @@ cudaError_t launch_paged_fork(PagedForkParams p, cudaStream_t stream) {
 cudaError_t launch_paged_reserve(const PagedReserveParams &p, cudaStream_t stream) {
     const long items = (static_cast<long>(p.c.T) >> p.t.page_shift) + 2l * p.t.B;
     const int ctas = items <= kReserveThreads && p.t.num_pages <= 8 * kReserveThreads ? 1 : kReserveCtas;
-    return launch_cluster(fa_paged_reserve_kernel, ctas, sizeof(int) * (p.t.B + 1), stream, p);
+    return launch_clusters(fa_paged_reserve_kernel, 1, ctas, kReserveThreads, sizeof(int) * (p.t.B + 1), stream,
+                           p);
 }
 
 cudaError_t launch_paged_compact(const PagedCompactParams &p, cudaStream_t stream) {
     const int ctas = p.t.num_pages <= 8 * kReserveThreads ? 1 : kReserveCtas;
-    const cudaError_t e = launch_cluster(fa_paged_plan_kernel, ctas, 0, stream, p);
+    const cudaError_t e = launch_clusters(fa_paged_plan_kernel, 1, ctas, kReserveThreads, 0, stream, p);
     if (e != cudaSuccess) return e;
     const long work = std::max(static_cast<long>(p.t.B) * p.t.max_pages, static_cast<long>(p.t.num_pages) / 2);
     const long blocks = std::min((work + 255) / 256, 152l * 8);

@@ -458,7 +458,8 @@ int fa_paged_copy(void *k_pages, void *v_pages, const long long *strides, const 
  * places left have score -inf, parent and token -1 and out_finished 1.
  * W V, B W and B K are below 2^31; K is at most 128 and W at most 2048 (otherwise
  * FA_ERR_UNSUPPORTED).  Sums are fp32.
- *   workspace : at least fa_beam_select_workspace_bytes() bytes, 16-byte aligned, as in fa_paged_attn.
+ *   workspace : at least fa_beam_select_workspace_bytes() bytes, 16-byte aligned, as in fa_paged_attn (may be
+ *               NULL when that is 0).
  */
 size_t fa_beam_select_workspace_bytes(int B, int W, int V, int K);
 int fa_beam_select(const void *logits, const long long *strides, const float *scores,

@@ -69,7 +69,10 @@ def beams(seed, B, W):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("B,W,V,K", [(1, 1, 1, 1), (1, 1, 1, 5), (2, 3, 7, 21), (2, 3, 7, 30), (3, 2, 255, 4),
                                      (1, 5, 8191, 10), (2, 2, 8192, 64), (1, 3, 8193, 65), (2, 4, 20001, 8),
-                                     (1, 2, 50002, 128), (5, 7, 1004, 14), (1, 40, 3001, 80)])
+                                     (1, 2, 50002, 128), (5, 7, 1004, 14), (1, 40, 3001, 80),
+                                     # a cluster per request up to 38 of them and 128 tiles (odd rows: 64); larger calls
+                                     (77, 1, 300, 5), (80, 2, 12301, 40), (300, 1, 20002, 3), (1, 50, 30001, 9),
+                                     (2, 130, 4097, 128), (38, 2, 4097, 4), (39, 2, 4097, 4)])
 def test_selection_is_the_definitions(cuda_lib, B, W, V, K, dtype):
     check(cuda_lib, normal(V + K, B, W, V, dtype=dtype), beams(V, B, W), K, exact=dtype == torch.float32)
 
@@ -175,9 +178,10 @@ def test_large_magnitudes(cuda_lib):
 
 
 def test_results_do_not_depend_on_what_the_buffers_held(cuda_lib):
-    x, s = normal(11, 3, 4, 30001, dtype=torch.bfloat16), beams(11, 3, 4)
+    x, s = normal(11, 80, 2, 30001, dtype=torch.bfloat16), beams(11, 80, 2)
     want = [t.clone() for t in cuda_lib.beam_select(x, s, k=9, end_token=3)]
-    n = cuda_lib.beam_select_workspace_bytes(3, 4, 30001, 9)
+    n = cuda_lib.beam_select_workspace_bytes(80, 2, 30001, 9)
+    assert n > 0
     for fill in (0, 255, 127):
         ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
         out = [torch.full_like(t, 77) for t in want]
@@ -196,7 +200,8 @@ def test_beam_arguments_that_are_refused(cuda_lib):
                  lambda: api.beam_select(x, s, finished=s, end_token=1),
                  lambda: api.beam_select(x.transpose(1, 2), s),
                  lambda: api.beam_select(x, s, out_tokens=torch.zeros(2, 3, device=DEV)),
-                 lambda: api.beam_select(x, s, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))):
+                 lambda: api.beam_select(x.repeat(300, 1, 1), s.repeat(300, 1),
+                                         workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))):
         with pytest.raises(ValueError):
             call()
     with pytest.raises(TypeError):

@@ -176,13 +176,15 @@ def test_beam_refusals(lib):
     odd = ctypes.c_void_p(17)
     for b in (dict(x=NONE), dict(x=odd), dict(x=ODD, dt=api.FA_FP32), dict(scores=NONE), dict(scores=ODD),
               dict(os=NONE), dict(op=ODD), dict(ot=NONE), dict(of=NONE), dict(B=0), dict(W=0), dict(V=0),
-              dict(K=0), dict(dt=3), dict(dt=-1), dict(end=50), dict(end=-2), dict(fin=P16), dict(ws=NONE),
-              dict(ws=ODD), dict(wsb=16), dict(W=2000, V=1 << 21), dict(B=1 << 22, W=1 << 10),
-              dict(st=(ctypes.c_longlong * 2)(-1, 50)), dict(st=(ctypes.c_longlong * 2)(150, 1 << 40))):
+              dict(K=0), dict(dt=3), dict(dt=-1), dict(end=50), dict(end=-2), dict(fin=P16),
+              dict(B=600, ws=NONE), dict(B=600, ws=ODD), dict(B=600, wsb=16), dict(W=2000, V=1 << 21),
+              dict(B=1 << 22, W=1 << 10), dict(st=(ctypes.c_longlong * 2)(-1, 50)), dict(st=(ctypes.c_longlong * 2)(150, 1 << 40))):
         assert beam(**b) == api.FA_ERR_INVALID, b
     for b in (dict(K=129), dict(W=2049)):
         assert beam(**b) == api.FA_ERR_UNSUPPORTED, b
-    assert api.beam_select_workspace_bytes(2, 3, 50, 3) == 256 + 256
+    assert api.beam_select_workspace_bytes(2, 3, 50, 3) == 0  # done in one launch
+    # 256 rows of 32 tiles of 4096 logits in two pieces each: 512 lists of 8 candidates, and sums
+    assert api.beam_select_workspace_bytes(64, 4, 131072, 8) == 512 * 8 * 8 + 512 * 8
     assert api.beam_select_workspace_bytes(0, 3, 50, 3) == 0
     assert api.beam_select_workspace_bytes(2, 3, 50, 129) == 0
 
