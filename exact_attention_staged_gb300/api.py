@@ -65,7 +65,7 @@ SIGNATURES = {
     "fa_paged_attn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
     "fa_paged_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                            _i, _i, _i, _f, _i, _vp, _sz, _vp]),
-    "fa_paged_reserve_workspace_bytes": (_sz, [_i, _i, _i]),
+    "fa_paged_reserve_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "fa_paged_reserve": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
     "fa_paged_fork": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp]),
     "fa_paged_free": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp]),
@@ -610,8 +610,8 @@ def paged_reserve(block_table, kv_len, refs, page_size: int, q_start=None, token
     return _calls().paged_reserve(block_table, kv_len, refs, page_size, q_start, tokens, copies, workspace)
 
 
-def paged_reserve_workspace_bytes(tokens: int, B: int, page_size: int) -> int:
-    return int(load().fa_paged_reserve_workspace_bytes(tokens, B, page_size))
+def paged_reserve_workspace_bytes(tokens: int, B: int, num_pages: int, page_size: int) -> int:
+    return int(load().fa_paged_reserve_workspace_bytes(tokens, B, num_pages, page_size))
 
 
 def paged_fork(block_table, parents, refs, kv_len=None, stream=None):

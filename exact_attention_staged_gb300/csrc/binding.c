@@ -26,7 +26,7 @@ typedef int (*attn_fn)(const void *, const void *, const void *, void *, float *
 typedef size_t (*attn_bytes_fn)(int, int, int, int, int, int, int, int);
 typedef int (*reserve_fn)(int *, const int *, const int *, int *, int *, int, int, int, int, int, void *,
                           size_t, void *);
-typedef size_t (*reserve_bytes_fn)(int, int, int);
+typedef size_t (*reserve_bytes_fn)(int, int, int, int);
 typedef int (*fork_fn)(int *, int *, const int *, int *, int, int, int, void *);
 typedef int (*free_fn)(int *, const int *, int *, int, int, int, int, void *);
 typedef int (*compact_fn)(int *, int *, int *, int *, int *, int, int, int, void *, size_t, void *);
@@ -632,7 +632,7 @@ static PyObject *py_reserve(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     rc = dense_result(&copies, g_i32, shape, 2, device, &pc);
     Py_DECREF(device);
     if (rc == NULL) return NULL;
-    const size_t need = T < 1 || page < 1 ? 0 : g_reserve_bytes((int)T, (int)B, (int)page);
+    const size_t need = T < 1 || page < 1 ? 0 : g_reserve_bytes((int)T, (int)B, (int)refs.shape[0], (int)page);
     if (workspace(&ws, need, table.obj, &pw, &rw) || stream_of(dev, &stream)) goto fail;
     {
         int code;

@@ -20,14 +20,14 @@ struct PagedReserveParams {
     PagedView c;              // the batch; c.table is t.table
     PageTables t;
     int *copies;              // [3, B]: page to copy from, page to copy to, rows; or nullptr
-    int *fresh;               // workspace: the pages given out, in order
+    int *fresh;               // workspace, where reserve_shape() has none: the pages given out, in order
 };
 
 struct PagedForkParams {
     PageTables t;
     int *kv_len;              // [B] or nullptr
     const int *parents;       // [B]
-    int cols;                 // columns of the table per block (set by the launcher)
+    int shift;                // 2^shift columns of the table per block (set by the launcher)
 };
 
 struct PagedFreeParams {
@@ -51,10 +51,10 @@ struct PagedCopyParams {
     PagedCopySide k, v;
     const int *src, *dst, *rows, *count;
     int n, L, num_pages;
-    // a page is `outers` runs of `inners` pieces of 16 * (1 << piece_shift) bytes; rows are the outer
-    // index or the inner one
+    // a page's runs are its heads, with the rows as inner index, or the other way round
     int heads, page_size, rows_inner;
-    int piece_shift;
+    int piece_shift;                 // a head's row is 2^piece_shift pieces of 16 bytes
+    unsigned parts, per;             // blocks of a pair, and runs of each (set by the launcher)
     int *status;
 };
 
@@ -77,10 +77,14 @@ cudaError_t launch_paged_reserve(const PagedReserveParams &p, cudaStream_t strea
 cudaError_t launch_paged_fork(PagedForkParams p, cudaStream_t stream);
 cudaError_t launch_paged_free(const PagedFreeParams &p, cudaStream_t stream);
 cudaError_t launch_paged_compact(const PagedCompactParams &p, cudaStream_t stream);
-cudaError_t launch_paged_copy(const PagedCopyParams &p, cudaStream_t stream);
+cudaError_t launch_paged_copy(PagedCopyParams p, cudaStream_t stream);
+struct ReserveShape {
+    int threads, ctas;
+};
+ReserveShape reserve_shape(int T, int B, int num_pages, int page_size);
 
 // Sequences that one call may have: their places are kept in shared memory.
-constexpr int kBranchMaxSeqs = 32768;
+constexpr int kBranchMaxSeqs = 16384;
 
 enum BeamType { kBeamF16 = 0, kBeamBF16 = 1, kBeamF32 = 2 };
 constexpr int kBeamThreads = 256;
@@ -123,7 +127,7 @@ cudaError_t launch_clusters(void (*kernel)(Params), int clusters, int ctas, int 
     attr[1].val.clusterDim.x = ctas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

@@ -1206,9 +1206,11 @@ int fa_paged_fork(int *block_table, int *kv_len, const int *parents, int *refs, 
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-size_t fa_paged_reserve_workspace_bytes(int T, int B, int page_size) {
+size_t fa_paged_reserve_workspace_bytes(int T, int B, int num_pages, int page_size) {
     fa::PagedView c = {};
-    if (check_paged(T, B, 1, 1, 64, 1, page_size, 1, FA_BF16, &c) != FA_OK) return 0;
+    if (check_paged(T, B, 1, 1, 64, num_pages, page_size, 1, FA_BF16, &c) != FA_OK ||
+        fa::reserve_shape(T, B, num_pages, page_size).threads > 0)
+        return 0;
     return round256(sizeof(int) * static_cast<size_t>(reserve_items(T, B, page_size)));
 }
 
@@ -1220,10 +1222,9 @@ int fa_paged_reserve(int *block_table, const int *kv_len, const int *q_start, in
     if (rc != FA_OK) return rc;
     rc = check_paged_index(block_table, kv_len, q_start, &p.c);
     if (rc != FA_OK) return rc;
-    rc = check_ptrs({workspace});
-    if (rc != FA_OK) return rc;
+    const size_t need = fa_paged_reserve_workspace_bytes(T, B, num_pages, page_size);
     if (!aligned4(copies) || reserve_items(T, B, page_size) >= (1l << 31) ||
-        workspace_bytes < fa_paged_reserve_workspace_bytes(T, B, page_size))
+        (need > 0 && (check_ptrs({workspace}) != FA_OK || workspace_bytes < need)))
         return FA_ERR_INVALID;
     rc = check_tables(block_table, refs, B, num_pages, page_size, max_pages, &p.t);
     if (rc != FA_OK) return rc;
@@ -1264,7 +1265,7 @@ int fa_paged_copy(void *k_pages, void *v_pages, const long long *strides, const 
     fa::PagedView c = {};
     int rc = check_paged(1, 1, H_kv, H_kv, d, num_pages, page_size, 1, FA_BF16, &c);
     if (rc != FA_OK) return rc;
-    if (n < 1 || L < 1) return FA_ERR_INVALID;
+    if (n < 1 || L < 1 || 2ll * L * std::max(H_kv, page_size) >= (1ll << 31)) return FA_ERR_INVALID;
     rc = check_ptrs({k_pages, v_pages});
     if (rc != FA_OK) return rc;
     if (src == nullptr || dst == nullptr) return FA_ERR_INVALID;

@@ -59,15 +59,17 @@ __global__ void __launch_bounds__(kFreeThreads) fa_paged_free_kernel(const Paged
 }
 
 // ------------------------------------------------------------------------------------------ fork
-// Row b becomes row parents[b].  A block takes `cols` columns of all rows, which are independent of
-// the others, into shared memory and writes them back permuted: in place, without a second table.  A
-// page's count changes by the row's new holders less one.
+// Row b becomes row parents[b].  A block takes 2^shift columns of all rows, which are independent of the
+// others, into shared memory and writes them back permuted: in place, without a second table.  A page's
+// count changes by the row's new holders less one.  Rows that stay as they are and have no other child are
+// neither read nor written.
 constexpr int kForkThreads = 256;
+constexpr int kForkBatch = 4;  // entries of a thread in flight together
 
 __global__ void __launch_bounds__(kForkThreads) fa_paged_fork_kernel(const PagedForkParams p) {
     extern __shared__ int fork_smem[];
     const PageTables &t = p.t;
-    const int B = t.B, cols = p.cols;
+    const int B = t.B, shift = p.shift;
     int *parent = fork_smem, *children = fork_smem + B, *tile = fork_smem + 2 * B;
     for (int b = threadIdx.x; b < B; b += kForkThreads) children[b] = 0;
     griddep_launch_dependents();
@@ -91,27 +93,38 @@ __global__ void __launch_bounds__(kForkThreads) fa_paged_fork_kernel(const Paged
             if (parent[b] != b) p.kv_len[b] = parent[b] >= 0 ? len[parent[b]] : 0;
         __syncthreads();
     }
-    const int c0 = blockIdx.x * cols, width = min(cols, t.max_pages - c0);
-    for (int x = threadIdx.x; x < B * cols; x += kForkThreads) {
-        const int b = x / cols, c = x - b * cols;
-        if (c >= width || (parent[b] == b && children[b] == 1)) continue;
-        tile[x] = t.table[static_cast<long>(b) * t.max_pages + c0 + c];
+    const int c0 = blockIdx.x << shift, c = threadIdx.x & ((1 << shift) - 1);
+    const int width = min(1 << shift, t.max_pages - c0), entries = B << shift;
+    // entry x is column c of row x >> shift, and so are the thread's others
+    auto used = [&](int x) {
+        const int b = x >> shift;
+        return x < entries && c < width && !(parent[b] == b && children[b] == 1);
+    };
+    auto place = [&](int x) { return static_cast<long>(x >> shift) * t.max_pages + c0 + c; };
+    for (int x0 = threadIdx.x; x0 < entries; x0 += kForkBatch * kForkThreads) {
+        int e[kForkBatch];
+#pragma unroll
+        for (int k = 0; k < kForkBatch; ++k) {
+            const int x = x0 + k * kForkThreads;
+            if (used(x)) e[k] = t.table[place(x)];
+        }
+#pragma unroll
+        for (int k = 0; k < kForkBatch; ++k) {
+            const int x = x0 + k * kForkThreads;
+            if (!used(x)) continue;
+            tile[x] = e[k];
+            const int more = children[x >> shift] - 1;
+            if (e[k] < 0 || more == 0) continue;
+            if (e[k] >= t.num_pages || atomicAdd(&t.refs[e[k]], more) + more < 0) page_report(t.status);
+        }
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < B * cols; x += kForkThreads) {
-        const int b = x / cols, c = x - b * cols;
-        if (c >= width || (parent[b] == b && children[b] == 1)) continue;
-        const int e = tile[x], more = children[b] - 1;
-        if (e >= 0 && more != 0) {
-            if (e >= t.num_pages) {
-                page_report(t.status);
-            } else if (atomicAdd(&t.refs[e], more) + more < 0) {
-                page_report(t.status);
-            }
-        }
-        if (parent[b] == b) continue;
-        const int now = parent[b] >= 0 ? tile[parent[b] * cols + c] : -1;
-        if (now != e) t.table[static_cast<long>(b) * t.max_pages + c0 + c] = now;
+    for (int x = threadIdx.x; x < entries; x += kForkThreads) {
+        if (!used(x)) continue;
+        const int b = x >> shift, q = parent[b];
+        if (q == b) continue;
+        const int now = q >= 0 ? tile[(q << shift) + c] : -1;
+        if (now != tile[x]) t.table[place(x)] = now;
     }
 }
 
@@ -119,14 +132,15 @@ __global__ void __launch_bounds__(kForkThreads) fa_paged_fork_kernel(const Paged
 // One cluster does all of it (a CTA where there is little), in steps with a barrier between them.
 // An item is a page place that a sequence's new tokens write to; items are numbered by sequence,
 // then place, and so are the pages that they get.
-//   1  every item that has a page gives its hold back: refs becomes the holders that do not write
-//   2  where none is left, the items that had the page compete for it with their numbers
-//   3  the lowest keeps it; all other items, and those that had none, are left with -1; needs and
-//      free pages are counted
-//   4  the free pages are listed by rank, as far as they are needed
-//   5  item after item takes the page of its rank
+//   1  items are numbered, free pages are listed by rank, as many as there are items
+//   2  every item that has a page gives its hold back: refs becomes the holders that do not write
+//   3  where none is left, the items that had the page compete for it with their numbers
+//   4  the lowest keeps it; all other items, and those that had none, are numbered again
+//   5  and take the page of their rank
+// A step is a round trip to L2 and a barrier, some 0.7 us; a thread keeps one item in registers.
 constexpr int kReserveThreads = 1024;
-constexpr int kReserveCtas = 8;  // the portable cluster size
+constexpr int kReserveCtas = 8;    // the portable cluster size
+constexpr int kReserveRounds = 8;  // groups of four pages whose state a thread keeps
 
 // Exclusive prefix of x over the CTA's threads, and the sum; `scratch` holds 33 ints.
 __device__ __forceinline__ int block_scan(int x, int *scratch, int *sum) {
@@ -169,7 +183,146 @@ __device__ __forceinline__ int free_bits(const int *refs, long i, long end) {
     return (r[0] == 0) | (r[1] == 0) << 1 | (r[2] == 0) << 2 | (r[3] == 0) << 3;
 }
 
+// A sequence's first place, and how many its tokens write to.
+__device__ __forceinline__ int reserve_places(const PagedReserveParams &p, int b, bool report, int *first,
+                                              int *ctx) {
+    const PagedSeq s = paged_seq(p.c, b);
+    *ctx = max(s.ctx, 0);
+    *first = *ctx >> p.t.page_shift;
+    if (s.bad && report) page_report(p.t.status);
+    if (s.bad || s.n == 0 || s.len == 0) return 0;
+    return ((s.len - 1) >> p.t.page_shift) + 1 - *first;
+}
+
+// Offsets in order are what bounds the items by the batch's tokens: with others nothing is reserved.
+__device__ __forceinline__ bool reserve_ordered(const PagedReserveParams &p, bool first_cta) {
+    bool ordered = true;
+    for (int b = threadIdx.x; b < p.t.B; b += blockDim.x) {
+        if (p.c.q_start != nullptr && p.c.q_start[b + 1] < p.c.q_start[b]) ordered = false;
+        if (p.copies != nullptr && first_cta) {
+            p.copies[b] = p.copies[p.t.B + b] = -1;
+            p.copies[2 * p.t.B + b] = 0;
+        }
+    }
+    if (__syncthreads_and(ordered) != 0) return true;
+    if (threadIdx.x == 0 && first_cta) page_report(p.t.status);
+    return false;
+}
+
+// No more items than threads, and no more pages than their registers hold.
 __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const PagedReserveParams p) {
+    extern __shared__ int before[];  // [B + 1] items before each sequence's
+    __shared__ int scratch[33];
+    __shared__ int counts[2];               // this CTA's free pages and needs
+    __shared__ int fresh[kReserveThreads];  // free pages of ranks cta * threads on
+    griddep_launch_dependents();
+    griddep_wait();
+    cg::cluster_group cluster = cg::this_cluster();
+    const PageTables &t = p.t;
+    const int B = t.B, tid = threadIdx.x, threads = static_cast<int>(blockDim.x);
+    const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
+    auto barrier = [&] {
+        if (ctas > 1) cluster.sync();
+        else __syncthreads();
+    };
+    // four pages a round, neighbouring groups in neighbouring threads
+    const long share = ((t.num_pages + 3l) / 4 + ctas - 1) / ctas * 4;
+    const long from = min(static_cast<long>(t.num_pages), cta * share);
+    const long to = min(static_cast<long>(t.num_pages), from + share);
+    unsigned free_of = 0;
+#pragma unroll
+    for (int r = 0; r < kReserveRounds; ++r)
+        free_of |= static_cast<unsigned>(free_bits(t.refs, from + 4l * (r * threads + tid), to)) << 4 * r;
+    if (!reserve_ordered(p, cta == 0)) return;
+    int items = 0, sum;
+    for (int b0 = 0; b0 < B; b0 += threads) {
+        const int b = b0 + tid;
+        int first, ctx;
+        const int x = block_scan(b < B ? reserve_places(p, b, cta == 0, &first, &ctx) : 0, scratch, &sum);
+        if (b < B) before[b] = items + x;
+        items += sum;
+    }
+    if (tid == 0) before[B] = items;
+    // free pages before each of the thread's groups: rounds one after the other
+    int free_mine[kReserveRounds], frees = 0;
+    const int rounds = static_cast<int>((to - from + 4l * threads - 1) / (4l * threads));
+#pragma unroll
+    for (int r = 0; r < kReserveRounds; ++r)
+        if (r < rounds) {
+            free_mine[r] = frees + block_scan(__popc(free_of >> 4 * r & 15u), scratch, &sum);
+            frees += sum;
+        }
+    if (tid == 0) counts[0] = frees;
+    barrier();
+    int free_before = 0, free_all = 0;
+    for (int c = 0; c < ctas; ++c) {
+        const int x = *cluster.map_shared_rank(&counts[0], c);
+        if (c < cta) free_before += x;
+        free_all += x;
+    }
+#pragma unroll
+    for (int r = 0; r < kReserveRounds; ++r)
+        if (r < rounds && (free_of >> 4 * r & 15u) != 0) {
+            int rank = free_before + free_mine[r];
+            for (int k = 0; k < 4; ++k)
+                if (free_of >> (4 * r + k) & 1) {
+                    if (rank < items)
+                        *cluster.map_shared_rank(&fresh[rank % threads], rank / threads) =
+                            static_cast<int>(from + 4l * (r * threads + tid)) + k;
+                    ++rank;
+                }
+        }
+
+    const int g = cta * threads + tid;  // this thread's item
+    int b = 0, e = -1, *at = nullptr;
+    bool had = false;
+    if (g < items) {
+        int r = B;  // before[b] <= g < before[r]
+        while (r - b > 1) {
+            const int m = (b + r) / 2;
+            if (before[m] <= g) b = m;
+            else r = m;
+        }
+        at = t.table + static_cast<long>(b) * t.max_pages + (max(paged_seq(p.c, b).ctx, 0) >> t.page_shift) + g -
+             before[b];
+        e = *at;
+        had = e >= 0 && e < t.num_pages;
+        if (had) atomicSub(&t.refs[e], 1);
+        else if (e != -1) page_report(t.status);
+    }
+    barrier();
+    if (had && __ldcg(&t.refs[e]) <= 0) atomicMin(&t.refs[e], INT_MIN + g);
+    barrier();
+    bool need = g < items;
+    if (had && __ldcg(&t.refs[e]) == INT_MIN + g) {
+        t.refs[e] = 1;
+        need = false;
+    }
+    int rank = block_scan(need, scratch, &sum);
+    if (tid == 0) counts[1] = sum;
+    barrier();
+    if (need) {
+        for (int c = 0; c < cta; ++c) rank += *cluster.map_shared_rank(&counts[1], c);
+        const int page = rank < free_all ? *cluster.map_shared_rank(&fresh[rank % threads], rank / threads) : -1;
+        *at = page;
+        if (page >= 0) {
+            t.refs[page] = 1;
+            const int rows = max(paged_seq(p.c, b).ctx, 0) & ((1 << t.page_shift) - 1);
+            if (had && p.copies != nullptr && g == before[b] && rows > 0) {
+                p.copies[b] = e;
+                p.copies[B + b] = page;
+                p.copies[2 * B + b] = rows;
+            }
+        } else {
+            page_report(t.status, kErrFull);
+        }
+    }
+    if (ctas > 1) cluster.sync();  // the others have read this CTA's shared memory
+}
+
+// Any number of items and pages: the same steps, in which every thread walks its share and finds it anew, and
+// free pages are counted and listed (in the workspace) once it is known how many are needed.
+__global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_many_kernel(const PagedReserveParams p) {
     extern __shared__ int before[];  // [B + 1] items before each sequence's
     __shared__ int scratch[33];
     __shared__ int counts[2];        // this CTA's needs and free pages
@@ -180,34 +333,12 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
     const int B = t.B, tid = threadIdx.x;
     const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
 
-    // a sequence's first place, and how many its tokens write to
-    auto places = [&](int b, int *first, int *ctx) {
-        const PagedSeq s = paged_seq(p.c, b);
-        *ctx = max(s.ctx, 0);
-        *first = *ctx >> t.page_shift;
-        if (s.bad && cta == 0) page_report(t.status);
-        if (s.bad || s.n == 0 || s.len == 0) return 0;
-        return ((s.len - 1) >> t.page_shift) + 1 - *first;
-    };
-    // offsets in order are what bounds the items by the batch's tokens: others reserve nothing
-    bool ordered = true;
-    for (int b = tid; b < B; b += kReserveThreads) {
-        if (p.c.q_start != nullptr && p.c.q_start[b + 1] < p.c.q_start[b]) ordered = false;
-        if (p.copies != nullptr && cta == 0) {
-            p.copies[b] = p.copies[B + b] = -1;
-            p.copies[2 * B + b] = 0;
-        }
-    }
-    if (__syncthreads_and(ordered) == 0) {
-        if (tid == 0 && cta == 0) page_report(t.status);
-        return;
-    }
+    if (!reserve_ordered(p, cta == 0)) return;
     int items = 0;
     for (int b0 = 0; b0 < B; b0 += kReserveThreads) {
         const int b = b0 + tid;
         int first, ctx, sum;
-        const int n = b < B ? places(b, &first, &ctx) : 0;
-        const int x = block_scan(n, scratch, &sum);
+        const int x = block_scan(b < B ? reserve_places(p, b, cta == 0, &first, &ctx) : 0, scratch, &sum);
         if (b < B) before[b] = items + x;
         items += sum;
     }
@@ -398,7 +529,8 @@ __global__ void __launch_bounds__(256) fa_paged_apply_kernel(const PagedCompactP
 
 // ------------------------------------------------------------------------------------------ copy
 // A warp copies a run: consecutive 16-byte pieces of one page of one layer.  Runs are a head's rows
-// or, where the heads of a token lie side by side, a row's heads.
+// or, where the heads of a token lie side by side, a row's heads.  A block takes some of the runs of one
+// pair of pages, so that the pair is looked up and the work divided once.
 constexpr int kCopyWarps = 8;
 constexpr int kCopyBatch = 8;  // pieces of a lane in flight together
 
@@ -406,40 +538,40 @@ __global__ void __launch_bounds__(kCopyWarps * 32) fa_paged_copy_kernel(const Pa
     griddep_launch_dependents();
     griddep_wait();
     const int n = p.count != nullptr ? min(max(*p.count, 0), p.n) : p.n;
-    const int runs = p.rows_inner ? p.heads : p.page_size;  // of a page
-    const long units = static_cast<long>(n) * p.L * 2 * runs;
-    const long warps = static_cast<long>(gridDim.x) * kCopyWarps;
-    for (long u = blockIdx.x * static_cast<long>(kCopyWarps) + warp_id(); u < units; u += warps) {
-        long x = u / runs;
-        const int run = static_cast<int>(u - x * runs);
-        const bool isv = x & 1;
-        x >>= 1;
-        const int e = static_cast<int>(x / p.L), layer = static_cast<int>(x - static_cast<long>(e) * p.L);
+    const unsigned parts = p.parts, per = p.per;  // blocks of a pair, and the runs that each takes
+    const long units = static_cast<long>(n) * parts;
+    for (long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int e = static_cast<int>(u / parts);
+        const unsigned part = static_cast<unsigned>(u - static_cast<long>(e) * parts);
         const int src = p.src[e], dst = p.dst[e];
-        int rows = p.rows != nullptr ? p.rows[e] : p.page_size;
+        const int rows = p.rows != nullptr ? p.rows[e] : p.page_size;
         if (src < 0 || dst < 0) continue;
         if (src >= p.num_pages || dst >= p.num_pages || rows < 0 || rows > p.page_size) {
-            if (lane_id() == 0) page_report(p.status);
+            if (threadIdx.x == 0) page_report(p.status);
             continue;
         }
-        if (!p.rows_inner && run >= rows) continue;
-        const int inners = p.rows_inner ? rows : p.heads;
-        const PagedCopySide &s = isv ? p.v : p.k;
-        const uint16_t *from = s.base + layer * s.layer + src * s.page + run * s.outer;
-        uint16_t *to = s.base + layer * s.layer + dst * s.page + run * s.outer;
-        const int pieces = inners << p.piece_shift;
-        for (int i0 = lane_id(); i0 < pieces; i0 += 32 * kCopyBatch) {
-            uint4 v[kCopyBatch];
-            long off[kCopyBatch];
+        // runs of a layer's K or V, in order (layer, K or V, run)
+        const unsigned runs = p.rows_inner ? p.heads : rows;
+        const int pieces = (p.rows_inner ? rows : p.heads) << p.piece_shift;
+        const unsigned end = min((part + 1) * per, static_cast<unsigned>(p.L) * 2 * runs);
+        for (unsigned x = part * per + warp_id(); x < end; x += kCopyWarps) {
+            const unsigned slab = x / runs, run = x - slab * runs;
+            const PagedCopySide &s = slab & 1 ? p.v : p.k;
+            const uint16_t *from = s.base + (slab >> 1) * s.layer + src * s.page + run * s.outer;
+            uint16_t *to = s.base + (slab >> 1) * s.layer + dst * s.page + run * s.outer;
+            for (int i0 = lane_id(); i0 < pieces; i0 += 32 * kCopyBatch) {
+                uint4 v[kCopyBatch];
+                long off[kCopyBatch];
 #pragma unroll
-            for (int k = 0; k < kCopyBatch; ++k) {
-                const int i = i0 + 32 * k;
-                off[k] = (i >> p.piece_shift) * s.inner + (i & ((1 << p.piece_shift) - 1)) * 8;
-                if (i < pieces) v[k] = *reinterpret_cast<const uint4 *>(from + off[k]);
+                for (int k = 0; k < kCopyBatch; ++k) {
+                    const int i = i0 + 32 * k;
+                    off[k] = (i >> p.piece_shift) * s.inner + (i & ((1 << p.piece_shift) - 1)) * 8;
+                    if (i < pieces) v[k] = *reinterpret_cast<const uint4 *>(from + off[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < kCopyBatch; ++k)
+                    if (i0 + 32 * k < pieces) *reinterpret_cast<uint4 *>(to + off[k]) = v[k];
             }
-#pragma unroll
-            for (int k = 0; k < kCopyBatch; ++k)
-                if (i0 + 32 * k < pieces) *reinterpret_cast<uint4 *>(to + off[k]) = v[k];
         }
     }
 }
@@ -452,23 +584,34 @@ cudaError_t launch_paged_free(const PagedFreeParams &p, cudaStream_t stream) {
 }
 
 cudaError_t launch_paged_fork(PagedForkParams p, cudaStream_t stream) {
-    p.cols = 32;
-    auto bytes = [&] { return sizeof(int) * p.t.B * (2 + static_cast<size_t>(p.cols)); };
-    while (p.cols > 1 && bytes() > 100 * 1024) p.cols /= 2;
-    if (bytes() > 48 * 1024) {
+    // columns of a block: a thousand entries or so, a sector of every row at least where that fits
+    p.shift = 5;
+    while (p.shift > 0 && (static_cast<long>(p.t.B) << p.shift) > (p.shift > 3 ? 1024 : 24 * 1024)) --p.shift;
+    const size_t bytes = sizeof(int) * p.t.B * (2 + (1ul << p.shift));
+    if (bytes > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(
-            fa_paged_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes()));
+            fa_paged_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
         if (e != cudaSuccess) return e;
     }
-    return launch_overlapped(fa_paged_fork_kernel, dim3((p.t.max_pages - 1) / p.cols + 1), kForkThreads,
-                             bytes(), stream, p);
+    return launch_overlapped(fa_paged_fork_kernel, dim3(((p.t.max_pages - 1) >> p.shift) + 1), kForkThreads,
+                             bytes, stream, p);
+}
+
+// Threads of each CTA and CTAs that hold the items and pages in registers, or {0, 0}.
+ReserveShape reserve_shape(int T, int B, int num_pages, int page_size) {
+    const long items = static_cast<long>(T) / page_size + 2l * B;
+    for (const ReserveShape s : {ReserveShape{256, 1}, ReserveShape{1024, 1}, ReserveShape{1024, kReserveCtas}}) {
+        const long all = static_cast<long>(s.threads) * s.ctas;
+        if (items <= all && num_pages <= 4 * kReserveRounds * all - 4 * s.ctas) return s;
+    }
+    return {0, 0};
 }
 
 cudaError_t launch_paged_reserve(const PagedReserveParams &p, cudaStream_t stream) {
-    const long items = (static_cast<long>(p.c.T) >> p.t.page_shift) + 2l * p.t.B;
-    const int ctas = items <= kReserveThreads && p.t.num_pages <= 8 * kReserveThreads ? 1 : kReserveCtas;
-    return launch_clusters(fa_paged_reserve_kernel, 1, ctas, kReserveThreads, sizeof(int) * (p.t.B + 1), stream,
-                           p);
+    const size_t smem = sizeof(int) * (p.t.B + 1);
+    const ReserveShape s = reserve_shape(p.c.T, p.t.B, p.t.num_pages, 1 << p.t.page_shift);
+    if (s.threads > 0) return launch_clusters(fa_paged_reserve_kernel, 1, s.ctas, s.threads, smem, stream, p);
+    return launch_clusters(fa_paged_reserve_many_kernel, 1, kReserveCtas, kReserveThreads, smem, stream, p);
 }
 
 cudaError_t launch_paged_compact(const PagedCompactParams &p, cudaStream_t stream) {
@@ -480,9 +623,14 @@ cudaError_t launch_paged_compact(const PagedCompactParams &p, cudaStream_t strea
     return launch_overlapped(fa_paged_apply_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, p);
 }
 
-cudaError_t launch_paged_copy(const PagedCopyParams &p, cudaStream_t stream) {
-    const long units = static_cast<long>(p.n) * p.L * 2 * (p.rows_inner ? p.heads : p.page_size);
-    const long blocks = std::min((units + kCopyWarps - 1) / kCopyWarps, 152l * 8);
+cudaError_t launch_paged_copy(PagedCopyParams p, cudaStream_t stream) {
+    // blocks of eight runs a warp, of fewer where the pairs are few
+    const long runs = 2l * p.L * (p.rows_inner ? p.heads : p.page_size);
+    long per = 8l * kCopyWarps;
+    while (per > kCopyWarps && p.n * ((runs + per - 1) / per) < 152 * 8) per /= 2;
+    p.per = static_cast<unsigned>(per);
+    p.parts = static_cast<unsigned>((runs + per - 1) / per);
+    const long blocks = std::min(static_cast<long>(p.n) * p.parts, 152l * 8);
     return launch_overlapped(fa_paged_copy_kernel, dim3(static_cast<unsigned>(blocks)), kCopyWarps * 32, 0,
                              stream, p);
 }

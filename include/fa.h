@@ -380,7 +380,7 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
  *               the caller adds for holds of its own (a prefix to be kept).  A page is free where refs
  *               is 0; refs starts out as zeros.
  * These two are the whole state; the calls leave them consistent, give pages out lowest id first, and
- * so always come to the same tables.  At most 32768 sequences (otherwise FA_ERR_UNSUPPORTED); calls on
+ * so always come to the same tables.  At most 16384 sequences (otherwise FA_ERR_UNSUPPORTED); calls on
  * one table or one refs array have to be ordered by the caller.  Values out of range are not
  * followed and reported as FA_ERR_INDEX by fa_sync_status(), as is a count that would fall below
  * zero or an entry that names a free page.
@@ -395,7 +395,8 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
  *   Sequences with a length or offset out of range get nothing, and none does where offsets decrease.
  *   Where the free pages run out, the places that are left get -1 (FA_ERR_FULL from fa_sync_status): a shared page's hold is given
  *   back, nobody else's pages are touched, and appending there is refused as usual.
- *   workspace : at least fa_paged_reserve_workspace_bytes() bytes, 16-byte aligned, as in fa_paged_attn.
+ *   workspace : at least fa_paged_reserve_workspace_bytes() bytes, 16-byte aligned, as in fa_paged_attn (may be
+ *               NULL when that is 0).
  *
  * fa_paged_fork: row b becomes what row parents[b] was; both hold its pages from then on.
  *   parents   : device int32 [B]: -1 leaves row b empty, parents[b] = b as it is; any row may have many
@@ -423,7 +424,7 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
  *               many; one that is copied to must not occur otherwise.
  *   count     : device int32: no more than that many pairs, or NULL.
  */
-size_t fa_paged_reserve_workspace_bytes(int T, int B, int page_size);
+size_t fa_paged_reserve_workspace_bytes(int T, int B, int num_pages, int page_size);
 int fa_paged_reserve(int *block_table, const int *kv_len, const int *q_start, int *refs, int *copies,
                      int T, int B, int num_pages, int page_size, int max_pages, void *workspace,
                      size_t workspace_bytes, void *stream);

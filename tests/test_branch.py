@@ -118,14 +118,16 @@ def reserve(lib, table=P16, lens=P16, qs=P16, refs=P16, copies=P16, T=6, B=2, pa
 def test_reserve_refusals(lib):
     for b in (dict(table=NONE), dict(table=ODD), dict(lens=NONE), dict(lens=ODD), dict(qs=ODD),
               dict(refs=NONE), dict(refs=ctypes.c_void_p(24)), dict(copies=ODD), dict(T=0), dict(B=0),
-              dict(pages=0), dict(width=0), dict(qs=NONE, T=7), dict(ws=NONE), dict(ws=ctypes.c_void_p(8)),
-              dict(wsb=255), dict(pages=1 << 28), dict(width=1 << 28), dict(T=1 << 30)):
+              dict(pages=0), dict(width=0), dict(qs=NONE, T=7), dict(B=9000, ws=NONE),
+              dict(B=9000, ws=ctypes.c_void_p(8)), dict(B=9000, wsb=255), dict(pages=1 << 28), dict(width=1 << 28), dict(T=1 << 30)):
         assert reserve(lib, **b) == api.FA_ERR_INVALID, b
-    for b in (dict(size=4), dict(size=24), dict(size=2048), dict(B=32769, T=32769)):
+    for b in (dict(size=4), dict(size=24), dict(size=2048), dict(B=16385, T=16385)):
         assert reserve(lib, **b) == api.FA_ERR_UNSUPPORTED, b
-    assert api.paged_reserve_workspace_bytes(64, 2, 16) == 256   # 4 + 2 * 2 places
-    assert api.paged_reserve_workspace_bytes(8192, 300, 8) == (1024 + 600) * 4 // 256 * 256 + 256
-    assert api.paged_reserve_workspace_bytes(0, 1, 16) == 0
+    assert api.paged_reserve_workspace_bytes(64, 2, 100, 16) == 0
+    assert api.paged_reserve_workspace_bytes(8192, 300, 100000, 8) == 0  # 1024 + 2 * 300 places in 8 CTAs
+    assert api.paged_reserve_workspace_bytes(1 << 20, 300, 1000, 8) == ((1 << 17) + 600) * 4 // 256 * 256 + 256
+    assert api.paged_reserve_workspace_bytes(300, 300, 300000, 8) == 600 * 4 // 256 * 256 + 256  # a large pool
+    assert api.paged_reserve_workspace_bytes(0, 1, 100, 16) == 0
 
 
 def test_fork_free_and_compact_refusals(lib):
@@ -145,7 +147,7 @@ def test_fork_free_and_compact_refusals(lib):
                                 dict(ws=ODD), dict(wsb=16)))):
         for b in both + more:
             assert fn(**b) == api.FA_ERR_INVALID, (fn.__name__, b)
-        assert fn(B=32769) == api.FA_ERR_UNSUPPORTED
+        assert fn(B=16385) == api.FA_ERR_UNSUPPORTED
     for size in (4, 24, 2048):
         assert free(size=size) == api.FA_ERR_UNSUPPORTED
     assert api.paged_compact_workspace_bytes(9) == 256

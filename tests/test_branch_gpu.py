@@ -69,7 +69,8 @@ class Pair:
 # one CTA and clusters, tables wider than a block's columns, one sequence and many
 @pytest.mark.parametrize("B,width,pages,page,steps", [
     (1, 1, 1, 8, 8), (1, 5, 7, 8, 20), (5, 33, 300, 16, 30), (64, 40, 9000, 8, 20), (37, 70, 33001, 32, 15),
-    (700, 11, 12345, 64, 12), (1500, 3, 4099, 1024, 10), (3, 2100, 8191, 8, 15),
+    (700, 11, 12345, 64, 12), (1500, 3, 4099, 1024, 10), (3, 2100, 8191, 8, 15), (130, 9, 8189, 16, 12),
+    (9, 40, 262145, 8, 10), (5000, 2, 9001, 64, 6), (16384, 2, 30000, 8, 5), (20, 300, 262111, 16, 8),
 ])
 def test_random_steps_come_to_the_definitions_tables(cuda_lib, B, width, pages, page, steps):
     c = Pair(cuda_lib, B, width, pages, page, seed=B)
@@ -310,7 +311,8 @@ def test_arguments_that_are_refused(cuda_lib):
             lambda: api.paged_reserve(t, n[:2], f, 16),
             lambda: api.paged_reserve(t, n.long(), f, 16),
             lambda: api.paged_reserve(t, n, f, 16, copies=torch.zeros(2, 3, dtype=torch.int32, device=DEV)),
-            lambda: api.paged_reserve(t, n, f, 16, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV)),
+            lambda: api.paged_reserve(t, n, f, 16, tokens=3 << 20,
+                                      workspace=torch.zeros(16, dtype=torch.uint8, device=DEV)),
             lambda: api.paged_reserve(t[:, :3], n, f, 16),
             lambda: api.paged_fork(t, n[:2], f), lambda: api.paged_fork(t, n, f.long()),
             lambda: api.paged_fork(t, n, f[::2]), lambda: api.paged_fork(t, n, f, kv_len=n[:1]),
