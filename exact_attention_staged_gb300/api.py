@@ -69,8 +69,7 @@ SIGNATURES = {
     "fa_paged_reserve": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
     "fa_paged_fork": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp]),
     "fa_paged_free": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp]),
-    "fa_paged_compact_workspace_bytes": (_sz, [_i]),
-    "fa_paged_compact": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _sz, _vp]),
+    "fa_paged_compact": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp]),
     "fa_paged_copy": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
     "fa_beam_select_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "fa_beam_select": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz,
@@ -434,8 +433,7 @@ def _calls():
         from . import _binding as ext
         names = ("fa_rope", "fa_paged_append", "fa_paged_attn", "fa_paged_attn_workspace_bytes",
                  "fa_paged_reserve", "fa_paged_reserve_workspace_bytes", "fa_paged_fork", "fa_paged_free",
-                 "fa_paged_compact", "fa_paged_compact_workspace_bytes", "fa_paged_copy",
-                 "fa_beam_select", "fa_beam_select_workspace_bytes")
+                 "fa_paged_compact", "fa_paged_copy", "fa_beam_select", "fa_beam_select_workspace_bytes")
         ext.setup(tuple(ctypes.cast(getattr(lib, n), _vp).value for n in names), torch.empty, _raw,
                   torch.bfloat16, torch.float16, torch.int32, torch.int64, torch.float32,
                   torch.uint8, FAError)
@@ -633,20 +631,16 @@ def paged_free(block_table, keep_len, refs, page_size: int, stream=None):
     return _calls().paged_free(block_table, keep_len, refs, page_size)
 
 
-def paged_compact(block_table, refs, moves=None, count=None, workspace=None, stream=None):
+def paged_compact(block_table, refs, moves=None, count=None, stream=None):
     """Moves the live pages to the front of the pool (fa_paged_compact).
 
     Returns moves, int32 [2, num_pages // 2 or more], and count, int32 [1]: paged_copy's src, dst and
     count, which move the data.  block_table and refs are updated.
     """
     if _away(block_table, stream):
-        return _elsewhere(lambda: paged_compact(block_table, refs, moves, count, workspace), stream,
-                          block_table.device, (block_table, refs, moves, count, workspace))
-    return _calls().paged_compact(block_table, refs, moves, count, workspace)
-
-
-def paged_compact_workspace_bytes(num_pages: int) -> int:
-    return int(load().fa_paged_compact_workspace_bytes(num_pages))
+        return _elsewhere(lambda: paged_compact(block_table, refs, moves, count), stream,
+                          block_table.device, (block_table, refs, moves, count))
+    return _calls().paged_compact(block_table, refs, moves, count)
 
 
 def paged_copy(k_pages, v_pages, src, dst, rows=None, count=None, stream=None):

@@ -29,8 +29,7 @@ typedef int (*reserve_fn)(int *, const int *, const int *, int *, int *, int, in
 typedef size_t (*reserve_bytes_fn)(int, int, int, int);
 typedef int (*fork_fn)(int *, int *, const int *, int *, int, int, int, void *);
 typedef int (*free_fn)(int *, const int *, int *, int, int, int, int, void *);
-typedef int (*compact_fn)(int *, int *, int *, int *, int *, int, int, int, void *, size_t, void *);
-typedef size_t (*compact_bytes_fn)(int);
+typedef int (*compact_fn)(int *, int *, int *, int *, int *, int, int, int, void *);
 typedef int (*copy_fn)(void *, void *, const long long *, const int *, const int *, const int *,
                        const int *, int, int, int, int, int, int, void *);
 typedef int (*beam_fn)(const void *, const long long *, const float *, const uint8_t *, float *, int *,
@@ -46,7 +45,6 @@ static reserve_bytes_fn g_reserve_bytes;
 static fork_fn g_fork;
 static free_fn g_free;
 static compact_fn g_compact;
-static compact_bytes_fn g_compact_bytes;
 static copy_fn g_copy;
 static beam_fn g_beam;
 static beam_bytes_fn g_beam_bytes;
@@ -690,31 +688,28 @@ static PyObject *py_free(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-/* paged_compact(block_table, refs, moves, count, workspace) */
+/* paged_compact(block_table, refs, moves, count) */
 static PyObject *py_compact(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
-    Tensor table, refs, moves, count, ws;
+    Tensor table, refs, moves, count;
     long dev;
-    if (count_args(n, 5) || take_tables(a[0], a[1], &dev, &table, &refs) ||
-        take(a[2], "moves", dev, &moves) || take(a[3], "count", dev, &count) ||
-        take(a[4], "workspace", dev, &ws))
+    if (count_args(n, 4) || take_tables(a[0], a[1], &dev, &table, &refs) ||
+        take(a[2], "moves", dev, &moves) || take(a[3], "count", dev, &count))
         return NULL;
     const long long pages = refs.shape[0], one[1] = {1};
     long long shape[2] = {2, pages > 1 ? pages / 2 : 1};
     if (moves.obj != NULL && moves.dims == 2 && moves.shape[1] > shape[1]) shape[1] = moves.shape[1];
-    PyObject *device = PyObject_GetAttr(table.obj, s_device), *rm = NULL, *rc = NULL, *rw = NULL, *out = NULL;
-    void *pm, *pc, *pw, *stream;
+    PyObject *device = PyObject_GetAttr(table.obj, s_device), *rm = NULL, *rc = NULL, *out = NULL;
+    void *pm, *pc, *stream;
     if (device == NULL) return NULL;
     if ((rm = dense_result(&moves, g_i32, shape, 2, device, &pm)) == NULL ||
-        (rc = dense_result(&count, g_i32, one, 1, device, &pc)) == NULL)
+        (rc = dense_result(&count, g_i32, one, 1, device, &pc)) == NULL || stream_of(dev, &stream))
         goto done;
-    const size_t need = g_compact_bytes((int)pages);
-    if (workspace(&ws, need, table.obj, &pw, &rw) || stream_of(dev, &stream)) goto done;
     {
         int code;
         Py_BEGIN_ALLOW_THREADS
         code = g_compact(table.ptr, refs.ptr, pm, (int *)pm + shape[1], pc, (int)table.shape[0], (int)pages,
-                         (int)table.shape[1], pw, need, stream);
+                         (int)table.shape[1], stream);
         Py_END_ALLOW_THREADS
         if (check_rc(code, "fa_paged_compact")) goto done;
     }
@@ -723,7 +718,6 @@ done:
     Py_DECREF(device);
     Py_XDECREF(rm);
     Py_XDECREF(rc);
-    Py_XDECREF(rw);
     return out;
 }
 
@@ -838,10 +832,10 @@ done:
  *       float16, int32, int64, float32, uint8, error class) */
 static PyObject *py_setup(PyObject *self, PyObject *args) {
     (void)self;
-    unsigned long long f[13];
+    unsigned long long f[12];
     PyObject *o[9];
-    if (!PyArg_ParseTuple(args, "(KKKKKKKKKKKKK)OOOOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6],
-                          &f[7], &f[8], &f[9], &f[10], &f[11], &f[12], &o[0], &o[1], &o[2], &o[3], &o[4],
+    if (!PyArg_ParseTuple(args, "(KKKKKKKKKKKK)OOOOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6],
+                          &f[7], &f[8], &f[9], &f[10], &f[11], &o[0], &o[1], &o[2], &o[3], &o[4],
                           &o[5], &o[6], &o[7], &o[8]))
         return NULL;
     g_rope = (rope_fn)(uintptr_t)f[0];
@@ -853,10 +847,9 @@ static PyObject *py_setup(PyObject *self, PyObject *args) {
     g_fork = (fork_fn)(uintptr_t)f[6];
     g_free = (free_fn)(uintptr_t)f[7];
     g_compact = (compact_fn)(uintptr_t)f[8];
-    g_compact_bytes = (compact_bytes_fn)(uintptr_t)f[9];
-    g_copy = (copy_fn)(uintptr_t)f[10];
-    g_beam = (beam_fn)(uintptr_t)f[11];
-    g_beam_bytes = (beam_bytes_fn)(uintptr_t)f[12];
+    g_copy = (copy_fn)(uintptr_t)f[9];
+    g_beam = (beam_fn)(uintptr_t)f[10];
+    g_beam_bytes = (beam_bytes_fn)(uintptr_t)f[11];
     PyObject **slots[9] = {&g_empty, &g_stream, &g_bf16, &g_fp16, &g_i32, &g_i64, &g_f32, &g_u8, &g_error};
     for (int i = 0; i < 9; ++i) {
         Py_INCREF(o[i]);

@@ -39,8 +39,7 @@ struct PagedCompactParams {
     PageTables t;
     int *src, *dst;           // [num_pages / 2]
     int *count;
-    int *live;                // workspace: live pages
-    int *rank;                // workspace [num_pages]: which move a page behind the live ones makes
+    int apply;                // table and refs too, in the same launch (set by the launcher)
 };
 
 struct PagedCopySide {
@@ -76,7 +75,7 @@ struct BeamParams {
 cudaError_t launch_paged_reserve(const PagedReserveParams &p, cudaStream_t stream);
 cudaError_t launch_paged_fork(PagedForkParams p, cudaStream_t stream);
 cudaError_t launch_paged_free(const PagedFreeParams &p, cudaStream_t stream);
-cudaError_t launch_paged_compact(const PagedCompactParams &p, cudaStream_t stream);
+cudaError_t launch_paged_compact(PagedCompactParams p, cudaStream_t stream);
 cudaError_t launch_paged_copy(PagedCopyParams p, cudaStream_t stream);
 struct ReserveShape {
     int threads, ctas;

@@ -1235,26 +1235,17 @@ int fa_paged_reserve(int *block_table, const int *kv_len, const int *q_start, in
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-size_t fa_paged_compact_workspace_bytes(int num_pages) {
-    return num_pages < 1 ? 0 : round256(sizeof(int) * (static_cast<size_t>(num_pages) + 4));
-}
-
 int fa_paged_compact(int *block_table, int *refs, int *src, int *dst, int *count, int B, int num_pages,
-                     int max_pages, void *workspace, size_t workspace_bytes, void *stream) {
+                     int max_pages, void *stream) {
     if (src == nullptr || dst == nullptr || count == nullptr || !aligned4(src) || !aligned4(dst) ||
         !aligned4(count))
         return FA_ERR_INVALID;
-    int rc = check_ptrs({workspace});
-    if (rc != FA_OK) return rc;
-    if (workspace_bytes < fa_paged_compact_workspace_bytes(num_pages)) return FA_ERR_INVALID;
     fa::PagedCompactParams p = {};
-    rc = check_tables(block_table, refs, B, num_pages, 8, max_pages, &p.t);
+    int rc = check_tables(block_table, refs, B, num_pages, 8, max_pages, &p.t);
     if (rc != FA_OK) return rc;
     p.src = src;
     p.dst = dst;
     p.count = count;
-    p.live = static_cast<int *>(workspace);
-    p.rank = p.live + 4;
     cudaError_t e = fa::launch_paged_compact(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -450,8 +450,33 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_many_kernel(
 // --------------------------------------------------------------------------------------- compact
 // n live pages; the k-th live page at or behind n moves to the k-th free page before n.  With
 // live(i) the live pages before i, a free page i < n is number i - live(i) of the free ones, and a
-// live page i >= n makes move live(i) - live(n).
-__global__ void __launch_bounds__(kReserveThreads) fa_paged_plan_kernel(const PagedCompactParams p) {
+// live page i >= n makes move live(i) - live(n).  Both lists ascend, so a table's entry finds its move by
+// bisection.
+__device__ __forceinline__ void compact_apply(const PagedCompactParams &p, int moves, long me, long threads) {
+    const PageTables &t = p.t;
+    for (long i = me; i < moves; i += threads) {
+        const int from = __ldcg(&p.src[i]);
+        t.refs[__ldcg(&p.dst[i])] = t.refs[from];
+        t.refs[from] = 0;
+    }
+    const int first = moves > 0 ? __ldcg(&p.src[0]) : t.num_pages;
+    const long entries = static_cast<long>(t.B) * t.max_pages;
+    for (long i = me; i < entries; i += threads) {
+        const int e = t.table[i];
+        if (e < first && e >= -1) continue;
+        int lo = 0, hi = moves;  // src[lo] <= e < src[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (__ldcg(&p.src[mid]) <= e) lo = mid;
+            else hi = mid;
+        }
+        if (e >= first && moves > 0 && __ldcg(&p.src[lo]) == e) t.table[i] = __ldcg(&p.dst[lo]);
+        else page_report(t.status);  // no page, or one that nobody holds
+    }
+}
+
+// The lists, and, where p.apply is set, what follows from them.
+__global__ void __launch_bounds__(kReserveThreads) fa_paged_compact_kernel(const PagedCompactParams p) {
     __shared__ int scratch[33];
     __shared__ int counts[2];  // this CTA's live pages; those of them before n
     griddep_launch_dependents();
@@ -486,10 +511,7 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_plan_kernel(const Pa
     cluster.sync();
     int front = 0;  // live pages before n
     for (int c = 0; c < ctas; ++c) front += cluster.map_shared_rank(counts, c)[1];
-    if (cta == 0 && tid == 0) {
-        *p.count = n - front;
-        *p.live = n;
-    }
+    if (cta == 0 && tid == 0) *p.count = n - front;
     for (long i0 = from; i0 < to; i0 += 4 * kReserveThreads) {
         const long i = i0 + 4 * tid;
         const int bits = free_bits(t.refs, i, to);
@@ -498,41 +520,28 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_plan_kernel(const Pa
             const int id = static_cast<int>(i + k);
             const bool is_free = bits >> k & 1;
             if (id < n && is_free) p.dst[id - at] = id;
-            if (id >= n) p.rank[id] = is_free ? -1 : at - front;
             if (id >= n && !is_free) p.src[at - front] = id;
             if (!is_free) ++at;
         }
         live += sum;
     }
-    cluster.sync();  // nobody's counts are read any more
+    cluster.sync();  // the lists are there, and nobody's counts are read any more
+    if (p.apply) compact_apply(p, n - front, cta * static_cast<long>(kReserveThreads) + tid, ctas * kReserveThreads);
 }
 
 __global__ void __launch_bounds__(256) fa_paged_apply_kernel(const PagedCompactParams p) {
     griddep_launch_dependents();
     griddep_wait();
-    const PageTables &t = p.t;
-    const int n = *p.live, moves = *p.count;
-    const long threads = static_cast<long>(gridDim.x) * 256, me = blockIdx.x * 256l + threadIdx.x;
-    for (long i = me; i < moves; i += threads) {
-        t.refs[p.dst[i]] = t.refs[p.src[i]];
-        t.refs[p.src[i]] = 0;
-    }
-    const long entries = static_cast<long>(t.B) * t.max_pages;
-    for (long i = me; i < entries; i += threads) {
-        const int e = t.table[i];
-        if (e < n && e >= -1) continue;
-        const int r = e >= 0 && e < t.num_pages ? p.rank[e] : -1;
-        if (r >= 0) t.table[i] = p.dst[r];
-        else page_report(t.status);  // no page, or one that nobody holds
-    }
+    compact_apply(p, *p.count, blockIdx.x * 256l + threadIdx.x, gridDim.x * 256l);
 }
 
 // ------------------------------------------------------------------------------------------ copy
-// A warp copies a run: consecutive 16-byte pieces of one page of one layer.  Runs are a head's rows
-// or, where the heads of a token lie side by side, a row's heads.  A block takes some of the runs of one
-// pair of pages, so that the pair is looked up and the work divided once.
+// A run is consecutive 16-byte pieces of one page of one layer: a head's rows or, where the heads of a token lie
+// side by side, a row's heads.  A block takes some of the runs of one pair of pages, so that the pair is
+// looked up once, and a warp as many runs at a time as give each lane four pieces in flight (48 copies of up to 63 rows
+// of 4 x 64 in 6 layers take 5.0 us; 7.4 with eight pieces, 9.7 with a run per warp).
 constexpr int kCopyWarps = 8;
-constexpr int kCopyBatch = 8;  // pieces of a lane in flight together
+constexpr int kCopyBatch = 4;  // pieces of a lane in flight together
 
 __global__ void __launch_bounds__(kCopyWarps * 32) fa_paged_copy_kernel(const PagedCopyParams p) {
     griddep_launch_dependents();
@@ -554,23 +563,30 @@ __global__ void __launch_bounds__(kCopyWarps * 32) fa_paged_copy_kernel(const Pa
         const unsigned runs = p.rows_inner ? p.heads : rows;
         const int pieces = (p.rows_inner ? rows : p.heads) << p.piece_shift;
         const unsigned end = min((part + 1) * per, static_cast<unsigned>(p.L) * 2 * runs);
-        for (unsigned x = part * per + warp_id(); x < end; x += kCopyWarps) {
+        int lanes = 32;  // of a run
+        while (lanes > 1 && lanes / 2 * kCopyBatch >= pieces) lanes /= 2;
+        const int at_once = 32 / lanes, part_lane = lane_id() & (lanes - 1);
+        for (unsigned x = part * per + warp_id() * at_once + lane_id() / lanes; x < end; x += kCopyWarps * at_once) {
             const unsigned slab = x / runs, run = x - slab * runs;
             const PagedCopySide &s = slab & 1 ? p.v : p.k;
             const uint16_t *from = s.base + (slab >> 1) * s.layer + src * s.page + run * s.outer;
-            uint16_t *to = s.base + (slab >> 1) * s.layer + dst * s.page + run * s.outer;
-            for (int i0 = lane_id(); i0 < pieces; i0 += 32 * kCopyBatch) {
+            const long over = (dst - static_cast<long>(src)) * s.page;
+            auto place = [&](int i) {
+                return const_cast<uint16_t *>(from) + (i >> p.piece_shift) * s.inner +
+                       (i & ((1 << p.piece_shift) - 1)) * 8;
+            };
+            for (int i0 = part_lane; i0 < pieces; i0 += lanes * kCopyBatch) {
                 uint4 v[kCopyBatch];
-                long off[kCopyBatch];
 #pragma unroll
                 for (int k = 0; k < kCopyBatch; ++k) {
-                    const int i = i0 + 32 * k;
-                    off[k] = (i >> p.piece_shift) * s.inner + (i & ((1 << p.piece_shift) - 1)) * 8;
-                    if (i < pieces) v[k] = *reinterpret_cast<const uint4 *>(from + off[k]);
+                    const int i = i0 + lanes * k;
+                    if (i < pieces) v[k] = *reinterpret_cast<const uint4 *>(place(i));
                 }
 #pragma unroll
-                for (int k = 0; k < kCopyBatch; ++k)
-                    if (i0 + 32 * k < pieces) *reinterpret_cast<uint4 *>(to + off[k]) = v[k];
+                for (int k = 0; k < kCopyBatch; ++k) {
+                    const int i = i0 + lanes * k;
+                    if (i < pieces) *reinterpret_cast<uint4 *>(place(i) + over) = v[k];
+                }
             }
         }
     }
@@ -614,23 +630,28 @@ cudaError_t launch_paged_reserve(const PagedReserveParams &p, cudaStream_t strea
     return launch_clusters(fa_paged_reserve_many_kernel, 1, kReserveCtas, kReserveThreads, smem, stream, p);
 }
 
-cudaError_t launch_paged_compact(const PagedCompactParams &p, cudaStream_t stream) {
-    const int ctas = p.t.num_pages <= 8 * kReserveThreads ? 1 : kReserveCtas;
-    const cudaError_t e = launch_clusters(fa_paged_plan_kernel, 1, ctas, kReserveThreads, 0, stream, p);
-    if (e != cudaSuccess) return e;
-    const long work = std::max(static_cast<long>(p.t.B) * p.t.max_pages, static_cast<long>(p.t.num_pages) / 2);
-    const long blocks = std::min((work + 255) / 256, 152l * 8);
+cudaError_t launch_paged_compact(PagedCompactParams p, cudaStream_t stream) {
+    // in the same launch where that is short: 24000 entries of a pool of 17000 pages take 7 us more so
+    const long entries = static_cast<long>(p.t.B) * p.t.max_pages, most = std::max(entries, p.t.num_pages + 0l);
+    p.apply = most <= kReserveCtas * kReserveThreads ? 1 : 0;  // an entry of a thread at most
+    const cudaError_t e = launch_clusters(fa_paged_compact_kernel, 1, most <= 8 * kReserveThreads ? 1 : kReserveCtas,
+                                          kReserveThreads, 0, stream, p);
+    if (e != cudaSuccess || p.apply) return e;
+    const long blocks = std::min((most + 255) / 256, 152l * 8);
     return launch_overlapped(fa_paged_apply_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, p);
 }
 
 cudaError_t launch_paged_copy(PagedCopyParams p, cudaStream_t stream) {
-    // blocks of eight runs a warp, of fewer where the pairs are few
+    // blocks of 32 KB or so (a full page's), of less where the pairs are few
     const long runs = 2l * p.L * (p.rows_inner ? p.heads : p.page_size);
-    long per = 8l * kCopyWarps;
+    const long pieces = static_cast<long>(p.rows_inner ? p.page_size : p.heads) << p.piece_shift;
+    long per = std::max(2048l / pieces, static_cast<long>(kCopyWarps));
     while (per > kCopyWarps && p.n * ((runs + per - 1) / per) < 152 * 8) per /= 2;
     p.per = static_cast<unsigned>(per);
     p.parts = static_cast<unsigned>((runs + per - 1) / per);
-    const long blocks = std::min(static_cast<long>(p.n) * p.parts, 152l * 8);
+    // Many short-lived blocks balance best (half of a pool moved in 358 us with 128 per SM, 360 with 64, 368
+    // with 32), but with a count on the device most may find nothing to do.
+    const long blocks = std::min(static_cast<long>(p.n) * p.parts, 152l * (p.count != nullptr ? 64 : 128));
     return launch_overlapped(fa_paged_copy_kernel, dim3(static_cast<unsigned>(blocks)), kCopyWarps * 32, 0,
                              stream, p);
 }

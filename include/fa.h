@@ -383,7 +383,7 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
  * so always come to the same tables.  At most 16384 sequences (otherwise FA_ERR_UNSUPPORTED); calls on
  * one table or one refs array have to be ordered by the caller.  Values out of range are not
  * followed and reported as FA_ERR_INDEX by fa_sync_status(), as is a count that would fall below
- * zero or an entry that names a free page.
+ * zero or an entry to be moved whose page is free.
  *
  * fa_paged_reserve: after it, every page that the batch's new tokens (kv_len, q_start, T as in
  * fa_paged_append) will be written to is held by their sequence alone.  In order of sequence and
@@ -411,7 +411,6 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
  * moved by fa_paged_copy with the lists that it leaves:
  *   src, dst  : device int32 [num_pages / 2], of which the first *count are written (the others stay).
  *   count     : device int32, how many pages move.
- *   workspace : at least fa_paged_compact_workspace_bytes() bytes, 16-byte aligned.
  * fa_paged_compact and fa_paged_fork need no page size: max_pages is below 2^28.
  *
  * fa_paged_copy: the first rows[i] rows (rows NULL: all) of page src[i] to page dst[i], of all heads, of K
@@ -432,9 +431,8 @@ int fa_paged_fork(int *block_table, int *kv_len, const int *parents, int *refs, 
                   int max_pages, void *stream);
 int fa_paged_free(int *block_table, const int *keep_len, int *refs, int B, int num_pages,
                   int page_size, int max_pages, void *stream);
-size_t fa_paged_compact_workspace_bytes(int num_pages);
 int fa_paged_compact(int *block_table, int *refs, int *src, int *dst, int *count, int B, int num_pages,
-                     int max_pages, void *workspace, size_t workspace_bytes, void *stream);
+                     int max_pages, void *stream);
 int fa_paged_copy(void *k_pages, void *v_pages, const long long *strides, const int *src,
                   const int *dst, const int *rows, const int *count, int n, int L, int H_kv, int d,
                   int num_pages, int page_size, void *stream);

@@ -139,7 +139,7 @@ class Cache:
             for i, e in enumerate(row):
                 if e in to:
                     row[i] = to[e]
-                elif e < -1 or e >= live:
+                elif e < -1 or e >= len(self.refs) or (high and e >= high[0]):
                     self.errors.add("index")
         for a, b in to.items():
             self.refs[b], self.refs[a] = self.refs[a], 0

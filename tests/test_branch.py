@@ -137,22 +137,18 @@ def test_fork_free_and_compact_refusals(lib):
     def free(table=P16, keep=P16, refs=P16, B=2, pages=9, size=16, width=4):
         return lib.fa_paged_free(table, keep, refs, B, pages, size, width, None)
 
-    def compact(table=P16, refs=P16, src=P16, dst=P16, count=P16, B=2, pages=9, width=4, ws=P16, wsb=256):
-        return lib.fa_paged_compact(table, refs, src, dst, count, B, pages, width, ws, wsb, None)
+    def compact(table=P16, refs=P16, src=P16, dst=P16, count=P16, B=2, pages=9, width=4):
+        return lib.fa_paged_compact(table, refs, src, dst, count, B, pages, width, None)
     both = (dict(table=NONE), dict(table=ODD), dict(refs=NONE), dict(refs=ODD), dict(B=0), dict(pages=0),
             dict(width=0), dict(pages=1 << 28), dict(width=1 << 28))
     for fn, more in ((fork, (dict(parents=NONE), dict(parents=ODD), dict(lens=ODD))),
                      (free, (dict(keep=NONE), dict(keep=ODD))),
-                     (compact, (dict(src=NONE), dict(dst=ODD), dict(count=NONE), dict(ws=NONE),
-                                dict(ws=ODD), dict(wsb=16)))):
+                     (compact, (dict(src=NONE), dict(dst=ODD), dict(count=NONE), dict(src=ODD)))):
         for b in both + more:
             assert fn(**b) == api.FA_ERR_INVALID, (fn.__name__, b)
         assert fn(B=16385) == api.FA_ERR_UNSUPPORTED
     for size in (4, 24, 2048):
         assert free(size=size) == api.FA_ERR_UNSUPPORTED
-    assert api.paged_compact_workspace_bytes(9) == 256
-    assert api.paged_compact_workspace_bytes(1000) == 4096  # 1004 ints, rounded up to 256 bytes
-    assert api.paged_compact_workspace_bytes(0) == 0
 
 
 def test_copy_refusals(lib):

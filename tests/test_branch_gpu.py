@@ -319,7 +319,7 @@ def test_arguments_that_are_refused(cuda_lib):
             lambda: api.paged_fork(t, None, f), lambda: api.paged_free(t, None, f, 16),
             lambda: api.paged_free(t, n.cpu(), f, 16), lambda: api.paged_fork(t, n, None),
             lambda: api.paged_compact(t, f, moves=torch.zeros(2, 3, dtype=torch.int32, device=DEV)),
-            lambda: api.paged_compact(t, f, count=f), lambda: api.paged_compact(t, f, workspace=f[:1]),
+            lambda: api.paged_compact(t, f, count=f), lambda: api.paged_compact(t, f, count=f[:1].long()),
             lambda: api.paged_copy(kv, kv[:, :1], n, n), lambda: api.paged_copy(kv, None, n, n),
             lambda: api.paged_copy(kv, kv, n, n[:2]), lambda: api.paged_copy(kv, kv, n, n, rows=n[:1]),
             lambda: api.paged_copy(kv[0], kv[0], n, n), lambda: api.paged_copy(kv, kv, n, n, count=n),
