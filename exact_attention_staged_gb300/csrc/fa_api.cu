@@ -542,14 +542,13 @@ bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 long reserve_items(int T, int B, int page_size) { return static_cast<long>(T) / page_size + 2l * B; }
 
-// Small requests take one launch, a cluster of up to 16 CTAs each: while these find places at once, and no CTA
-// has more than 8 tiles of 4096 logits; those of odd rows, loaded one by one, count twice.  One request of
-// four beams over 131072 bf16 logits takes 7.6 us so and 7.4 in two launches, but 4 us less on the host
-// (one launch and no workspace); 16 requests of five over 50001 fp16 logits 15.6 and 11.7.
+// Small calls take one launch, a cluster of up to 16 CTAs for each request: up to 128 tiles of 4096 logits in
+// all, those of odd rows (loaded one by one) counting twice.  That saves a launch and the workspace, 4 us on
+// the host; on the GPU one request of four beams over 131072 bf16 logits takes 12.3 us so and 10.3 in two
+// launches (a graph each), four of four over 32000 10.3 and 11.6, 16 of five over 50000 20.6 and 14.4.
 constexpr int kBeamCtas = 16;
 bool beam_small(int B, int W, int V) {
-    const long tiles = W * ((V + 4095l) / 4096) * (V % 4 != 0 ? 2 : 1);
-    return static_cast<long>(B) * kBeamCtas <= 4 * 152 && tiles <= kBeamCtas * 8;
+    return static_cast<long>(B) * W * ((V + 4095l) / 4096) * (V % 4 != 0 ? 2 : 1) <= 128;
 }
 
 // Pieces of a beam's logits: whole tiles, of `elems` logits for each of a CTA's threads.

@@ -31,9 +31,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = kBeamThreads;
 constexpr int kCap = 512;                     // candidates that there is room for
-constexpr int kJoinThreads = 1024;
 constexpr int kJoinCap = 1024;
 constexpr int kJoinOwn = 4;                   // a thread's candidates that stay in registers
+constexpr int kPlaces = 64;                   // of a warp's list
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -62,28 +62,37 @@ __device__ __forceinline__ unsigned kth_of_32(const unsigned *values, int k) {
     return __shfl_sync(kAll, mine, __ffs(static_cast<int>(__ballot_sync(kAll, rank == k - 1))) - 1);
 }
 
-// The CTA's k-th largest of values[0 .. n), n a multiple of 4 no more than the threads; every thread calls
-// it and gets the result, which `out` passes on.
+// Lanes that share the work on one of n things (a power of two up to 32).
+template <int THREADS>
+__device__ __forceinline__ int lanes_each(int n) {
+    int p = 32;
+    while (p > 1 && n * p > THREADS) p /= 2;
+    return p;
+}
+__device__ __forceinline__ int sum_lanes(int x, int p) {
+    for (int o = p / 2; o > 0; o /= 2) x += __shfl_xor_sync(kAll, x, o);
+    return x;
+}
+
+// The CTA's k-th largest of values[0 .. n), n a power of two no more than the threads; every thread calls it
+// and gets the result, which `out` passes on.
+template <int THREADS>
 __device__ __forceinline__ unsigned kth_largest(const unsigned *values, int n, int k, unsigned *out) {
-    const int tid = threadIdx.x;
-    if (tid < n) {
-        const unsigned mine = values[tid];
+    const int lanes = lanes_each<THREADS>(n), i = static_cast<int>(threadIdx.x) / lanes, part = threadIdx.x % lanes;
+    if (i < n) {  // whole warps
+        const unsigned mine = values[i];
         int rank = 0;
-        const uint4 *all = reinterpret_cast<const uint4 *>(values);
-#pragma unroll 4
-        for (int j = 0; j < n / 4; ++j) {
-            const uint4 x = all[j];
-            const int i = 4 * j;
-            rank += x.x > mine || (x.x == mine && i < tid);
-            rank += x.y > mine || (x.y == mine && i + 1 < tid);
-            rank += x.z > mine || (x.z == mine && i + 2 < tid);
-            rank += x.w > mine || (x.w == mine && i + 3 < tid);
-        }
-        if (rank == k - 1) *out = mine;
+#pragma unroll 8
+        for (int j = part; j < n; j += lanes) rank += values[j] > mine || (values[j] == mine && j < i);
+        rank = sum_lanes(rank, lanes);
+        if (part == 0 && rank == k - 1) *out = mine;
     }
     __syncthreads();
     return *out;
 }
+
+// Groups whose maxima bound the K largest.
+__device__ __forceinline__ int group_count(int K) { return K <= 16 ? 32 : K <= 32 ? 64 : K <= 64 ? 128 : 256; }
 
 // The sum of x over the CTA's threads, the same in each; `scratch` holds a word per warp.
 template <int THREADS = kThreads>
@@ -132,9 +141,9 @@ struct BeamTile {
     // x: the tile's first logit; left: how many there are to the end
     __device__ __forceinline__ void load(const Elem *x, int left) {
         if (left >= kSize) {
+            const Vec *from = reinterpret_cast<const Vec *>(x) + threadIdx.x;
 #pragma unroll
-            for (int i = 0; i < kElems / VEC; ++i)
-                raw[i] = __ldcs(reinterpret_cast<const Vec *>(x + place(i * VEC)));
+            for (int i = 0; i < kElems / VEC; ++i) raw[i] = __ldcs(from + i * THREADS);
             return;
         }
 #pragma unroll
@@ -157,8 +166,13 @@ struct BeamTile {
             memcpy(word, raw, sizeof(raw));
 #pragma unroll
             for (int k = 0; k < kElems / 2; ++k) {
-                const float2 f = unpack2<TYPE == kBeamBF16>(word[k]);
-                v[2 * k] = f.x, v[2 * k + 1] = f.y;
+                if constexpr (TYPE == kBeamBF16) {  // one instruction each
+                    v[2 * k] = __uint_as_float(word[k] << 16);
+                    v[2 * k + 1] = __uint_as_float(word[k] & 0xffff0000u);
+                } else {
+                    const float2 f = unpack2<false>(word[k]);
+                    v[2 * k] = f.x, v[2 * k + 1] = f.y;
+                }
             }
         } else {
             const Elem *e = reinterpret_cast<const Elem *>(raw);
@@ -181,6 +195,7 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
     __shared__ int found;
     __shared__ int scratch[THREADS / 32];
     __shared__ unsigned tops_of[THREADS / 32];  // each warp's maximum
+    __shared__ unsigned short places[THREADS / 32][kPlaces];
     __shared__ float sums[THREADS / 32];
     __shared__ unsigned long long cand[kCap];
     const int tid = threadIdx.x, lane = lane_id();
@@ -224,8 +239,8 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
         s += q.x + q.y;
     }
 
-    // groups of threads: about four times as many as wanted
-    const int count = K <= 16 ? 32 : K <= 64 ? 128 : 256, width = THREADS / count;
+    // groups of threads, at least twice as many as wanted
+    const int count = group_count(K), width = THREADS / count;
     float g = m;
     for (int o = 1; o < width; o *= 2) g = fmaxf(g, __shfl_xor_sync(kAll, g, o));
     if (tid % width == 0) groups[tid / width] = order_of(g);
@@ -233,7 +248,7 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
     if (lane == 0) tops_of[warp_id()] = mine;
     if (tid == 0) found = 0;
     __syncthreads();
-    const unsigned least = count == 32 ? kth_of_32(groups, K) : kth_largest(groups, count, K, &bound);
+    const unsigned least = count == 32 ? kth_of_32(groups, K) : kth_largest<THREADS>(groups, count, K, &bound);
     unsigned most = tops_of[0];
 #pragma unroll
     for (int i = 1; i < THREADS / 32; ++i) most = max(most, tops_of[i]);
@@ -243,17 +258,6 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
     if (lane == 0) sums[warp_id()] = s;
     const float bar = value_of(least);
-    // f(logit, its place in the piece) for this thread's logits of the tiles whose maximum is at least bar
-    auto each = [&](auto f) {
-        for (int t = 0; t < tiles; ++t) {
-            if (!(tops[t][tid] >= bar)) continue;
-#pragma unroll 1
-            for (int i = 0; i < kElems / VEC; ++i) {
-                const int at = t * Tile::kSize + Tile::place(i * VEC);
-                for (int k = 0; k < VEC && at + k < len; ++k) f(beam_float<TYPE>(x[at + k]), at + k);
-            }
-        }
-    };
     auto key_of = [&](float v, int place) {  // larger: a larger logit, or the first of equal ones
         return static_cast<unsigned long long>(order_of(v)) << 32 | ~static_cast<unsigned>(v0 + place);
     };
@@ -261,61 +265,107 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
         const int at = atomicAdd(&found, 1);
         if (at < kCap) cand[at] = key_of(v, place);
     };
-    // a warp reads each of its threads' places again together, a logit per lane
-    if (__any_sync(kAll, m >= bar && m > -INFINITY))
-#pragma unroll 1
-        for (int t = 0; t < tiles; ++t)
-            for (unsigned who = __ballot_sync(kAll, tops[t][tid] >= bar); who != 0; who &= who - 1) {
-                const int owner = (tid & ~31) + __ffs(static_cast<int>(who)) - 1;
-                if (lane >= kElems) continue;
-                const int at = t * Tile::kSize + Tile::place(lane, owner);
-                if (at >= len) continue;
-                const float v = beam_float<TYPE>(x[at]);
-                if (v >= bar && v > -INFINITY) take(v, at);
+    // The threads' tiles that have a logit to collect are listed and read again by the warp, a logit per lane.
+    // (The chain of ballots and reads is as long as the list; its reads are not waited for one by one.)
+    if (__any_sync(kAll, m >= bar && m > -INFINITY)) {
+        unsigned short *list = places[warp_id()];
+        int listed = 0;
+        for (int t = 0; t <= tiles; ++t) {
+            const unsigned who = t < tiles ? __ballot_sync(kAll, tops[t][tid] >= bar) : 0;
+            if (t == tiles || listed + __popc(who) > kPlaces) {
+                constexpr int kAtOnce = 32 / kElems, kBatch = 4;
+                __syncwarp();
+                for (int i0 = lane / kElems; i0 < listed; i0 += kAtOnce * kBatch) {
+                    float v[kBatch];
+                    int at[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        v[k] = -INFINITY;
+                        if (i0 + k * kAtOnce >= listed) continue;
+                        const int from = list[i0 + k * kAtOnce];
+                        at[k] = from / 32 * Tile::kSize + Tile::place(lane % kElems, (tid & ~31) + from % 32);
+                        if (at[k] < len) v[k] = beam_float<TYPE>(x[at[k]]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        if (v[k] >= bar && v[k] > -INFINITY) take(v[k], at[k]);
+                }
+                __syncwarp();
+                listed = 0;
+                // too many already: they are found in another way
+                if (__any_sync(kAll, *static_cast<volatile int *>(&found) > kCap)) break;
             }
+            if (who >> lane & 1) list[listed + __popc(who & ((1u << lane) - 1))] = static_cast<unsigned short>(32 * t + lane);
+            listed += __popc(who);
+        }
+    }
     __syncthreads();
     int n = found;
     if (n > kCap) {
-        // the K-th largest logit `lo` is the bound, or above it
-        unsigned lo = least;
+        // f(logit, its place in the piece) for this thread's logits of tiles that have one of order `least`
+        auto each = [&](unsigned least, auto f) {
+            for (int t = 0; t < tiles; ++t) {
+                if (!(order_of(tops[t][tid]) >= least)) continue;
+#pragma unroll 1
+                for (int i = 0; i < kElems / VEC; ++i) {
+                    const int at = t * Tile::kSize + Tile::place(i * VEC);
+                    for (int k = 0; k < VEC && at + k < len; ++k) f(beam_float<TYPE>(x[at + k]), at + k);
+                }
+            }
+        };
         auto reach = [&](unsigned want) {
             int c = 0;
-            each([&](float v, int) { c += v > -INFINITY && order_of(v) >= want; });
+            each(want, [&](float v, int) { c += v > -INFINITY && order_of(v) >= want; });
             return block_sum<THREADS>(c, scratch);
         };
-        if (reach(lo + 1) >= K) {
+        // the K-th largest logit `lo` is the bound, or above it
+        unsigned lo = least;
+        int above = reach(lo + 1);
+        if (above >= K) {
             unsigned hi = ~0u;
             while (hi - lo > 1) {
                 const unsigned mid = lo + (hi - lo) / 2;
                 if (reach(mid) >= K) lo = mid;
                 else hi = mid;
             }
+            above = reach(lo + 1);
         }
-        // of its equals, the first that make K: those before place `end`
-        const int room = K - reach(lo + 1);
+        // of its equals, the first that make K: up to place `end`
+        const int room = K - above;
         const float equal = value_of(lo);
-        int end = 0, before = 0;
-        for (int span = 1 << (31 - __clz(len)); span > 0; span /= 2) {
+        auto equals = [&](int from, int to) {
             int c = 0;
-            for (int i = end + tid; i < min(end + span, len); i += THREADS) c += beam_float<TYPE>(x[i]) == equal;
-            c = block_sum<THREADS>(c, scratch);
+#pragma unroll 8
+            for (int i = from + tid; i < min(to, len); i += THREADS) c += beam_float<TYPE>(x[i]) == equal;
+            return block_sum<THREADS>(c, scratch);
+        };
+        int end = 0, before = 0;
+        for (int span = 8 * THREADS; end < len;) {
+            const int c = equals(end, end + span);
             if (before + c < room) before += c, end += span;
+            else if (span == 1) break;
+            else span /= 2;
         }
         if (tid == 0) found = 0;
         __syncthreads();
-        each([&](float v, int place) {
-            if (v > equal || (v == equal && place <= end)) take(v, place);
+        each(lo + 1, [&](float v, int place) {
+            if (v > equal) take(v, place);
         });
+        for (int i = tid; i <= end; i += THREADS)
+            if (beam_float<TYPE>(x[i]) == equal) take(equal, i);
         __syncthreads();
         n = found;
     }
-    // the K largest, largest first, by counting
-    for (int i = tid; i < n; i += THREADS) {
-        const unsigned long long k = cand[i];
+    // the K largest, largest first, by counting: a warp's work where there are few
+    const int lanes = n <= 32 ? 1 : lanes_each<THREADS>(n), part = tid & (lanes - 1), own = tid / lanes;
+    for (int i0 = 0; i0 + (tid & ~31) / lanes < n; i0 += THREADS / lanes) {  // whole warps
+        const int i = i0 + own;
+        const unsigned long long k = i < n ? cand[i] : 0;
         int rank = 0;
 #pragma unroll 4
-        for (int j = 0; j < n; ++j) rank += cand[j] > k;
-        if (rank < K) keys[rank] = k;
+        for (int j = part; j < n; j += lanes) rank += cand[j] > k;
+        rank = sum_lanes(rank, lanes);
+        if (i < n && part == 0 && rank < K) keys[rank] = k;
     }
     for (int i = n + tid; i < K; i += THREADS) keys[i] = 0;
     if (tid == THREADS - 1) {
@@ -361,19 +411,8 @@ __device__ __forceinline__ float2 pair_log(float s) {
 // whatever their size.
 struct BeamBase {
     float hi, lo, ref;
+    int ended;  // the beam has one candidate, the end token at score hi
 };
-
-// Lanes that share the work on one of n things (a power of two up to 32).
-template <int THREADS>
-__device__ __forceinline__ int lanes_each(int n) {
-    int p = 32;
-    while (p > 1 && n * p > THREADS) p /= 2;
-    return p;
-}
-__device__ __forceinline__ int sum_lanes(int x, int p) {
-    for (int o = p / 2; o > 0; o /= 2) x += __shfl_xor_sync(kAll, x, o);
-    return x;
-}
 
 // One CTA joins the pieces of request b: the sums, then the K best candidates, by a bound and counting as for
 // the pieces.  A request has up to a few thousand candidates and the time is that of the chain of steps,
@@ -390,25 +429,24 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, int b, BeamBase *
     __shared__ int where[kJoinCap];
     const int tid = threadIdx.x, lane = lane_id();
     const int W = p.W, K = p.K, S = p.pieces, V = p.V;
-    const int list = S * K, total = W * list;
     const uint8_t *finished = p.finished != nullptr ? p.finished + static_cast<long>(b) * W : nullptr;
-    // Candidate i is one of list i / K.  The lists are sorted, and each is turned by a step of its own, so that
-    // the good ones fall to different threads.
-    const int step = K * 5 / 8 + 1;
-    auto key_at = [&](int i) {
-        const int l = i / K;
-        return list_of(l)[(i - l * K + l % K * step) % K];
-    };
+    // `lanes` threads take a list, each every lanes-th of its candidates; a thread's first ones stay in registers
+    int lanes = 1;
+    while (lanes < K && lanes < 32) lanes *= 2;
+    const int part = tid % lanes, each_turn = THREADS / lanes, lists = W * S;
+    const int deep = (K + lanes - 1) / lanes;  // candidates of a list for each thread
     unsigned long long own[kJoinOwn];
+    int l0 = tid / lanes, d0 = 0;  // where the thread's candidates go on behind the registers
 #pragma unroll
     for (int r = 0; r < kJoinOwn; ++r) {
-        const int i = tid + r * THREADS;
-        own[r] = i < total && (finished == nullptr || finished[i / list] == 0) ? key_at(i) : 0;
+        const int j = part + d0 * lanes;
+        own[r] = l0 < lists && j < K && (finished == nullptr || finished[l0 / S] == 0) ? list_of(l0)[j] : 0;
+        if (++d0 == deep) d0 = 0, l0 += each_turn;
     }
     for (int w = warp_id(); w < W; w += THREADS / 32) {
         const float score = p.scores[static_cast<long>(b) * W + w];
         if (finished != nullptr && finished[w] != 0) {
-            if (lane == 0) base[w] = {score, 0.f, 0.f};
+            if (lane == 0) base[w] = {score, 0.f, 0.f, 1};
             continue;
         }
         float m = -INFINITY;
@@ -426,19 +464,19 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, int b, BeamBase *
             const float2 l = pair_log(s), r = two_sum(score, -l.x);
             // nothing to choose from, or a logit that is no number
             const bool none = !(m > -INFINITY && s < INFINITY);
-            base[w] = {none ? NAN : r.x, r.y - l.y, m};
+            base[w] = {none ? NAN : r.x, r.y - l.y, m, 0};
         }
     }
     if (tid == 0) found = 0;
     if (tid < 256) groups[tid] = 0;
     __syncthreads();
-    // the order (0: none) of candidate i of the request, whose key is k, and its place w V + v
-    auto order = [&](int i, unsigned long long k, int *at) -> unsigned long long {
-        const int w = i / list;
+    // the order (0: none) of candidate j of list l, whose key is k, and its place w V + v
+    auto order = [&](int l, int j, unsigned long long k, int *at) -> unsigned long long {
+        const int w = l / S;
         const BeamBase c = base[w];
-        if (finished != nullptr && finished[w] != 0) {
+        if (c.ended) {
             *at = w * V + p.end_token;
-            return i == w * list ? pair_order(c.hi, 0.f) : 0;
+            return l == w * S && j == 0 ? pair_order(c.hi, 0.f) : 0;
         }
         if (k == 0) return 0;
         *at = w * V + static_cast<int>(~static_cast<unsigned>(k));
@@ -447,48 +485,49 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, int b, BeamBase *
         const float2 r = two_sum(s.x, s.y + (d.y + c.lo));
         return pair_order(r.x, r.y);
     };
+    // K candidates at least reach the K-th largest of the best ones of groups, to which they go scattered
+    const int count = group_count(K);
     int place[kJoinOwn];
+    {
+        int l = tid / lanes, d = 0;
 #pragma unroll
-    for (int r = 0; r < kJoinOwn; ++r) {
-        const int i = tid + r * THREADS;
-        place[r] = 0;
-        own[r] = i < total ? order(i, own[r], &place[r]) : 0;
+        for (int r = 0; r < kJoinOwn; ++r) {
+            const int j = part + d * lanes;
+            place[r] = 0;
+            own[r] = l < lists && j < K ? order(l, j, own[r], &place[r]) : 0;
+            if (own[r] != 0) atomicMax(&groups[(37 * l + 11 * j) % count], static_cast<unsigned>(own[r] >> 32));
+            if (++d == deep) d = 0, l += each_turn;
+        }
     }
-    // f(order, place) for this thread's candidates
+    // f(order, place) for this thread's candidates from behind the registers on
+    auto rest = [&](auto f) {
+        for (int l = l0, d = d0; l < lists; l += each_turn, d = 0)
+            for (; d < deep; ++d) {
+                const int j = part + d * lanes;
+                if (j >= K) continue;
+                int at = 0;
+                const unsigned long long k = order(l, j, base[l / S].ended ? 0 : list_of(l)[j], &at);
+                f(k, at, 37 * l + 11 * j);
+            }
+    };
+    rest([&](unsigned long long k, int, int group) {
+        if (k != 0) atomicMax(&groups[group % count], static_cast<unsigned>(k >> 32));
+    });
     auto each = [&](auto f) {
 #pragma unroll
         for (int r = 0; r < kJoinOwn; ++r) f(own[r], place[r]);
-        for (int i = tid + kJoinOwn * THREADS; i < total; i += THREADS) {
-            int at = 0;
-            const unsigned long long k = order(i, key_at(i), &at);
-            f(k, at);
-        }
+        rest([&](unsigned long long k, int at, int) { f(k, at); });
     };
     auto take = [&](unsigned long long k, int at) {
         const int n = atomicAdd(&found, 1);
         if (n < kJoinCap) cand[n] = k, where[n] = at;
     };
-    // K candidates at least reach the K-th largest of the best ones of groups of threads
-    unsigned long long most = 0;
-    each([&](unsigned long long k, int) { most = max(most, k); });
-    const int count = K <= 8 ? 32 : K <= 32 ? 128 : 256, width = THREADS / count;
-    if (most != 0) atomicMax(&groups[tid % count], static_cast<unsigned>(most >> 32));
     __syncthreads();
-    {
-        const int i = tid / width, part = tid % width;
-        const unsigned mine = groups[i];
-        int rank = 0;
-#pragma unroll 4
-        for (int j = part; j < count; j += width) rank += groups[j] > mine || (groups[j] == mine && j < i);
-        rank = sum_lanes(rank, width);
-        if (part == 0 && rank == K - 1) bound = mine;
-    }
-    __syncthreads();
+    kth_largest<THREADS>(groups, count, K, &bound);
     const unsigned long long t = max(static_cast<unsigned long long>(bound) << 32, 1ull);
-    if (most >= t)
-        each([&](unsigned long long k, int at) {
-            if (k >= t) take(k, at);
-        });
+    each([&](unsigned long long k, int at) {
+        if (k >= t) take(k, at);
+    });
     __syncthreads();
     int n = found;
     if (n > kJoinCap) {
@@ -520,23 +559,23 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, int b, BeamBase *
         n = found;
     }
     const long out = static_cast<long>(b) * K;
-    const int lanes = lanes_each<THREADS>(n), part = tid % lanes;
-    for (int i0 = 0; i0 < n; i0 += THREADS / lanes) {
-        const int i = i0 + tid / lanes;
+    const int share = lanes_each<THREADS>(n), turn = tid % share;
+    for (int i0 = 0; i0 < n; i0 += THREADS / share) {
+        const int i = i0 + tid / share;
         const bool there = i < n;
         if (!__any_sync(kAll, there)) continue;
         const unsigned long long mine = there ? cand[i] : 0;
         const int spot = there ? where[i] : 0;
         int rank = 0;
 #pragma unroll 4
-        for (int j = part; j < n; j += lanes) rank += cand[j] > mine || (cand[j] == mine && where[j] < spot);
-        rank = sum_lanes(rank, lanes);
-        if (there && part == 0 && rank < K) {
+        for (int j = turn; j < n; j += share) rank += cand[j] > mine || (cand[j] == mine && where[j] < spot);
+        rank = sum_lanes(rank, share);
+        if (there && turn == 0 && rank < K) {
             const int w = spot / V, v = spot - w * V;
             p.out_scores[out + rank] = value_of(static_cast<unsigned>(mine >> 32));
             p.parents[out + rank] = b * W + w;
             p.tokens[out + rank] = v;
-            p.out_finished[out + rank] = v == p.end_token || (finished != nullptr && finished[w] != 0);
+            p.out_finished[out + rank] = v == p.end_token || base[w].ended != 0;
         }
     }
     for (int k = n + tid; k < K; k += THREADS) {
@@ -546,12 +585,13 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, int b, BeamBase *
     }
 }
 
-__global__ void __launch_bounds__(kJoinThreads) fa_beam_join_kernel(const BeamParams p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) fa_beam_join_kernel(const BeamParams p) {
     extern __shared__ BeamBase base[];  // [W]
     griddep_launch_dependents();
     griddep_wait();
     const long first = static_cast<long>(blockIdx.x) * p.W * p.pieces;  // of the request's pieces
-    beam_join<kJoinThreads>(
+    beam_join<THREADS>(
         p, blockIdx.x, base, [&](int l) { return p.keys + (first + l) * p.K; },
         [&](int l) { return p.stats[first + l]; });
 }
@@ -589,9 +629,12 @@ cudaError_t launch_vec(const BeamParams &p, cudaStream_t stream) {
     if (p.ctas == 0) {
         const cudaError_t e = launch_overlapped(fa_beam_piece_kernel<TYPE, VEC>, dim3(p.pieces * p.B * p.W),
                                                 kThreads, 0, stream, p);
-        return e != cudaSuccess ? e
-                                : launch_overlapped(fa_beam_join_kernel, dim3(p.B), kJoinThreads,
-                                                    sizeof(BeamBase) * p.W, stream, p);
+        if (e != cudaSuccess) return e;
+        // few candidates: many small CTAs instead of ones that take half an SM each
+        const size_t smem = sizeof(BeamBase) * p.W;
+        return static_cast<long>(p.W) * p.pieces * p.K <= 4 * kThreads
+                   ? launch_overlapped(fa_beam_join_kernel<kThreads>, dim3(p.B), kThreads, smem, stream, p)
+                   : launch_overlapped(fa_beam_join_kernel<1024>, dim3(p.B), 1024, smem, stream, p);
     }
     const int slots = (p.W * p.pieces + p.ctas - 1) / p.ctas;
     const size_t smem = slots * (p.K * sizeof(unsigned long long) + sizeof(float2)) + p.W * sizeof(BeamBase);

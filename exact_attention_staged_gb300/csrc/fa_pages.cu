@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
         }
 
     const int g = cta * threads + tid;  // this thread's item
-    int b = 0, e = -1, *at = nullptr;
+    int b = 0, e = -1, held = 1, *at = nullptr;
     bool had = false;
     if (g < items) {
         int r = B;  // before[b] <= g < before[r]
@@ -283,11 +283,11 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
             if (before[m] <= g) b = m;
             else r = m;
         }
-        at = t.table + static_cast<long>(b) * t.max_pages + (max(paged_seq(p.c, b).ctx, 0) >> t.page_shift) + g -
-             before[b];
+        const int place = (max(paged_seq(p.c, b).ctx, 0) >> t.page_shift) + g - before[b];
+        at = t.table + static_cast<long>(b) * t.max_pages + min(place, t.max_pages - 1);
         e = *at;
         had = e >= 0 && e < t.num_pages;
-        if (had) atomicSub(&t.refs[e], 1);
+        if (had) held = atomicSub(&t.refs[e], 1);
         else if (e != -1) page_report(t.status);
     }
     barrier();
@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
             page_report(t.status, kErrFull);
         }
     }
+    if (held <= 0) page_report(t.status);  // held by more entries than were counted
     if (ctas > 1) cluster.sync();  // the others have read this CTA's shared memory
 }
 
@@ -356,14 +357,18 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_many_kernel(
         }
         *b = l;
         const PagedSeq s = paged_seq(p.c, l);
-        return t.table + static_cast<long>(l) * t.max_pages + (max(s.ctx, 0) >> t.page_shift) + g - before[l];
+        const int place = (max(s.ctx, 0) >> t.page_shift) + g - before[l];
+        return t.table + static_cast<long>(l) * t.max_pages + min(place, t.max_pages - 1);
     };
 
     for (int g = lo + tid; g < hi; g += kReserveThreads) {
         int b;
         const int e = *find(g, &b);
-        if (e >= 0 && e < t.num_pages) atomicSub(&t.refs[e], 1);
-        else if (e != -1) page_report(t.status);
+        if (e >= 0 && e < t.num_pages) {
+            if (atomicSub(&t.refs[e], 1) <= 0) page_report(t.status);  // more entries than were counted
+        } else if (e != -1) {
+            page_report(t.status);
+        }
     }
     cluster.sync();
     for (int g = lo + tid; g < hi; g += kReserveThreads) {

@@ -409,7 +409,7 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
  * fa_paged_compact: moves the live pages to the front of the pool: with n of them, the k-th of those with
  * ids from n on takes the place of the k-th free page before n.  Table and refs follow; the data has to be
  * moved by fa_paged_copy with the lists that it leaves:
- *   src, dst  : device int32 [num_pages / 2], of which the first *count are written (the others stay).
+ *   src, dst  : device int32 [num_pages / 2] (at least one), of which the first *count are written (the others stay).
  *   count     : device int32, how many pages move.
  * fa_paged_compact and fa_paged_fork need no page size: max_pages is below 2^28.
  *
@@ -451,7 +451,8 @@ int fa_paged_copy(void *k_pages, void *v_pages, const long long *strides, const 
  *   end_token : -1 for none (only without finished).
  *   out_scores, parents, tokens, out_finished : device [B, K]; parents (int32) are places in the batch,
  *               b W + w, as fa_paged_fork wants them where K = W; out_finished (uint8) is 1 where the
- *               token is end_token or the parent had ended.
+ *               token is end_token or the parent had ended.  Where K = W, out_scores may be scores and
+ *               out_finished finished (in place).
  * Only finite scores are candidates: a token of logit -inf is none, nor is any of a beam whose score or
  * whose logits' sum is not finite (a NaN or +inf among them).  Where a request has fewer than K, the
  * places left have score -inf, parent and token -1 and out_finished 1.

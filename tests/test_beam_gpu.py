@@ -70,9 +70,9 @@ def beams(seed, B, W):
 @pytest.mark.parametrize("B,W,V,K", [(1, 1, 1, 1), (1, 1, 1, 5), (2, 3, 7, 21), (2, 3, 7, 30), (3, 2, 255, 4),
                                      (1, 5, 8191, 10), (2, 2, 8192, 64), (1, 3, 8193, 65), (2, 4, 20001, 8),
                                      (1, 2, 50002, 128), (5, 7, 1004, 14), (1, 40, 3001, 80),
-                                     # a cluster per request up to 38 of them and 128 tiles (odd rows: 64); larger calls
+                                     # a cluster per request up to 128 tiles in all (odd rows: 64); larger calls
                                      (77, 1, 300, 5), (80, 2, 12301, 40), (300, 1, 20002, 3), (1, 50, 30001, 9),
-                                     (2, 130, 4097, 128), (38, 2, 4097, 4), (39, 2, 4097, 4)])
+                                     (2, 130, 4097, 128), (64, 1, 4096, 4), (32, 2, 4100, 4), (33, 2, 4100, 4)])
 def test_selection_is_the_definitions(cuda_lib, B, W, V, K, dtype):
     check(cuda_lib, normal(V + K, B, W, V, dtype=dtype), beams(V, B, W), K, exact=dtype == torch.float32)
 
@@ -192,6 +192,21 @@ def test_results_do_not_depend_on_what_the_buffers_held(cuda_lib):
     assert cuda_lib.sync_status() == 0
 
 
+@pytest.mark.parametrize("B,W,V", [(3, 4, 3001), (70, 4, 30001), (20, 40, 3001)])
+def test_scores_and_flags_in_place(cuda_lib, B, W, V):
+    """A step's buffers are the next step's: also beams that have ended."""
+    x, s = normal(12, B, W, V), beams(12, B, W)
+    f = (torch.rand(B, W, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV) < 0.5).to(torch.uint8)
+    s2, f2 = s.clone(), f.clone()
+    for _ in range(3):
+        want = cuda_lib.beam_select(x, s, finished=f, end_token=9)
+        got = cuda_lib.beam_select(x, s2, finished=f2, end_token=9, out_scores=s2, out_finished=f2)
+        assert got[0] is s2 and got[3] is f2
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        s, f = want[0], want[3]
+    assert cuda_lib.sync_status() == 0
+
+
 def test_beam_arguments_that_are_refused(cuda_lib):
     api, x, s = cuda_lib, normal(1, 2, 3, 50), beams(1, 2, 3)
     for call in (lambda: api.beam_select(x[0], s), lambda: api.beam_select(x, s[:1]),
@@ -212,8 +227,9 @@ def test_beam_arguments_that_are_refused(cuda_lib):
             api.beam_select(x, s, **kw)
 
 
-def test_selection_captured_and_on_two_streams(cuda_lib):
-    xs, ss = [normal(i, 2, 4, 20001, dtype=torch.float16) for i in range(3)], [beams(i, 2, 4) for i in range(3)]
+@pytest.mark.parametrize("B", [2, 60])
+def test_selection_captured_and_on_two_streams(cuda_lib, B):
+    xs, ss = [normal(i, B, 4, 20001, dtype=torch.float16) for i in range(3)], [beams(i, B, 4) for i in range(3)]
     want = [[t.clone() for t in cuda_lib.beam_select(x, s)] for x, s in zip(xs, ss)]
     x, s = xs[0].clone(), ss[0].clone()
     torch.cuda.synchronize()

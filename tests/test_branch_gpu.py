@@ -200,6 +200,10 @@ def test_values_out_of_range_are_reported_and_not_followed(cuda_lib):
     c.refs[9] = 0
     c.o.refs[9] = 0
     c.free([0, 24, 24, 8, 0, 0], expect=bad)
+    c = bad_state(cuda_lib)
+    c.refs[9] = 0
+    cuda_lib.paged_reserve(c.table, index([16, 24, 24, 8, 24, 0]), c.refs, 8, index([0, 0, 0, 0, 0, 1, 1]), tokens=1)
+    assert cuda_lib.sync_status() == bad
 
 
 def test_tables_that_do_not_start_on_a_sector(cuda_lib):
