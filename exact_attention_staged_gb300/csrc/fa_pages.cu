@@ -225,53 +225,40 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
         if (ctas > 1) cluster.sync();
         else __syncthreads();
     };
-    // four pages a round, neighbouring groups in neighbouring threads
-    const long share = ((t.num_pages + 3l) / 4 + ctas - 1) / ctas * 4;
-    const long from = min(static_cast<long>(t.num_pages), cta * share);
-    const long to = min(static_cast<long>(t.num_pages), from + share);
+    // a thread keeps the state of `rounds` neighbouring groups of four pages
+    const int rounds = static_cast<int>(((t.num_pages + 3l) / 4 + threads * ctas - 1) / (threads * ctas));
+    const long from = 4l * rounds * (cta * threads + tid);
     unsigned free_of = 0;
 #pragma unroll
     for (int r = 0; r < kReserveRounds; ++r)
-        free_of |= static_cast<unsigned>(free_bits(t.refs, from + 4l * (r * threads + tid), to)) << 4 * r;
+        if (r < rounds)
+            free_of |= static_cast<unsigned>(free_bits(t.refs, from + 4 * r, t.num_pages)) << 4 * r;
     if (!reserve_ordered(p, cta == 0)) return;
-    int items = 0, sum;
+    // items and free pages before this thread's: with the first sequences in one scan, frees in the lower half
+    int items = 0, frees = 0, free_mine = 0, sum;
     for (int b0 = 0; b0 < B; b0 += threads) {
         const int b = b0 + tid;
         int first, ctx;
-        const int x = block_scan(b < B ? reserve_places(p, b, cta == 0, &first, &ctx) : 0, scratch, &sum);
-        if (b < B) before[b] = items + x;
-        items += sum;
+        const unsigned n = b < B ? reserve_places(p, b, cta == 0, &first, &ctx) : 0;
+        const unsigned x = block_scan(n << 16 | (b0 == 0 ? __popc(free_of) : 0), scratch, &sum);
+        if (b < B) before[b] = items + static_cast<int>(x >> 16);
+        items += static_cast<int>(static_cast<unsigned>(sum) >> 16);
+        if (b0 == 0) frees = sum & 0xffff, free_mine = static_cast<int>(x & 0xffff);
     }
-    if (tid == 0) before[B] = items;
-    // free pages before each of the thread's groups: rounds one after the other
-    int free_mine[kReserveRounds], frees = 0;
-    const int rounds = static_cast<int>((to - from + 4l * threads - 1) / (4l * threads));
-#pragma unroll
-    for (int r = 0; r < kReserveRounds; ++r)
-        if (r < rounds) {
-            free_mine[r] = frees + block_scan(__popc(free_of >> 4 * r & 15u), scratch, &sum);
-            frees += sum;
-        }
-    if (tid == 0) counts[0] = frees;
+    if (tid == 0) {
+        before[B] = items;
+        counts[0] = frees;
+    }
     barrier();
-    int free_before = 0, free_all = 0;
+    int free_before = free_mine, free_all = 0;
     for (int c = 0; c < ctas; ++c) {
         const int x = *cluster.map_shared_rank(&counts[0], c);
         if (c < cta) free_before += x;
         free_all += x;
     }
-#pragma unroll
-    for (int r = 0; r < kReserveRounds; ++r)
-        if (r < rounds && (free_of >> 4 * r & 15u) != 0) {
-            int rank = free_before + free_mine[r];
-            for (int k = 0; k < 4; ++k)
-                if (free_of >> (4 * r + k) & 1) {
-                    if (rank < items)
-                        *cluster.map_shared_rank(&fresh[rank % threads], rank / threads) =
-                            static_cast<int>(from + 4l * (r * threads + tid)) + k;
-                    ++rank;
-                }
-        }
+    for (unsigned bits = free_of; bits != 0 && free_before < items; bits &= bits - 1, ++free_before)
+        *cluster.map_shared_rank(&fresh[free_before % threads], free_before / threads) =
+            static_cast<int>(from) + __ffs(static_cast<int>(bits)) - 1;
 
     const int g = cta * threads + tid;  // this thread's item
     int b = 0, e = -1, held = 1, *at = nullptr;
@@ -623,7 +610,7 @@ ReserveShape reserve_shape(int T, int B, int num_pages, int page_size) {
     const long items = static_cast<long>(T) / page_size + 2l * B;
     for (const ReserveShape s : {ReserveShape{256, 1}, ReserveShape{1024, 1}, ReserveShape{1024, kReserveCtas}}) {
         const long all = static_cast<long>(s.threads) * s.ctas;
-        if (items <= all && num_pages <= 4 * kReserveRounds * all - 4 * s.ctas) return s;
+        if (items <= all && num_pages <= 4 * kReserveRounds * all) return s;
     }
     return {0, 0};
 }
