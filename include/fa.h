@@ -456,7 +456,7 @@ int fa_paged_copy(void *k_pages, void *v_pages, const long long *strides, const 
  * Only finite scores are candidates: a token of logit -inf is none, nor is any of a beam whose score or
  * whose logits' sum is not finite (a NaN or +inf among them).  Where a request has fewer than K, the
  * places left have score -inf, parent and token -1 and out_finished 1.
- * W V, B W and B K are below 2^31; K is at most 128 and W at most 2048 (otherwise
+ * W V, B K and B W (V div 4096 + 1) are below 2^31; K is at most 128 and W at most 2048 (otherwise
  * FA_ERR_UNSUPPORTED).  Sums are fp32.
  *   workspace : at least fa_beam_select_workspace_bytes() bytes, 16-byte aligned, as in fa_paged_attn (may be
  *               NULL when that is 0).
