@@ -265,17 +265,20 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
         const int at = atomicAdd(&found, 1);
         if (at < kCap) cand[at] = key_of(v, place);
     };
-    // The threads' tiles that have a logit to collect are listed and read again by the warp, a logit per lane.
-    // (The chain of ballots and reads is as long as the list; its reads are not waited for one by one.)
+    // The threads' tiles that have a logit to collect are listed and read again by the warp, a logit per lane,
+    // four reads in flight.
     if (__any_sync(kAll, m >= bar && m > -INFINITY)) {
         unsigned short *list = places[warp_id()];
         int listed = 0;
         for (int t = 0; t <= tiles; ++t) {
-            const unsigned who = t < tiles ? __ballot_sync(kAll, tops[t][tid] >= bar) : 0;
+            const float here = t < tiles ? tops[t][tid] : -INFINITY;
+            const unsigned who = __ballot_sync(kAll, here >= bar && here > -INFINITY);
             if (t == tiles || listed + __popc(who) > kPlaces) {
                 constexpr int kAtOnce = 32 / kElems, kBatch = 4;
                 __syncwarp();
-                for (int i0 = lane / kElems; i0 < listed; i0 += kAtOnce * kBatch) {
+                // too many already: they are found in another way
+                auto full = [&] { return *static_cast<volatile int *>(&found) > kCap; };
+                for (int i0 = lane / kElems; i0 < listed && !full(); i0 += kAtOnce * kBatch) {
                     float v[kBatch];
                     int at[kBatch];
 #pragma unroll
@@ -292,8 +295,7 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
                 }
                 __syncwarp();
                 listed = 0;
-                // too many already: they are found in another way
-                if (__any_sync(kAll, *static_cast<volatile int *>(&found) > kCap)) break;
+                if (__any_sync(kAll, full())) break;
             }
             if (who >> lane & 1) list[listed + __popc(who & ((1u << lane) - 1))] = static_cast<unsigned short>(32 * t + lane);
             listed += __popc(who);
@@ -351,7 +353,7 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
         each(lo + 1, [&](float v, int place) {
             if (v > equal) take(v, place);
         });
-        for (int i = tid; i <= end; i += THREADS)
+        for (int i = tid; i < min(end + 1, len); i += THREADS)
             if (beam_float<TYPE>(x[i]) == equal) take(equal, i);
         __syncthreads();
         n = found;

@@ -8,6 +8,7 @@ softmax, whose mean of y is below ln V < 12.  The logarithm's mantissa adds 2^-2
 order is exact; between rows it may differ where two scores lie within 2 |dL|.
 """
 import random
+import threading
 
 import numpy as np
 import pytest
@@ -252,6 +253,64 @@ def test_selection_captured_and_on_two_streams(cuda_lib, B):
         for got in out[j]:
             assert all(torch.equal(a, b) for a, b in zip(got, want[j]))
     assert cuda_lib.sync_status() == 0
+
+
+def test_long_rows_and_far_requests(cuda_lib):
+    """Places near 2^31 and requests further apart than 2^31 elements: zeros but for a few logits, so that the sums
+    are known."""
+    V = (1 << 29) + 5
+    x = torch.zeros(1, 3, V, dtype=torch.bfloat16, device=DEV)
+    at = [(0, 7), (0, V - 1), (1, 8191), (1, 8192), (2, V - 3), (2, 1 << 28)]
+    for i, (w, v) in enumerate(at):
+        x[0, w, v] = 16.0 + i
+    scores = torch.tensor([[-1.0, -2.0, -4.0]], device=DEV)
+    got = cuda_lib.beam_select(x, scores, k=8)
+    assert cuda_lib.sync_status() == 0
+    L = [np.log(V - 2 + sum(np.exp(16.0 + i) for i, (b, _) in enumerate(at) if b == w)) for w in range(3)]
+    want = sorted(((float(scores[0, w]) + 16.0 + i - L[w], w, v) for i, (w, v) in enumerate(at)), reverse=True)
+    low = [(float(scores[0, 0]) - L[0], 0, 0), (float(scores[0, 0]) - L[0], 0, 1)]
+    want = (want + low if L[0] + 1.0 < min(L[1] + 2.0, L[2] + 4.0) else want)[:8]
+    n = len(want)
+    assert got[1][0, :n].tolist() == [w for _, w, _ in want] and got[2][0, :n].tolist() == [v for _, _, v in want]
+    # sums of half a billion terms: up to 16 tiles of 32 in a row, then trees and 4097 pieces: 64 roundings of 2^-24
+    assert np.allclose(got[0][0, :n].cpu(), [s for s, _, _ in want], rtol=2.0 ** -23, atol=2e-5)
+    del x
+    far = torch.empty((1 << 31) + 4096, dtype=torch.float16, device=DEV)
+    y = far.as_strided((2, 2, 2000), ((1 << 31) + 8, 2001, 1))
+    y.copy_(normal(3, 2, 2, 2000, dtype=torch.float16))
+    check(cuda_lib, y, beams(3, 2, 2), 5, exact=False)
+
+
+def test_calls_from_several_threads(cuda_lib):
+    xs, ss = [normal(i, 4, 3, 5001) for i in range(4)], [beams(i, 4, 3) for i in range(4)]
+    want = [[t.clone() for t in cuda_lib.beam_select(x, s)] for x, s in zip(xs, ss)]
+    torch.cuda.synchronize()
+    streams, wrong = [torch.cuda.Stream() for _ in range(4)], []
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            table = torch.full((5, 9), -1, dtype=torch.int32, device=DEV)
+            refs = torch.zeros(60, dtype=torch.int32, device=DEV)
+            kv = torch.tensor([30, 1, 70, 8, 9], dtype=torch.int32, device=DEV)
+            par = torch.tensor([2, 2, -1, 0, 4], dtype=torch.int32, device=DEV)
+            o = branch.Cache(table.tolist(), refs.tolist(), 8)
+            for _ in range(20):
+                got = cuda_lib.beam_select(xs[i], ss[i])
+                cuda_lib.paged_reserve(table, kv, refs, 8)
+                cuda_lib.paged_fork(table, par, refs)
+                cuda_lib.paged_compact(table, refs)
+                o.reserve(kv.tolist(), list(range(6)))
+                o.fork(par.tolist())
+                o.compact()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])) or table.tolist() != o.table \
+                        or refs.tolist() != o.refs:
+                    wrong.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and cuda_lib.sync_status() == 0
 
 
 def test_beam_search_over_the_paged_cache(cuda_lib):
