@@ -257,7 +257,6 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
     if (lane == 0) sums[warp_id()] = s;
-    const float bar = value_of(least);
     auto key_of = [&](float v, int place) {  // larger: a larger logit, or the first of equal ones
         return static_cast<unsigned long long>(order_of(v)) << 32 | ~static_cast<unsigned>(v0 + place);
     };
@@ -265,49 +264,62 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
         const int at = atomicAdd(&found, 1);
         if (at < kCap) cand[at] = key_of(v, place);
     };
-    // The threads' tiles that have a logit to collect are listed and read again by the warp, a logit per lane,
-    // four reads in flight.
-    if (__any_sync(kAll, m >= bar && m > -INFINITY)) {
-        unsigned short *list = places[warp_id()];
-        int listed = 0;
-        for (int t = 0; t <= tiles; ++t) {
-            const float here = t < tiles ? tops[t][tid] : -INFINITY;
-            const unsigned who = __ballot_sync(kAll, here >= bar && here > -INFINITY);
-            if (t == tiles || listed + __popc(who) > kPlaces) {
-                constexpr int kAtOnce = 32 / kElems, kBatch = 4;
-                __syncwarp();
-                // too many already: they are found in another way
-                auto full = [&] { return *static_cast<volatile int *>(&found) > kCap; };
-                for (int i0 = lane / kElems; i0 < listed && !full(); i0 += kAtOnce * kBatch) {
-                    float v[kBatch];
-                    int at[kBatch];
+    const float bar = value_of(least);
+    // First the logits that reach the bound: what is above the next lower number (below +0 that is not -0; -inf is
+    // never a candidate).  Where these are too many, those above the bound.
+    float over = least <= order_of(-INFINITY) ? -INFINITY : value_of(least - (least == 0x80000000u ? 2 : 1));
+    int n = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        // The threads' tiles that have a logit to collect are listed and read again by the warp, a logit per
+        // lane, four reads in flight.
+        if (__any_sync(kAll, m > over)) {
+            unsigned short *list = places[warp_id()];
+            int listed = 0;
+            for (int t = 0; t <= tiles; ++t) {
+                const unsigned who = __ballot_sync(kAll, t < tiles && tops[t < tiles ? t : 0][tid] > over);
+                if (t == tiles || listed + __popc(who) > kPlaces) {
+                    constexpr int kAtOnce = 32 / kElems, kBatch = 4;
+                    __syncwarp();
+                    auto full = [&] { return *static_cast<volatile int *>(&found) > kCap; };
+                    for (int i0 = lane / kElems; i0 < listed && !full(); i0 += kAtOnce * kBatch) {
+                        float v[kBatch];
+                        int at[kBatch];
 #pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        v[k] = -INFINITY;
-                        if (i0 + k * kAtOnce >= listed) continue;
-                        const int from = list[i0 + k * kAtOnce];
-                        at[k] = from / 32 * Tile::kSize + Tile::place(lane % kElems, (tid & ~31) + from % 32);
-                        if (at[k] < len) v[k] = beam_float<TYPE>(x[at[k]]);
+                        for (int k = 0; k < kBatch; ++k) {
+                            v[k] = -INFINITY;
+                            if (i0 + k * kAtOnce >= listed) continue;
+                            const int from = list[i0 + k * kAtOnce];
+                            at[k] = from / 32 * Tile::kSize + Tile::place(lane % kElems, (tid & ~31) + from % 32);
+                            if (at[k] < len) v[k] = beam_float<TYPE>(x[at[k]]);
+                        }
+#pragma unroll
+                        for (int k = 0; k < kBatch; ++k)
+                            if (v[k] > over) take(v[k], at[k]);
                     }
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k)
-                        if (v[k] >= bar && v[k] > -INFINITY) take(v[k], at[k]);
+                    __syncwarp();
+                    listed = 0;
+                    if (__any_sync(kAll, full())) break;
                 }
-                __syncwarp();
-                listed = 0;
-                if (__any_sync(kAll, full())) break;
+                if (who >> lane & 1)
+                    list[listed + __popc(who & ((1u << lane) - 1))] = static_cast<unsigned short>(32 * t + lane);
+                listed += __popc(who);
             }
-            if (who >> lane & 1) list[listed + __popc(who & ((1u << lane) - 1))] = static_cast<unsigned short>(32 * t + lane);
-            listed += __popc(who);
         }
+        __syncthreads();
+        n = found;
+        if (n <= kCap || pass == 1) break;
+        __syncthreads();
+        if (tid == 0) found = 0;
+        over = bar;
+        __syncthreads();
     }
-    __syncthreads();
-    int n = found;
-    if (n > kCap) {
-        // f(logit, its place in the piece) for this thread's logits of tiles that have one of order `least`
-        auto each = [&](unsigned least, auto f) {
+    if (n > kCap || (over == bar && bar > -INFINITY)) {
+        // Too many reach the bound.  f(logit, its place in the piece) for this thread's logits of tiles that have
+        // one of that order or a higher one
+        auto each = [&](unsigned want, auto f) {
             for (int t = 0; t < tiles; ++t) {
-                if (!(order_of(tops[t][tid]) >= least)) continue;
+                if (!(order_of(tops[t][tid]) >= want)) continue;
 #pragma unroll 1
                 for (int i = 0; i < kElems / VEC; ++i) {
                     const int at = t * Tile::kSize + Tile::place(i * VEC);
@@ -320,43 +332,44 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
             each(want, [&](float v, int) { c += v > -INFINITY && order_of(v) >= want; });
             return block_sum<THREADS>(c, scratch);
         };
-        // the K-th largest logit `lo` is the bound, or above it
-        unsigned lo = least;
-        int above = reach(lo + 1);
-        if (above >= K) {
+        unsigned lo = least;  // the K-th largest: the bound, or, where too many are above it too, found by bisection
+        if (n > kCap) {
             unsigned hi = ~0u;
             while (hi - lo > 1) {
                 const unsigned mid = lo + (hi - lo) / 2;
                 if (reach(mid) >= K) lo = mid;
                 else hi = mid;
             }
-            above = reach(lo + 1);
+            if (tid == 0) found = 0;
+            __syncthreads();
+            each(lo + 1, [&](float v, int place) {
+                if (order_of(v) > lo && v > -INFINITY) take(v, place);
+            });
+            __syncthreads();
+            n = found;
         }
         // of its equals, the first that make K: up to place `end`
-        const int room = K - above;
+        const int room = K - n;
         const float equal = value_of(lo);
-        auto equals = [&](int from, int to) {
-            int c = 0;
+        if (room > 0) {
+            auto equals = [&](int from, int to) {
+                int c = 0;
 #pragma unroll 8
-            for (int i = from + tid; i < min(to, len); i += THREADS) c += beam_float<TYPE>(x[i]) == equal;
-            return block_sum<THREADS>(c, scratch);
-        };
-        int end = 0, before = 0;
-        for (int span = 8 * THREADS; end < len;) {
-            const int c = equals(end, end + span);
-            if (before + c < room) before += c, end += span;
-            else if (span == 1) break;
-            else span /= 2;
+                for (int i = from + tid; i < min(to, len); i += THREADS) c += beam_float<TYPE>(x[i]) == equal;
+                return block_sum<THREADS>(c, scratch);
+            };
+            int end = 0, before = 0;
+            for (int span = 8 * THREADS; end < len;) {
+                const int c = equals(end, end + span);
+                if (before + c < room) before += c, end += span;
+                else if (span == 1) break;
+                else span /= 2;
+            }
+            for (int i = tid; i < min(end + 1, len); i += THREADS)
+                if (beam_float<TYPE>(x[i]) == equal) take(equal, i);
+            __syncthreads();
+            n = found;
         }
-        if (tid == 0) found = 0;
-        __syncthreads();
-        each(lo + 1, [&](float v, int place) {
-            if (v > equal) take(v, place);
-        });
-        for (int i = tid; i < min(end + 1, len); i += THREADS)
-            if (beam_float<TYPE>(x[i]) == equal) take(equal, i);
-        __syncthreads();
-        n = found;
     }
     // the K largest, largest first, by counting: a warp's work where there are few
     const int lanes = n <= 32 ? 1 : lanes_each<THREADS>(n), part = tid & (lanes - 1), own = tid / lanes;

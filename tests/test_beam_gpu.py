@@ -152,6 +152,25 @@ def test_masked_tokens_dead_beams_and_beams_that_have_ended(cuda_lib, dtype):
     check(cuda_lib, torch.full_like(x, lowest), torch.zeros(B, W, device=DEV), 12)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lowest", [False, True])
+def test_masks_that_leave_some_tokens(cuda_lib, lowest, dtype):
+    """From one token to all of them, scattered or in blocks that few threads see; the others -inf or the type's
+    lowest value, whose places follow once the others run out."""
+    V = 30000
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x = normal(4, 1, 2, V, dtype=dtype)
+    mask = torch.finfo(dtype).min if lowest else float("-inf")
+    spread = torch.rand(V, generator=g, device=DEV).argsort()
+    place = torch.arange(V, device=DEV)
+    for n in (1, 7, 8, 9, 31, 100, 700, 5000):
+        for block in (False, True):
+            keep = (place % 2048 < 8 * n / V * 256) & (place // 8 % 3 < 2) if block else spread < n
+            y = torch.where(keep, x, torch.tensor(mask, dtype=dtype, device=DEV))
+            for K in (1, 8, 40, 128):
+                check(cuda_lib, y, torch.tensor([[-1.0, -1.5]], device=DEV), K, exact=False)
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("at", [0, 8191, 8192, 12344])
 def test_a_row_that_is_no_distribution_offers_nothing(cuda_lib, value, at):
