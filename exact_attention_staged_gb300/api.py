@@ -435,7 +435,7 @@ def _calls():
                  "fa_paged_reserve", "fa_paged_reserve_workspace_bytes", "fa_paged_fork", "fa_paged_free",
                  "fa_paged_compact", "fa_paged_copy", "fa_beam_select", "fa_beam_select_workspace_bytes")
         ext.setup(tuple(ctypes.cast(getattr(lib, n), _vp).value for n in names), torch.empty, _raw,
-                  torch.bfloat16, torch.float16, torch.int32, torch.int64, torch.float32,
+                  _current_device, torch.bfloat16, torch.float16, torch.int32, torch.int64, torch.float32,
                   torch.uint8, FAError)
         _binding = ext
     return _binding
@@ -600,12 +600,14 @@ def paged_reserve(block_table, kv_len, refs, page_size: int, q_start=None, token
     None: one for each sequence).  Returns copies, int32 [3, B]: paged_copy's src, dst and rows for the
     pages that were shared and are partly filled.
     """
-    if _away(block_table, stream):
-        return _elsewhere(lambda: paged_reserve(block_table, kv_len, refs, page_size, q_start, tokens,
-                                                copies, workspace),
-                          stream, block_table.device, (block_table, kv_len, refs, q_start, copies,
-                                                       workspace))
-    return _calls().paged_reserve(block_table, kv_len, refs, page_size, q_start, tokens, copies, workspace)
+    if stream is None:
+        done = _calls().paged_reserve(block_table, kv_len, refs, page_size, q_start, tokens, copies, workspace)
+        if done is not NotImplemented:
+            return done
+    return _elsewhere(lambda: paged_reserve(block_table, kv_len, refs, page_size, q_start, tokens,
+                                            copies, workspace),
+                      stream, block_table.device, (block_table, kv_len, refs, q_start, copies,
+                                                   workspace))
 
 
 def paged_reserve_workspace_bytes(tokens: int, B: int, num_pages: int, page_size: int) -> int:
@@ -617,18 +619,22 @@ def paged_fork(block_table, parents, refs, kv_len=None, stream=None):
 
     parents: int32 [B], as beam_select returns them (flattened).  refs follows.
     """
-    if _away(block_table, stream):
-        return _elsewhere(lambda: paged_fork(block_table, parents, refs, kv_len), stream,
-                          block_table.device, (block_table, parents, refs, kv_len))
-    return _calls().paged_fork(block_table, parents, refs, kv_len)
+    if stream is None:
+        done = _calls().paged_fork(block_table, parents, refs, kv_len)
+        if done is not NotImplemented:
+            return done
+    return _elsewhere(lambda: paged_fork(block_table, parents, refs, kv_len), stream,
+                      block_table.device, (block_table, parents, refs, kv_len))
 
 
 def paged_free(block_table, keep_len, refs, page_size: int, stream=None):
     """Sequence b keeps the pages of its first keep_len[b] positions (int32 [B]; fa_paged_free)."""
-    if _away(block_table, stream):
-        return _elsewhere(lambda: paged_free(block_table, keep_len, refs, page_size), stream,
-                          block_table.device, (block_table, keep_len, refs))
-    return _calls().paged_free(block_table, keep_len, refs, page_size)
+    if stream is None:
+        done = _calls().paged_free(block_table, keep_len, refs, page_size)
+        if done is not NotImplemented:
+            return done
+    return _elsewhere(lambda: paged_free(block_table, keep_len, refs, page_size), stream,
+                      block_table.device, (block_table, keep_len, refs))
 
 
 def paged_compact(block_table, refs, moves=None, count=None, stream=None):
@@ -637,10 +643,12 @@ def paged_compact(block_table, refs, moves=None, count=None, stream=None):
     Returns moves, int32 [2, num_pages // 2 or more], and count, int32 [1]: paged_copy's src, dst and
     count, which move the data.  block_table and refs are updated.
     """
-    if _away(block_table, stream):
-        return _elsewhere(lambda: paged_compact(block_table, refs, moves, count), stream,
-                          block_table.device, (block_table, refs, moves, count))
-    return _calls().paged_compact(block_table, refs, moves, count)
+    if stream is None:
+        done = _calls().paged_compact(block_table, refs, moves, count)
+        if done is not NotImplemented:
+            return done
+    return _elsewhere(lambda: paged_compact(block_table, refs, moves, count), stream,
+                      block_table.device, (block_table, refs, moves, count))
 
 
 def paged_copy(k_pages, v_pages, src, dst, rows=None, count=None, stream=None):
@@ -649,10 +657,12 @@ def paged_copy(k_pages, v_pages, src, dst, rows=None, count=None, stream=None):
     k_pages, v_pages: one layer's [num_pages, H_kv, page_size, d], or all layers' [L, num_pages, H_kv,
     page_size, d].  Pairs with a negative page are left out, and those from count (int32 [1]) on.
     """
-    if _away(k_pages, stream):
-        return _elsewhere(lambda: paged_copy(k_pages, v_pages, src, dst, rows, count), stream,
-                          k_pages.device, (k_pages, v_pages, src, dst, rows, count))
-    return _calls().paged_copy(k_pages, v_pages, src, dst, rows, count)
+    if stream is None:
+        done = _calls().paged_copy(k_pages, v_pages, src, dst, rows, count)
+        if done is not NotImplemented:
+            return done
+    return _elsewhere(lambda: paged_copy(k_pages, v_pages, src, dst, rows, count), stream,
+                      k_pages.device, (k_pages, v_pages, src, dst, rows, count))
 
 
 def beam_select(logits, scores, k: Optional[int] = None, finished=None, end_token: Optional[int] = None,
@@ -665,13 +675,15 @@ def beam_select(logits, scores, k: Optional[int] = None, finished=None, end_toke
     scores (fp32), parents (int32, b * W + beam; -1: no candidate was left), tokens (int32) and finished
     (uint8), each [B, k], best first.
     """
-    if _away(logits, stream):
-        return _elsewhere(lambda: beam_select(logits, scores, k, finished, end_token, out_scores,
-                                              out_parents, out_tokens, out_finished, workspace),
-                          stream, logits.device, (logits, scores, finished, out_scores, out_parents,
-                                                  out_tokens, out_finished, workspace))
-    return _calls().beam_select(logits, scores, k, finished, end_token, out_scores, out_parents,
-                                out_tokens, out_finished, workspace)
+    if stream is None:
+        done = _calls().beam_select(logits, scores, k, finished, end_token, out_scores, out_parents,
+                                    out_tokens, out_finished, workspace)
+        if done is not NotImplemented:
+            return done
+    return _elsewhere(lambda: beam_select(logits, scores, k, finished, end_token, out_scores,
+                                          out_parents, out_tokens, out_finished, workspace),
+                      stream, logits.device, (logits, scores, finished, out_scores, out_parents,
+                                              out_tokens, out_finished, workspace))
 
 
 def beam_select_workspace_bytes(B: int, W: int, V: int, k: int) -> int:

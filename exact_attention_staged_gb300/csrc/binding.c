@@ -48,9 +48,10 @@ static compact_fn g_compact;
 static copy_fn g_copy;
 static beam_fn g_beam;
 static beam_bytes_fn g_beam_bytes;
-/* torch.empty, the current raw stream of a device, the dtypes, the error class: set by setup() */
-static PyObject *g_empty, *g_stream, *g_bf16, *g_fp16, *g_i32, *g_i64, *g_f32, *g_u8, *g_error;
-static PyObject *s_get_device, *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_device, *s_kwnames;
+/* torch.empty, the current raw stream of a device, the current device, the dtypes, the error class: set by
+ * setup() */
+static PyObject *g_empty, *g_stream, *g_current, *g_bf16, *g_fp16, *g_i32, *g_i64, *g_f32, *g_u8, *g_error;
+static PyObject *s_get_device, *s_contiguous, *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_device, *s_kwnames;
 
 #define MAX_DIMS 5
 typedef struct {
@@ -122,7 +123,14 @@ static int take(PyObject *obj, const char *name, long dev, Tensor *t) {
     Py_DECREF(t->dtype);
     t->dims = ints_of(PyObject_GetAttr(obj, s_shape), t->shape);
     if (t->dims < 0) return -1;
-    if (ints_of(call0(obj, s_stride), t->stride) < 0) return -1;
+    if (t->dims == 1) { /* dense or not is all that is asked of index arrays */
+        PyObject *dense = call0(obj, s_contiguous);
+        if (dense == NULL) return -1;
+        t->stride[0] = dense == Py_True ? 1 : 2;
+        Py_DECREF(dense);
+    } else if (ints_of(call0(obj, s_stride), t->stride) < 0) {
+        return -1;
+    }
     PyObject *p = call0(obj, s_data_ptr);
     if (p == NULL) return -1;
     t->ptr = PyLong_AsVoidPtr(p);
@@ -269,6 +277,22 @@ static int first_device(PyObject *obj, const char *name, long *dev) {
     }
     return 0;
 }
+
+/* Whether another device than dev is current: 0, 1, or -1 for an error. */
+static int is_away(long dev) {
+    PyObject *d = PyObject_CallNoArgs(g_current);
+    if (d == NULL) return -1;
+    const long now = PyLong_AsLong(d);
+    Py_DECREF(d);
+    return PyErr_Occurred() ? -1 : now != dev;
+}
+/* The calls below leave a tensor of another device to their Python wrapper: they return NotImplemented. */
+#define LEAVE_IF_AWAY(dev)                       \
+    do {                                         \
+        const int away_ = is_away(dev);          \
+        if (away_ < 0) return NULL;              \
+        if (away_) Py_RETURN_NOTIMPLEMENTED;     \
+    } while (0)
 
 static int count_args(Py_ssize_t got, Py_ssize_t want) {
     return got == want ? 0 : fail(PyExc_TypeError, "wrong number of arguments");
@@ -581,10 +605,8 @@ static PyObject *dense_result(const Tensor *given, PyObject *dtype, const long l
 }
 
 /* block_table [B, max_pages] and refs [num_pages]. */
-static int take_tables(PyObject *table, PyObject *refs, long *dev, Tensor *t, Tensor *r) {
-    if (first_device(table, "block_table", dev) || take(table, "block_table", *dev, t) ||
-        take(refs, "refs", *dev, r))
-        return -1;
+static int take_tables(PyObject *table, PyObject *refs, long dev, Tensor *t, Tensor *r) {
+    if (take(table, "block_table", dev, t) || take(refs, "refs", dev, r)) return -1;
     if (t->dims != 2 || t->dtype != g_i32 || !is_dense(t))
         return fail(PyExc_ValueError, "block_table must be contiguous int32 [B, max_pages]");
     if (r->obj == NULL || r->dims != 1 || r->dtype != g_i32 || !is_dense(r))
@@ -608,8 +630,9 @@ static PyObject *py_reserve(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     Tensor table, refs, len, start, copies, ws;
     long dev;
     long long page, T;
-    if (count_args(n, 8) || take_tables(a[0], a[2], &dev, &table, &refs) ||
-        take(a[1], "kv_len", dev, &len) || take(a[4], "q_start", dev, &start) ||
+    if (count_args(n, 8) || first_device(a[0], "block_table", &dev)) return NULL;
+    LEAVE_IF_AWAY(dev);
+    if (take_tables(a[0], a[2], dev, &table, &refs) || take(a[1], "kv_len", dev, &len) || take(a[4], "q_start", dev, &start) ||
         take(a[6], "copies", dev, &copies) || take(a[7], "workspace", dev, &ws) ||
         int_arg(a[3], "page_size", &page))
         return NULL;
@@ -654,8 +677,9 @@ static PyObject *py_fork(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     Tensor table, refs, parents, len;
     long dev;
     void *stream;
-    if (count_args(n, 4) || take_tables(a[0], a[2], &dev, &table, &refs) ||
-        take(a[1], "parents", dev, &parents) || take(a[3], "kv_len", dev, &len) ||
+    if (count_args(n, 4) || first_device(a[0], "block_table", &dev)) return NULL;
+    LEAVE_IF_AWAY(dev);
+    if (take_tables(a[0], a[2], dev, &table, &refs) || take(a[1], "parents", dev, &parents) || take(a[3], "kv_len", dev, &len) ||
         need_index(&parents, table.shape[0]) || check_index(&len, table.shape[0], -1) ||
         stream_of(dev, &stream))
         return NULL;
@@ -675,8 +699,9 @@ static PyObject *py_free(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     long dev;
     long long page;
     void *stream;
-    if (count_args(n, 4) || take_tables(a[0], a[2], &dev, &table, &refs) ||
-        take(a[1], "keep_len", dev, &keep) || need_index(&keep, table.shape[0]) ||
+    if (count_args(n, 4) || first_device(a[0], "block_table", &dev)) return NULL;
+    LEAVE_IF_AWAY(dev);
+    if (take_tables(a[0], a[2], dev, &table, &refs) || take(a[1], "keep_len", dev, &keep) || need_index(&keep, table.shape[0]) ||
         int_arg(a[3], "page_size", &page) || stream_of(dev, &stream))
         return NULL;
     int code;
@@ -693,8 +718,9 @@ static PyObject *py_compact(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
     Tensor table, refs, moves, count;
     long dev;
-    if (count_args(n, 4) || take_tables(a[0], a[1], &dev, &table, &refs) ||
-        take(a[2], "moves", dev, &moves) || take(a[3], "count", dev, &count))
+    if (count_args(n, 4) || first_device(a[0], "block_table", &dev)) return NULL;
+    LEAVE_IF_AWAY(dev);
+    if (take_tables(a[0], a[1], dev, &table, &refs) || take(a[2], "moves", dev, &moves) || take(a[3], "count", dev, &count))
         return NULL;
     const long long pages = refs.shape[0], one[1] = {1};
     long long shape[2] = {2, pages > 1 ? pages / 2 : 1};
@@ -727,8 +753,9 @@ static PyObject *py_copy(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     Tensor k, v, src, dst, rows, count;
     long dev;
     void *stream;
-    if (count_args(n, 6) || first_device(a[0], "k_pages", &dev) || take(a[0], "k_pages", dev, &k) ||
-        take(a[1], "v_pages", dev, &v) || take(a[2], "src", dev, &src) || take(a[3], "dst", dev, &dst) ||
+    if (count_args(n, 6) || first_device(a[0], "k_pages", &dev)) return NULL;
+    LEAVE_IF_AWAY(dev);
+    if (take(a[0], "k_pages", dev, &k) || take(a[1], "v_pages", dev, &v) || take(a[2], "src", dev, &src) || take(a[3], "dst", dev, &dst) ||
         take(a[4], "rows", dev, &rows) || take(a[5], "count", dev, &count))
         return NULL;
     if (v.obj == NULL || (k.dims != 4 && k.dims != 5) || !same_shape(&k, &v) || k.dtype != v.dtype) {
@@ -767,8 +794,9 @@ static PyObject *py_beam(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     Tensor x, scores, fin, out[4], ws;
     static const char *names[4] = {"out_scores", "out_parents", "out_tokens", "out_finished"};
     long dev;
-    if (count_args(n, 10) || first_device(a[0], "logits", &dev) || take(a[0], "logits", dev, &x) ||
-        take(a[1], "scores", dev, &scores) || take(a[3], "finished", dev, &fin) ||
+    if (count_args(n, 10) || first_device(a[0], "logits", &dev)) return NULL;
+    LEAVE_IF_AWAY(dev);
+    if (take(a[0], "logits", dev, &x) || take(a[1], "scores", dev, &scores) || take(a[3], "finished", dev, &fin) ||
         take(a[9], "workspace", dev, &ws))
         return NULL;
     for (int i = 0; i < 4; ++i)
@@ -828,15 +856,15 @@ done:
     return res;
 }
 
-/* setup(addresses of the entry points in the order below, torch.empty, raw stream of a device, bfloat16,
- *       float16, int32, int64, float32, uint8, error class) */
+/* setup(addresses of the entry points in the order below, torch.empty, raw stream of a device, current device,
+ *       bfloat16, float16, int32, int64, float32, uint8, error class) */
 static PyObject *py_setup(PyObject *self, PyObject *args) {
     (void)self;
     unsigned long long f[12];
-    PyObject *o[9];
-    if (!PyArg_ParseTuple(args, "(KKKKKKKKKKKK)OOOOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6],
+    PyObject *o[10];
+    if (!PyArg_ParseTuple(args, "(KKKKKKKKKKKK)OOOOOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6],
                           &f[7], &f[8], &f[9], &f[10], &f[11], &o[0], &o[1], &o[2], &o[3], &o[4],
-                          &o[5], &o[6], &o[7], &o[8]))
+                          &o[5], &o[6], &o[7], &o[8], &o[9]))
         return NULL;
     g_rope = (rope_fn)(uintptr_t)f[0];
     g_append = (append_fn)(uintptr_t)f[1];
@@ -850,8 +878,8 @@ static PyObject *py_setup(PyObject *self, PyObject *args) {
     g_copy = (copy_fn)(uintptr_t)f[9];
     g_beam = (beam_fn)(uintptr_t)f[10];
     g_beam_bytes = (beam_bytes_fn)(uintptr_t)f[11];
-    PyObject **slots[9] = {&g_empty, &g_stream, &g_bf16, &g_fp16, &g_i32, &g_i64, &g_f32, &g_u8, &g_error};
-    for (int i = 0; i < 9; ++i) {
+    PyObject **slots[10] = {&g_empty, &g_stream, &g_current, &g_bf16, &g_fp16, &g_i32, &g_i64, &g_f32, &g_u8, &g_error};
+    for (int i = 0; i < 10; ++i) {
         Py_INCREF(o[i]);
         Py_XSETREF(*slots[i], o[i]);
     }
@@ -876,13 +904,14 @@ static struct PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1
 
 PyMODINIT_FUNC PyInit__binding(void) {
     s_get_device = PyUnicode_InternFromString("get_device");
+    s_contiguous = PyUnicode_InternFromString("is_contiguous");
     s_dtype = PyUnicode_InternFromString("dtype");
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_device = PyUnicode_InternFromString("device");
     s_kwnames = Py_BuildValue("(ss)", "dtype", "device");
-    if (!s_get_device || !s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_device || !s_kwnames)
+    if (!s_get_device || !s_contiguous || !s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_device || !s_kwnames)
         return NULL;
     return PyModule_Create(&kModule);
 }
