@@ -617,7 +617,7 @@ def paged_reserve_workspace_bytes(tokens: int, B: int, num_pages: int, page_size
 def paged_fork(block_table, parents, refs, kv_len=None, stream=None):
     """Row b of block_table (and kv_len) becomes what row parents[b] was; -1: empty (fa_paged_fork).
 
-    parents: int32 [B], as beam_select returns them (flattened).  refs follows.
+    parents: int32 [B], or [requests, beams] of B in all, as beam_select returns them.  refs follows.
     """
     if stream is None:
         done = _calls().paged_fork(block_table, parents, refs, kv_len)

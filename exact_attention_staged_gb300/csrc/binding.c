@@ -679,10 +679,16 @@ static PyObject *py_fork(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     void *stream;
     if (count_args(n, 4) || first_device(a[0], "block_table", &dev)) return NULL;
     LEAVE_IF_AWAY(dev);
-    if (take_tables(a[0], a[2], dev, &table, &refs) || take(a[1], "parents", dev, &parents) || take(a[3], "kv_len", dev, &len) ||
-        need_index(&parents, table.shape[0]) || check_index(&len, table.shape[0], -1) ||
-        stream_of(dev, &stream))
+    if (take_tables(a[0], a[2], dev, &table, &refs) || take(a[1], "parents", dev, &parents) ||
+        take(a[3], "kv_len", dev, &len) || check_index(&len, table.shape[0], -1))
         return NULL;
+    /* [B], or the [requests, beams] of a selection */
+    if (parents.obj == NULL || parents.dtype != g_i32 || !is_dense(&parents) || parents.dims < 1 ||
+        parents.dims > 2 || parents.shape[0] * (parents.dims == 2 ? parents.shape[1] : 1) != table.shape[0]) {
+        PyErr_Format(PyExc_ValueError, "parents must be contiguous int32 of %lld values", table.shape[0]);
+        return NULL;
+    }
+    if (stream_of(dev, &stream)) return NULL;
     int code;
     Py_BEGIN_ALLOW_THREADS
     code = g_fork(table.ptr, len.ptr, parents.ptr, refs.ptr, (int)table.shape[0], (int)refs.shape[0],

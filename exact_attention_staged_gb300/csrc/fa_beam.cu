@@ -45,23 +45,6 @@ __device__ __forceinline__ unsigned order_of(float x) {
 __device__ __forceinline__ float value_of(unsigned u) {
     return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
-// The k-th largest of values[0 .. 32), which every lane of the warp gets.
-__device__ __forceinline__ unsigned kth_of_32(const unsigned *values, int k) {
-    const uint4 *all = reinterpret_cast<const uint4 *>(values);
-    const int lane = lane_id();
-    const unsigned mine = values[lane];
-    int rank = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {  // equal ones in order
-        const uint4 x = all[j];
-        rank += x.x > mine || (x.x == mine && 4 * j < lane);
-        rank += x.y > mine || (x.y == mine && 4 * j + 1 < lane);
-        rank += x.z > mine || (x.z == mine && 4 * j + 2 < lane);
-        rank += x.w > mine || (x.w == mine && 4 * j + 3 < lane);
-    }
-    return __shfl_sync(kAll, mine, __ffs(static_cast<int>(__ballot_sync(kAll, rank == k - 1))) - 1);
-}
-
 // Lanes that share the work on one of n things (a power of two up to 32).
 template <int THREADS>
 __device__ __forceinline__ int lanes_each(int n) {
@@ -74,18 +57,34 @@ __device__ __forceinline__ int sum_lanes(int x, int p) {
     return x;
 }
 
-// The CTA's k-th largest of values[0 .. n), n a power of two no more than the threads; every thread calls it
-// and gets the result, which `out` passes on.
+// The k-th largest of values[0 .. n), n a power of two from 32 to the CTA's threads: the largest that k of them
+// reach.  Every thread calls it and gets the result; *out has to be 0 before.
 template <int THREADS>
 __device__ __forceinline__ unsigned kth_largest(const unsigned *values, int n, int k, unsigned *out) {
-    const int lanes = lanes_each<THREADS>(n), i = static_cast<int>(threadIdx.x) / lanes, part = threadIdx.x % lanes;
+    const uint4 *fours = reinterpret_cast<const uint4 *>(values);
+    if (n == 32) {  // every warp for itself
+        const unsigned mine = values[lane_id()];
+        int reached = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint4 x = fours[j];
+            reached += (x.x >= mine) + (x.y >= mine) + (x.z >= mine) + (x.w >= mine);
+        }
+        return __reduce_max_sync(kAll, reached >= k ? mine : 0);
+    }
+    const int lanes = min(lanes_each<THREADS>(n), n / 4), part = threadIdx.x % lanes;
+    const int i = static_cast<int>(threadIdx.x) / lanes;
     if (i < n) {  // whole warps
         const unsigned mine = values[i];
-        int rank = 0;
-#pragma unroll 8
-        for (int j = part; j < n; j += lanes) rank += values[j] > mine || (values[j] == mine && j < i);
-        rank = sum_lanes(rank, lanes);
-        if (part == 0 && rank == k - 1) *out = mine;
+        int reached = 0;
+#pragma unroll 4
+        for (int j = part; j < n / 4; j += lanes) {
+            const uint4 x = fours[j];
+            reached += (x.x >= mine) + (x.y >= mine) + (x.z >= mine) + (x.w >= mine);
+        }
+        reached = sum_lanes(reached, lanes);
+        const unsigned best = __reduce_max_sync(kAll, reached >= k ? mine : 0);
+        if (lane_id() == 0) atomicMax(out, best);
     }
     __syncthreads();
     return *out;
@@ -246,9 +245,9 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
     if (tid % width == 0) groups[tid / width] = order_of(g);
     const unsigned mine = __reduce_max_sync(kAll, order_of(m));
     if (lane == 0) tops_of[warp_id()] = mine;
-    if (tid == 0) found = 0;
+    if (tid == 0) found = 0, bound = 0;
     __syncthreads();
-    const unsigned least = count == 32 ? kth_of_32(groups, K) : kth_largest<THREADS>(groups, count, K, &bound);
+    const unsigned least = kth_largest<THREADS>(groups, count, K, &bound);
     unsigned most = tops_of[0];
 #pragma unroll
     for (int i = 1; i < THREADS / 32; ++i) most = max(most, tops_of[i]);
@@ -272,14 +271,14 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         // The threads' tiles that have a logit to collect are listed and read again by the warp, a logit per
-        // lane, four reads in flight.
+        // lane, eight reads in flight.
         if (__any_sync(kAll, m > over)) {
             unsigned short *list = places[warp_id()];
             int listed = 0;
             for (int t = 0; t <= tiles; ++t) {
                 const unsigned who = __ballot_sync(kAll, t < tiles && tops[t < tiles ? t : 0][tid] > over);
                 if (t == tiles || listed + __popc(who) > kPlaces) {
-                    constexpr int kAtOnce = 32 / kElems, kBatch = 4;
+                    constexpr int kAtOnce = 32 / kElems, kBatch = 8;
                     __syncwarp();
                     auto full = [&] { return *static_cast<volatile int *>(&found) > kCap; };
                     for (int i0 = lane / kElems; i0 < listed && !full(); i0 += kAtOnce * kBatch) {
@@ -436,7 +435,7 @@ struct BeamBase {
 template <int THREADS, class Lists, class Stats>
 __device__ __forceinline__ void beam_join(const BeamParams &p, int b, BeamBase *base, Lists list_of,
                                           Stats stats_of) {
-    __shared__ unsigned groups[256];
+    __shared__ __align__(16) unsigned groups[256];
     __shared__ unsigned bound;
     __shared__ int found;
     __shared__ int scratch[THREADS / 32];
@@ -482,7 +481,7 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, int b, BeamBase *
             base[w] = {none ? NAN : r.x, r.y - l.y, m, 0};
         }
     }
-    if (tid == 0) found = 0;
+    if (tid == 0) found = 0, bound = 0;
     if (tid < 256) groups[tid] = 0;
     __syncthreads();
     // the order (0: none) of candidate j of list l, whose key is k, and its place w V + v
@@ -538,8 +537,8 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, int b, BeamBase *
         if (n < kJoinCap) cand[n] = k, where[n] = at;
     };
     __syncthreads();
-    kth_largest<THREADS>(groups, count, K, &bound);
-    const unsigned long long t = max(static_cast<unsigned long long>(bound) << 32, 1ull);
+    const unsigned least = kth_largest<THREADS>(groups, count, K, &bound);
+    const unsigned long long t = max(static_cast<unsigned long long>(least) << 32, 1ull);
     each([&](unsigned long long k, int at) {
         if (k >= t) take(k, at);
     });
@@ -614,7 +613,7 @@ __global__ void __launch_bounds__(THREADS) fa_beam_join_kernel(const BeamParams 
 // Small requests in one launch, without a workspace: a cluster per request, whose CTAs take pieces in turns
 // and leave lists and sums in their shared memory, where the first CTA reads them.
 template <int TYPE, int VEC>
-__global__ void __launch_bounds__(kThreads) fa_beam_cluster_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kThreads, 2) fa_beam_cluster_kernel(const BeamParams p) {
     extern __shared__ __align__(16) unsigned char beam_smem[];
     cg::cluster_group cluster = cg::this_cluster();
     const int cta = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());

@@ -364,12 +364,11 @@ def test_beam_search_over_the_paged_cache(cuda_lib):
         for g in range(G):
             want = branch.select(x[g], sc[g], W, fin[g], 7)
             assert np.allclose(scores[g].cpu(), want["scores"], atol=2 * DL + 1e-5)
-        parents = parents.view(-1)
         api.paged_fork(table, parents, refs, kv_len)
         kv_len += 1
         copies = api.paged_reserve(table, kv_len, refs, page)
         api.paged_copy(k, v, copies[0], copies[1], copies[2])
-        par = parents.tolist()
+        par = parents.view(-1).tolist()
         assert min(par) >= 0
         for layer in range(L):
             nk = normal(1000 + 10 * step + layer, S, Hkv, d, dtype=dtype, scale=1.0)

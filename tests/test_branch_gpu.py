@@ -320,7 +320,8 @@ def test_arguments_that_are_refused(cuda_lib):
             lambda: api.paged_reserve(t[:, :3], n, f, 16),
             lambda: api.paged_fork(t, n[:2], f), lambda: api.paged_fork(t, n, f.long()),
             lambda: api.paged_fork(t, n, f[::2]), lambda: api.paged_fork(t, n, f, kv_len=n[:1]),
-            lambda: api.paged_fork(t, None, f), lambda: api.paged_free(t, None, f, 16),
+            lambda: api.paged_fork(t, None, f), lambda: api.paged_fork(t, n.view(3, 1).expand(3, 2), f),
+            lambda: api.paged_free(t, None, f, 16),
             lambda: api.paged_free(t, n.cpu(), f, 16), lambda: api.paged_fork(t, n, None),
             lambda: api.paged_compact(t, f, moves=torch.zeros(2, 3, dtype=torch.int32, device=DEV)),
             lambda: api.paged_compact(t, f, count=f), lambda: api.paged_compact(t, f, count=f[:1].long()),
