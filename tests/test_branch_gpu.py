@@ -121,6 +121,39 @@ def test_reserving_again_changes_nothing(cuda_lib):
     c.reserve([45, 0, 17, 16, 300, 1], [0, 5, 5, 5, 5, 5, 5], tokens=20)
 
 
+def test_as_many_tokens_for_every_sequence(cuda_lib):
+    for B, each, pages in ((3, 5, 40), (40, 20, 400), (500, 33, 20000), (900, 100, 40000)):
+        c = Pair(cuda_lib, B, 30, pages, 8, seed=B)
+        lens = [c.r.randint(0, 60) for _ in range(B)]
+        c.reserve([x + each for x in lens], None, tokens=B * each)
+        c.fork([c.r.randrange(B) for _ in range(B)])
+        c.free([c.r.randint(0, 100) for _ in range(B)])
+
+
+def test_pages_that_the_caller_holds(cuda_lib):
+    """A prefix kept by the caller: never given out, never written to, moved like the others."""
+    c = Pair(cuda_lib, 3, 6, 20, 8)
+    c.reserve([17, 9, 0], [0, 17, 26, 26], tokens=26)
+    for e in c.o.table[0][:3]:
+        c.o.refs[e] += 1
+        c.refs[e] += 1
+    kept = list(c.o.table[0][:3])
+    c.free([0, 9, 0])
+    assert [c.o.refs[e] for e in kept] == [1, 1, 1]
+    c.table[2, :3] = c.table.new_tensor(kept)  # a new sequence on the kept prefix
+    c.o.table[2][:3] = kept
+    for e in kept:
+        c.o.refs[e] += 1
+        c.refs[e] += 1
+    copies = c.reserve([0, 9, 18], [0, 0, 0, 1], tokens=1)  # its own copy of the part-filled page
+    assert copies[:, 2].tolist() == [kept[2], c.o.table[2][2], 1]
+    c.free([0, 0, 0])
+    c.o.refs[kept[0]] -= 1  # the front page is given up: the others move into its place and behind
+    c.refs[kept[0]] -= 1
+    c.compact()
+    assert sum(c.o.refs) == 2
+
+
 def test_a_long_prompt_and_a_large_pool(cuda_lib):
     c = Pair(cuda_lib, 3, 20000, 100003, 8)
     c.reserve([150000, 3, 100], [0, 150000, 150003, 150103], tokens=150103)
@@ -333,7 +366,8 @@ def test_arguments_that_are_refused(cuda_lib):
             call()
     with pytest.raises(TypeError):
         api.paged_copy(kv.float(), kv.float(), n, n)
-    for call in (lambda: api.paged_free(t, n, f, 12), lambda: api.paged_reserve(t, n, f, 16, tokens=4),
+    for call in (lambda: api.paged_free(t, n, torch.zeros(10, dtype=torch.int32, device=DEV)[1:], 16),  # not aligned
+                 lambda: api.paged_free(t, n, f, 12), lambda: api.paged_reserve(t, n, f, 16, tokens=4),
                  lambda: api.paged_copy(kv, kv, n[:0], n[:0])):
         with pytest.raises(api.FAError):
             call()
