@@ -13,8 +13,9 @@
 // groups being a random partition as it were, not many more; they stand where the noted maxima reach it, and
 // those few places are read again.  The loop has neither barriers nor shared counters (collecting
 // candidates in it took 34 us for 256 rows of 131072 bf16 logits, of which streaming alone is 14.4).
-// Where more logits reach the bound than there is room for (long runs of rising or equal logits), the
-// K-th largest is found by bisection over them.
+// Where more logits reach the bound than there is room for (equal ones, or few groups that have nearly all), the
+// bound is raised by those that were kept, twice at most; the K-th largest of what may still be too many (rows
+// that rise throughout) is found by bisection.
 //
 // s is formed as an unevaluated sum of two fp32 numbers, so candidates of different beams are told apart
 // well below the fp32 spacing of the scores, to which the result is rounded once.
@@ -197,6 +198,7 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
     __shared__ unsigned short places[THREADS / 32][kPlaces];
     __shared__ float sums[THREADS / 32];
     __shared__ unsigned long long cand[kCap];
+    static_assert(kCap == 2 * THREADS && THREADS == 256);
     const int tid = threadIdx.x, lane = lane_id();
     const int b = row / p.W, w = row - b * p.W;
     const int v0 = piece * p.piece_len, len = min(p.V - v0, p.piece_len);
@@ -247,7 +249,7 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
     if (lane == 0) tops_of[warp_id()] = mine;
     if (tid == 0) found = 0, bound = 0;
     __syncthreads();
-    const unsigned least = kth_largest<THREADS>(groups, count, K, &bound);
+    unsigned least = kth_largest<THREADS>(groups, count, K, &bound);  // K logits at least reach it
     unsigned most = tops_of[0];
 #pragma unroll
     for (int i = 1; i < THREADS / 32; ++i) most = max(most, tops_of[i]);
@@ -263,13 +265,16 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
         const int at = atomicAdd(&found, 1);
         if (at < kCap) cand[at] = key_of(v, place);
     };
-    const float bar = value_of(least);
     // First the logits that reach the bound: what is above the next lower number (below +0 that is not -0; -inf is
-    // never a candidate).  Where these are too many, those above the bound.
+    // never a candidate).  Where these are too many, a few groups having most of what is to be had, those that were
+    // kept are a sample of them: the K-th largest of its pairs' maxima is the next bound, and the logits above that
+    // are collected, or those above the bound that was, where too few pairs exceed it.  (256 rows of 131072 bf16
+    // logits, all but a run of 1000 masked, K 64: 41 us, 177 by bisection at once; 80 rows of 50000, the last 848
+    // logits a piece's last, K 16: 23 and 49.)
     float over = least <= order_of(-INFINITY) ? -INFINITY : value_of(least - (least == 0x80000000u ? 2 : 1));
-    int n = 0;
+    int n = 0, pass = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
+    for (;; ++pass) {
         // The threads' tiles that have a logit to collect are listed and read again by the warp, a logit per
         // lane, eight reads in flight.
         if (__any_sync(kAll, m > over)) {
@@ -307,14 +312,17 @@ __device__ __forceinline__ void beam_piece(const BeamParams &p, int row, int pie
         }
         __syncthreads();
         n = found;
-        if (n <= kCap || pass == 1) break;
+        if (n <= kCap || pass == 2) break;
+        const unsigned pair = static_cast<unsigned>(max(cand[tid], cand[tid + THREADS]) >> 32);
+        groups[tid] = pair;
+        const int above = __syncthreads_count(pair > least);
+        if (tid == 0) found = 0, bound = 0;
         __syncthreads();
-        if (tid == 0) found = 0;
-        over = bar;
-        __syncthreads();
+        if (above >= K) least = kth_largest<THREADS>(groups, THREADS, K, &bound);
+        over = value_of(least);
     }
-    if (n > kCap || (over == bar && bar > -INFINITY)) {
-        // Too many reach the bound.  f(logit, its place in the piece) for this thread's logits of tiles that have
+    if (pass > 0) {
+        // Too many reached the first bound.  f(logit, its place in the piece) for this thread's logits of tiles that have
         // one of that order or a higher one
         auto each = [&](unsigned want, auto f) {
             for (int t = 0; t < tiles; ++t) {
@@ -582,7 +590,11 @@ __device__ __forceinline__ void beam_join(const BeamParams &p, int b, BeamBase *
         const int spot = there ? where[i] : 0;
         int rank = 0;
 #pragma unroll 4
-        for (int j = turn; j < n; j += share) rank += cand[j] > mine || (cand[j] == mine && where[j] < spot);
+        for (int j = turn; j < n; j += share) {
+            const unsigned long long other = cand[j];
+            const int at = where[j];  // read in any case: nothing waits for the comparison
+            rank += other > mine || (other == mine && at < spot);
+        }
         rank = sum_lanes(rank, share);
         if (there && turn == 0 && rank < K) {
             const int w = spot / V, v = spot - w * V;

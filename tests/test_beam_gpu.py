@@ -171,6 +171,26 @@ def test_masks_that_leave_some_tokens(cuda_lib, lowest, dtype):
                 check(cuda_lib, y, torch.tensor([[-1.0, -1.5]], device=DEV), K, exact=False)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [513, 848, 1024, 2000, 8192 + 600, 20000])
+def test_the_best_stand_in_few_places(cuda_lib, V, dtype):
+    """Short rows and ends of rows, and rows of which a range is allowed or far above the rest: few threads see all
+    that reach a bound, more than there is room for.  One beam, so that the order is the logits' and exact."""
+    x = normal(11, 2, 1, V, dtype=dtype)
+    s = torch.tensor([[-1.0], [-2.0]], device=DEV)
+    for K in (1, 9, 16, 17, 33, 64, 65, 128):
+        check(cuda_lib, x, s, K)
+        for lo, hi in ((0, V), (V - 600, V), (3, 520), (V // 3, V // 3 + 900), (V // 2 - 700, V // 2 + 900)):
+            lo, hi = max(lo, 0), min(hi, V)
+            for rest in (float("-inf"), torch.finfo(dtype).min, -20.0):
+                y = torch.full_like(x, rest)
+                y[..., lo:hi] = x[..., lo:hi]
+                check(cuda_lib, y, s, K)
+            y = x.clone()
+            y[..., lo:hi] += 30
+            check(cuda_lib, y, s, K)
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("at", [0, 8191, 8192, 12344])
 def test_a_row_that_is_no_distribution_offers_nothing(cuda_lib, value, at):
