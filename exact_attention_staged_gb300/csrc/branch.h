@@ -14,6 +14,7 @@ struct PageTables {
     int *refs;                // [num_pages] holders of each page
     int B, num_pages, max_pages, page_shift;
     int *status;              // device status word
+    int device;               // host only: the current device
 };
 
 struct PagedReserveParams {
@@ -101,17 +102,13 @@ constexpr int kBeamMaxK = 128;
 constexpr int kBeamMaxWidth = 2048;     // beams of a request
 cudaError_t launch_beam_select(const BeamParams &p, int type, int vec, cudaStream_t stream);
 
-// A launch of `clusters` clusters of `ctas` CTAs that may overlap the end of the grid before it.
+// A launch of `clusters` clusters of `ctas` CTAs that may overlap the end of the grid before it.  `smem` and the
+// kernel's static part are 48 KB at most, or allowed by allow_smem() before.
 template <class Params>
 cudaError_t launch_clusters(void (*kernel)(Params), int clusters, int ctas, int threads, size_t smem,
                             cudaStream_t stream, const Params &p) {
     if (ctas > 8) {  // more than every device has to allow
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
-    if (smem > 8 * 1024) {  // beside the static part
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

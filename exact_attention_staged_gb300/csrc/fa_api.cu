@@ -534,8 +534,7 @@ int check_tables(int *table, int *refs, int B, int num_pages, int page_size, int
     t->num_pages = num_pages;
     t->max_pages = max_pages;
     t->page_shift = c.page_shift;
-    int dev = 0;
-    return device_setup(&dev, &t->status);
+    return device_setup(&t->device, &t->status);
 }
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

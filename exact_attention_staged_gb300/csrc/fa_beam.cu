@@ -663,6 +663,7 @@ cudaError_t launch_vec(const BeamParams &p, cudaStream_t stream) {
                    : launch_overlapped(fa_beam_join_kernel<1024>, dim3(p.B), 1024, smem, stream, p);
     }
     const int slots = (p.W * p.pieces + p.ctas - 1) / p.ctas;
+    // 128 pieces in 16 CTAs: 10 KB at most, beside 36
     const size_t smem = slots * (p.K * sizeof(unsigned long long) + sizeof(float2)) + p.W * sizeof(BeamBase);
     return launch_clusters(fa_beam_cluster_kernel<TYPE, VEC>, p.B, p.ctas, kThreads, smem, stream, p);
 }

@@ -44,7 +44,6 @@
 // softmax groups.  MMA order per step: PV_0 of the step before, S_0, PV_1, S_1, as in the forward.
 #include "paged.cuh"
 
-#include <atomic>
 #include <type_traits>
 
 namespace fa {
@@ -1267,17 +1266,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_paged_merge_kernel(const 
                                 pack2<BF16>(acc[e + 1].x * inv, acc[e + 1].y * inv),
                                 pack2<BF16>(acc[e + 1].z * inv, acc[e + 1].w * inv));
     if (warp == 0) p.lse[static_cast<long>(tok0 + tok) * p.c.H + head] = row_lse(M, l);
-}
-
-// The dynamic shared memory of a kernel, allowed once per device (the attribute holds from then on).
-cudaError_t allow_smem(std::atomic<unsigned long long> &ready, const void *kernel, int bytes,
-                       int device) {
-    const unsigned long long bit = 1ull << (device & 63);
-    if ((ready.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
-    return e;
 }
 
 template <int D, bool BF16, int QT>

@@ -600,8 +600,12 @@ cudaError_t launch_paged_fork(PagedForkParams p, cudaStream_t stream) {
     while (p.shift > 0 && (static_cast<long>(p.t.B) << p.shift) > (p.shift > 3 ? 1024 : 24 * 1024)) --p.shift;
     const size_t bytes = sizeof(int) * p.t.B * (2 + (1ul << p.shift));
     if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            fa_paged_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        // most with one column of all sequences, or with the last that have two
+        constexpr int kMost = static_cast<int>(sizeof(int)) * 3 * kBranchMaxSeqs;
+        static_assert(kMost >= static_cast<int>(sizeof(int)) * (2 * 24 * 1024 / 2 + 24 * 1024));
+        static std::atomic<unsigned long long> ready{0};
+        const cudaError_t e =
+            allow_smem(ready, reinterpret_cast<const void *>(fa_paged_fork_kernel), kMost, p.t.device);
         if (e != cudaSuccess) return e;
     }
     return launch_overlapped(fa_paged_fork_kernel, dim3(((p.t.max_pages - 1) >> p.shift) + 1), kForkThreads,
@@ -621,7 +625,14 @@ ReserveShape reserve_shape(int T, int B, int num_pages, int page_size) {
 cudaError_t launch_paged_reserve(const PagedReserveParams &p, cudaStream_t stream) {
     const size_t smem = sizeof(int) * (p.t.B + 1);
     const ReserveShape s = reserve_shape(p.c.T, p.t.B, p.t.num_pages, 1 << p.t.page_shift);
+    // up to 4096 sequences (two items each): 16 KB, beside 5
     if (s.threads > 0) return launch_clusters(fa_paged_reserve_kernel, 1, s.ctas, s.threads, smem, stream, p);
+    if (smem > 32 * 1024) {
+        static std::atomic<unsigned long long> ready{0};
+        const cudaError_t e = allow_smem(ready, reinterpret_cast<const void *>(fa_paged_reserve_many_kernel),
+                                         sizeof(int) * (kBranchMaxSeqs + 1), p.t.device);
+        if (e != cudaSuccess) return e;
+    }
     return launch_clusters(fa_paged_reserve_many_kernel, 1, kReserveCtas, kReserveThreads, smem, stream, p);
 }
 

@@ -3,6 +3,8 @@
 
 #include "fa_internal.h"
 
+#include <atomic>
+
 namespace fa {
 
 // Rotary positions (see fa_rope.cu).  Strides in elements.
@@ -80,6 +82,18 @@ struct PagedMaps {
 constexpr int kPagedCtas = 152;      // one per SM
 
 constexpr int kErrIndex = -6;  // an index array on the device holds a value out of range
+
+// The dynamic shared memory of a kernel, allowed once per device (the attribute holds from then on).  All
+// host threads share the attribute, so `bytes` is the most that any call of the kernel asks for.
+inline cudaError_t allow_smem(std::atomic<unsigned long long> &ready, const void *kernel, int bytes,
+                              int device) {
+    const unsigned long long bit = 1ull << (device & 63);
+    if ((ready.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // A launch that may overlap the end of the grid before it in the stream (programmatic stream
 // serialization): the kernel calls griddep_wait() before it touches global memory, so only its
