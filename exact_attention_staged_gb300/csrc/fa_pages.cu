@@ -65,7 +65,9 @@ __global__ void __launch_bounds__(kFreeThreads) fa_paged_free_kernel(const Paged
 // Row b becomes row parents[b].  A block takes 2^shift columns of all rows, which are independent of the
 // others, into shared memory and writes them back permuted: in place, without a second table.  A page's
 // count changes by the row's new holders less one.  Rows that stay as they are and have no other child are
-// neither read nor written.
+// neither read nor written.  A count that ends below zero, a page having had more entries than were counted, is
+// put back to zero once the block's entries are all counted: on the way there it may be below zero where some
+// rows are dropped and others multiplied.
 constexpr int kForkThreads = 256;
 constexpr int kForkBatch = 4;  // entries of a thread in flight together
 
@@ -104,6 +106,8 @@ __global__ void __launch_bounds__(kForkThreads) fa_paged_fork_kernel(const Paged
         return x < entries && c < width && !(parent[b] == b && children[b] == 1);
     };
     auto place = [&](int x) { return static_cast<long>(x >> shift) * t.max_pages + c0 + c; };
+    auto real = [&](int e) { return e >= 0 && e < t.num_pages; };
+    bool below = false;
     for (int x0 = threadIdx.x; x0 < entries; x0 += kForkBatch * kForkThreads) {
         int e[kForkBatch];
 #pragma unroll
@@ -117,11 +121,18 @@ __global__ void __launch_bounds__(kForkThreads) fa_paged_fork_kernel(const Paged
             if (!used(x)) continue;
             tile[x] = e[k];
             const int more = children[x >> shift] - 1;
-            if (e[k] < 0 || more == 0) continue;
-            if (e[k] >= t.num_pages || atomicAdd(&t.refs[e[k]], more) + more < 0) page_report(t.status);
+            if (!real(e[k])) {
+                if (e[k] != -1) page_report(t.status);
+            } else if (more != 0 && atomicAdd(&t.refs[e[k]], more) + more < 0) {
+                below = true;
+            }
         }
     }
-    __syncthreads();
+    if (__syncthreads_or(below) != 0) {
+        for (int x = threadIdx.x; x < entries; x += kForkThreads)
+            if (used(x) && children[x >> shift] != 1 && real(tile[x]) && atomicMax(&t.refs[tile[x]], 0) < 0)
+                page_report(t.status);
+    }
     for (int x = threadIdx.x; x < entries; x += kForkThreads) {
         if (!used(x)) continue;
         const int b = x >> shift, q = parent[b];

@@ -383,7 +383,7 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
  * so always come to the same tables.  At most 16384 sequences (otherwise FA_ERR_UNSUPPORTED); calls on
  * one table or one refs array have to be ordered by the caller.  Values out of range are not
  * followed and reported as FA_ERR_INDEX by fa_sync_status(), as is a count that would fall below
- * zero or an entry to be moved whose page is free.
+ * zero (it is left at zero) or an entry to be moved whose page is free.
  *
  * fa_paged_reserve: after it, every page that the batch's new tokens (kv_len, q_start, T as in
  * fa_paged_append) will be written to is held by their sequence alone.  In order of sequence and
@@ -402,6 +402,8 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
  *   parents   : device int32 [B]: -1 leaves row b empty, parents[b] = b as it is; any row may have many
  *               children or none (its pages are given back).
  *   kv_len    : device int32 [B], permuted likewise (0 for an empty row), or NULL.
+ *   Entries out of range are handed on as they are; rows that stay as they are and have no other child are not
+ *   looked at.
  *
  * fa_paged_free: sequence b keeps the pages of its first keep_len[b] positions (device int32 [B]; 0: a
  * sequence that ends, less than its length: drafted tokens that were refused) and gives the others back.

@@ -81,11 +81,22 @@ class Cache:
         old = [list(row) for row in self.table]
         for b, p in enumerate(parents):
             self.table[b] = list(old[p]) if p >= 0 else [-1] * len(old[b])
-        for rows, by in ((old, -1), (self.table, 1)):
-            for row in rows:
-                for e in row:
-                    if 0 <= e < len(self.refs):
-                        self.refs[e] += by
+        children = [0] * B
+        for p in parents:
+            if p >= 0:
+                children[p] += 1
+        changed = set()
+        for b, row in enumerate(old):
+            if parents[b] == b and children[b] == 1:
+                continue  # not looked at
+            for e in row:
+                if self.real(e) and children[b] != 1:
+                    self.refs[e] += children[b] - 1
+                    changed.add(e)
+        for e in changed:
+            if self.refs[e] < 0:
+                self.errors.add("index")
+                self.refs[e] = 0
         if kv_len is not None:
             return [kv_len[p] if p >= 0 else 0 for p in parents]
         return None
