@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
     extern __shared__ int before[];  // [B + 1] items before each sequence's
     __shared__ int scratch[33];
     __shared__ int counts[2];               // this CTA's free pages and needs
+    __shared__ int low;                     // 1: some page has more entries than were counted
     __shared__ int fresh[kReserveThreads];  // free pages of ranks cta * threads on
     griddep_launch_dependents();
     griddep_wait();
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
     if (tid == 0) {
         before[B] = items;
         counts[0] = frees;
+        low = 0;
     }
     barrier();
     int free_before = free_mine, free_all = 0;
@@ -291,6 +293,10 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
         if (had) held = atomicSub(&t.refs[e], 1);
         else if (e != -1) page_report(t.status);
     }
+    if (held <= 0) {  // held by more entries than were counted
+        page_report(t.status);
+        for (int c = 0; c < ctas; ++c) *cluster.map_shared_rank(&low, c) = 1;
+    }
     barrier();
     if (had && __ldcg(&t.refs[e]) <= 0) atomicMin(&t.refs[e], INT_MIN + g);
     barrier();
@@ -302,9 +308,25 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
     int rank = block_scan(need, scratch, &sum);
     if (tid == 0) counts[1] = sum;
     barrier();
+    int page = -1;
+    auto fresh_page = [&](int r) { return *cluster.map_shared_rank(&fresh[r % threads], r / threads); };
     if (need) {
         for (int c = 0; c < cta; ++c) rank += *cluster.map_shared_rank(&counts[1], c);
-        const int page = rank < free_all ? *cluster.map_shared_rank(&fresh[rank % threads], rank / threads) : -1;
+        if (low == 0 && rank < free_all) page = fresh_page(rank);
+    }
+    if (low != 0) {
+        // A page that was listed as free may be kept by an item by now, and is left out.  There are enough others,
+        // as that item needs none.
+        for (int r = 0, left = rank; need && r < min(items, free_all); ++r) {
+            const int id = fresh_page(r);
+            if (__ldcg(&t.refs[id]) == 0 && left-- == 0) {
+                page = id;
+                break;
+            }
+        }
+        barrier();  // nobody takes a page while others look
+    }
+    if (need) {
         *at = page;
         if (page >= 0) {
             t.refs[page] = 1;
@@ -318,7 +340,6 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
             page_report(t.status, kErrFull);
         }
     }
-    if (held <= 0) page_report(t.status);  // held by more entries than were counted
     if (ctas > 1) cluster.sync();  // the others have read this CTA's shared memory
 }
 

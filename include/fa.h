@@ -393,8 +393,10 @@ int fa_paged_attn(const void *q, const void *k_pages, const void *v_pages, void 
  *               and row 2 the rows to copy, for every sequence whose first new token goes behind tokens
  *               on a page that it shared (-1, -1, 0 for the others): arguments for fa_paged_copy.
  *   Sequences with a length or offset out of range get nothing, and none does where offsets decrease.
- *   Where the free pages run out, the places that are left get -1 (FA_ERR_FULL from fa_sync_status): a shared page's hold is given
- *   back, nobody else's pages are touched, and appending there is refused as usual.
+ *   A page that more of the places hold than refs counts is reported (FA_ERR_INDEX) and kept by the first of them,
+ *   also where refs has it as free.
+ *   Where the free pages run out, the places that are left get -1 (FA_ERR_FULL from fa_sync_status): a shared
+ *   page's hold is given back, nobody else's pages are touched, and appending there is refused as usual.
  *   workspace : at least fa_paged_reserve_workspace_bytes() bytes, 16-byte aligned, as in fa_paged_attn (may be
  *               NULL when that is 0).
  *

@@ -122,6 +122,8 @@ class Cache:
                 writers.setdefault(self.table[b][i], []).append((b, i))
         keep = {w[0] for e, w in writers.items() if self.refs[e] <= len(w)}
         for e, w in writers.items():
+            if self.refs[e] < len(w):  # more entries than were counted
+                self.errors.add("index")
             self.refs[e] -= len(w)
         free = [e for e, r in enumerate(self.refs) if r == 0 and e not in writers]
         for b, i in writing:

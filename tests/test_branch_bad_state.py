@@ -1,5 +1,7 @@
 """The paged cache's upkeep on tables that are not as they should be: entries that are no pages, counts that are too
 low.  What is reported, and the state that is left, entry by entry; the definitions on the CPU first."""
+import random
+
 import pytest
 
 from oracle import branch
@@ -81,3 +83,71 @@ def test_fork_of_many_rows_of_pages_that_nobody_is_said_to_hold(cuda_lib):
         assert min(c.refs.tolist()) == 0
         c.o.errors.clear()
         c.reserve([1 if b == 1 else 0 for b in range(B)], [0, 0] + [1] * (B - 1), tokens=1)
+
+
+def undercounted(B, seed):
+    """B rows of two pages, the second partly filled and sometimes the row before's too; a quarter of the counts are
+    zero, so that pages which are in use look free, another one less than they should be."""
+    r = random.Random(seed)
+    table, refs = [], [0] * (4 * B + 40)
+    for b in range(B):
+        row = [2 * b + 11, 2 * b + 12, -1]
+        if b > 0 and r.random() < 0.3:
+            row[1] = table[b - 1][1]
+        table.append(row)
+        for e in row[:2]:
+            refs[e] += 1
+    for e, n in enumerate(refs):
+        refs[e] = r.choice([n, n, 0, max(n - 1, 0)])
+    return table, refs
+
+
+def lengths(B, seed):
+    """Half of the sequences write behind their two pages, the others on the second one."""
+    r = random.Random(seed)
+    n = [r.choice([1, 1, 5, 0]) for _ in range(B)]
+    return [13 + k if r.random() < 0.5 else 11 + k for k in n], [sum(n[:b]) for b in range(B + 1)]
+
+
+def test_oracle_reserve_gives_no_page_out_that_is_written_to():
+    """Page 1 is row 0's, though nobody is said to hold it: row 1 gets another one."""
+    o = branch.Cache([[1], [-1]], [1, 0, 0], 8)
+    copies = o.reserve([3, 1], [0, 1, 2])
+    assert o.table == [[1], [2]] and o.refs == [1, 1, 1] and o.errors == {"index"}
+    assert copies == [[-1, -1], [-1, -1], [0, 0]]
+    for seed in range(20):
+        table, refs = undercounted(30, seed)
+        lens, start = lengths(30, seed)
+        o = branch.Cache(table, refs, 8)
+        o.reserve(lens, start)
+        mine = [o.table[b][i] for b in range(30) if start[b + 1] > start[b]
+                for i in range((lens[b] - start[b + 1] + start[b]) // 8, (lens[b] - 1) // 8 + 1)]
+        assert len(set(mine)) == len(mine) and all(o.refs[e] >= 1 for e in mine)
+
+
+# a CTA, a larger one, a cluster, and the form for any number (sequences, or pages)
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,more", [(2, 0), (40, 0), (300, 0), (1200, 0), (3000, 0), (7000, 0), (40, 300000)])
+def test_reserve_gives_no_page_out_that_is_written_to(cuda_lib, B, more):
+    from test_branch_gpu import Pair, index
+    for seed in range(6):
+        table, refs = undercounted(B, seed)
+        lens, start = lengths(B, seed)
+        if start[-1] == 0:
+            continue
+        c = Pair(cuda_lib, B, 3, len(refs) + more, 8, table=table, refs=refs + [0] * more)
+        want = branch.Cache(table, refs, 8)
+        want.reserve(lens, start)
+        c.reserve(lens, start, tokens=start[-1], expect=cuda_lib.FA_ERR_INDEX if want.errors else 0)
+    # few pages: the last places get none
+    codes = {"index": cuda_lib.FA_ERR_INDEX, "full": cuda_lib.FA_ERR_FULL}
+    for seed in range(6):
+        table, refs = undercounted(B, seed)
+        refs = refs[:2 * B + 13]
+        lens, start = [12 if b % 3 == 0 else 17 for b in range(B)], list(range(B + 1))
+        c = Pair(cuda_lib, B, 3, len(refs), 8, table=table, refs=refs)
+        got = cuda_lib.paged_reserve(c.table, index(lens), c.refs, 8)
+        want = c.o.reserve(lens, start)
+        assert cuda_lib.sync_status() in ({codes[e] for e in c.o.errors} or {0})  # the first that was met
+        c.same()
+        assert got.tolist() == want
