@@ -502,7 +502,7 @@ __device__ __forceinline__ void compact_apply(const PagedCompactParams &p, int m
     }
 }
 
-// The lists, and, where p.apply is set, what follows from them.
+// The lists, and, where p.apply is set (a single CTA), what follows from them.
 __global__ void __launch_bounds__(kReserveThreads) fa_paged_compact_kernel(const PagedCompactParams p) {
     __shared__ int scratch[33];
     __shared__ int counts[2];  // this CTA's live pages; those of them before n
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_compact_kernel(const
         live += sum;
     }
     cluster.sync();  // the lists are there, and nobody's counts are read any more
-    if (p.apply) compact_apply(p, n - front, cta * static_cast<long>(kReserveThreads) + tid, ctas * kReserveThreads);
+    if (p.apply) compact_apply(p, n - front, tid, kReserveThreads);
 }
 
 __global__ void __launch_bounds__(256) fa_paged_apply_kernel(const PagedCompactParams p) {
@@ -669,11 +669,12 @@ cudaError_t launch_paged_reserve(const PagedReserveParams &p, cudaStream_t strea
 }
 
 cudaError_t launch_paged_compact(PagedCompactParams p, cudaStream_t stream) {
-    // in the same launch where that is short: 24000 entries of a pool of 17000 pages take 7 us more so
+    // Small pools and tables take one CTA, which applies the lists too: eight pages and entries of a thread at
+    // most (24000 entries of a pool of 17000 pages take 7 us more in the same launch).
     const long entries = static_cast<long>(p.t.B) * p.t.max_pages, most = std::max(entries, p.t.num_pages + 0l);
-    p.apply = most <= kReserveCtas * kReserveThreads ? 1 : 0;  // an entry of a thread at most
-    const cudaError_t e = launch_clusters(fa_paged_compact_kernel, 1, most <= 8 * kReserveThreads ? 1 : kReserveCtas,
-                                          kReserveThreads, 0, stream, p);
+    p.apply = most <= 8 * kReserveThreads ? 1 : 0;
+    const cudaError_t e = launch_clusters(fa_paged_compact_kernel, 1, p.apply ? 1 : kReserveCtas, kReserveThreads,
+                                          0, stream, p);
     if (e != cudaSuccess || p.apply) return e;
     const long blocks = std::min((most + 255) / 256, 152l * 8);
     return launch_overlapped(fa_paged_apply_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, p);
