@@ -65,9 +65,9 @@ __global__ void __launch_bounds__(kFreeThreads) fa_paged_free_kernel(const Paged
 // Row b becomes row parents[b].  A block takes 2^shift columns of all rows, which are independent of the
 // others, into shared memory and writes them back permuted: in place, without a second table.  A page's
 // count changes by the row's new holders less one.  Rows that stay as they are and have no other child are
-// neither read nor written.  A count that ends below zero, a page having had more entries than were counted, is
-// put back to zero once the block's entries are all counted: on the way there it may be below zero where some
-// rows are dropped and others multiplied.
+// neither read nor written.  Where an entry is no page, or a count falls below zero, the block looks at its entries
+// again once all are counted, reports, and puts to zero what is still below: a count that is too low may be
+// below zero on the way, some rows being dropped before others are multiplied.
 constexpr int kForkThreads = 256;
 constexpr int kForkBatch = 4;  // entries of a thread in flight together
 
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kForkThreads) fa_paged_fork_kernel(const Paged
     };
     auto place = [&](int x) { return static_cast<long>(x >> shift) * t.max_pages + c0 + c; };
     auto real = [&](int e) { return e >= 0 && e < t.num_pages; };
-    bool below = false;
+    bool bad = false;
     for (int x0 = threadIdx.x; x0 < entries; x0 += kForkBatch * kForkThreads) {
         int e[kForkBatch];
 #pragma unroll
@@ -121,17 +121,17 @@ __global__ void __launch_bounds__(kForkThreads) fa_paged_fork_kernel(const Paged
             if (!used(x)) continue;
             tile[x] = e[k];
             const int more = children[x >> shift] - 1;
-            if (!real(e[k])) {
-                if (e[k] != -1) page_report(t.status);
-            } else if (more != 0 && atomicAdd(&t.refs[e[k]], more) + more < 0) {
-                below = true;
-            }
+            bad |= static_cast<unsigned>(e[k]) + 1 > static_cast<unsigned>(t.num_pages);  // -1: none
+            if (more != 0 && real(e[k])) bad |= atomicAdd(&t.refs[e[k]], more) + more < 0;
         }
     }
-    if (__syncthreads_or(below) != 0) {
-        for (int x = threadIdx.x; x < entries; x += kForkThreads)
-            if (used(x) && children[x >> shift] != 1 && real(tile[x]) && atomicMax(&t.refs[tile[x]], 0) < 0)
+    if (__builtin_expect(__syncthreads_or(bad), 0)) {  // out of the way: in the loop below it took 2 us of 12 more
+#pragma unroll 1
+        for (int x = threadIdx.x; x < entries; x += kForkThreads) {
+            if (!used(x) || tile[x] == -1) continue;
+            if (!real(tile[x]) || (children[x >> shift] != 1 && atomicMax(&t.refs[tile[x]], 0) < 0))
                 page_report(t.status);
+        }
     }
     for (int x = threadIdx.x; x < entries; x += kForkThreads) {
         if (!used(x)) continue;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
 
     const int g = cta * threads + tid;  // this thread's item
     int b = 0, e = -1, held = 1, *at = nullptr;
-    bool had = false;
+    bool had = false, bad = false;
     if (g < items) {
         int r = B;  // before[b] <= g < before[r]
         while (r - b > 1) {
@@ -291,11 +291,7 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
         e = *at;
         had = e >= 0 && e < t.num_pages;
         if (had) held = atomicSub(&t.refs[e], 1);
-        else if (e != -1) page_report(t.status);
-    }
-    if (held <= 0) {  // held by more entries than were counted
-        page_report(t.status);
-        for (int c = 0; c < ctas; ++c) *cluster.map_shared_rank(&low, c) = 1;
+        else bad = e != -1;
     }
     barrier();
     if (had && __ldcg(&t.refs[e]) <= 0) atomicMin(&t.refs[e], INT_MIN + g);
@@ -305,8 +301,15 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
         t.refs[e] = 1;
         need = false;
     }
-    int rank = block_scan(need, scratch, &sum);
-    if (tid == 0) counts[1] = sum;
+    // items before this one that need a page, and, in the upper half, those whose page was held by more entries
+    // than were counted (the barriers do not wait for `held` so)
+    int rank = block_scan(need | (held <= 0) << 16, scratch, &sum);
+    rank &= 0xffff;
+    bad |= held <= 0;
+    if (tid == 0) counts[1] = sum & 0xffff;
+    if (sum >> 16 != 0)
+#pragma unroll 1
+        for (int c = 0; c < ctas; ++c) *cluster.map_shared_rank(&low, c) = 1;
     barrier();
     int page = -1;
     auto fresh_page = [&](int r) { return *cluster.map_shared_rank(&fresh[r % threads], r / threads); };
@@ -314,9 +317,10 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
         for (int c = 0; c < cta; ++c) rank += *cluster.map_shared_rank(&counts[1], c);
         if (low == 0 && rank < free_all) page = fresh_page(rank);
     }
-    if (low != 0) {
+    if (__builtin_expect(low != 0, 0)) {
         // A page that was listed as free may be kept by an item by now, and is left out.  There are enough others,
         // as that item needs none.
+#pragma unroll 1
         for (int r = 0, left = rank; need && r < min(items, free_all); ++r) {
             const int id = fresh_page(r);
             if (__ldcg(&t.refs[id]) == 0 && left-- == 0) {
@@ -340,6 +344,7 @@ __global__ void __launch_bounds__(kReserveThreads) fa_paged_reserve_kernel(const
             page_report(t.status, kErrFull);
         }
     }
+    if (bad) page_report(t.status);
     if (ctas > 1) cluster.sync();  // the others have read this CTA's shared memory
 }
 
