@@ -1,5 +1,6 @@
 /* binding.c - the per-call path of the Python binding for the calls that are short on the GPU (rotary
- * positions, the paged cache and its tables, beam selection): argument checks, result allocation and the call into libfa.so.
+ * positions, the paged cache and its tables, beam selection): argument checks, result allocation and the
+ * call into libfa.so.
  *
  * A single token's append or attention takes 3 to 10 us on the GPU; the same checks in Python and
  * ctypes took 15 to 22 us on the host, this module takes about half.  It knows nothing of torch but
@@ -632,8 +633,8 @@ static PyObject *py_reserve(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     long long page, T;
     if (count_args(n, 8) || first_device(a[0], "block_table", &dev)) return NULL;
     LEAVE_IF_AWAY(dev);
-    if (take_tables(a[0], a[2], dev, &table, &refs) || take(a[1], "kv_len", dev, &len) || take(a[4], "q_start", dev, &start) ||
-        take(a[6], "copies", dev, &copies) || take(a[7], "workspace", dev, &ws) ||
+    if (take_tables(a[0], a[2], dev, &table, &refs) || take(a[1], "kv_len", dev, &len) ||
+        take(a[4], "q_start", dev, &start) || take(a[6], "copies", dev, &copies) || take(a[7], "workspace", dev, &ws) ||
         int_arg(a[3], "page_size", &page))
         return NULL;
     const long long B = table.shape[0];
@@ -707,7 +708,8 @@ static PyObject *py_free(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     void *stream;
     if (count_args(n, 4) || first_device(a[0], "block_table", &dev)) return NULL;
     LEAVE_IF_AWAY(dev);
-    if (take_tables(a[0], a[2], dev, &table, &refs) || take(a[1], "keep_len", dev, &keep) || need_index(&keep, table.shape[0]) ||
+    if (take_tables(a[0], a[2], dev, &table, &refs) || take(a[1], "keep_len", dev, &keep) ||
+        need_index(&keep, table.shape[0]) ||
         int_arg(a[3], "page_size", &page) || stream_of(dev, &stream))
         return NULL;
     int code;
@@ -726,7 +728,8 @@ static PyObject *py_compact(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     long dev;
     if (count_args(n, 4) || first_device(a[0], "block_table", &dev)) return NULL;
     LEAVE_IF_AWAY(dev);
-    if (take_tables(a[0], a[1], dev, &table, &refs) || take(a[2], "moves", dev, &moves) || take(a[3], "count", dev, &count))
+    if (take_tables(a[0], a[1], dev, &table, &refs) || take(a[2], "moves", dev, &moves) ||
+        take(a[3], "count", dev, &count))
         return NULL;
     const long long pages = refs.shape[0], one[1] = {1};
     long long shape[2] = {2, pages > 1 ? pages / 2 : 1};
@@ -761,8 +764,8 @@ static PyObject *py_copy(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     void *stream;
     if (count_args(n, 6) || first_device(a[0], "k_pages", &dev)) return NULL;
     LEAVE_IF_AWAY(dev);
-    if (take(a[0], "k_pages", dev, &k) || take(a[1], "v_pages", dev, &v) || take(a[2], "src", dev, &src) || take(a[3], "dst", dev, &dst) ||
-        take(a[4], "rows", dev, &rows) || take(a[5], "count", dev, &count))
+    if (take(a[0], "k_pages", dev, &k) || take(a[1], "v_pages", dev, &v) || take(a[2], "src", dev, &src) ||
+        take(a[3], "dst", dev, &dst) || take(a[4], "rows", dev, &rows) || take(a[5], "count", dev, &count))
         return NULL;
     if (v.obj == NULL || (k.dims != 4 && k.dims != 5) || !same_shape(&k, &v) || k.dtype != v.dtype) {
         fail(PyExc_ValueError, "k_pages and v_pages must be [num_pages, H_kv, page_size, d] or [L, num_pages, "

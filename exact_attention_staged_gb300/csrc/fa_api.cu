@@ -542,9 +542,11 @@ bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 long reserve_items(int T, int B, int page_size) { return static_cast<long>(T) / page_size + 2l * B; }
 
 // Small calls take one launch, a cluster of up to 16 CTAs for each request: up to 128 tiles of 4096 logits in
-// all, those of odd rows (loaded one by one) counting twice.  That saves a launch and the workspace, 4 us on
-// the host; on the GPU one request of four beams over 131072 bf16 logits takes 12.3 us so and 10.3 in two
-// launches (a graph each), four of four over 32000 10.3 and 11.6, 16 of five over 50000 20.6 and 14.4.
+// all, those of odd rows (loaded one by one) counting twice.  That saves a launch and the workspace of calls made
+// one by one, not time on the GPU.  One request of four beams over 131072 bf16 logits: 12.8 us a call so and
+// 17.2 in two launches, but 8.4 and 7.5 a call in a captured row of twenty; four of four over 32000: 13.0 and 16.9,
+// 8.1 and 7.6; three beams over 997 fp32: 12.0 and 17.7, 6.9 and 6.6.  One of 32 beams over 4096 with 32 candidates is
+// slower both ways, 19.2 and 17.2, 19.3 and 14.1.
 constexpr int kBeamCtas = 16;
 bool beam_small(int B, int W, int V) {
     return static_cast<long>(B) * W * ((V + 4095l) / 4096) * (V % 4 != 0 ? 2 : 1) <= 128;
