@@ -17,12 +17,13 @@
 // those few places are read again.  The loop has neither barriers nor shared counters (collecting
 // candidates in it took 34 us for 256 rows of 131072 bf16 logits, of which streaming alone is 14.4).
 // Where more logits reach the bound than there is room for (equal ones, or few groups that have nearly all), the
-// bound is raised by those that were kept, twice at most; the K-th largest of what may still be too many (rows
-// that rise throughout) is found by bisection.
+// bound is raised by those that were kept, twice at most; the K-th largest of what may still be too many (fewer
+// groups than K have thousands of the largest) is found by bisection.
 //
 // s is formed as an unevaluated sum of two fp32 numbers and rounded to fp32 once.  Their order within a row, and that
 // of equal rows, is exact; between rows L is as good as its sum, which is fp32: off by 4.2e-6 at most, counting
-// roundings (rows of up to 160000 logits), and with that last rounding by up to 7e-7 where it was measured (logits of spread 1 to 10, six shapes).
+// roundings (rows of up to 160000 logits), and with that last rounding by up to 7e-7 where it was measured (logits
+// of spread 1 to 10, six shapes).
 #include "branch.h"
 
 #include <cooperative_groups.h>
